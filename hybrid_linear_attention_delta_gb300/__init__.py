@@ -26,7 +26,9 @@ EXPORTS = ("kda_prefill_varlen", "kda_prefill_varlen_retain", "kda_decode", "kda
            "kda_prefill_varlen_fused", "kda_decode_fused", "kda_fused_scratch_bytes",
            "kda_workspace_bytes",
            "kda_snapshot_count", "kda_device_status", "kda_status_string",
-           "kda_last_launch_count")
+           "kda_last_launch_count",
+           "kda_paged_plan", "kda_paged_append", "kda_paged_attn", "kda_verify_drafts",
+           "kda_paged_workspace_bytes")
 
 
 class KdaArgs(ctypes.Structure):
@@ -48,6 +50,36 @@ class KdaFusedArgs(ctypes.Structure):
 
 
 CONV_ACT = {"none": 0, "silu": 1}
+
+
+class KdaPagedArgs(ctypes.Structure):
+    """Mirror of ``kda_paged_args`` in include/kda_paged.h."""
+    _fields_ = [("B", ctypes.c_int32), ("T_total", ctypes.c_int32), ("Hq", ctypes.c_int32),
+                ("Hkv", ctypes.c_int32), ("d", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("stream", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t), ("ev_begin", ctypes.c_void_p),
+                ("ev_end", ctypes.c_void_p)]
+
+
+class KdaAppendArgs(ctypes.Structure):
+    """Mirror of ``kda_append_args`` in include/kda_paged.h."""
+    _fields_ = [("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p),
+                ("rope", ctypes.c_void_p), ("max_pos", ctypes.c_int32),
+                ("rot_dim", ctypes.c_int32), ("rope_mode", ctypes.c_int32),
+                ("norm_eps", ctypes.c_float)]
+
+
+class KdaVerifyArgs(ctypes.Structure):
+    """Mirror of ``kda_verify_args`` in include/kda_paged.h."""
+    _fields_ = [("N", ctypes.c_int32), ("n_draft", ctypes.c_int32), ("V", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("stream", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+                ("ev_begin", ctypes.c_void_p), ("ev_end", ctypes.c_void_p)]
+
+
+ROPE_MODE = {"half": 0, "interleaved": 1}
 
 
 class KdaError(RuntimeError):
@@ -98,6 +130,17 @@ def lib(path: Optional[str] = None) -> ctypes.CDLL:
         L.kda_decode_fused.restype = ctypes.c_int
         L.kda_fused_scratch_bytes.argtypes = [A]
         L.kda_fused_scratch_bytes.restype = ctypes.c_size_t
+        P = ctypes.POINTER(KdaPagedArgs)
+        L.kda_paged_workspace_bytes.argtypes = [P]
+        L.kda_paged_workspace_bytes.restype = ctypes.c_size_t
+        L.kda_paged_plan.argtypes = [V] * 11 + [P]
+        L.kda_paged_plan.restype = ctypes.c_int
+        L.kda_paged_append.argtypes = [V] * 6 + [ctypes.POINTER(KdaAppendArgs), P]
+        L.kda_paged_append.restype = ctypes.c_int
+        L.kda_paged_attn.argtypes = [V] * 7 + [ctypes.c_float, I32, P]
+        L.kda_paged_attn.restype = ctypes.c_int
+        L.kda_verify_drafts.argtypes = [V] * 8 + [ctypes.POINTER(KdaVerifyArgs)]
+        L.kda_verify_drafts.restype = ctypes.c_int
         if path:
             return L
         _lib = L
@@ -326,6 +369,215 @@ def kda_decode_fused(xq, xk, xv, g, beta, gate, conv_w, norm_w, slot_ids, state_
                                 ctypes.byref(f), ctypes.byref(a))
     if st != KDA_OK:
         raise KdaError(st, "kda_decode_fused")
+
+
+# ------------------------------------------- full-attention layers, draft verification
+
+def _check(name, t, shape, dtype, device):
+    """A tensor argument of the calls below: its shape (None: any extent), dtype
+    and device are what the library would otherwise take on trust."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.dim() != len(shape) or any(want is not None and have != want
+                                    for have, want in zip(t.shape, shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, wanted "
+                         f"{tuple('any' if s is None else s for s in shape)}")
+    if t.device != device or device.type != "cuda":
+        raise ValueError(f"{name} is on {t.device}; every tensor of a call is on one CUDA device")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+def _paged_call(what, device, stream, call):
+    """Runs one library call on ``device``: on ``stream``, or on that device's
+    current stream."""
+    import torch
+    with torch.cuda.device(device):
+        st = call(_stream_ptr(stream))
+    if st != KDA_OK:
+        raise KdaError(st, what)
+
+
+def _common(a, workspace, events, device):
+    import torch
+    _check("workspace", workspace, (None,), torch.uint8, device)
+    a.workspace = workspace.data_ptr()
+    a.workspace_bytes = workspace.numel()
+    if events is not None:
+        a.ev_begin = events[0].cuda_event
+        a.ev_end = events[1].cuda_event
+
+
+def kda_paged_workspace_bytes(T_total: int, Hq: int, Hkv: int, d: int) -> int:
+    a = KdaPagedArgs(T_total=T_total, Hq=Hq, Hkv=Hkv, d=d)
+    return int(lib().kda_paged_workspace_bytes(ctypes.byref(a)))
+
+
+def paged_workspace_for(T_total: int = 0, Hq: int = 0, Hkv: int = 0, d: int = 0, device="cuda"):
+    """A zero-filled workspace for kda_paged_attn on batches of up to T_total
+    tokens (and for the other calls of this section, which need 256 bytes: no
+    sizes).  Not to be shared with the calls of include/kda.h."""
+    import torch
+    n = kda_paged_workspace_bytes(T_total, Hq, Hkv, d) if Hq else 0
+    return torch.zeros(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def rope_table(max_pos: int, rot_dim: int, theta: float = 10000.0, device="cuda"):
+    """The rotation table of kda_paged_append, [max_pos, rot_dim] fp32: cosines,
+    then sines, of pos * theta^(-2i / rot_dim).  Angles in 64 bits: in fp32 the
+    angle of position 10^6 is off by 2^-4 of a radian.  Made once, and kept."""
+    import torch
+    if rot_dim <= 0 or rot_dim % 2 or max_pos <= 0:
+        raise ValueError("rope_table wants a positive, even rot_dim and max_pos > 0")
+    i = torch.arange(rot_dim // 2, dtype=torch.float64, device=device)
+    pos = torch.arange(max_pos, dtype=torch.float64, device=device)
+    angle = pos[:, None] * theta ** (-2.0 * i / rot_dim)
+    return torch.cat([angle.cos(), angle.sin()], 1).float()
+
+
+def kda_paged_plan(cu_seqlens, cached_lens, block_table, held, free_ring, ring, held_out,
+                   ring_out, kv_lens, positions, slot_map, *, page_size: int, workspace,
+                   stream=None, events=None) -> None:
+    """Pages, positions and cache slots of a step's new tokens (see
+    kda_paged_plan in include/kda_paged.h).  int32 CUDA tensors; block_table
+    [B, max_pages] and free_ring [n_pages] are updated in place."""
+    import torch
+    i32, dev = torch.int32, free_ring.device
+    B, T = held.numel(), slot_map.numel()
+    _check("cu_seqlens", cu_seqlens, (B + 1,), i32, dev)
+    for name, t in (("cached_lens", cached_lens), ("held", held), ("held_out", held_out),
+                    ("kv_lens", kv_lens)):
+        _check(name, t, (B,), i32, dev)
+    _check("block_table", block_table, (B, None), i32, dev)
+    _check("free_ring", free_ring, (None,), i32, dev)
+    _check("ring", ring, (2,), i32, dev)
+    _check("ring_out", ring_out, (2,), i32, dev)
+    _check("positions", positions, (T,), i32, dev)
+    _check("slot_map", slot_map, (T,), i32, dev)
+    a = KdaPagedArgs(B=B, T_total=T, page_size=int(page_size), n_pages=free_ring.numel(),
+                     max_pages=block_table.shape[1])
+    _common(a, workspace, events, dev)
+
+    def call(s):
+        a.stream = s
+        return lib().kda_paged_plan(
+            _ptr(cu_seqlens), _ptr(cached_lens), _ptr(block_table), _ptr(held), _ptr(free_ring),
+            _ptr(ring), _ptr(held_out), _ptr(ring_out), _ptr(kv_lens), _ptr(positions),
+            _ptr(slot_map), ctypes.byref(a))
+    _paged_call("kda_paged_plan", dev, stream, call)
+
+
+def _pages(k_pages, v_pages, dtype, dev):
+    _check("k_pages", k_pages, (None, None, None, None), dtype, dev)
+    _check("v_pages", v_pages, tuple(k_pages.shape), dtype, dev)
+
+
+def kda_paged_append(qkv, q_norm, k_norm, rope, positions, slot_map, q_out, k_pages, v_pages, *,
+                     workspace, rope_mode: str = "half", norm_eps: float = 1e-6, stream=None,
+                     events=None) -> None:
+    """Per-head RMSNorm and rotation of q and k, q out, k and v into their cache
+    slots (see kda_paged_append in include/kda_paged.h).  qkv [T, Hq + 2 Hkv, d];
+    q_norm, k_norm [d] fp32 or None; rope [max_pos, rot_dim] fp32 or None (see
+    rope_table); pages [n_pages, page_size, Hkv, d]."""
+    import torch
+    dt, dev = qkv.dtype, qkv.device
+    code = _dtype_code(qkv)
+    _pages(k_pages, v_pages, dt, dev)
+    n_pages, page_size, Hkv, d = k_pages.shape
+    _check("q_out", q_out, (None, None, d), dt, dev)
+    T, Hq = q_out.shape[:2]
+    _check("qkv", qkv, (T, Hq + 2 * Hkv, d), dt, dev)
+    for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
+        if w is not None:
+            _check(name, w, (d,), torch.float32, dev)
+    _check("slot_map", slot_map, (T,), torch.int32, dev)
+    if rope is not None:
+        _check("rope", rope, (None, None), torch.float32, dev)
+        _check("positions", positions, (T,), torch.int32, dev)
+    f = KdaAppendArgs(q_norm=_ptr(q_norm), k_norm=_ptr(k_norm), rope=_ptr(rope),
+                      max_pos=0 if rope is None else rope.shape[0],
+                      rot_dim=0 if rope is None else rope.shape[1],
+                      rope_mode=ROPE_MODE[rope_mode], norm_eps=float(norm_eps))
+    a = KdaPagedArgs(T_total=T, Hq=Hq, Hkv=Hkv, d=d, page_size=page_size, n_pages=n_pages,
+                     dtype=code)
+    _common(a, workspace, events, dev)
+
+    def call(s):
+        a.stream = s
+        return lib().kda_paged_append(_ptr(qkv), None if rope is None else _ptr(positions),
+                                      _ptr(slot_map), _ptr(q_out), _ptr(k_pages), _ptr(v_pages),
+                                      ctypes.byref(f), ctypes.byref(a))
+    _paged_call("kda_paged_append", dev, stream, call)
+
+
+def kda_paged_attn(q, k_pages, v_pages, block_table, cu_seqlens, kv_lens, out, *, workspace,
+                   scale: Optional[float] = None, causal: bool = True, stream=None,
+                   events=None) -> None:
+    """Attention of the requests' new tokens over their pages (see
+    kda_paged_attn in include/kda_paged.h).  q, out [T, Hq, d]; pages [n_pages,
+    page_size, Hkv, d]; block_table [B, max_pages], cu_seqlens [B + 1] and
+    kv_lens [B] int32.  scale: 1 / sqrt(d) when not given."""
+    import torch
+    dt, dev = q.dtype, q.device
+    code = _dtype_code(q)
+    _pages(k_pages, v_pages, dt, dev)
+    n_pages, page_size, Hkv, d = k_pages.shape
+    _check("q", q, (None, None, d), dt, dev)
+    T, Hq = q.shape[:2]
+    _check("out", out, (T, Hq, d), dt, dev)
+    _check("kv_lens", kv_lens, (None,), torch.int32, dev)
+    B = kv_lens.numel()
+    _check("cu_seqlens", cu_seqlens, (B + 1,), torch.int32, dev)
+    _check("block_table", block_table, (B, None), torch.int32, dev)
+    a = KdaPagedArgs(B=B, T_total=T, Hq=Hq, Hkv=Hkv, d=d, page_size=page_size, n_pages=n_pages,
+                     max_pages=block_table.shape[1], dtype=code)
+    _common(a, workspace, events, dev)
+    c = d ** -0.5 if scale is None else float(scale)
+
+    def call(s):
+        a.stream = s
+        return lib().kda_paged_attn(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(block_table),
+                                    _ptr(cu_seqlens), _ptr(kv_lens), _ptr(out), c,
+                                    int(bool(causal)), ctypes.byref(a))
+    _paged_call("kda_paged_attn", dev, stream, call)
+
+
+def kda_verify_drafts(target_probs, draft_probs, draft_tokens, u_accept, u_sample, accepted,
+                      tokens, draft_lens=None, *, workspace, stream=None, events=None) -> None:
+    """Which drafted tokens stand, and the token after them (see
+    kda_verify_drafts in include/kda_paged.h).  target_probs [N, n_draft + 1, V];
+    draft_probs [N, n_draft, V] or None (looked-up drafts); draft_tokens and
+    u_accept [N, n_draft]; u_sample [N].  accepted [N] is kda_decode_spec's
+    accepted_prev; tokens [N, n_draft + 1]."""
+    import torch
+    dt, dev = target_probs.dtype, target_probs.device
+    code = _dtype_code(target_probs)
+    _check("target_probs", target_probs, (None, None, None), dt, dev)
+    N, n1, V = target_probs.shape
+    if n1 < 1:
+        raise ValueError("target_probs has n_draft + 1 >= 1 rows per sequence")
+    if draft_probs is not None:
+        _check("draft_probs", draft_probs, (N, n1 - 1, V), dt, dev)
+    _check("draft_tokens", draft_tokens, (N, n1 - 1), torch.int32, dev)
+    _check("u_accept", u_accept, (N, n1 - 1), torch.float32, dev)
+    _check("u_sample", u_sample, (N,), torch.float32, dev)
+    _check("accepted", accepted, (N,), torch.int32, dev)
+    _check("tokens", tokens, (N, n1), torch.int32, dev)
+    if draft_lens is not None:
+        _check("draft_lens", draft_lens, (N,), torch.int32, dev)
+    a = KdaVerifyArgs(N=N, n_draft=n1 - 1, V=V, dtype=code)
+    _common(a, workspace, events, dev)
+
+    def call(s):
+        a.stream = s
+        return lib().kda_verify_drafts(_ptr(target_probs), _ptr(draft_probs), _ptr(draft_tokens),
+                                       _ptr(draft_lens), _ptr(u_accept), _ptr(u_sample),
+                                       _ptr(accepted), _ptr(tokens), ctypes.byref(a))
+    _paged_call("kda_verify_drafts", dev, stream, call)
 
 
 def kda_device_status(workspace, stream=None):

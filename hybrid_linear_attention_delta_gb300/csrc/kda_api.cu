@@ -8,6 +8,7 @@
 #include <utility>
 
 #include "kda_internal.cuh"
+#include "kda_paged.cuh"
 
 namespace {
 
@@ -72,6 +73,8 @@ void record(void *ev, cudaStream_t s) {
 }  // namespace
 
 namespace kda {
+
+void set_last_launches(int32_t n) { g_last_launches = n; }
 
 cudaError_t set_smem_limit_once(const void *func, int bytes) {
   static std::mutex mu;

@@ -1,0 +1,216 @@
+// kda_paged_sched.cuh -- how a paged attention call is cut over the CTAs.
+//
+// An item is (request, key/value head, run of query tokens) with all query
+// heads of the group: its rows share every key.  It costs the keys it sees
+// plus kItemCost keys for its start and end.  All items in a row (request,
+// head, run) make one long line of cost; CTA c of the grid takes the stretch
+// [c * per_cta, (c + 1) * per_cta).  A stretch cuts at most its first and its
+// last item; cuts fall on key tiles.  Long contexts of few rows are so spread
+// over all SMs, and a batch of many items needs no balance between long and
+// short ones.  The pieces of a cut item leave partial results (output, maximum
+// and sum of each row) and the last one to arrive joins them, in order.
+//
+// Every CTA finds its stretch itself from cu_seqlens and kv_lens (a block scan
+// of one number per request), so no plan is stored and nothing is cleared.
+#pragma once
+
+#include "kda_paged.cuh"
+
+namespace kda {
+
+struct PagedItems {
+  int32_t tokens;  // query tokens of an item at most
+  int32_t tile;    // keys of a tile
+};
+
+// Fixed cost of an item, in keys.
+constexpr int kItemCost = 128;
+
+// A request as the line sees it; n = 0 for one that is skipped.
+struct PagedReq {
+  int32_t tok0, n, kv;
+};
+
+struct PagedPiece {
+  int32_t tok0;      // first token row of the item
+  int32_t n;         // query tokens of the item (0: no more pieces)
+  int32_t head;      // key/value head
+  int32_t req;       // request
+  int32_t kv;        // keys of the request
+  int32_t seen0;     // keys that the item's first token sees (may be below 1)
+  int32_t tile0, tile1;  // key tiles of this piece
+  int32_t n_pieces;  // pieces of the item (0: this one only)
+  int32_t index;     // which of them
+  int32_t first_cta; // CTA of the item's first piece (n_pieces > 0)
+  int32_t first_slot;  // partial-result slot of that piece; piece k > 0 is in slot
+                       // 2 * (first_cta + k)
+};
+
+__device__ __forceinline__ int64_t paged_prefix(const PagedReq &r, int64_t i, int tokens,
+                                                bool causal) {
+  // cost of the request's first i runs of one head
+  const int64_t n = (r.n + tokens - 1) / tokens;
+  if (!causal || r.kv < r.n) return i * (r.kv + kItemCost);
+  int64_t c = i * (r.kv - r.n + kItemCost) + (int64_t)tokens * (i * (i + 1) / 2);
+  if (i == n) c += r.n - n * tokens;  // the last run is shorter
+  return c;
+}
+__device__ __forceinline__ int64_t paged_head_cost(const PagedReq &r, int tokens, bool causal) {
+  return r.n == 0 ? 0 : paged_prefix(r, (r.n + tokens - 1) / tokens, tokens, causal);
+}
+
+__device__ __forceinline__ PagedReq paged_request(const PagedAttnPlan &p, int b) {
+  PagedReq r;
+  r.tok0 = p.cu[b];
+  r.n = p.cu[b + 1] - r.tok0;
+  r.kv = p.kv_lens[b];
+  if (r.n <= 0 || r.kv < 0 || (int64_t)r.kv > (int64_t)p.max_pages * p.page_size) r.n = 0;
+  return r;
+}
+
+struct PagedSched {
+  int64_t pos, end, base;  // place on the line, end of the stretch, start of request b
+  int64_t per_cta;
+  int32_t b;
+  PagedReq r;
+
+  // All threads of the CTA; scratch: THREADS / 32 + 4 words of 64 bits.  False:
+  // bad cu_seqlens (nothing is to be done).
+  template <int THREADS>
+  __device__ bool init(const PagedAttnPlan &p, const PagedItems &it, int64_t *scratch) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int W = THREADS / 32;
+    const int run = (p.B + THREADS - 1) / THREADS;
+    const int b0 = min(p.B, tid * run), b1 = min(p.B, b0 + run);
+    int64_t mine = 0;
+    bool bad = tid == 0 && (p.cu[0] != 0 || p.cu[p.B] > p.T);
+    for (int i = b0; i < b1; ++i) {
+      bad |= p.cu[i + 1] < p.cu[i];
+      const PagedReq q = paged_request(p, i);
+      const int kvl = p.kv_lens[i];
+      if (blockIdx.x == 0 && (kvl < 0 || (int64_t)kvl > (int64_t)p.max_pages * p.page_size))
+        raise_error(p.err, ERR_BAD_LEN);
+      mine += paged_head_cost(q, it.tokens, p.causal) * p.Hkv;
+    }
+    int64_t inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    if (lane == 31) scratch[warp] = inc;
+    if (tid == 0) scratch[W] = -1;
+    if (__syncthreads_or(bad)) {
+      if (blockIdx.x == 0 && tid == 0) raise_error(p.err, ERR_BAD_CU);
+      return false;
+    }
+    int64_t before = inc - mine, total = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      if (w < warp) before += scratch[w];
+      total += scratch[w];
+    }
+    // no stretch shorter than two tiles and an item's fixed cost: a cut costs a
+    // round trip of partials, and a stretch inside an item always has a tile
+    per_cta = max((int64_t)2 * it.tile + kItemCost, (total + gridDim.x - 1) / gridDim.x);
+    pos = blockIdx.x * per_cta;
+    end = min(total, pos + per_cta);
+    if (pos < end && before <= pos && pos < before + mine) {  // this thread's requests hold it
+      int64_t at = before;
+      for (int i = b0; i < b1; ++i) {
+        const int64_t c = paged_head_cost(paged_request(p, i), it.tokens, p.causal) * p.Hkv;
+        if (pos < at + c) {
+          scratch[W] = i;
+          scratch[W + 1] = at;
+          break;
+        }
+        at += c;
+      }
+    }
+    __syncthreads();
+    b = (int32_t)scratch[W];
+    base = scratch[W + 1];
+    if (b < 0) pos = end = 0;
+    else r = paged_request(p, b);
+    return true;
+  }
+
+  // The tile that a cut at cost x of the item falls on.  Items of a request
+  // that brings more tokens than it has keys (their cost does not follow the
+  // keys they see) are left whole.
+  static __device__ __forceinline__ int cut(int64_t x, int64_t cost, int tiles, int tile,
+                                            bool whole) {
+    if (x <= 0) return 0;
+    if (x >= cost) return tiles;
+    if (whole) return 0;
+    const int64_t k = x - kItemCost + tile / 2;
+    return k <= 0 ? 0 : (int)min((int64_t)tiles, k / tile);
+  }
+
+  // The next piece of the stretch (n = 0 when there is none).
+  __device__ PagedPiece next(const PagedAttnPlan &p, const PagedItems &it) {
+    PagedPiece o;
+    o.n = 0;
+    while (pos < end) {
+      const int64_t head_cost = paged_head_cost(r, it.tokens, p.causal);
+      if (pos >= base + head_cost * p.Hkv) {  // on to the next request with work
+        base += head_cost * p.Hkv;
+        if (++b >= p.B) {
+          pos = end;
+          break;
+        }
+        r = paged_request(p, b);
+        continue;
+      }
+      const int head = (int)((pos - base) / head_cost);
+      const int64_t head_base = base + head * head_cost;
+      const int runs = (r.n + it.tokens - 1) / it.tokens;
+      int lo = 0, hi = runs - 1;  // largest run that starts at or before pos
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (head_base + paged_prefix(r, mid, it.tokens, p.causal) <= pos) lo = mid; else hi = mid - 1;
+      }
+      const int64_t start = head_base + paged_prefix(r, lo, it.tokens, p.causal);
+      const int64_t cost = head_base + paged_prefix(r, lo + 1, it.tokens, p.causal) - start;
+      const int64_t stop = min(end, start + cost);
+      o.n = min(it.tokens, r.n - lo * it.tokens);
+      o.tok0 = r.tok0 + lo * it.tokens;
+      o.head = head;
+      o.req = b;
+      o.kv = r.kv;
+      o.seen0 = p.causal ? r.kv - r.n + lo * it.tokens + 1 : r.kv;
+      const int keys = max(0, p.causal ? min(r.kv, o.seen0 + o.n - 1) : r.kv);
+      const int tiles = (keys + it.tile - 1) / it.tile;
+      const bool whole = p.causal && r.kv < r.n;
+      const bool starts = pos == start;
+      o.tile0 = cut(pos - start, cost, tiles, it.tile, whole);
+      o.tile1 = cut(stop - start, cost, tiles, it.tile, whole);
+      o.n_pieces = o.index = o.first_cta = o.first_slot = 0;
+      pos = stop;
+      const int64_t c0 = start / per_cta, c1 = (start + cost - 1) / per_cta;
+      if (c0 != c1) {
+        // an item without keys belongs to the CTA it starts in
+        if (tiles == 0 ? !starts : o.tile0 == o.tile1) continue;
+        // only the first and the last stretch can be left without a tile
+        const bool skip0 = cut((c0 + 1) * per_cta - start, cost, tiles, it.tile, whole) == 0;
+        const bool skip1 = cut(c1 * per_cta - start, cost, tiles, it.tile, whole) == tiles;
+        const int n = (int)(c1 - c0) + 1 - skip0 - skip1;
+        if (tiles > 0 && !whole && n > 1) {
+          o.n_pieces = n;
+          o.index = (int)blockIdx.x - (int)c0 - skip0;
+          o.first_cta = (int32_t)c0 + skip0;
+          o.first_slot = 2 * o.first_cta + !skip0;
+        }
+      }
+      return o;
+    }
+    o.n = 0;
+    return o;
+  }
+};
+
+__device__ __forceinline__ int paged_part_slot(const PagedPiece &o, int k) {
+  return k == 0 ? o.first_slot : 2 * (o.first_cta + k);
+}
+
+}  // namespace kda

@@ -1,0 +1,278 @@
+// kda_paged_simt.cu -- paged attention in fp32 arithmetic (CUDA cores).
+//
+//     out = sum_j softmax_j(scale q . k_j) v_j
+//
+// One pass over the keys with a running maximum m and sum l per row: for each
+// tile of keys, P = exp(S - m'), l = l exp(m - m') + sum P, O = O exp(m - m') +
+// P V.  A tile's scores and probabilities stay in registers and shared memory.
+// Thread (ty, tx) of the 16 x 16 holds rows ty * R .. + R - 1 and keys tx + 16 j of
+// the scores, and the same rows with D / 16 channels of the output.  Bound by
+// the fp32 pipes and the shared-memory reads that feed them.
+#include "kda_paged_sched.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kKeys = 64;  // keys of a tile
+
+template <int D, int R>
+struct Smem {
+  static constexpr int kRows = 16 * R;
+  static constexpr int kLd = D + 4;      // floats of a Q / K row
+  static constexpr int kLdP = kKeys + 4;
+  float q[kRows * kLd];
+  float k[kKeys * kLd];
+  float v[kKeys * D];
+  float p[kRows * kLdP];
+  int page[kKeys];
+  PagedPiece piece;
+  int64_t scratch[kThreads / 32 + 4];
+  int last;
+};
+
+template <typename T>
+__device__ __forceinline__ float4 load4(const T *p) {
+  if constexpr (sizeof(T) == 4) {
+    return *reinterpret_cast<const float4 *>(p);
+  } else {
+    const uint2 w = *reinterpret_cast<const uint2 *>(p);
+    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
+                       __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u));
+  }
+}
+
+// Element offset of row r of an item: token r / G, query head r % G of the group.
+__device__ __forceinline__ int64_t row_offset(const PagedAttnPlan &p, const PagedPiece &o, int r) {
+  const int t = r / p.G;
+  return ((int64_t)(o.tok0 + t) * p.Hq + o.head * p.G + (r - t * p.G)) * p.d;
+}
+
+template <typename T, int D, int R>
+__global__ void __launch_bounds__(kThreads) attn_kernel(PagedAttnPlan p) {
+  extern __shared__ __align__(16) unsigned char raw[];
+  using S = Smem<D, R>;
+  S &sm = *reinterpret_cast<S *>(raw);
+  constexpr int NC = D / 16;  // output channels of a thread, in groups of four
+  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+  const PagedItems items = {S::kRows / p.G, kKeys};
+  PagedSched sched;
+  if (!sched.init<kThreads>(p, items, sm.scratch)) return;
+  const float c = p.scale * 1.4426950408889634f;  // scores in powers of two
+
+  for (;;) {
+    __syncthreads();
+    if (tid == 0) sm.piece = sched.next(p, items);
+    __syncthreads();
+    const PagedPiece o = sm.piece;
+    if (o.n == 0) break;
+    const int rows = o.n * p.G;
+    const T *q = static_cast<const T *>(p.q);
+    for (int i = tid; i < S::kRows * (D / 4); i += kThreads) {
+      const int r = i / (D / 4), e = (i % (D / 4)) * 4;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < rows) x = load4<T>(q + row_offset(p, o, r) + e);
+      *reinterpret_cast<float4 *>(&sm.q[r * S::kLd + e]) = x;
+    }
+    int lim[R];  // keys that each row sees
+    float m[R], l[R], acc[R][NC];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int r = ty * R + i;
+      lim[i] = r < rows ? min(o.kv, p.causal ? o.seen0 + r / p.G : o.kv) : 0;
+      m[i] = -INFINITY, l[i] = 0.f;
+#pragma unroll
+      for (int j = 0; j < NC; ++j) acc[i][j] = 0.f;
+    }
+
+    for (int tile = o.tile0; tile < o.tile1; ++tile) {
+      const int key0 = tile * kKeys;
+      __syncthreads();
+      if (tid < kKeys) {
+        const int key = key0 + tid;
+        int page = -1;
+        if (key < o.kv) {
+          page = p.table[(int64_t)o.req * p.max_pages + (key >> p.page_shift)];
+          if (page < 0 || page >= p.n_pages) {
+            raise_error(p.err, ERR_BAD_PAGE);
+            page = -1;
+          }
+        }
+        sm.page[tid] = page;
+      }
+      __syncthreads();
+      for (int i = tid; i < kKeys * (D / 4); i += kThreads) {
+        const int k = i / (D / 4), e = (i % (D / 4)) * 4;
+        const int page = sm.page[k];
+        float4 kx = make_float4(0.f, 0.f, 0.f, 0.f), vx = kx;
+        if (page >= 0) {
+          const int64_t at =
+              ((((int64_t)page << p.page_shift) + ((key0 + k) & (p.page_size - 1))) * p.Hkv +
+               o.head) * D + e;
+          kx = load4<T>(static_cast<const T *>(p.k) + at);
+          vx = load4<T>(static_cast<const T *>(p.v) + at);
+        }
+        *reinterpret_cast<float4 *>(&sm.k[k * S::kLd + e]) = kx;
+        *reinterpret_cast<float4 *>(&sm.v[k * D + e]) = vx;
+      }
+      __syncthreads();
+
+      float s[R][4];
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 4
+      for (int e = 0; e < D; e += 4) {
+        float4 a[R], b[4];
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+          a[i] = *reinterpret_cast<const float4 *>(&sm.q[(ty * R + i) * S::kLd + e]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          b[j] = *reinterpret_cast<const float4 *>(&sm.k[(tx + 16 * j) * S::kLd + e]);
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            s[i][j] = fmaf(a[i].x, b[j].x, s[i][j]);
+            s[i][j] = fmaf(a[i].y, b[j].y, s[i][j]);
+            s[i][j] = fmaf(a[i].z, b[j].z, s[i][j]);
+            s[i][j] = fmaf(a[i].w, b[j].w, s[i][j]);
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        float top = m[i];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s[i][j] = key0 + tx + 16 * j < lim[i] ? s[i][j] * c : -INFINITY;
+          top = fmaxf(top, s[i][j]);
+        }
+#pragma unroll
+        for (int x = 8; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        const float ref = top == -INFINITY ? 0.f : top;  // a row that has seen no key yet
+        const float keep = exp2f(m[i] - ref);
+        m[i] = top;
+        l[i] *= keep;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float e = exp2f(s[i][j] - ref);
+          l[i] += e;  // this thread's keys only; joined at the end
+          sm.p[(ty * R + i) * S::kLdP + tx + 16 * j] = e;
+        }
+#pragma unroll
+        for (int j = 0; j < NC; ++j) acc[i][j] *= keep;
+      }
+      __syncwarp();  // a row's sixteen threads are in one warp
+#pragma unroll 4
+      for (int k = 0; k < kKeys; k += 4) {
+        float4 w[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+          w[i] = *reinterpret_cast<const float4 *>(&sm.p[(ty * R + i) * S::kLdP + k]);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+          for (int j = 0; j < NC; j += 4) {
+            const float4 x = *reinterpret_cast<const float4 *>(&sm.v[(k + kk) * D + j * 16 + tx * 4]);
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+              const float f = kk == 0 ? w[i].x : kk == 1 ? w[i].y : kk == 2 ? w[i].z : w[i].w;
+              acc[i][j] = fmaf(f, x.x, acc[i][j]);
+              acc[i][j + 1] = fmaf(f, x.y, acc[i][j + 1]);
+              acc[i][j + 2] = fmaf(f, x.z, acc[i][j + 2]);
+              acc[i][j + 3] = fmaf(f, x.w, acc[i][j + 3]);
+            }
+          }
+      }
+    }
+
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int x = 8; x > 0; x >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
+
+    if (o.n_pieces > 0) {
+      const int64_t slot = paged_part_slot(o, o.index);
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const int r = ty * R + i;
+        if (r >= rows) continue;
+        const int64_t at = slot * p.part_rows + r;
+        if (tx == 0) p.part_ml[at * 2] = m[i], p.part_ml[at * 2 + 1] = l[i];
+#pragma unroll
+        for (int j = 0; j < NC; j += 4)
+          *reinterpret_cast<float4 *>(&p.part[at * D + j * 16 + tx * 4]) =
+              make_float4(acc[i][j], acc[i][j + 1], acc[i][j + 2], acc[i][j + 3]);
+      }
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        uint32_t *count = p.arrivals + o.first_cta * 2;
+        sm.last = atomicAdd(count, 1u) == (uint32_t)o.n_pieces - 1;
+        if (sm.last) *count = 0;  // as it was found
+        __threadfence();
+      }
+      __syncthreads();
+      if (!sm.last) continue;
+      // the last piece to arrive joins them all, first piece first
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const int r = ty * R + i;
+        m[i] = -INFINITY, l[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < NC; ++j) acc[i][j] = 0.f;
+        if (r >= rows) continue;
+        for (int k = 0; k < o.n_pieces; ++k)
+          m[i] = fmaxf(m[i], __ldcg(&p.part_ml[((int64_t)paged_part_slot(o, k) * p.part_rows + r) * 2]));
+        const float ref = m[i] == -INFINITY ? 0.f : m[i];
+        for (int k = 0; k < o.n_pieces; ++k) {
+          const int64_t at = (int64_t)paged_part_slot(o, k) * p.part_rows + r;
+          const float w = exp2f(__ldcg(&p.part_ml[at * 2]) - ref);
+          l[i] = fmaf(w, __ldcg(&p.part_ml[at * 2 + 1]), l[i]);
+#pragma unroll
+          for (int j = 0; j < NC; j += 4) {
+            const float4 x = __ldcg(reinterpret_cast<const float4 *>(&p.part[at * D + j * 16 + tx * 4]));
+            acc[i][j] = fmaf(w, x.x, acc[i][j]);
+            acc[i][j + 1] = fmaf(w, x.y, acc[i][j + 1]);
+            acc[i][j + 2] = fmaf(w, x.z, acc[i][j + 2]);
+            acc[i][j + 3] = fmaf(w, x.w, acc[i][j + 3]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int r = ty * R + i;
+      if (r >= rows) continue;
+      const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;  // a row without keys: zeros
+      T *out = static_cast<T *>(p.out) + row_offset(p, o, r);
+#pragma unroll
+      for (int j = 0; j < NC; ++j)
+        out[(j / 4) * 64 + tx * 4 + j % 4] = from_f32<T>(acc[i][j] * inv);
+    }
+  }
+}
+
+template <typename T, int D, int R>
+cudaError_t launch_r(const PagedAttnPlan &p) {
+  const void *f = reinterpret_cast<const void *>(attn_kernel<T, D, R>);
+  const cudaError_t e = set_smem_limit_once(f, sizeof(Smem<D, R>));
+  if (e != cudaSuccess) return e;
+  attn_kernel<T, D, R><<<kPagedMaxCtas, kThreads, sizeof(Smem<D, R>), p.stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_t(const PagedAttnPlan &p) {
+  return p.d == 128 ? launch_r<T, 128, 4>(p) : launch_r<T, 64, 4>(p);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_attn_simt(const PagedAttnPlan &p) {
+  return p.dtype == KDA_BF16 ? launch_t<__nv_bfloat16>(p) : launch_t<float>(p);
+}
+
+}  // namespace kda

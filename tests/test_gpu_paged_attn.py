@@ -1,0 +1,240 @@
+"""GPU parity of kda_paged_attn with a 64-bit plain form: one token to long
+chunks, odd lengths and tile borders, every page size and group size, rows that
+see nothing, pages that end inside a tile, poisoned memory around the keys;
+determinism, graphs and the device-side checks."""
+
+import pytest
+import torch
+
+import hybrid_linear_attention_delta_gb300 as kda
+from kda_cases import TOL
+from paged_cases import AttnCase
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    kda.build()
+    kda.lib()
+
+
+def _run(case, causal=True, scale=None, dev=None, ws=None, out=None):
+    t = dev or case.cuda()
+    if out is None:
+        out = torch.full_like(t["q"], AttnCase.MARK)
+    if ws is None:
+        ws = kda.paged_workspace_for(t["q"].shape[0], case.Hq, case.Hkv, case.d)
+    kda.kda_paged_attn(t["q"], t["k"], t["v"], t["table"], t["cu"], t["kv"], out, scale=scale,
+                       causal=causal, workspace=ws)
+    return out, ws
+
+
+def _check(case, causal=True, scale=None, norm_bar=True):
+    out, ws = _run(case, causal, scale)
+    assert kda.kda_device_status(ws) == (kda.KDA_OK, 0)
+    assert kda.kda_last_launch_count() == 1
+    used = int(case.cu[-1])
+    ref, size, top = case.reference(causal, scale)
+    got = out.double().cpu()
+    assert torch.isfinite(got).all()
+    err = (got - ref)[:used].abs()
+    over = err > case.bound(ref, size, top)[:used]
+    assert not over.any(), (float(err.max()), int(over.sum()), over.nonzero()[:4].tolist())
+    name = "bf16" if case.dtype == torch.bfloat16 else "f32"
+    if norm_bar and used and float(ref.norm()) > 0:
+        assert float((got - ref)[:used].norm() / ref.norm()) <= TOL[name]
+    assert (out[used:] == AttnCase.MARK).all()          # rows behind the last request
+    assert int(ws[256:256 + 8 * 152].sum()) == 0        # counters are left as they were found
+    return out
+
+
+LENGTHS = [
+    ([1], [1]), ([1], [777]), ([1, 1, 1], [127, 128, 129]), ([5], [5]), ([64], [200]),
+    ([130], [130]), ([1, 0, 7, 33], [40, 0, 7, 300]), ([200, 3], [200, 1000]),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new,total", LENGTHS)
+def test_lengths(dtype, d, new, total):
+    _check(AttnCase(new, total, Hq=8, Hkv=2, d=d, page=16, dtype=dtype, seed=len(new), pad=3))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+def test_page_sizes(dtype, page):
+    _check(AttnCase([70, 1, 9], [333, 257, 256], Hq=4, Hkv=2, d=128, page=page, dtype=dtype,
+                    seed=page))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (4, 4), (3, 1), (10, 2), (7, 1), (16, 1), (24, 1),
+                                    (64, 1), (33, 3)])
+def test_groups(dtype, Hq, Hkv):
+    """Groups that fill a tile of rows and groups that leave some of it empty."""
+    _check(AttnCase([43, 1, 150], [300, 200, 151], Hq=Hq, Hkv=Hkv, d=64, page=32, dtype=dtype,
+                    seed=Hq))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("causal", [True, False])
+def test_rows_that_see_nothing(dtype, causal):
+    """No keys at all, and more new tokens than keys: their rows are zeros."""
+    case = AttnCase([4, 9, 1, 300], [0, 3, 50, 20], Hq=6, Hkv=2, d=64, page=16, dtype=dtype)
+    out = _check(case, causal)
+    assert (out[:4] == 0).all()
+    if causal:
+        assert (out[4:10] == 0).all() and (out[10:13] != 0).any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_not_causal_and_scale(dtype):
+    case = AttnCase([40, 1], [500, 77], Hq=4, Hkv=1, d=128, page=64, dtype=dtype)
+    _check(case, causal=False)
+    _check(case, scale=0.02)
+    _check(case, scale=0.0)
+    _check(case, scale=-0.05)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Hq,Hkv,d", [(1, 1, 128), (8, 1, 128), (16, 8, 64)])
+def test_long_context_is_split_and_joined(dtype, Hq, Hkv, d):
+    """Few rows over many keys: pieces on every SM, joined in order."""
+    case = AttnCase([1], [20011], Hq=Hq, Hkv=Hkv, d=d, page=16, dtype=dtype, seed=5)
+    a = _check(case)
+    b, _ = _run(case)
+    assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_large_scores(dtype):
+    """Scores that differ by hundreds: the running maximum moves often and a few
+    keys carry all the weight.  (A score of 300 is summed to 300 half steps of
+    fp32, which the element bound counts and the norm's bar does not.)"""
+    case = AttnCase([50, 1], [700, 2900], Hq=4, Hkv=2, d=64, page=16, dtype=dtype, seed=9,
+                    scale_q=40.0)
+    _check(case, norm_bar=False)
+
+
+def test_rising_scores_move_the_maximum_every_tile():
+    """Keys whose score grows along the sequence, so that every tile has a new
+    maximum far above the last one, and keys that fall, so that none has."""
+    for sign in (1.0, -1.0):
+        case = AttnCase([130], [1500], Hq=2, Hkv=1, d=64, page=16, dtype="bf16", seed=3)
+        ramp = sign * torch.linspace(-40, 40, 1500)
+        ids = case.table[0].long()
+        k = case.k[ids].reshape(-1, 1, 64)
+        k[:1500, :, 0] = ramp[:, None].to(torch.bfloat16)
+        case.k[ids] = k.reshape(-1, 16, 1, 64)
+        case.q[..., 0] = 6.0
+        _check(case, norm_bar=False)
+
+
+def test_mixed_batch_of_many_requests():
+    g = torch.Generator().manual_seed(11)
+    new = torch.randint(0, 60, (90,), generator=g).tolist()
+    total = [n + c for n, c in zip(new, torch.randint(0, 400, (90,), generator=g).tolist())]
+    _check(AttnCase(new, total, Hq=6, Hkv=2, d=128, page=16, dtype="bf16", seed=12, pad=17))
+
+
+def test_chunk_against_a_long_prefix():
+    _check(AttnCase([519], [4100], Hq=8, Hkv=2, d=128, page=128, dtype="bf16", seed=21))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_values_beyond_32_bit_offsets(dtype):
+    """A pool of more than 2^31 elements, with the request's pages at its end."""
+    Hkv, d, page = 8, 128, 256
+    case = AttnCase([3, 1], [600, 90], Hq=8, Hkv=Hkv, d=d, page=page, dtype=dtype, seed=4)
+    t = case.cuda()
+    n_small = case.k.shape[0]
+    n_pages = (1 << 31) // (page * Hkv * d) + 40
+    big = {}
+    for n in ("k", "v"):
+        big[n] = torch.zeros((n_pages, page, Hkv, d), dtype=case.dtype, device="cuda")
+        big[n][n_pages - n_small:] = t[n]
+    t.update(big)
+    t["table"] = t["table"] + (n_pages - n_small)
+    out, _ = _run(case, dev=t)
+    ref, size, top = case.reference()
+    assert ((out.double().cpu() - ref).abs() <= case.bound(ref, size, top)).all()
+
+
+def test_captured_graphs_share_a_workspace_and_follow_the_lengths():
+    """Two graphs over one workspace, replayed in turn with other lengths."""
+    cases = [AttnCase([1, 1], [900, 300], Hq=8, Hkv=2, d=128, page=16, dtype="bf16", seed=1),
+             AttnCase([40, 9], [140, 2000], Hq=8, Hkv=2, d=128, page=32, dtype="bf16", seed=2)]
+    ws = kda.paged_workspace_for(64, 8, 2, 128)
+    devs = [c.cuda() for c in cases]
+    outs = [torch.zeros_like(t["q"]) for t in devs]
+    for c, t, o in zip(cases, devs, outs):
+        _run(c, dev=t, ws=ws, out=o)
+    torch.cuda.synchronize()
+    graphs = []
+    for c, t, o in zip(cases, devs, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            _run(c, dev=t, ws=ws, out=o)
+        graphs.append(g)
+    for _ in range(3):
+        for g, o in zip(graphs, outs):
+            o.zero_()
+            g.replay()
+    for c, o in zip(cases, outs):
+        ref, size, top = c.reference()
+        assert ((o.double().cpu() - ref).abs() <= c.bound(ref, size, top)).all()
+    # shorter requests in the captured call
+    cases[0].total = [500, 17]
+    devs[0]["kv"].copy_(torch.tensor([500, 17], dtype=torch.int32))
+    graphs[0].replay()
+    ref, size, top = cases[0].reference()
+    assert ((outs[0].double().cpu() - ref).abs() <= cases[0].bound(ref, size, top)).all()
+    assert kda.kda_device_status(ws) == (kda.KDA_OK, 0)
+
+
+def test_another_stream():
+    case = AttnCase([9], [300], Hq=4, Hkv=2, d=64, page=16, dtype="bf16")
+    t = case.cuda()
+    s = torch.cuda.Stream()
+    ws = kda.paged_workspace_for(9, 4, 2, 64)
+    out = torch.zeros_like(t["q"])
+    s.wait_stream(torch.cuda.current_stream())
+    kda.kda_paged_attn(t["q"], t["k"], t["v"], t["table"], t["cu"], t["kv"], out, workspace=ws,
+                       stream=s)
+    s.synchronize()
+    ref, size, top = case.reference()
+    assert ((out.double().cpu() - ref).abs() <= case.bound(ref, size, top)).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_bad_lengths_tables_and_pages(dtype):
+    """Inputs that the device checks refuse: an error bit, and nothing else."""
+    mk = lambda: AttnCase([3, 5], [40, 60], Hq=4, Hkv=2, d=64, page=16, dtype=dtype)
+    for cu in ([0, 9, 8], [1, 3, 8], [0, 3, 9]):
+        case = mk()
+        case.cu = torch.tensor(cu, dtype=torch.int32)
+        out, ws = _run(case)
+        assert kda.kda_device_status(ws) == (kda.KDA_ERR_DEVICE_CHECK, 4)
+        assert (out == AttnCase.MARK).all()
+    for bad in (-1, 65):     # negative; beyond the table's four pages
+        case = mk()
+        ref, size, top = case.reference()
+        case.kv[1] = bad
+        out, ws = _run(case)
+        assert kda.kda_device_status(ws) == (kda.KDA_ERR_DEVICE_CHECK, 128)
+        assert (out[3:] == AttnCase.MARK).all()
+        assert ((out.double().cpu() - ref)[:3].abs() <= case.bound(ref, size, top)[:3]).all()
+    for page in (-5, 1 << 20):   # reads as zeros: keys and values 16..31 of request 0
+        case = mk()
+        good = int(case.table[0, 1])
+        t = case.cuda()
+        t["table"][0, 1] = page
+        case.k[good], case.v[good] = 0, 0
+        out, ws = _run(case, dev=t)
+        assert kda.kda_device_status(ws) == (kda.KDA_ERR_DEVICE_CHECK, 512)
+        ref, size, top = case.reference()
+        assert ((out.double().cpu() - ref).abs() <= case.bound(ref, size, top)).all()
