@@ -88,7 +88,8 @@ struct VerifyPlan {
 
 cudaError_t launch_paged_plan(const PagedPlanArgs &p);
 cudaError_t launch_paged_append(const AppendPlan &p);
-cudaError_t launch_paged_attn_simt(const PagedAttnPlan &p);
+cudaError_t launch_paged_attn_bf16(const PagedAttnPlan &p);
+cudaError_t launch_paged_attn_f32(const PagedAttnPlan &p);
 cudaError_t launch_verify(const VerifyPlan &p);
 
 // launches of the last successful call on this host thread (kda_api.cu)

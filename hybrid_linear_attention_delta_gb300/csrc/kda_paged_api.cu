@@ -160,7 +160,9 @@ kda_status kda_paged_attn(const void *q, const void *k_pages, const void *v_page
   p.part_ml = reinterpret_cast<float *>(ws + lay.ml_off);
   p.part_rows = kda::paged_part_rows(a->T_total, G);
   p.stream = static_cast<cudaStream_t>(a->stream);
-  return launch(a->stream, a->ev_begin, a->ev_end, [&] { return kda::launch_paged_attn_simt(p); });
+  return launch(a->stream, a->ev_begin, a->ev_end, [&] {
+    return a->dtype == KDA_BF16 ? kda::launch_paged_attn_bf16(p) : kda::launch_paged_attn_f32(p);
+  });
 }
 
 kda_status kda_verify_drafts(const void *target_probs, const void *draft_probs,

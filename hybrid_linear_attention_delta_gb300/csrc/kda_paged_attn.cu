@@ -1,0 +1,786 @@
+// kda_paged_attn.cu -- paged attention in bf16 on the tensor cores.
+//
+//     out = sum_j softmax_j(scale q . k_j) v_j
+//
+// One pass over the keys.  A tile is 128 query rows (token, head of the group)
+// by 128 keys: S = Q K^T into tensor memory, a thread per row takes the row's
+// maximum, P = 2^(c S - c m) as bf16 back into tensor memory over S, and
+// O += P V.  The reference m of a row moves only when the maximum has grown by
+// more than 2^8 in weight (P then stays below 2^8, which costs bf16 nothing);
+// only then are O and the sum rescaled, in place.
+//
+// One CTA per SM works on two streams of tiles, so that one's softmax runs
+// under the other's products:
+//   * an item with more rows than a tile has: two tiles of rows, every key
+//     tile read once for both;
+//   * an item whose rows fit one tile (decode): the same rows, key tiles in
+//     turn, the two results joined at the end.
+// Warps 0-3 and 4-7: the softmax and the outputs of stream 0 and 1; warp 8
+// issues the products; warp 9 loads Q and the K / V tiles, page by page, into a
+// ring of stages; warp 10 cuts the work into pieces (PagedSched).
+#include <cuda.h>
+
+#include <cstring>
+
+#include "kda_paged_sched.cuh"
+#include "kda_sm100.cuh"
+
+namespace kda {
+namespace {
+
+using namespace sm100;
+
+constexpr int kThreads = 384;
+constexpr int kRows = 128;  // query rows of a stream's tile
+constexpr int kKeys = 128;  // keys of a tile
+constexpr int kPieces = 4;  // pieces published ahead
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kSchedWarp = 10;
+// readers of a published piece: the softmax warps, the MMA and the load warp
+constexpr int kPieceReaders = 10;
+
+// Bytes of one half (64 channels) of a 128-row tile.
+constexpr uint32_t kHalf = 128 * 128;
+
+template <int D>
+struct Layout {
+  static constexpr int kHalves = D / 64;
+  static constexpr uint32_t kTile = kHalves * kHalf;  // Q, K or V tile
+  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr uint32_t kQ = 0;
+  static constexpr uint32_t kStage = 2 * kTile;
+  static constexpr uint32_t kCtl = kStage + kStages * kTile;
+};
+
+// A piece as the warps see it.
+struct Work {
+  PagedPiece o;
+  int32_t keys;   // 1 + last key that the item sees
+  int32_t split;  // 1: one tile of rows, key tiles in turn over the streams
+  int32_t cnt0, cnt1;  // key tiles of the streams
+};
+
+struct Ctl {
+  uint64_t kv_full[8], kv_empty[8];
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
+  uint64_t ml_full;
+  uint64_t piece_full[kPieces], piece_empty[kPieces];
+  uint64_t drain;
+  Work work[kPieces];
+  float ml[kRows][2];  // maxima and sums of stream 1 when the streams are joined
+  int64_t scratch[kThreads / 32 + 4];
+  uint32_t tmem;
+  int32_t last[2];
+};
+
+template <int D>
+constexpr uint32_t smem_bytes() {
+  return Layout<D>::kCtl + (uint32_t)sizeof(Ctl);
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *tmap, int x, int y, int z,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+// 16 consecutive 32-bit columns of this thread's lane.  (The load is valid after
+// tmem_wait_ld() and reg_fence16, the store complete after tmem_wait_st().)
+__device__ __forceinline__ void tmem_ld16_async(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15])
+      : "memory");
+}
+
+// Two fp32 values in one 64-bit register and the operations on both at once.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float &lo, float &hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// A bounded wait of a whole warp: every lane gets the same answer.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity));
+}
+// Arrives once for the warp, after everything its lanes did before.
+__device__ __forceinline__ void warp_arrive(uint64_t *bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(bar));
+}
+
+struct AttnArgs {
+  PagedAttnPlan p;
+  float c;         // |scale| log2(e)
+  uint32_t neg_q;  // scale < 0: Q is negated by the product
+};
+
+// Reads the published pieces; a piece stays where it is until it is released.
+struct PieceReader {
+  uint32_t n = 0;
+  // nullptr: the wait gave up
+  __device__ const Work *next(Ctl &ctl) {
+    const uint32_t slot = n % kPieces;
+    return warp_wait(&ctl.piece_full[slot], (n / kPieces) & 1) ? &ctl.work[slot] : nullptr;
+  }
+  __device__ void release(Ctl &ctl) { warp_arrive(&ctl.piece_empty[n++ % kPieces]); }
+};
+
+// ------------------------------------------------------------------ pieces
+__device__ bool sched_role(Ctl &ctl, const AttnArgs &a, PagedSched &sched, const PagedItems &it) {
+  const int tpt = kRows / a.p.G;  // tokens of a tile
+  for (uint32_t n = 0;; ++n) {
+    const uint32_t slot = n % kPieces;
+    Work w;
+    w.o = sched.next(a.p, it);
+    w.keys = max(0, a.p.causal ? min(w.o.kv, w.o.seen0 + w.o.n - 1) : w.o.kv);
+    w.split = w.o.n <= tpt;
+    const int tiles = w.o.tile1 - w.o.tile0;
+    if (w.split) {
+      w.cnt0 = (tiles + 1) / 2;
+      w.cnt1 = tiles / 2;
+    } else {  // the first tile of rows may see fewer keys
+      const int keys0 = max(0, a.p.causal ? min(w.o.kv, w.o.seen0 + tpt - 1) : w.o.kv);
+      w.cnt0 = min(tiles, max(0, (keys0 + kKeys - 1) / kKeys - w.o.tile0));
+      w.cnt1 = tiles;
+    }
+    if (n >= kPieces && !mbar_wait(smem_u32(&ctl.piece_empty[slot]), (n / kPieces - 1) & 1))
+      return false;
+    ctl.work[slot] = w;
+    mbar_arrive(smem_u32(&ctl.piece_full[slot]));
+    if (w.o.n == 0) return true;
+  }
+}
+
+// Ring entries of a piece of n key tiles, in the order they are needed: K_0,
+// then K_{i+1}, V_i.
+__device__ __forceinline__ int entry_k(int i) { return i == 0 ? 0 : 2 * i - 1; }
+__device__ __forceinline__ int entry_v(int i, int n) { return i < n - 1 ? 2 * i + 2 : 2 * n - 1; }
+
+// ------------------------------------------------------------------ loads
+template <int D>
+__device__ bool load_role(uint32_t sbase, Ctl &ctl, const AttnArgs &a, const CUtensorMap *tq,
+                          const CUtensorMap *tk, const CUtensorMap *tv) {
+  using Ly = Layout<D>;
+  const PagedAttnPlan &p = a.p;
+  const int lane = threadIdx.x & 31;
+  const int rows = min(p.page_size, kKeys);  // key rows of a box
+  const int tpt = kRows / p.G;
+  const uint32_t q_bytes = (uint32_t)(tpt * p.G * 128 * Ly::kHalves);
+  // lane l fetches half l % kHalves of page l / kHalves of a tile
+  const int half = lane % Ly::kHalves, box = lane / Ly::kHalves;
+  PieceReader pieces;
+  uint32_t e = 0, nq = 0;  // ring entries and Q tiles requested so far
+  bool ok = true;
+  for (;; pieces.release(ctl)) {
+    const Work *wp = pieces.next(ctl);
+    if (!(ok = wp != nullptr) || wp->o.n == 0) break;
+    const Work &w = *wp;
+    const int n = w.o.tile1 - w.o.tile0;
+    if (n == 0) continue;
+    if (nq > 0 && !(ok = warp_wait(&ctl.q_empty, (nq - 1) & 1))) break;
+    if (lane == 0) {
+      const uint32_t bar = smem_u32(&ctl.q_full);
+      mbar_expect_tx(bar, w.split ? q_bytes : 2 * q_bytes);
+      for (int s = 0; s < (w.split ? 1 : 2); ++s)
+        for (int h = 0; h < Ly::kHalves; ++h)
+          tma_load_3d(sbase + Ly::kQ + s * Ly::kTile + h * kHalf, tq, h * 64, w.o.head * p.G,
+                      w.o.tok0 + s * tpt, bar);
+    }
+    ++nq;
+    const int32_t *row = p.table + (int64_t)w.o.req * p.max_pages;
+    // boxes of tile i (pages that hold a key of the item's request), and this
+    // lane's page of it
+    auto boxes = [&](int i) {
+      const int left = min(kKeys, w.o.kv - (w.o.tile0 + i) * kKeys);
+      return (left + rows - 1) / rows;
+    };
+    auto page_of = [&](int i) {
+      if (box >= boxes(i)) return 0;
+      const int key = (w.o.tile0 + i) * kKeys + box * rows;
+      const int page = row[key >> p.page_shift];
+      if (page < 0 || page >= p.n_pages) {
+        raise_error(p.err, ERR_BAD_PAGE);
+        return -1;
+      }
+      return page;
+    };
+    auto fetch = [&](const CUtensorMap *map, int i, int page) {
+      const uint32_t st = e % Ly::kStages, use = e / Ly::kStages;
+      if (use > 0 && !warp_wait(&ctl.kv_empty[st], (use - 1) & 1)) return false;
+      const uint32_t bar = smem_u32(&ctl.kv_full[st]);
+      const int nb = boxes(i);
+      if (lane == 0) mbar_expect_tx(bar, (uint32_t)(nb * rows * 128 * Ly::kHalves));
+      __syncwarp();
+      if (box < nb) {
+        const int key = (w.o.tile0 + i) * kKeys + box * rows;
+        // a page that is none reads as zeros: a head behind the last one
+        const int z = page < 0 ? 0 : (page << p.page_shift) + (key & (p.page_size - 1));
+        tma_load_3d(sbase + Ly::kStage + st * Ly::kTile + half * kHalf + box * rows * 128, map,
+                    half * 64, page < 0 ? p.Hkv : w.o.head, z, bar);
+      }
+      ++e;
+      return true;
+    };
+    int page = page_of(0);
+    if (!(ok = fetch(tk, 0, page))) break;
+    for (int i = 0; i < n && ok; ++i) {
+      int next = 0;
+      if (i + 1 < n) {
+        next = page_of(i + 1);
+        ok = fetch(tk, i + 1, next);
+      }
+      ok = ok && fetch(tv, i, page);
+      page = next;
+    }
+    if (!ok) break;
+  }
+  if (!ok) {  // copies in flight land before the CTA leaves
+    for (uint32_t i = e > Ly::kStages ? e - Ly::kStages : 0; i < e; ++i)
+      warp_wait(&ctl.kv_full[i % Ly::kStages], (i / Ly::kStages) & 1);
+    if (nq > 0) warp_wait(&ctl.q_full, (nq - 1) & 1);
+  }
+  return ok;
+}
+
+// ------------------------------------------------------------------ products
+template <int D>
+__device__ bool mma_role(uint32_t sbase, Ctl &ctl, const AttnArgs &a, uint32_t tmem) {
+  using Ly = Layout<D>;
+  const int lane = threadIdx.x & 31;
+  const uint32_t idesc_s = idesc_bf16(kRows, kKeys, 0, 0) | (a.neg_q << 13);
+  const uint32_t idesc_o = idesc_bf16(kRows, D, 0, 1);
+  PieceReader pieces;
+  uint32_t e = 0, nq = 0;
+  uint32_t n_p[2] = {0, 0};   // tiles of each stream so far
+  uint32_t n_o[2] = {0, 0};   // outputs started
+  bool ok = true, any = false;
+
+  // S of stream s for tile i
+  auto scores = [&](const Work &w, int s, int i, bool last_use, bool last_q) {
+    const uint32_t at = e + entry_k(i), st = at % Ly::kStages;
+    if (!warp_wait(&ctl.kv_full[st], (at / Ly::kStages) & 1)) return false;
+    if (lane == 0) {
+      tc_fence_after();
+      const uint32_t q = sbase + Ly::kQ + (w.split ? 0 : s) * Ly::kTile;
+      const uint32_t k = sbase + Ly::kStage + st * Ly::kTile;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+        mma_bf16(tmem + s * 128, sw128_desc(q + (kk >> 2) * kHalf + (kk & 3) * 32, 16, 1024),
+                 sw128_desc(k + (kk >> 2) * kHalf + (kk & 3) * 32, 16, 1024), idesc_s, kk > 0);
+      mma_commit(smem_u32(&ctl.s_full[s]));
+      if (last_use) mma_commit(smem_u32(&ctl.kv_empty[st]));
+      if (last_q) mma_commit(smem_u32(&ctl.q_empty));
+    }
+    __syncwarp();
+    any = true;
+    return true;
+  };
+  // O of stream s += P V of tile i (of n); j: the stream's own count of tiles
+  auto outputs = [&](const Work &w, int s, int i, int n, int j, int cnt, bool last_use) {
+    const uint32_t at = e + entry_v(i, n), st = at % Ly::kStages;
+    const uint32_t v = sbase + Ly::kStage + st * Ly::kTile;
+    if (!warp_wait(&ctl.kv_full[st], (at / Ly::kStages) & 1)) return false;
+    const int left = w.o.kv - (w.o.tile0 + i) * kKeys;
+    if (left < kKeys) {
+      // slots behind the request's last key may hold anything: their weights
+      // are zero, and so must their values be
+      for (int x = lane; x < (kKeys - left) * 8 * Ly::kHalves; x += 32) {
+        const int h = x / ((kKeys - left) * 8), y = x - h * ((kKeys - left) * 8);
+        st_shared_v4(v + h * kHalf + left * 128 + y * 16, 0, 0, 0, 0);
+      }
+      fence_async_smem();
+      __syncwarp();
+    }
+    if (j == 0 && n_o[s] > 0 && !warp_wait(&ctl.o_empty[s], (n_o[s] - 1) & 1)) return false;
+    if (!warp_wait(&ctl.p_full[s], n_p[s] & 1)) return false;
+    if (lane == 0) {
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < kKeys / 16; ++kk)
+        mma_bf16_ts(tmem + 256 + s * D, tmem + s * 128 + kk * 8, sw128_desc(v + kk * 2048, kHalf, 1024),
+                    idesc_o, j > 0 || kk > 0);
+      if (j == cnt - 1) mma_commit(smem_u32(&ctl.o_full[s]));
+      if (last_use) mma_commit(smem_u32(&ctl.kv_empty[st]));
+    }
+    __syncwarp();
+    ++n_p[s];
+    if (j == cnt - 1) ++n_o[s];
+    return true;
+  };
+
+  for (;; pieces.release(ctl)) {
+    const Work *wp = pieces.next(ctl);
+    if (!(ok = wp != nullptr) || wp->o.n == 0) break;
+    const Work &w = *wp;
+    const int n = w.o.tile1 - w.o.tile0;
+    if (n == 0) continue;
+    if (!(ok = warp_wait(&ctl.q_full, nq & 1))) break;
+    ++nq;
+    if (w.split) {
+      ok = scores(w, 0, 0, true, n == 1);
+      if (ok && n > 1) ok = scores(w, 1, 1, true, n == 2);
+      for (int i = 0; i < n && ok; ++i) {
+        const int s = i & 1;
+        ok = outputs(w, s, i, n, i >> 1, s ? w.cnt1 : w.cnt0, true);
+        if (ok && i + 2 < n) ok = scores(w, s, i + 2, true, i + 3 == n);
+      }
+    } else {
+      if (w.cnt0 > 0) ok = scores(w, 0, 0, false, false);
+      ok = ok && scores(w, 1, 0, true, n == 1);
+      for (int i = 0; i < n && ok; ++i) {
+        if (i < w.cnt0) ok = outputs(w, 0, i, n, i, w.cnt0, false);
+        if (ok && i + 1 < w.cnt0) ok = scores(w, 0, i + 1, false, false);
+        ok = ok && outputs(w, 1, i, n, i, n, true);
+        if (ok && i + 1 < n) ok = scores(w, 1, i + 1, true, i + 2 == n);
+      }
+    }
+    if (!ok) break;
+    e += 2 * n;
+  }
+  if (!ok && any) {  // products in flight end before tensor memory is freed
+    if (lane == 0) mma_commit(smem_u32(&ctl.drain));
+    __syncwarp();
+    warp_wait(&ctl.drain, 0);
+  }
+  return ok;
+}
+
+// ------------------------------------------------------------------ softmax and outputs
+__device__ __forceinline__ int64_t row_offset(const PagedAttnPlan &p, const PagedPiece &o, int t,
+                                              int g) {
+  return ((int64_t)(o.tok0 + t) * p.Hq + o.head * p.G + g) * p.d;
+}
+
+// One warp writes row x of a result, lane l the channels VEC * l ...
+template <int D>
+__device__ __forceinline__ void store_row(__nv_bfloat16 *dst, const float (&x)[D / 32]) {
+  const int lane = threadIdx.x & 31;
+  if constexpr (D == 128) {
+    *reinterpret_cast<uint2 *>(dst + lane * 4) =
+        make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+  } else {
+    *reinterpret_cast<uint32_t *>(dst + lane * 2) = pack_bf16x2(x[0], x[1]);
+  }
+}
+
+// Joins the pieces of an item, first piece first: a warp per row, rows [r0, r1)
+// of the item strided over the calling warps.
+template <int D>
+__device__ void join_pieces(const PagedAttnPlan &p, const PagedPiece &o, int r0, int r1, int warp,
+                            int n_warps) {
+  constexpr int N = D / 32;
+  const int lane = threadIdx.x & 31;
+  for (int r = r0 + warp; r < r1; r += n_warps) {
+    float m = -INFINITY;
+    for (int k = lane; k < o.n_pieces; k += 32)
+      m = fmaxf(m, __ldcg(&p.part_ml[((int64_t)paged_part_slot(o, k) * p.part_rows + r) * 2]));
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+    float l = 0.f, acc[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) acc[j] = 0.f;
+    for (int k0 = 0; k0 < o.n_pieces; k0 += 32) {
+      float w = 0.f, lk = 0.f;
+      if (k0 + lane < o.n_pieces) {
+        const int64_t at = (int64_t)paged_part_slot(o, k0 + lane) * p.part_rows + r;
+        lk = __ldcg(&p.part_ml[at * 2 + 1]);
+        // a piece in which the row saw no key left no output
+        w = lk > 0.f ? exp2f(__ldcg(&p.part_ml[at * 2]) - m) : 0.f;
+      }
+      float wl = w * lk;
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) wl += __shfl_xor_sync(0xffffffffu, wl, x);
+      l += wl;
+      const int kn = min(32, o.n_pieces - k0);
+#pragma unroll 4
+      for (int k = 0; k < kn; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, w, k);
+        const float *src =
+            p.part + ((int64_t)paged_part_slot(o, k0 + k) * p.part_rows + r) * D + lane * N;
+        float x[N];
+        if constexpr (N == 4) {
+          const float4 f = __ldcg(reinterpret_cast<const float4 *>(src));
+          x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
+        } else {
+          const float2 f = __ldcg(reinterpret_cast<const float2 *>(src));
+          x[0] = f.x, x[1] = f.y;
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j) acc[j] = wk > 0.f ? fmaf(wk, x[j], acc[j]) : acc[j];
+      }
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+    for (int j = 0; j < N; ++j) acc[j] *= inv;
+    store_row<D>(static_cast<__nv_bfloat16 *>(p.out) + row_offset(p, o, r / p.G, r % p.G), acc);
+  }
+}
+
+template <int D>
+__device__ bool softmax_role(Ctl &ctl, const AttnArgs &a, uint32_t tmem, int s) {
+  const PagedAttnPlan &p = a.p;
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
+  const int r = warp * 32 + lane;          // this thread's row of the tile
+  const int t = r / p.G, g = r - t * p.G;  // its token and head
+  const int tpt = kRows / p.G;
+  const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+  const uint32_t ts = tmem + lanes + s * 128, to = tmem + lanes + 256 + s * D;
+  const float c = a.c;
+  PieceReader pieces;
+  uint32_t n_s = 0, n_o[2] = {0, 0}, n_ml = 0;
+  for (;; pieces.release(ctl)) {
+    const Work *wp = pieces.next(ctl);
+    if (!wp) return false;
+    const Work &w = *wp;
+    if (w.o.n == 0) return true;
+    const int row_tok = w.split ? t : s * tpt + t;  // token of this row within the item
+    const bool live = t < tpt && row_tok < w.o.n;
+    const int cnt = s ? w.cnt1 : w.cnt0;
+    const int seen = live ? (p.causal ? min(w.o.kv, w.o.seen0 + row_tok) : w.o.kv) : 0;
+    const bool warp_live = __any_sync(0xffffffffu, live);
+    float m = -INFINITY, l = 0.f;  // reference (of the unscaled scores) and sum
+
+    for (int j = 0; j < cnt; ++j) {
+      if (!warp_wait(&ctl.s_full[s], n_s & 1)) return false;
+      ++n_s;
+      if (warp_live) {
+        tc_fence_after();
+        const int tile = w.o.tile0 + (w.split ? 2 * j + s : j);
+        const int left = seen - tile * kKeys;  // keys of the tile that the row sees
+        uint32_t x[4][32];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld32_async(ts + q * 32, x[q]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) reg_fence(x[q]);
+        const bool masked = __any_sync(0xffffffffu, left < kKeys);
+        if (masked) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (q * 32 + i >= left) x[q][i] = 0xff800000u;  // -inf
+        }
+        float top[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          top[q] = fmaxf(__uint_as_float(x[q][0]), __uint_as_float(x[q][1]));
+#pragma unroll
+          for (int i = 2; i < 32; i += 2)
+            top[q] = max3(top[q], __uint_as_float(x[q][i]), __uint_as_float(x[q][i + 1]));
+        }
+        const float tm = fmaxf(max3(top[0], top[1], top[2]), top[3]);
+        // the reference moves when the weights would pass 2^8, or from nothing
+        const bool move = tm > m && (m == -INFINITY || (tm - m) * c > 8.f);
+        if (__any_sync(0xffffffffu, move)) {
+          const float old = m;
+          if (move) m = tm;
+          const float keep = !move ? 1.f : old == -INFINITY ? 0.f : ex2_approx((old - m) * c);
+          l *= keep;
+          if (j > 0) {  // the products before this tile's scores have ended
+#pragma unroll
+            for (int q = 0; q < D / 16; ++q) {
+              uint32_t o[16];
+              tmem_ld16_async(to + q * 16, o);
+              tmem_wait_ld();
+              reg_fence16(o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
+              tmem_st16(to + q * 16, o);
+            }
+          }
+        }
+        const float ref = m == -INFINITY ? 0.f : m * c;
+        const uint64_t c2 = pair(c, c), ref2 = pair(-ref, -ref);
+        uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float u, v;
+            unpair(fma2(pair(__uint_as_float(x[q][2 * i]), __uint_as_float(x[q][2 * i + 1])), c2,
+                        ref2), u, v);
+            u = ex2_approx(u);
+            v = ex2_approx(v);
+            sum[i & 1] = add2(sum[i & 1], pair(u, v));
+            pk[i] = pack_bf16x2(u, v);
+          }
+          tmem_st16(ts + q * 16, pk);
+        }
+        float su, sv;
+        unpair(add2(sum[0], sum[1]), su, sv);
+        l += su + sv;
+        tmem_wait_st();
+        tc_fence_before();
+      }
+      warp_arrive(&ctl.p_full[s]);
+    }
+
+    // ---- outputs
+    const float ml = m == -INFINITY ? m : m * c;  // as the partial results carry it
+    float l0 = l, w1 = 0.f, w0 = 1.f;  // weights of the two streams' outputs
+    float mm = ml;
+    if (w.split && s == 1) {
+      if (cnt > 0) {
+        if (!warp_wait(&ctl.o_full[1], n_o[1] & 1)) return false;
+        ++n_o[1];
+        ctl.ml[r][0] = ml;
+        ctl.ml[r][1] = l;
+        warp_arrive(&ctl.ml_full);
+      }
+      continue;  // stream 0 takes it from here
+    }
+    if (cnt > 0) {
+      if (!warp_wait(&ctl.o_full[s], n_o[s] & 1)) return false;
+      ++n_o[s];
+    }
+    const bool join = w.split && w.cnt1 > 0;
+    if (join) {
+      if (!warp_wait(&ctl.ml_full, n_ml & 1)) return false;
+      ++n_ml;
+      // (stream 1's products ended before its warps said so)
+      const float m1 = ctl.ml[r][0], l1 = ctl.ml[r][1];
+      mm = fmaxf(ml, m1);
+      const float ref = mm == -INFINITY ? 0.f : mm;
+      w0 = l > 0.f ? exp2f(ml - ref) : 0.f;
+      w1 = l1 > 0.f ? exp2f(m1 - ref) : 0.f;
+      l0 = w0 * l + w1 * l1;
+    }
+    tc_fence_after();
+    const bool parts = w.o.n_pieces > 0;
+    const float f = parts ? 1.f : l0 > 0.f ? 1.f / l0 : 0.f;
+    const int item_row = row_tok * p.G + g;
+    const int64_t part_at =
+        parts ? (int64_t)paged_part_slot(w.o, w.o.index) * p.part_rows + item_row : 0;
+    if (warp_live) {
+      const float f0 = l > 0.f ? f * w0 : 0.f, f1 = f * w1;
+#pragma unroll
+      for (int q = 0; q < D / 32; ++q) {
+        float y[32];
+        uint32_t o[32];
+        if (cnt > 0) {
+          tmem_ld32_async(to + q * 32, o);
+          tmem_wait_ld();
+          reg_fence(o);
+        }
+        // (an output that no key went into is not read: it may hold anything)
+#pragma unroll
+        for (int i = 0; i < 32; ++i) y[i] = cnt > 0 && f0 > 0.f ? __uint_as_float(o[i]) * f0 : 0.f;
+        if (join) {
+          tmem_ld32_async(to + D + q * 32, o);
+          tmem_wait_ld();
+          reg_fence(o);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) y[i] = f1 > 0.f ? fmaf(__uint_as_float(o[i]), f1, y[i]) : y[i];
+        }
+        if (live && parts) {
+          float *dst = p.part + part_at * D + q * 32;
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<float4 *>(dst + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+        } else if (live) {
+          __nv_bfloat16 *dst =
+              static_cast<__nv_bfloat16 *>(p.out) + row_offset(p, w.o, row_tok, g) + q * 32;
+#pragma unroll
+          for (int i = 0; i < 32; i += 8)
+            *reinterpret_cast<uint4 *>(dst + i) =
+                make_uint4(pack_bf16x2(y[i], y[i + 1]), pack_bf16x2(y[i + 2], y[i + 3]),
+                           pack_bf16x2(y[i + 4], y[i + 5]), pack_bf16x2(y[i + 6], y[i + 7]));
+        }
+      }
+    }
+    tc_fence_before();
+    if (cnt > 0) warp_arrive(&ctl.o_empty[s]);
+    if (join) warp_arrive(&ctl.o_empty[1]);
+
+    if (parts) {
+      if (live) {
+        p.part_ml[part_at * 2] = mm;
+        p.part_ml[part_at * 2 + 1] = l0;
+      }
+      __threadfence();
+      named_bar_sync(1 + s, 128);
+      if (r == 0) {
+        uint32_t *count = p.arrivals + w.o.first_cta * 2 + s;
+        const bool last = atomicAdd(count, 1u) == (uint32_t)w.o.n_pieces - 1;
+        if (last) *count = 0;  // as it was found
+        __threadfence();
+        ctl.last[s] = last;
+      }
+      named_bar_sync(1 + s, 128);
+      const int r0 = (w.split ? 0 : s * tpt) * p.G;
+      const int r1 = w.split ? w.o.n * p.G : min(w.o.n, (s + 1) * tpt) * p.G;
+      if (ctl.last[s]) join_pieces<D>(p, w.o, r0, r1, warp, 4);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ kernel
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+            const __grid_constant__ CUtensorMap tv, const AttnArgs a) {
+  using Ly = Layout<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5;
+  const uint32_t sbase = smem_u32(smem);
+  Ctl &ctl = *reinterpret_cast<Ctl *>(smem + Ly::kCtl);
+  if (sbase & 1023) {  // the swizzled layouts need a 1024-byte aligned base
+    if (tid == 0) raise_error(a.p.err, ERR_TIMEOUT);
+    return;
+  }
+  const PagedItems items = {2 * (kRows / a.p.G), kKeys};
+  PagedSched sched;
+  if (!sched.init<kThreads>(a.p, items, ctl.scratch)) return;
+  if (tid == 0) {
+    for (int i = 0; i < Ly::kStages; ++i) {
+      mbar_init(smem_u32(&ctl.kv_full[i]), 1);
+      mbar_init(smem_u32(&ctl.kv_empty[i]), 1);
+    }
+    mbar_init(smem_u32(&ctl.q_full), 1);
+    mbar_init(smem_u32(&ctl.q_empty), 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(smem_u32(&ctl.s_full[s]), 1);
+      mbar_init(smem_u32(&ctl.p_full[s]), 4);
+      mbar_init(smem_u32(&ctl.o_full[s]), 1);
+      mbar_init(smem_u32(&ctl.o_empty[s]), 4);
+    }
+    mbar_init(smem_u32(&ctl.ml_full), 4);
+    for (int i = 0; i < kPieces; ++i) {
+      mbar_init(smem_u32(&ctl.piece_full[i]), 1);
+      mbar_init(smem_u32(&ctl.piece_empty[i]), kPieceReaders);
+    }
+    mbar_init(smem_u32(&ctl.drain), 1);
+    fence_mbar_init();
+  }
+  if (warp == kLoadWarp && (tid & 31) == 0) {
+    prefetch_tmap(&tq);
+    prefetch_tmap(&tk);
+    prefetch_tmap(&tv);
+  }
+  if (warp == kMmaWarp) tmem_alloc(smem_u32(&ctl.tmem), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&ctl.tmem);
+
+  // a softmax thread holds a row of 128 scores: registers go from the third
+  // warpgroup to the other two (168 a thread at the launch, 2 * 216 + 72 = 3 * 168)
+  bool ok = true;
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    ok = softmax_role<D>(ctl, a, tmem, warp >> 2);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == kMmaWarp) {
+      ok = mma_role<D>(sbase, ctl, a, tmem);
+    } else if (warp == kLoadWarp) {
+      ok = load_role<D>(sbase, ctl, a, &tq, &tk, &tv);
+    } else if (tid == kSchedWarp * 32) {
+      ok = sched_role(ctl, a, sched, items);
+    }
+  }
+  if (!ok) raise_error(a.p.err, ERR_TIMEOUT);
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                              const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                              const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn encode_fn() {
+  static EncodeFn fn = [] {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeFn>(f);
+  }();
+  return fn;
+}
+
+// bf16 [rows][heads][d] in 128-byte swizzled boxes of 64 channels x box_heads x
+// box_rows
+bool make_map(CUtensorMap *map, const void *base, uint64_t d, uint64_t heads, uint64_t rows,
+              uint32_t box_heads, uint32_t box_rows) {
+  const EncodeFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {d, heads, rows};
+  const cuuint64_t strides[2] = {d * 2, heads * d * 2};
+  const cuuint32_t box[3] = {64, box_heads, box_rows};
+  const cuuint32_t step[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
+            step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch_d(const PagedAttnPlan &p) {
+  static_assert(smem_bytes<D>() <= 232448, "shared memory of one CTA");
+  const void *f = reinterpret_cast<const void *>(attn_kernel<D>);
+  const cudaError_t e = set_smem_limit_once(f, smem_bytes<D>());
+  if (e != cudaSuccess) return e;
+  CUtensorMap tq, tk, tv;
+  const uint64_t slots = (uint64_t)p.n_pages * p.page_size;
+  const uint32_t box = p.page_size < kKeys ? p.page_size : kKeys;
+  if (!make_map(&tq, p.q, D, p.Hq, p.T, p.G, kRows / p.G) ||
+      !make_map(&tk, p.k, D, p.Hkv, slots, 1, box) || !make_map(&tv, p.v, D, p.Hkv, slots, 1, box))
+    return cudaErrorInvalidValue;
+  AttnArgs a;
+  a.p = p;
+  // (never 0: a masked score stays -inf in powers of two, and scores below
+  // 10^22 times 10^-30 are 0 to any rounding)
+  a.c = fmaxf(fabsf(p.scale) * 1.4426950408889634f, 1e-30f);
+  a.neg_q = p.scale < 0.f;
+  attn_kernel<D><<<kPagedMaxCtas, kThreads, smem_bytes<D>(), p.stream>>>(tq, tk, tv, a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_attn_bf16(const PagedAttnPlan &p) {
+  return p.d == 128 ? launch_d<128>(p) : launch_d<64>(p);
+}
+
+}  // namespace kda

@@ -1,4 +1,4 @@
-// kda_paged_simt.cu -- paged attention in fp32 arithmetic (CUDA cores).
+// kda_paged_attn_f32.cu -- paged attention in fp32 arithmetic (CUDA cores).
 //
 //     out = sum_j softmax_j(scale q . k_j) v_j
 //
@@ -31,24 +31,13 @@ struct Smem {
   int last;
 };
 
-template <typename T>
-__device__ __forceinline__ float4 load4(const T *p) {
-  if constexpr (sizeof(T) == 4) {
-    return *reinterpret_cast<const float4 *>(p);
-  } else {
-    const uint2 w = *reinterpret_cast<const uint2 *>(p);
-    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
-                       __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u));
-  }
-}
-
 // Element offset of row r of an item: token r / G, query head r % G of the group.
 __device__ __forceinline__ int64_t row_offset(const PagedAttnPlan &p, const PagedPiece &o, int r) {
   const int t = r / p.G;
   return ((int64_t)(o.tok0 + t) * p.Hq + o.head * p.G + (r - t * p.G)) * p.d;
 }
 
-template <typename T, int D, int R>
+template <int D, int R>
 __global__ void __launch_bounds__(kThreads) attn_kernel(PagedAttnPlan p) {
   extern __shared__ __align__(16) unsigned char raw[];
   using S = Smem<D, R>;
@@ -67,11 +56,11 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(PagedAttnPlan p) {
     const PagedPiece o = sm.piece;
     if (o.n == 0) break;
     const int rows = o.n * p.G;
-    const T *q = static_cast<const T *>(p.q);
+    const float *q = static_cast<const float *>(p.q);
     for (int i = tid; i < S::kRows * (D / 4); i += kThreads) {
       const int r = i / (D / 4), e = (i % (D / 4)) * 4;
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r < rows) x = load4<T>(q + row_offset(p, o, r) + e);
+      if (r < rows) x = *reinterpret_cast<const float4 *>(q + row_offset(p, o, r) + e);
       *reinterpret_cast<float4 *>(&sm.q[r * S::kLd + e]) = x;
     }
     int lim[R];  // keys that each row sees
@@ -109,8 +98,8 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(PagedAttnPlan p) {
           const int64_t at =
               ((((int64_t)page << p.page_shift) + ((key0 + k) & (p.page_size - 1))) * p.Hkv +
                o.head) * D + e;
-          kx = load4<T>(static_cast<const T *>(p.k) + at);
-          vx = load4<T>(static_cast<const T *>(p.v) + at);
+          kx = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.k) + at);
+          vx = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.v) + at);
         }
         *reinterpret_cast<float4 *>(&sm.k[k * S::kLd + e]) = kx;
         *reinterpret_cast<float4 *>(&sm.v[k * D + e]) = vx;
@@ -247,32 +236,28 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(PagedAttnPlan p) {
       const int r = ty * R + i;
       if (r >= rows) continue;
       const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;  // a row without keys: zeros
-      T *out = static_cast<T *>(p.out) + row_offset(p, o, r);
+      float *out = static_cast<float *>(p.out) + row_offset(p, o, r);
 #pragma unroll
-      for (int j = 0; j < NC; ++j)
-        out[(j / 4) * 64 + tx * 4 + j % 4] = from_f32<T>(acc[i][j] * inv);
+      for (int j = 0; j < NC; j += 4)
+        *reinterpret_cast<float4 *>(out + j * 16 + tx * 4) = make_float4(
+            acc[i][j] * inv, acc[i][j + 1] * inv, acc[i][j + 2] * inv, acc[i][j + 3] * inv);
     }
   }
 }
 
-template <typename T, int D, int R>
+template <int D, int R>
 cudaError_t launch_r(const PagedAttnPlan &p) {
-  const void *f = reinterpret_cast<const void *>(attn_kernel<T, D, R>);
+  const void *f = reinterpret_cast<const void *>(attn_kernel<D, R>);
   const cudaError_t e = set_smem_limit_once(f, sizeof(Smem<D, R>));
   if (e != cudaSuccess) return e;
-  attn_kernel<T, D, R><<<kPagedMaxCtas, kThreads, sizeof(Smem<D, R>), p.stream>>>(p);
+  attn_kernel<D, R><<<kPagedMaxCtas, kThreads, sizeof(Smem<D, R>), p.stream>>>(p);
   return cudaGetLastError();
-}
-
-template <typename T>
-cudaError_t launch_t(const PagedAttnPlan &p) {
-  return p.d == 128 ? launch_r<T, 128, 4>(p) : launch_r<T, 64, 4>(p);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_attn_simt(const PagedAttnPlan &p) {
-  return p.dtype == KDA_BF16 ? launch_t<__nv_bfloat16>(p) : launch_t<float>(p);
+cudaError_t launch_paged_attn_f32(const PagedAttnPlan &p) {
+  return p.d == 128 ? launch_r<128, 4>(p) : launch_r<64, 4>(p);
 }
 
 }  // namespace kda
