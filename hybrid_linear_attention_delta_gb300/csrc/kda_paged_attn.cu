@@ -133,6 +133,18 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
+// One lane of a converged warp, always the same.  Code under it, unlike code
+// under a comparison of the lane, keeps its operands in uniform registers: a
+// product takes 64 cycles of the tensor cores and must not take longer to
+// issue (165 measured with per-lane operands, 64 with uniform ones).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(yes));
+  return yes != 0;
+}
+
 // A bounded wait of a whole warp: every lane gets the same answer.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity));
@@ -294,14 +306,15 @@ __device__ bool mma_role(uint32_t sbase, Ctl &ctl, const AttnArgs &a, uint32_t t
   auto scores = [&](const Work &w, int s, int i, bool last_use, bool last_q) {
     const uint32_t at = e + entry_k(i), st = at % Ly::kStages;
     if (!warp_wait(&ctl.kv_full[st], (at / Ly::kStages) & 1)) return false;
-    if (lane == 0) {
+    const uint64_t q = sw128_desc(sbase + Ly::kQ + (w.split ? 0 : s) * Ly::kTile, 16, 1024);
+    const uint64_t k = sw128_desc(sbase + Ly::kStage + st * Ly::kTile, 16, 1024);
+    if (elect_one()) {
       tc_fence_after();
-      const uint32_t q = sbase + Ly::kQ + (w.split ? 0 : s) * Ly::kTile;
-      const uint32_t k = sbase + Ly::kStage + st * Ly::kTile;
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)
-        mma_bf16(tmem + s * 128, sw128_desc(q + (kk >> 2) * kHalf + (kk & 3) * 32, 16, 1024),
-                 sw128_desc(k + (kk >> 2) * kHalf + (kk & 3) * 32, 16, 1024), idesc_s, kk > 0);
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t step = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+        mma_bf16(tmem + s * 128, q + step, k + step, idesc_s, kk > 0);
+      }
       mma_commit(smem_u32(&ctl.s_full[s]));
       if (last_use) mma_commit(smem_u32(&ctl.kv_empty[st]));
       if (last_q) mma_commit(smem_u32(&ctl.q_empty));
@@ -328,12 +341,13 @@ __device__ bool mma_role(uint32_t sbase, Ctl &ctl, const AttnArgs &a, uint32_t t
     }
     if (j == 0 && n_o[s] > 0 && !warp_wait(&ctl.o_empty[s], (n_o[s] - 1) & 1)) return false;
     if (!warp_wait(&ctl.p_full[s], n_p[s] & 1)) return false;
-    if (lane == 0) {
+    const uint64_t vd = sw128_desc(v, kHalf, 1024);
+    if (elect_one()) {
       tc_fence_after();
 #pragma unroll
       for (int kk = 0; kk < kKeys / 16; ++kk)
-        mma_bf16_ts(tmem + 256 + s * D, tmem + s * 128 + kk * 8, sw128_desc(v + kk * 2048, kHalf, 1024),
-                    idesc_o, j > 0 || kk > 0);
+        mma_bf16_ts(tmem + 256 + s * D, tmem + s * 128 + kk * 8, vd + kk * (2048 >> 4), idesc_o,
+                    kk > 0 || j > 0);
       if (j == cnt - 1) mma_commit(smem_u32(&ctl.o_full[s]));
       if (last_use) mma_commit(smem_u32(&ctl.kv_empty[st]));
     }
@@ -373,7 +387,7 @@ __device__ bool mma_role(uint32_t sbase, Ctl &ctl, const AttnArgs &a, uint32_t t
     e += 2 * n;
   }
   if (!ok && any) {  // products in flight end before tensor memory is freed
-    if (lane == 0) mma_commit(smem_u32(&ctl.drain));
+    if (elect_one()) mma_commit(smem_u32(&ctl.drain));
     __syncwarp();
     warp_wait(&ctl.drain, 0);
   }
@@ -658,7 +672,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
             const __grid_constant__ CUtensorMap tv, const AttnArgs a) {
   using Ly = Layout<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  const int tid = threadIdx.x, warp = tid >> 5;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const uint32_t sbase = smem_u32(smem);
   Ctl &ctl = *reinterpret_cast<Ctl *>(smem + Ly::kCtl);
   if (sbase & 1023) {  // the swizzled layouts need a 1024-byte aligned base
