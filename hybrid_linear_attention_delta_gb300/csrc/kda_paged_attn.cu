@@ -15,9 +15,12 @@
 //     tile read once for both;
 //   * an item whose rows fit one tile (decode): the same rows, key tiles in
 //     turn, the two results joined at the end.
-// Warps 0-3 and 4-7: the softmax and the outputs of stream 0 and 1; warp 8
-// issues the products; warp 9 loads Q and the K / V tiles, page by page, into a
-// ring of stages; warp 10 cuts the work into pieces (PagedSched).
+// Sixteen softmax warps: a row's 128 scores are halved over two threads, so
+// that a tile's softmax (the maximum, 64 exponentials a thread, the stores) takes
+// less time than the other stream's products; with a whole row per thread it
+// took longer, and the tensor cores waited for it.  Warp 16 issues the
+// products, warp 17 loads Q and the K / V tiles, page by page, into a ring of
+// stages, warp 18 cuts the work into pieces (PagedSched).
 #include <cuda.h>
 
 #include <cstring>
@@ -34,9 +37,10 @@ constexpr int kThreads = 384;
 constexpr int kRows = 128;  // query rows of a stream's tile
 constexpr int kKeys = 128;  // keys of a tile
 constexpr int kPieces = 4;  // pieces published ahead
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kSchedWarp = 10;
+constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kSchedWarp = 10;
+constexpr int kStreamWarps = kSoftmaxWarps / 2;
 // readers of a published piece: the softmax warps, the MMA and the load warp
-constexpr int kPieceReaders = 10;
+constexpr int kPieceReaders = kSoftmaxWarps + 2;
 
 // Bytes of one half (64 channels) of a 128-row tile.
 constexpr uint32_t kHalf = 128 * 128;
@@ -67,7 +71,7 @@ struct Ctl {
   uint64_t piece_full[kPieces], piece_empty[kPieces];
   uint64_t drain;
   Work work[kPieces];
-  float ml[kRows][2];  // maxima and sums of stream 1 when the streams are joined
+  float ml[kRows][2];    // stream 1's references and sums when the streams are joined
   int64_t scratch[kThreads / 32 + 4];
   uint32_t tmem;
   int32_t last[2];
@@ -144,6 +148,9 @@ __device__ __forceinline__ bool elect_one() {
       : "=r"(yes));
   return yes != 0;
 }
+
+// The value of lane 0: tells the compiler that it is the same in every lane.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // A bounded wait of a whole warp: every lane gets the same answer.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
@@ -301,86 +308,98 @@ __device__ bool mma_role(uint32_t sbase, Ctl &ctl, const AttnArgs &a, uint32_t t
   uint32_t n_p[2] = {0, 0};   // tiles of each stream so far
   uint32_t n_o[2] = {0, 0};   // outputs started
   bool ok = true, any = false;
+  int n = 0, tail = 0;  // the piece's key tiles; keys of the last one
+  bool split = false;
 
-  // S of stream s for tile i
-  auto scores = [&](const Work &w, int s, int i, bool last_use, bool last_q) {
-    const uint32_t at = e + entry_k(i), st = at % Ly::kStages;
-    if (!warp_wait(&ctl.kv_full[st], (at / Ly::kStages) & 1)) return false;
-    const uint64_t q = sw128_desc(sbase + Ly::kQ + (w.split ? 0 : s) * Ly::kTile, 16, 1024);
-    const uint64_t k = sw128_desc(sbase + Ly::kStage + st * Ly::kTile, 16, 1024);
+  // One turn of stream s: O += P V of tile i (its j-th of cnt), then S of tile
+  // i_next.  i < 0: scores only, i_next < 0: no more scores.  landed: the tiles
+  // have been waited for (by the other stream); last_use: nobody else reads
+  // them; last_q: nor Q.
+  auto turn = [&](int s, int i, int j, int cnt, int i_next, bool landed, bool last_use,
+                  bool last_q) {
+    const uint32_t at_v = e + entry_v(max(i, 0), n), at_k = e + entry_k(max(i_next, 0));
+    const uint32_t st_v = at_v % Ly::kStages, st_k = at_k % Ly::kStages;
+    const uint64_t v = sw128_desc(uniform(sbase + Ly::kStage + st_v * Ly::kTile), kHalf, 1024);
+    const uint64_t k = sw128_desc(uniform(sbase + Ly::kStage + st_k * Ly::kTile), 16, 1024);
+    const uint64_t q = sw128_desc(uniform(sbase + Ly::kQ + (split ? 0 : s) * Ly::kTile), 16, 1024);
+    const uint32_t ds = uniform(tmem + s * 128), d_o = uniform(tmem + 256 + s * D);
+    const uint32_t more = uniform(j > 0);
+    if (!landed) {
+      if (i >= 0) {
+        if (!warp_wait(&ctl.kv_full[st_v], (at_v / Ly::kStages) & 1)) return false;
+        if (i == n - 1 && tail < kKeys) {
+          // slots behind the request's last key may hold anything: their
+          // weights are zero, and so must their values be
+          const uint32_t rows = sbase + Ly::kStage + st_v * Ly::kTile + tail * 128;
+          const int left = (kKeys - tail) * 8;
+          for (int x = lane; x < left; x += 32)
+            for (int h = 0; h < Ly::kHalves; ++h)
+              st_shared_v4(rows + h * kHalf + x * 16, 0, 0, 0, 0);
+          fence_async_smem();
+          __syncwarp();
+        }
+      }
+      if (i_next >= 0 && !warp_wait(&ctl.kv_full[st_k], (at_k / Ly::kStages) & 1)) return false;
+    }
+    if (i >= 0) {
+      if (j == 0 && n_o[s] > 0 && !warp_wait(&ctl.o_empty[s], (n_o[s] - 1) & 1)) return false;
+      if (!warp_wait(&ctl.p_full[s], n_p[s] & 1)) return false;
+    }
     if (elect_one()) {
       tc_fence_after();
+      if (i >= 0) {
+        // the halves of P lie where the halves of S did
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t step = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
-        mma_bf16(tmem + s * 128, q + step, k + step, idesc_s, kk > 0);
+        for (int kk = 0; kk < kKeys / 16; ++kk)
+          mma_bf16_ts(d_o, ds + kk * 8, v + kk * (2048 >> 4), idesc_o,
+                      kk > 0 ? 1 : more);
+        if (last_use) mma_commit(smem_u32(&ctl.kv_empty[st_v]));
+        if (j == cnt - 1) mma_commit(smem_u32(&ctl.o_full[s]));
       }
-      mma_commit(smem_u32(&ctl.s_full[s]));
-      if (last_use) mma_commit(smem_u32(&ctl.kv_empty[st]));
-      if (last_q) mma_commit(smem_u32(&ctl.q_empty));
+      if (i_next >= 0) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t step = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+          mma_bf16(ds, q + step, k + step, idesc_s, kk > 0);
+        }
+        mma_commit(smem_u32(&ctl.s_full[s]));
+        if (last_use) mma_commit(smem_u32(&ctl.kv_empty[st_k]));
+        if (last_q) mma_commit(smem_u32(&ctl.q_empty));
+      }
     }
     __syncwarp();
     any = true;
-    return true;
-  };
-  // O of stream s += P V of tile i (of n); j: the stream's own count of tiles
-  auto outputs = [&](const Work &w, int s, int i, int n, int j, int cnt, bool last_use) {
-    const uint32_t at = e + entry_v(i, n), st = at % Ly::kStages;
-    const uint32_t v = sbase + Ly::kStage + st * Ly::kTile;
-    if (!warp_wait(&ctl.kv_full[st], (at / Ly::kStages) & 1)) return false;
-    const int left = w.o.kv - (w.o.tile0 + i) * kKeys;
-    if (left < kKeys) {
-      // slots behind the request's last key may hold anything: their weights
-      // are zero, and so must their values be
-      for (int x = lane; x < (kKeys - left) * 8 * Ly::kHalves; x += 32) {
-        const int h = x / ((kKeys - left) * 8), y = x - h * ((kKeys - left) * 8);
-        st_shared_v4(v + h * kHalf + left * 128 + y * 16, 0, 0, 0, 0);
-      }
-      fence_async_smem();
-      __syncwarp();
+    if (i >= 0) {
+      ++n_p[s];
+      if (j == cnt - 1) ++n_o[s];
     }
-    if (j == 0 && n_o[s] > 0 && !warp_wait(&ctl.o_empty[s], (n_o[s] - 1) & 1)) return false;
-    if (!warp_wait(&ctl.p_full[s], n_p[s] & 1)) return false;
-    const uint64_t vd = sw128_desc(v, kHalf, 1024);
-    if (elect_one()) {
-      tc_fence_after();
-#pragma unroll
-      for (int kk = 0; kk < kKeys / 16; ++kk)
-        mma_bf16_ts(tmem + 256 + s * D, tmem + s * 128 + kk * 8, vd + kk * (2048 >> 4), idesc_o,
-                    kk > 0 || j > 0);
-      if (j == cnt - 1) mma_commit(smem_u32(&ctl.o_full[s]));
-      if (last_use) mma_commit(smem_u32(&ctl.kv_empty[st]));
-    }
-    __syncwarp();
-    ++n_p[s];
-    if (j == cnt - 1) ++n_o[s];
     return true;
   };
 
   for (;; pieces.release(ctl)) {
-    const Work *wp = pieces.next(ctl);
-    if (!(ok = wp != nullptr) || wp->o.n == 0) break;
-    const Work &w = *wp;
-    const int n = w.o.tile1 - w.o.tile0;
+    const Work *w = pieces.next(ctl);
+    if (!(ok = w != nullptr) || w->o.n == 0) break;
+    n = w->o.tile1 - w->o.tile0;
     if (n == 0) continue;
+    split = w->split;
+    const int cnt0 = w->cnt0, cnt1 = w->cnt1;
+    tail = w->o.kv - (w->o.tile1 - 1) * kKeys;
     if (!(ok = warp_wait(&ctl.q_full, nq & 1))) break;
     ++nq;
-    if (w.split) {
-      ok = scores(w, 0, 0, true, n == 1);
-      if (ok && n > 1) ok = scores(w, 1, 1, true, n == 2);
+    if (split) {
+      ok = turn(0, -1, 0, 0, 0, false, true, n == 1);
+      if (ok && n > 1) ok = turn(1, -1, 0, 0, 1, false, true, n == 2);
       for (int i = 0; i < n && ok; ++i) {
         const int s = i & 1;
-        ok = outputs(w, s, i, n, i >> 1, s ? w.cnt1 : w.cnt0, true);
-        if (ok && i + 2 < n) ok = scores(w, s, i + 2, true, i + 3 == n);
+        ok = turn(s, i, i >> 1, s ? cnt1 : cnt0, i + 2 < n ? i + 2 : -1, false, true, i + 3 == n);
       }
     } else {
-      if (w.cnt0 > 0) ok = scores(w, 0, 0, false, false);
-      ok = ok && scores(w, 1, 0, true, n == 1);
+      if (cnt0 > 0) ok = turn(0, -1, 0, 0, 0, false, false, false);
+      ok = ok && turn(1, -1, 0, 0, 0, cnt0 > 0, true, n == 1);
       for (int i = 0; i < n && ok; ++i) {
-        if (i < w.cnt0) ok = outputs(w, 0, i, n, i, w.cnt0, false);
-        if (ok && i + 1 < w.cnt0) ok = scores(w, 0, i + 1, false, false);
-        ok = ok && outputs(w, 1, i, n, i, n, true);
-        if (ok && i + 1 < n) ok = scores(w, 1, i + 1, true, i + 2 == n);
+        const bool both = i + 1 < cnt0;  // stream 0 waits for this turn's tiles
+        if (i < cnt0) ok = turn(0, i, i, cnt0, both ? i + 1 : -1, false, false, false);
+        ok = ok && turn(1, i, i, n, i + 1 < n ? i + 1 : -1, both, true, i + 2 == n);
       }
     }
     if (!ok) break;
@@ -691,11 +710,11 @@ attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
     mbar_init(smem_u32(&ctl.q_empty), 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(smem_u32(&ctl.s_full[s]), 1);
-      mbar_init(smem_u32(&ctl.p_full[s]), 4);
+      mbar_init(smem_u32(&ctl.p_full[s]), kStreamWarps);
       mbar_init(smem_u32(&ctl.o_full[s]), 1);
-      mbar_init(smem_u32(&ctl.o_empty[s]), 4);
+      mbar_init(smem_u32(&ctl.o_empty[s]), kStreamWarps);
     }
-    mbar_init(smem_u32(&ctl.ml_full), 4);
+    mbar_init(smem_u32(&ctl.ml_full), kStreamWarps);
     for (int i = 0; i < kPieces; ++i) {
       mbar_init(smem_u32(&ctl.piece_full[i]), 1);
       mbar_init(smem_u32(&ctl.piece_empty[i]), kPieceReaders);
@@ -714,10 +733,10 @@ attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&ctl.tmem);
 
-  // a softmax thread holds a row of 128 scores: registers go from the third
-  // warpgroup to the other two (168 a thread at the launch, 2 * 216 + 72 = 3 * 168)
+  // registers go from the last warpgroup to the softmax warps (96 a thread at
+  // the launch, 4 * 104 + 64 = 5 * 96)
   bool ok = true;
-  if (warp < 8) {
+  if (warp < kSoftmaxWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     ok = softmax_role<D>(ctl, a, tmem, warp >> 2);
   } else {
