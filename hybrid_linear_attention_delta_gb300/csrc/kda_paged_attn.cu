@@ -15,12 +15,9 @@
 //     tile read once for both;
 //   * an item whose rows fit one tile (decode): the same rows, key tiles in
 //     turn, the two results joined at the end.
-// Sixteen softmax warps: a row's 128 scores are halved over two threads, so
-// that a tile's softmax (the maximum, 64 exponentials a thread, the stores) takes
-// less time than the other stream's products; with a whole row per thread it
-// took longer, and the tensor cores waited for it.  Warp 16 issues the
-// products, warp 17 loads Q and the K / V tiles, page by page, into a ring of
-// stages, warp 18 cuts the work into pieces (PagedSched).
+// Warps 0-3 and 4-7: the softmax and the outputs of stream 0 and 1; warps 8 and
+// 9 issue the streams' products; warp 10 loads Q and the K / V tiles, page by
+// page, into a ring of stages; warp 11 cuts the work into pieces (PagedSched).
 #include <cuda.h>
 
 #include <cstring>
@@ -37,10 +34,10 @@ constexpr int kThreads = 384;
 constexpr int kRows = 128;  // query rows of a stream's tile
 constexpr int kKeys = 128;  // keys of a tile
 constexpr int kPieces = 4;  // pieces published ahead
-constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kSchedWarp = 10;
+constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kLoadWarp = 10, kSchedWarp = 11;
 constexpr int kStreamWarps = kSoftmaxWarps / 2;
-// readers of a published piece: the softmax warps, the MMA and the load warp
-constexpr int kPieceReaders = kSoftmaxWarps + 2;
+// readers of a published piece: the softmax, the MMA and the load warps
+constexpr int kPieceReaders = kSoftmaxWarps + 3;
 
 // Bytes of one half (64 channels) of a 128-row tile.
 constexpr uint32_t kHalf = 128 * 128;
@@ -69,7 +66,7 @@ struct Ctl {
   uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
   uint64_t ml_full;
   uint64_t piece_full[kPieces], piece_empty[kPieces];
-  uint64_t drain;
+  uint64_t drain[2];
   Work work[kPieces];
   float ml[kRows][2];    // stream 1's references and sums when the streams are joined
   int64_t scratch[kThreads / 32 + 4];
@@ -297,64 +294,73 @@ __device__ bool load_role(uint32_t sbase, Ctl &ctl, const AttnArgs &a, const CUt
 }
 
 // ------------------------------------------------------------------ products
+// The products of stream s.  Each stream has a warp of its own: between two
+// turns a warp spends several hundred cycles on barriers and descriptors, and
+// the tensor cores' queue is too short to cover them.
 template <int D>
-__device__ bool mma_role(uint32_t sbase, Ctl &ctl, const AttnArgs &a, uint32_t tmem) {
+__device__ bool mma_role(uint32_t sbase, Ctl &ctl, const AttnArgs &a, uint32_t tmem, int s) {
   using Ly = Layout<D>;
   const int lane = threadIdx.x & 31;
   const uint32_t idesc_s = idesc_bf16(kRows, kKeys, 0, 0) | (a.neg_q << 13);
   const uint32_t idesc_o = idesc_bf16(kRows, D, 0, 1);
+  const uint32_t ds = uniform(tmem + s * 128), d_o = uniform(tmem + 256 + s * D);
   PieceReader pieces;
-  uint32_t e = 0, nq = 0;
-  uint32_t n_p[2] = {0, 0};   // tiles of each stream so far
-  uint32_t n_o[2] = {0, 0};   // outputs started
+  uint32_t e = 0, nq = 0;      // ring entries and Q tiles of the pieces before
+  uint32_t n_p = 0, n_o = 0;   // tiles and outputs of the stream so far
   bool ok = true, any = false;
-  int n = 0, tail = 0;  // the piece's key tiles; keys of the last one
-  bool split = false;
+  int n = 0, tail = 0;         // the piece's key tiles; keys of the last one
+  int i_last = 0;              // the stream's last tile
+  uint64_t q = 0;
 
-  // One turn of stream s: O += P V of tile i (its j-th of cnt), then S of tile
-  // i_next.  i < 0: scores only, i_next < 0: no more scores.  landed: the tiles
-  // have been waited for (by the other stream); last_use: nobody else reads
-  // them; last_q: nor Q.
-  auto turn = [&](int s, int i, int j, int cnt, int i_next, bool landed, bool last_use,
-                  bool last_q) {
+  // The ring is read in order: entries up to x are behind this stream.  Both
+  // streams wait for every entry and hand every entry back, so that neither
+  // runs a whole ring ahead of the other.
+  uint32_t x = 0;
+  auto landed = [&](uint32_t at) {
+    return warp_wait(&ctl.kv_full[at % Ly::kStages], (at / Ly::kStages) & 1);
+  };
+  auto pass_to = [&](uint32_t upto) {  // entries that only the other stream uses
+    for (; x < upto; ++x) {
+      if (!landed(x)) return false;
+      warp_arrive(&ctl.kv_empty[x % Ly::kStages]);
+    }
+    return true;
+  };
+  auto take = [&](uint32_t at) { return pass_to(at) && landed(x++); };
+
+  // One turn: O += P V of tile i (the stream's j-th), then S of tile i_next.
+  // i < 0: scores only, i_next < 0: no more scores.
+  auto turn = [&](int i, int j, int i_next) {
     const uint32_t at_v = e + entry_v(max(i, 0), n), at_k = e + entry_k(max(i_next, 0));
     const uint32_t st_v = at_v % Ly::kStages, st_k = at_k % Ly::kStages;
     const uint64_t v = sw128_desc(uniform(sbase + Ly::kStage + st_v * Ly::kTile), kHalf, 1024);
     const uint64_t k = sw128_desc(uniform(sbase + Ly::kStage + st_k * Ly::kTile), 16, 1024);
-    const uint64_t q = sw128_desc(uniform(sbase + Ly::kQ + (split ? 0 : s) * Ly::kTile), 16, 1024);
-    const uint32_t ds = uniform(tmem + s * 128), d_o = uniform(tmem + 256 + s * D);
     const uint32_t more = uniform(j > 0);
-    if (!landed) {
-      if (i >= 0) {
-        if (!warp_wait(&ctl.kv_full[st_v], (at_v / Ly::kStages) & 1)) return false;
-        if (i == n - 1 && tail < kKeys) {
-          // slots behind the request's last key may hold anything: their
-          // weights are zero, and so must their values be
-          const uint32_t rows = sbase + Ly::kStage + st_v * Ly::kTile + tail * 128;
-          const int left = (kKeys - tail) * 8;
-          for (int x = lane; x < left; x += 32)
-            for (int h = 0; h < Ly::kHalves; ++h)
-              st_shared_v4(rows + h * kHalf + x * 16, 0, 0, 0, 0);
-          fence_async_smem();
-          __syncwarp();
-        }
-      }
-      if (i_next >= 0 && !warp_wait(&ctl.kv_full[st_k], (at_k / Ly::kStages) & 1)) return false;
-    }
+    if (i_next >= 0 && (i < 0 || at_k < at_v) && !take(at_k)) return false;
     if (i >= 0) {
-      if (j == 0 && n_o[s] > 0 && !warp_wait(&ctl.o_empty[s], (n_o[s] - 1) & 1)) return false;
-      if (!warp_wait(&ctl.p_full[s], n_p[s] & 1)) return false;
+      if (!take(at_v)) return false;
+      if (i == n - 1 && tail < kKeys) {
+        // slots behind the request's last key may hold anything: their weights
+        // are zero, and so must their values be
+        const uint32_t rows = sbase + Ly::kStage + st_v * Ly::kTile + tail * 128;
+        const int left = (kKeys - tail) * 8;
+        for (int y = lane; y < left; y += 32)
+          for (int h = 0; h < Ly::kHalves; ++h) st_shared_v4(rows + h * kHalf + y * 16, 0, 0, 0, 0);
+        fence_async_smem();
+        __syncwarp();
+      }
+      if (i_next >= 0 && at_k > at_v && !take(at_k)) return false;
+      if (j == 0 && n_o > 0 && !warp_wait(&ctl.o_empty[s], (n_o - 1) & 1)) return false;
+      if (!warp_wait(&ctl.p_full[s], n_p & 1)) return false;
     }
     if (elect_one()) {
       tc_fence_after();
       if (i >= 0) {
-        // the halves of P lie where the halves of S did
 #pragma unroll
         for (int kk = 0; kk < kKeys / 16; ++kk)
-          mma_bf16_ts(d_o, ds + kk * 8, v + kk * (2048 >> 4), idesc_o,
-                      kk > 0 ? 1 : more);
-        if (last_use) mma_commit(smem_u32(&ctl.kv_empty[st_v]));
-        if (j == cnt - 1) mma_commit(smem_u32(&ctl.o_full[s]));
+          mma_bf16_ts(d_o, ds + kk * 8, v + kk * (2048 >> 4), idesc_o, kk > 0 ? 1 : more);
+        mma_commit(smem_u32(&ctl.kv_empty[st_v]));
+        if (i_next < 0) mma_commit(smem_u32(&ctl.o_full[s]));
       }
       if (i_next >= 0) {
 #pragma unroll
@@ -363,15 +369,15 @@ __device__ bool mma_role(uint32_t sbase, Ctl &ctl, const AttnArgs &a, uint32_t t
           mma_bf16(ds, q + step, k + step, idesc_s, kk > 0);
         }
         mma_commit(smem_u32(&ctl.s_full[s]));
-        if (last_use) mma_commit(smem_u32(&ctl.kv_empty[st_k]));
-        if (last_q) mma_commit(smem_u32(&ctl.q_empty));
+        mma_commit(smem_u32(&ctl.kv_empty[st_k]));
+        if (i_next == i_last) mma_commit(smem_u32(&ctl.q_empty));
       }
     }
     __syncwarp();
     any = true;
     if (i >= 0) {
-      ++n_p[s];
-      if (j == cnt - 1) ++n_o[s];
+      ++n_p;
+      if (i_next < 0) ++n_o;
     }
     return true;
   };
@@ -381,34 +387,27 @@ __device__ bool mma_role(uint32_t sbase, Ctl &ctl, const AttnArgs &a, uint32_t t
     if (!(ok = w != nullptr) || w->o.n == 0) break;
     n = w->o.tile1 - w->o.tile0;
     if (n == 0) continue;
-    split = w->split;
-    const int cnt0 = w->cnt0, cnt1 = w->cnt1;
+    const bool split = w->split;
+    const int cnt = s ? w->cnt1 : w->cnt0;
     tail = w->o.kv - (w->o.tile1 - 1) * kKeys;
-    if (!(ok = warp_wait(&ctl.q_full, nq & 1))) break;
-    ++nq;
-    if (split) {
-      ok = turn(0, -1, 0, 0, 0, false, true, n == 1);
-      if (ok && n > 1) ok = turn(1, -1, 0, 0, 1, false, true, n == 2);
-      for (int i = 0; i < n && ok; ++i) {
-        const int s = i & 1;
-        ok = turn(s, i, i >> 1, s ? cnt1 : cnt0, i + 2 < n ? i + 2 : -1, false, true, i + 3 == n);
-      }
+    if (!(ok = warp_wait(&ctl.q_full, nq++ & 1))) break;
+    if (cnt > 0) {
+      q = sw128_desc(uniform(sbase + Ly::kQ + (split ? 0 : s) * Ly::kTile), 16, 1024);
+      const int i0 = split ? s : 0, step = split ? 2 : 1;  // tiles i0, i0 + step, ...
+      i_last = i0 + (cnt - 1) * step;
+      ok = turn(-1, 0, i0);
+      for (int i = i0, j = 0; j < cnt && ok; i += step, ++j)
+        ok = turn(i, j, i < i_last ? i + step : -1);
     } else {
-      if (cnt0 > 0) ok = turn(0, -1, 0, 0, 0, false, false, false);
-      ok = ok && turn(1, -1, 0, 0, 0, cnt0 > 0, true, n == 1);
-      for (int i = 0; i < n && ok; ++i) {
-        const bool both = i + 1 < cnt0;  // stream 0 waits for this turn's tiles
-        if (i < cnt0) ok = turn(0, i, i, cnt0, both ? i + 1 : -1, false, false, false);
-        ok = ok && turn(1, i, i, n, i + 1 < n ? i + 1 : -1, both, true, i + 2 == n);
-      }
+      warp_arrive(&ctl.q_empty);
     }
-    if (!ok) break;
+    if (!(ok = ok && pass_to(e + 2 * n))) break;
     e += 2 * n;
   }
   if (!ok && any) {  // products in flight end before tensor memory is freed
-    if (elect_one()) mma_commit(smem_u32(&ctl.drain));
+    if (elect_one()) mma_commit(smem_u32(&ctl.drain[s]));
     __syncwarp();
-    warp_wait(&ctl.drain, 0);
+    warp_wait(&ctl.drain[s], 0);
   }
   return ok;
 }
@@ -704,10 +703,10 @@ attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
   if (tid == 0) {
     for (int i = 0; i < Ly::kStages; ++i) {
       mbar_init(smem_u32(&ctl.kv_full[i]), 1);
-      mbar_init(smem_u32(&ctl.kv_empty[i]), 1);
+      mbar_init(smem_u32(&ctl.kv_empty[i]), 2);
     }
     mbar_init(smem_u32(&ctl.q_full), 1);
-    mbar_init(smem_u32(&ctl.q_empty), 1);
+    mbar_init(smem_u32(&ctl.q_empty), 2);
     for (int s = 0; s < 2; ++s) {
       mbar_init(smem_u32(&ctl.s_full[s]), 1);
       mbar_init(smem_u32(&ctl.p_full[s]), kStreamWarps);
@@ -719,7 +718,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
       mbar_init(smem_u32(&ctl.piece_full[i]), 1);
       mbar_init(smem_u32(&ctl.piece_empty[i]), kPieceReaders);
     }
-    mbar_init(smem_u32(&ctl.drain), 1);
+    for (int s = 0; s < 2; ++s) mbar_init(smem_u32(&ctl.drain[s]), 1);
     fence_mbar_init();
   }
   if (warp == kLoadWarp && (tid & 31) == 0) {
@@ -733,16 +732,16 @@ attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&ctl.tmem);
 
-  // registers go from the last warpgroup to the softmax warps (96 a thread at
-  // the launch, 4 * 104 + 64 = 5 * 96)
+  // a softmax thread holds a row of 128 scores: registers go from the last
+  // warpgroup to the other two (168 a thread at the launch, 2 * 216 + 72 = 3 * 168)
   bool ok = true;
   if (warp < kSoftmaxWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     ok = softmax_role<D>(ctl, a, tmem, warp >> 2);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == kMmaWarp) {
-      ok = mma_role<D>(sbase, ctl, a, tmem);
+    if (warp < kLoadWarp) {
+      ok = mma_role<D>(sbase, ctl, a, tmem, warp - kMmaWarp);
     } else if (warp == kLoadWarp) {
       ok = load_role<D>(sbase, ctl, a, &tq, &tk, &tv);
     } else if (tid == kSchedWarp * 32) {
