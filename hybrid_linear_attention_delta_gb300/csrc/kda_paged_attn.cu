@@ -3,11 +3,12 @@
 //     out = sum_j softmax_j(scale q . k_j) v_j
 //
 // One pass over the keys.  A tile is 128 query rows (token, head of the group)
-// by 128 keys: S = Q K^T into tensor memory, a thread per row takes the row's
-// maximum, P = 2^(c S - c m) as bf16 back into tensor memory over S, and
-// O += P V.  The reference m of a row moves only when the maximum has grown by
-// more than 2^8 in weight (P then stays below 2^8, which costs bf16 nothing);
-// only then are O and the sum rescaled, in place.
+// by 128 keys: S = Q K^T into tensor memory, a thread per row turns its scores
+// into P = 2^(c S - m), bf16, back into tensor memory over S, and O += P V.  Any
+// reference m gives the same quotient O / sum P as long as nothing overflows:
+// it is the maximum of the row's first tile, and moves (O and the sum are then
+// rescaled in place) only when a later tile's weights sum to more than 2^16.
+// The sum is there anyway, so the maximum of a tile is not taken at all.
 //
 // One CTA per SM works on two streams of tiles, so that one's softmax runs
 // under the other's products:
@@ -452,7 +453,7 @@ __device__ void join_pieces(const PagedAttnPlan &p, const PagedPiece &o, int r0,
         const int64_t at = (int64_t)paged_part_slot(o, k0 + lane) * p.part_rows + r;
         lk = __ldcg(&p.part_ml[at * 2 + 1]);
         // a piece in which the row saw no key left no output
-        w = lk > 0.f ? exp2f(__ldcg(&p.part_ml[at * 2]) - m) : 0.f;
+        w = lk == 0.f ? 0.f : exp2f(__ldcg(&p.part_ml[at * 2]) - m);
       }
       float wl = w * lk;
 #pragma unroll
@@ -473,10 +474,10 @@ __device__ void join_pieces(const PagedAttnPlan &p, const PagedPiece &o, int r0,
           x[0] = f.x, x[1] = f.y;
         }
 #pragma unroll
-        for (int j = 0; j < N; ++j) acc[j] = wk > 0.f ? fmaf(wk, x[j], acc[j]) : acc[j];
+        for (int j = 0; j < N; ++j) acc[j] = wk == 0.f ? acc[j] : fmaf(wk, x[j], acc[j]);
       }
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
     for (int j = 0; j < N; ++j) acc[j] *= inv;
     store_row<D>(static_cast<__nv_bfloat16 *>(p.out) + row_offset(p, o, r / p.G, r % p.G), acc);
@@ -505,7 +506,7 @@ __device__ bool softmax_role(Ctl &ctl, const AttnArgs &a, uint32_t tmem, int s) 
     const int cnt = s ? w.cnt1 : w.cnt0;
     const int seen = live ? (p.causal ? min(w.o.kv, w.o.seen0 + row_tok) : w.o.kv) : 0;
     const bool warp_live = __any_sync(0xffffffffu, live);
-    float m = -INFINITY, l = 0.f;  // reference (of the unscaled scores) and sum
+    float ref = 0.f, l = 0.f;  // reference, in powers of two, and sum of the row
 
     for (int j = 0; j < cnt; ++j) {
       if (!warp_wait(&ctl.s_full[s], n_s & 1)) return false;
@@ -520,64 +521,75 @@ __device__ bool softmax_role(Ctl &ctl, const AttnArgs &a, uint32_t tmem, int s) 
         tmem_wait_ld();
 #pragma unroll
         for (int q = 0; q < 4; ++q) reg_fence(x[q]);
-        const bool masked = __any_sync(0xffffffffu, left < kKeys);
-        if (masked) {
+        if (__any_sync(0xffffffffu, live && left < kKeys)) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
+          for (int q = 0; q < 4; ++q) {
+            const int k = min(32, max(0, left - q * 32));
+            const uint32_t bits = k == 32 ? 0xffffffffu : (1u << k) - 1u;
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (q * 32 + i >= left) x[q][i] = 0xff800000u;  // -inf
+              if (!(bits >> i & 1u)) x[q][i] = 0xff800000u;  // -inf
+          }
         }
-        float top[4];
+        // The first tile's maximum is the reference.  It holds while a tile's
+        // weights sum to 2^16 at most, which the sum itself tells; else the
+        // tile is taken again with its own maximum.  (A row that sees no key in
+        // its first tile sees none in the later ones.)
+        float sum_j;
+        for (bool again = j == 0;; again = true) {
+          if (again) {
+            float top[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          top[q] = fmaxf(__uint_as_float(x[q][0]), __uint_as_float(x[q][1]));
+            for (int q = 0; q < 4; ++q) {
+              top[q] = fmaxf(__uint_as_float(x[q][0]), __uint_as_float(x[q][1]));
 #pragma unroll
-          for (int i = 2; i < 32; i += 2)
-            top[q] = max3(top[q], __uint_as_float(x[q][i]), __uint_as_float(x[q][i + 1]));
-        }
-        const float tm = fmaxf(max3(top[0], top[1], top[2]), top[3]);
-        // the reference moves when the weights would pass 2^8, or from nothing
-        const bool move = tm > m && (m == -INFINITY || (tm - m) * c > 8.f);
-        if (__any_sync(0xffffffffu, move)) {
-          const float old = m;
-          if (move) m = tm;
-          const float keep = !move ? 1.f : old == -INFINITY ? 0.f : ex2_approx((old - m) * c);
-          l *= keep;
-          if (j > 0) {  // the products before this tile's scores have ended
+              for (int i = 2; i < 32; i += 2)
+                top[q] = max3(top[q], __uint_as_float(x[q][i]), __uint_as_float(x[q][i + 1]));
+            }
+            const float tm = fmaxf(max3(top[0], top[1], top[2]), top[3]) * c;
+            if (j == 0) {
+              if (live && tm > -INFINITY) ref = tm;
+            } else {
+              const bool move = live && tm > ref;
+              const float keep = move ? ex2_approx(ref - tm) : 1.f;
+              if (move) ref = tm;
+              l *= keep;
+              // (the products before this tile's scores have ended)
 #pragma unroll
-            for (int q = 0; q < D / 16; ++q) {
-              uint32_t o[16];
-              tmem_ld16_async(to + q * 16, o);
-              tmem_wait_ld();
-              reg_fence16(o);
+              for (int q = 0; q < D / 16; ++q) {
+                uint32_t o[16];
+                tmem_ld16_async(to + q * 16, o);
+                tmem_wait_ld();
+                reg_fence16(o);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
-              tmem_st16(to + q * 16, o);
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
+                tmem_st16(to + q * 16, o);
+              }
             }
           }
-        }
-        const float ref = m == -INFINITY ? 0.f : m * c;
-        const uint64_t c2 = pair(c, c), ref2 = pair(-ref, -ref);
-        uint64_t sum[2] = {0ull, 0ull};
+          const uint64_t c2 = pair(c, c), ref2 = pair(-ref, -ref);
+          uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t pk[16];
+          for (int q = 0; q < 4; ++q) {
+            uint32_t pk[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float u, v;
-            unpair(fma2(pair(__uint_as_float(x[q][2 * i]), __uint_as_float(x[q][2 * i + 1])), c2,
-                        ref2), u, v);
-            u = ex2_approx(u);
-            v = ex2_approx(v);
-            sum[i & 1] = add2(sum[i & 1], pair(u, v));
-            pk[i] = pack_bf16x2(u, v);
+            for (int i = 0; i < 16; ++i) {
+              float u, v;
+              unpair(fma2(pair(__uint_as_float(x[q][2 * i]), __uint_as_float(x[q][2 * i + 1])), c2,
+                          ref2), u, v);
+              u = ex2_approx(u);
+              v = ex2_approx(v);
+              sum[i & 1] = add2(sum[i & 1], pair(u, v));
+              pk[i] = pack_bf16x2(u, v);
+            }
+            tmem_st16(ts + q * 16, pk);
           }
-          tmem_st16(ts + q * 16, pk);
+          float su, sv;
+          unpair(add2(sum[0], sum[1]), su, sv);
+          sum_j = su + sv;
+          if (again || !__any_sync(0xffffffffu, live && !(sum_j <= 65536.f))) break;
         }
-        float su, sv;
-        unpair(add2(sum[0], sum[1]), su, sv);
-        l += su + sv;
+        l += sum_j;
         tmem_wait_st();
         tc_fence_before();
       }
@@ -585,7 +597,7 @@ __device__ bool softmax_role(Ctl &ctl, const AttnArgs &a, uint32_t tmem, int s) 
     }
 
     // ---- outputs
-    const float ml = m == -INFINITY ? m : m * c;  // as the partial results carry it
+    const float ml = l == 0.f ? -INFINITY : ref;  // as the partial results carry it
     float l0 = l, w1 = 0.f, w0 = 1.f;  // weights of the two streams' outputs
     float mm = ml;
     if (w.split && s == 1) {
@@ -609,19 +621,19 @@ __device__ bool softmax_role(Ctl &ctl, const AttnArgs &a, uint32_t tmem, int s) 
       // (stream 1's products ended before its warps said so)
       const float m1 = ctl.ml[r][0], l1 = ctl.ml[r][1];
       mm = fmaxf(ml, m1);
-      const float ref = mm == -INFINITY ? 0.f : mm;
-      w0 = l > 0.f ? exp2f(ml - ref) : 0.f;
-      w1 = l1 > 0.f ? exp2f(m1 - ref) : 0.f;
+      const float top = mm == -INFINITY ? 0.f : mm;
+      w0 = l == 0.f ? 0.f : exp2f(ml - top);
+      w1 = l1 == 0.f ? 0.f : exp2f(m1 - top);
       l0 = w0 * l + w1 * l1;
     }
     tc_fence_after();
     const bool parts = w.o.n_pieces > 0;
-    const float f = parts ? 1.f : l0 > 0.f ? 1.f / l0 : 0.f;
+    const float f = parts ? 1.f : l0 == 0.f ? 0.f : 1.f / l0;
     const int item_row = row_tok * p.G + g;
     const int64_t part_at =
         parts ? (int64_t)paged_part_slot(w.o, w.o.index) * p.part_rows + item_row : 0;
     if (warp_live) {
-      const float f0 = l > 0.f ? f * w0 : 0.f, f1 = f * w1;
+      const float f0 = l == 0.f ? 0.f : f * w0, f1 = f * w1;
 #pragma unroll
       for (int q = 0; q < D / 32; ++q) {
         float y[32];
@@ -633,13 +645,13 @@ __device__ bool softmax_role(Ctl &ctl, const AttnArgs &a, uint32_t tmem, int s) 
         }
         // (an output that no key went into is not read: it may hold anything)
 #pragma unroll
-        for (int i = 0; i < 32; ++i) y[i] = cnt > 0 && f0 > 0.f ? __uint_as_float(o[i]) * f0 : 0.f;
+        for (int i = 0; i < 32; ++i) y[i] = f0 == 0.f ? 0.f : __uint_as_float(o[i]) * f0;
         if (join) {
           tmem_ld32_async(to + D + q * 32, o);
           tmem_wait_ld();
           reg_fence(o);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) y[i] = f1 > 0.f ? fmaf(__uint_as_float(o[i]), f1, y[i]) : y[i];
+          for (int i = 0; i < 32; ++i) y[i] = f1 == 0.f ? y[i] : fmaf(__uint_as_float(o[i]), f1, y[i]);
         }
         if (live && parts) {
           float *dst = p.part + part_at * D + q * 32;

@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(PagedAttnPlan p) {
     for (int i = 0; i < R; ++i) {
       const int r = ty * R + i;
       if (r >= rows) continue;
-      const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;  // a row without keys: zeros
+      const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];  // a row without keys: zeros
       float *out = static_cast<float *>(p.out) + row_offset(p, o, r);
 #pragma unroll
       for (int j = 0; j < NC; j += 4)
