@@ -153,8 +153,19 @@ def status_string(status: int) -> str:
 
 # ---------------------------------------------------------------- marshalling
 
+_torch = None
+
+
+def _get_torch():
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
 def _dtype_code(t) -> int:
-    import torch
+    torch = _get_torch()
     if t.dtype == torch.bfloat16:
         return KDA_BF16
     if t.dtype == torch.float32:
@@ -373,43 +384,49 @@ def kda_decode_fused(xq, xk, xv, g, beta, gate, conv_w, norm_w, slot_ids, state_
 
 # ------------------------------------------- full-attention layers, draft verification
 
-def _check(name, t, shape, dtype, device):
+# A decode step makes these calls once per layer, so what they cost on the host
+# is kept small: a device is its index, a check is four comparisons.
+def _check(name, t, shape, dtype, dev):
     """A tensor argument of the calls below: its shape (None: any extent), dtype
-    and device are what the library would otherwise take on trust."""
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a tensor")
+    and device index are what the library would otherwise take on trust.
+    Returns its address."""
+    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+        have = t.shape
+        if have == shape or (len(have) == len(shape) and
+                             all(w is None or w == h for w, h in zip(shape, have))):
+            return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.dim() != len(shape) or any(want is not None and have != want
-                                    for have, want in zip(t.shape, shape)):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, wanted "
-                         f"{tuple('any' if s is None else s for s in shape)}")
-    if t.device != device or device.type != "cuda":
-        raise ValueError(f"{name} is on {t.device}; every tensor of a call is on one CUDA device")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}: every tensor of a call is on one CUDA device")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t
+    raise ValueError(f"{name} has shape {tuple(t.shape)}, wanted "
+                     f"{tuple('any' if s is None else s for s in shape)}")
 
 
-def _paged_call(what, device, stream, call):
-    """Runs one library call on ``device``: on ``stream``, or on that device's
-    current stream."""
-    import torch
-    with torch.cuda.device(device):
-        st = call(_stream_ptr(stream))
-    if st != KDA_OK:
-        raise KdaError(st, what)
-
-
-def _common(a, workspace, events, device):
-    import torch
-    _check("workspace", workspace, (None,), torch.uint8, device)
-    a.workspace = workspace.data_ptr()
+def _launch(what, fn, args, a, dev, workspace, stream, events):
+    """Fills in what every call's arguments end with and runs the call on the
+    tensors' device: on ``stream``, or on that device's current stream."""
+    torch = _torch
+    if dev < 0:
+        raise ValueError(f"{what} takes tensors on a CUDA device")
+    a.workspace = _check("workspace", workspace, (None,), torch.uint8, dev)
     a.workspace_bytes = workspace.numel()
     if events is not None:
         a.ev_begin = events[0].cuda_event
         a.ev_end = events[1].cuda_event
+    if stream is None:
+        a.stream = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        a.stream = _stream_ptr(stream)
+    if dev == torch.cuda.current_device():
+        st = fn(*args, ctypes.byref(a))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, ctypes.byref(a))
+    if st != KDA_OK:
+        raise KdaError(st, what)
 
 
 def kda_paged_workspace_bytes(T_total: int, Hq: int, Hkv: int, d: int) -> int:
@@ -445,35 +462,22 @@ def kda_paged_plan(cu_seqlens, cached_lens, block_table, held, free_ring, ring, 
     """Pages, positions and cache slots of a step's new tokens (see
     kda_paged_plan in include/kda_paged.h).  int32 CUDA tensors; block_table
     [B, max_pages] and free_ring [n_pages] are updated in place."""
-    import torch
-    i32, dev = torch.int32, free_ring.device
+    i32, dev = _get_torch().int32, free_ring.get_device()
     B, T = held.numel(), slot_map.numel()
-    _check("cu_seqlens", cu_seqlens, (B + 1,), i32, dev)
-    for name, t in (("cached_lens", cached_lens), ("held", held), ("held_out", held_out),
-                    ("kv_lens", kv_lens)):
-        _check(name, t, (B,), i32, dev)
-    _check("block_table", block_table, (B, None), i32, dev)
-    _check("free_ring", free_ring, (None,), i32, dev)
-    _check("ring", ring, (2,), i32, dev)
-    _check("ring_out", ring_out, (2,), i32, dev)
-    _check("positions", positions, (T,), i32, dev)
-    _check("slot_map", slot_map, (T,), i32, dev)
-    a = KdaPagedArgs(B=B, T_total=T, page_size=int(page_size), n_pages=free_ring.numel(),
-                     max_pages=block_table.shape[1])
-    _common(a, workspace, events, dev)
-
-    def call(s):
-        a.stream = s
-        return lib().kda_paged_plan(
-            _ptr(cu_seqlens), _ptr(cached_lens), _ptr(block_table), _ptr(held), _ptr(free_ring),
-            _ptr(ring), _ptr(held_out), _ptr(ring_out), _ptr(kv_lens), _ptr(positions),
-            _ptr(slot_map), ctypes.byref(a))
-    _paged_call("kda_paged_plan", dev, stream, call)
-
-
-def _pages(k_pages, v_pages, dtype, dev):
-    _check("k_pages", k_pages, (None, None, None, None), dtype, dev)
-    _check("v_pages", v_pages, tuple(k_pages.shape), dtype, dev)
+    per_req, per_tok = (B,), (T,)
+    args = (_check("cu_seqlens", cu_seqlens, (B + 1,), i32, dev),
+            _check("cached_lens", cached_lens, per_req, i32, dev),
+            _check("block_table", block_table, (B, None), i32, dev),
+            _check("held", held, per_req, i32, dev),
+            _check("free_ring", free_ring, (None,), i32, dev),
+            _check("ring", ring, (2,), i32, dev),
+            _check("held_out", held_out, per_req, i32, dev),
+            _check("ring_out", ring_out, (2,), i32, dev),
+            _check("kv_lens", kv_lens, per_req, i32, dev),
+            _check("positions", positions, per_tok, i32, dev),
+            _check("slot_map", slot_map, per_tok, i32, dev))
+    a = KdaPagedArgs(B, T, 0, 0, 0, page_size, free_ring.numel(), block_table.shape[1])
+    _launch("kda_paged_plan", lib().kda_paged_plan, args, a, dev, workspace, stream, events)
 
 
 def kda_paged_append(qkv, q_norm, k_norm, rope, positions, slot_map, q_out, k_pages, v_pages, *,
@@ -482,36 +486,30 @@ def kda_paged_append(qkv, q_norm, k_norm, rope, positions, slot_map, q_out, k_pa
     """Per-head RMSNorm and rotation of q and k, q out, k and v into their cache
     slots (see kda_paged_append in include/kda_paged.h).  qkv [T, Hq + 2 Hkv, d];
     q_norm, k_norm [d] fp32 or None; rope [max_pos, rot_dim] fp32 or None (see
-    rope_table); pages [n_pages, page_size, Hkv, d]."""
-    import torch
-    dt, dev = qkv.dtype, qkv.device
+    rope_table; without it positions are not read and may be None); pages
+    [n_pages, page_size, Hkv, d]."""
+    torch = _get_torch()
+    dt, dev, i32, f32 = qkv.dtype, qkv.get_device(), torch.int32, torch.float32
     code = _dtype_code(qkv)
-    _pages(k_pages, v_pages, dt, dev)
+    pk = _check("k_pages", k_pages, (None,) * 4, dt, dev)
     n_pages, page_size, Hkv, d = k_pages.shape
-    _check("q_out", q_out, (None, None, d), dt, dev)
-    T, Hq = q_out.shape[:2]
-    _check("qkv", qkv, (T, Hq + 2 * Hkv, d), dt, dev)
-    for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
-        if w is not None:
-            _check(name, w, (d,), torch.float32, dev)
-    _check("slot_map", slot_map, (T,), torch.int32, dev)
+    pq = _check("q_out", q_out, (None, None, d), dt, dev)
+    T, Hq, _ = q_out.shape
+    f = KdaAppendArgs(None, None, None, 0, 0, ROPE_MODE[rope_mode], norm_eps)
+    if q_norm is not None:
+        f.q_norm = _check("q_norm", q_norm, (d,), f32, dev)
+    if k_norm is not None:
+        f.k_norm = _check("k_norm", k_norm, (d,), f32, dev)
+    pos = None
     if rope is not None:
-        _check("rope", rope, (None, None), torch.float32, dev)
-        _check("positions", positions, (T,), torch.int32, dev)
-    f = KdaAppendArgs(q_norm=_ptr(q_norm), k_norm=_ptr(k_norm), rope=_ptr(rope),
-                      max_pos=0 if rope is None else rope.shape[0],
-                      rot_dim=0 if rope is None else rope.shape[1],
-                      rope_mode=ROPE_MODE[rope_mode], norm_eps=float(norm_eps))
-    a = KdaPagedArgs(T_total=T, Hq=Hq, Hkv=Hkv, d=d, page_size=page_size, n_pages=n_pages,
-                     dtype=code)
-    _common(a, workspace, events, dev)
-
-    def call(s):
-        a.stream = s
-        return lib().kda_paged_append(_ptr(qkv), None if rope is None else _ptr(positions),
-                                      _ptr(slot_map), _ptr(q_out), _ptr(k_pages), _ptr(v_pages),
-                                      ctypes.byref(f), ctypes.byref(a))
-    _paged_call("kda_paged_append", dev, stream, call)
+        f.rope = _check("rope", rope, (None, None), f32, dev)
+        f.max_pos, f.rot_dim = rope.shape
+        pos = _check("positions", positions, (T,), i32, dev)
+    args = (_check("qkv", qkv, (T, Hq + 2 * Hkv, d), dt, dev), pos,
+            _check("slot_map", slot_map, (T,), i32, dev), pq, pk,
+            _check("v_pages", v_pages, k_pages.shape, dt, dev), ctypes.byref(f))
+    a = KdaPagedArgs(0, T, Hq, Hkv, d, page_size, n_pages, 0, code)
+    _launch("kda_paged_append", lib().kda_paged_append, args, a, dev, workspace, stream, events)
 
 
 def kda_paged_attn(q, k_pages, v_pages, block_table, cu_seqlens, kv_lens, out, *, workspace,
@@ -521,29 +519,21 @@ def kda_paged_attn(q, k_pages, v_pages, block_table, cu_seqlens, kv_lens, out, *
     kda_paged_attn in include/kda_paged.h).  q, out [T, Hq, d]; pages [n_pages,
     page_size, Hkv, d]; block_table [B, max_pages], cu_seqlens [B + 1] and
     kv_lens [B] int32.  scale: 1 / sqrt(d) when not given."""
-    import torch
-    dt, dev = q.dtype, q.device
+    i32, dt, dev = _get_torch().int32, q.dtype, q.get_device()
     code = _dtype_code(q)
-    _pages(k_pages, v_pages, dt, dev)
+    pk = _check("k_pages", k_pages, (None,) * 4, dt, dev)
     n_pages, page_size, Hkv, d = k_pages.shape
-    _check("q", q, (None, None, d), dt, dev)
-    T, Hq = q.shape[:2]
-    _check("out", out, (T, Hq, d), dt, dev)
-    _check("kv_lens", kv_lens, (None,), torch.int32, dev)
+    pq = _check("q", q, (None, None, d), dt, dev)
+    T, Hq, _ = q.shape
     B = kv_lens.numel()
-    _check("cu_seqlens", cu_seqlens, (B + 1,), torch.int32, dev)
-    _check("block_table", block_table, (B, None), torch.int32, dev)
-    a = KdaPagedArgs(B=B, T_total=T, Hq=Hq, Hkv=Hkv, d=d, page_size=page_size, n_pages=n_pages,
-                     max_pages=block_table.shape[1], dtype=code)
-    _common(a, workspace, events, dev)
-    c = d ** -0.5 if scale is None else float(scale)
-
-    def call(s):
-        a.stream = s
-        return lib().kda_paged_attn(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(block_table),
-                                    _ptr(cu_seqlens), _ptr(kv_lens), _ptr(out), c,
-                                    int(bool(causal)), ctypes.byref(a))
-    _paged_call("kda_paged_attn", dev, stream, call)
+    args = (pq, pk, _check("v_pages", v_pages, k_pages.shape, dt, dev),
+            _check("block_table", block_table, (B, None), i32, dev),
+            _check("cu_seqlens", cu_seqlens, (B + 1,), i32, dev),
+            _check("kv_lens", kv_lens, (B,), i32, dev),
+            _check("out", out, q.shape, dt, dev),
+            d ** -0.5 if scale is None else scale, 1 if causal else 0)
+    a = KdaPagedArgs(B, T, Hq, Hkv, d, page_size, n_pages, block_table.shape[1], code)
+    _launch("kda_paged_attn", lib().kda_paged_attn, args, a, dev, workspace, stream, events)
 
 
 def kda_verify_drafts(target_probs, draft_probs, draft_tokens, u_accept, u_sample, accepted,
@@ -553,31 +543,25 @@ def kda_verify_drafts(target_probs, draft_probs, draft_tokens, u_accept, u_sampl
     draft_probs [N, n_draft, V] or None (looked-up drafts); draft_tokens and
     u_accept [N, n_draft]; u_sample [N].  accepted [N] is kda_decode_spec's
     accepted_prev; tokens [N, n_draft + 1]."""
-    import torch
-    dt, dev = target_probs.dtype, target_probs.device
+    torch = _get_torch()
+    i32, f32 = torch.int32, torch.float32
+    dt, dev = target_probs.dtype, target_probs.get_device()
     code = _dtype_code(target_probs)
-    _check("target_probs", target_probs, (None, None, None), dt, dev)
+    pp = _check("target_probs", target_probs, (None,) * 3, dt, dev)
     N, n1, V = target_probs.shape
-    if n1 < 1:
+    n = n1 - 1
+    if n < 0:
         raise ValueError("target_probs has n_draft + 1 >= 1 rows per sequence")
-    if draft_probs is not None:
-        _check("draft_probs", draft_probs, (N, n1 - 1, V), dt, dev)
-    _check("draft_tokens", draft_tokens, (N, n1 - 1), torch.int32, dev)
-    _check("u_accept", u_accept, (N, n1 - 1), torch.float32, dev)
-    _check("u_sample", u_sample, (N,), torch.float32, dev)
-    _check("accepted", accepted, (N,), torch.int32, dev)
-    _check("tokens", tokens, (N, n1), torch.int32, dev)
-    if draft_lens is not None:
-        _check("draft_lens", draft_lens, (N,), torch.int32, dev)
-    a = KdaVerifyArgs(N=N, n_draft=n1 - 1, V=V, dtype=code)
-    _common(a, workspace, events, dev)
-
-    def call(s):
-        a.stream = s
-        return lib().kda_verify_drafts(_ptr(target_probs), _ptr(draft_probs), _ptr(draft_tokens),
-                                       _ptr(draft_lens), _ptr(u_accept), _ptr(u_sample),
-                                       _ptr(accepted), _ptr(tokens), ctypes.byref(a))
-    _paged_call("kda_verify_drafts", dev, stream, call)
+    args = (pp,
+            None if draft_probs is None else _check("draft_probs", draft_probs, (N, n, V), dt, dev),
+            _check("draft_tokens", draft_tokens, (N, n), i32, dev),
+            None if draft_lens is None else _check("draft_lens", draft_lens, (N,), i32, dev),
+            _check("u_accept", u_accept, (N, n), f32, dev),
+            _check("u_sample", u_sample, (N,), f32, dev),
+            _check("accepted", accepted, (N,), i32, dev),
+            _check("tokens", tokens, (N, n1), i32, dev))
+    a = KdaVerifyArgs(N, n, V, code)
+    _launch("kda_verify_drafts", lib().kda_verify_drafts, args, a, dev, workspace, stream, events)
 
 
 def kda_device_status(workspace, stream=None):
