@@ -10,7 +10,9 @@
 // border by its rounding error, and a border that moves past u picks another
 // token: fp32 sums would change about one draw in a hundred.  Differences and
 // sums are therefore carried as pairs of floats (the rounding error of every
-// addition is kept, about 48 bits) and joined in doubles.
+// addition is kept, about 46 bits); doubles would do, but a GB300 SM adds two
+// of them per cycle, and the joins of a row's partial sums alone then take
+// longer than its loads (64 x 7 drafts, V = 131072: 38.9 us with doubles).
 #include <cooperative_groups.h>
 
 #include "kda_paged.cuh"
@@ -25,6 +27,10 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxSegs = 4096;  // segments a CTA keeps (32 KB)
 
+// hi + lo, |lo| at most half a step of hi
+struct F2 {
+  float hi, lo;
+};
 // s + e += x, the error of the addition kept exactly (Knuth's two-sum)
 __device__ __forceinline__ void add_exact(float &s, float &e, float x) {
   const float t = __fadd_rn(s, x);
@@ -32,6 +38,27 @@ __device__ __forceinline__ void add_exact(float &s, float &e, float x) {
   e = __fadd_rn(e, __fadd_rn(__fsub_rn(s, __fsub_rn(t, b)), __fsub_rn(x, b)));
   s = t;
 }
+__device__ __forceinline__ F2 normal(float s, float e) {
+  const float hi = __fadd_rn(s, e);
+  return {hi, __fsub_rn(e, __fsub_rn(hi, s))};
+}
+__device__ __forceinline__ F2 add(F2 a, F2 b) {
+  float s = a.hi, e = __fadd_rn(a.lo, b.lo);
+  add_exact(s, e, b.hi);
+  return normal(s, e);
+}
+__device__ __forceinline__ F2 times(F2 a, float u) {
+  const float p = __fmul_rn(a.hi, u);
+  return normal(p, fmaf(a.lo, u, fmaf(a.hi, u, -p)));
+}
+__device__ __forceinline__ bool above(F2 a, F2 b) {
+  return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo);
+}
+template <typename Shfl>
+__device__ __forceinline__ F2 shuffled(F2 v, Shfl f) {
+  return {f(v.hi), f(v.lo)};
+}
+
 // max(p - q, 0) as hi + lo, exactly
 __device__ __forceinline__ void rest(float p, float q, float &hi, float &lo) {
   const float d = __fsub_rn(p, q);
@@ -49,20 +76,31 @@ struct Row {
   int gone;        // -1: none
 };
 
-template <typename T>
-__device__ __forceinline__ void mass(const Row<T> &r, float p, float q, int i, float &hi,
-                                     float &lo) {
-  rest(p, i == r.gone ? p : q, hi, lo);
+template <bool Q>
+__device__ __forceinline__ void mass(float p, float q, bool gone, float &hi, float &lo) {
+  if constexpr (Q) {
+    rest(p, q, hi, lo);
+  } else {
+    hi = p > 0.f && !gone ? p : 0.f;
+    lo = 0.f;
+  }
 }
 
 // Sum of elements [i0, i1) of the row, over one warp.  VECT: rows start on 16
-// bytes (then i0 is a multiple of the vector too).
-template <typename T, bool VECT>
-__device__ double segment_sum(const Row<T> &r, int i0, int i1) {
+// bytes (then i0 is a multiple of the vector too).  Without q an element takes
+// half the instructions, and twice the loads fit the registers.
+template <typename T, bool VECT, bool Q>
+__device__ F2 segment_sum(const Row<T> &r, int i0, int i1) {
   constexpr int N = VECT ? 16 / (int)sizeof(T) : 1;
-  constexpr int U = VECT ? 4 : 8;  // loads in flight per row
+  constexpr int U = VECT ? (Q ? 2 : 4) : 8;  // loads in flight per row
   const int lane = threadIdx.x & 31;
   float s = 0.f, e = 0.f;
+  auto take = [&](float p, float q, int i) {
+    float hi, lo;
+    mass<Q>(p, q, i == r.gone, hi, lo);
+    add_exact(s, e, hi);
+    if constexpr (Q) e = __fadd_rn(e, lo);
+  };
   for (int base = i0; base < i1; base += 32 * N * U) {
     if (VECT && base + 32 * N * U <= i1) {
       uint4 pv[U], qv[U];
@@ -70,67 +108,69 @@ __device__ double segment_sum(const Row<T> &r, int i0, int i1) {
       for (int u = 0; u < U; ++u) {
         const int i = base + (u * 32 + lane) * N;
         pv[u] = *reinterpret_cast<const uint4 *>(r.p + i);
-        qv[u] = r.q ? *reinterpret_cast<const uint4 *>(r.q + i) : make_uint4(0, 0, 0, 0);
+        if constexpr (Q) qv[u] = *reinterpret_cast<const uint4 *>(r.q + i);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int i = base + (u * 32 + lane) * N;
         const T *pt = reinterpret_cast<const T *>(&pv[u]);
         const T *qt = reinterpret_cast<const T *>(&qv[u]);
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-          float hi, lo;
-          mass(r, to_f32<T>(pt[k]), to_f32<T>(qt[k]), i + k, hi, lo);
-          add_exact(s, e, hi);
-          e = __fadd_rn(e, lo);
-        }
+        for (int k = 0; k < N; ++k)
+          take(to_f32<T>(pt[k]), Q ? to_f32<T>(qt[k]) : 0.f, base + (u * 32 + lane) * N + k);
       }
     } else {
-      float pv[N * U], qv[N * U];
+#pragma unroll 1
+      for (int h = 0; h < N * U; h += 8) {
+        float pv[8], qv[8];
 #pragma unroll
-      for (int u = 0; u < N * U; ++u) {
-        const int i = base + u * 32 + lane;
-        pv[u] = i < i1 ? to_f32<T>(r.p[i]) : 0.f;
-        qv[u] = r.q && i < i1 ? to_f32<T>(r.q[i]) : 0.f;
-      }
+        for (int u = 0; u < 8; ++u) {
+          const int i = base + (h + u) * 32 + lane;
+          pv[u] = i < i1 ? to_f32<T>(r.p[i]) : 0.f;
+          qv[u] = Q && i < i1 ? to_f32<T>(r.q[i]) : 0.f;
+        }
 #pragma unroll
-      for (int u = 0; u < N * U; ++u) {
-        float hi, lo;
-        mass(r, pv[u], qv[u], base + u * 32 + lane, hi, lo);
-        add_exact(s, e, hi);
-        e = __fadd_rn(e, lo);
+        for (int u = 0; u < 8; ++u) take(pv[u], qv[u], base + (h + u) * 32 + lane);
       }
     }
   }
-  double v = (double)s + (double)e;
+  F2 v = normal(s, e);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = 16; o > 0; o >>= 1)
+    v = add(v, shuffled(v, [o](float x) { return __shfl_xor_sync(0xffffffffu, x, o); }));
   return v;
 }
 
-// Inclusive block scan of doubles in a fixed order.
-__device__ double block_scan(double v, double *warp_sums) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Inclusive scan of v over the lanes of a warp.
+__device__ __forceinline__ F2 warp_scan(F2 v) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const double x = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += x;
+    const F2 x = shuffled(v, [o](float y) { return __shfl_up_sync(0xffffffffu, y, o); });
+    if (lane >= o) v = add(x, v);
   }
+  return v;
+}
+// Inclusive scan over the CTA's threads; *total: the sum over all of them.
+__device__ F2 block_scan(F2 v, F2 *warp_sums, F2 *total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  v = warp_scan(v);
   __syncthreads();
   if (lane == 31) warp_sums[warp] = v;
   __syncthreads();
-  double before = 0.;
-  for (int w = 0; w < warp; ++w) before += warp_sums[w];
-  return before + v;
+  const F2 all = warp_scan(lane < kWarps ? warp_sums[lane] : F2{0.f, 0.f});
+  *total = shuffled(all, [](float x) { return __shfl_sync(0xffffffffu, x, kWarps - 1); });
+  const F2 before =
+      shuffled(all, [warp](float x) { return __shfl_sync(0xffffffffu, x, (warp + 31) & 31); });
+  return warp ? add(before, v) : v;
 }
 
 // One cluster per sequence; CTA `rank` owns segments [rank * n_local, ...) of
 // seg_len elements.
 template <typename T, bool VECT>
-__global__ void __launch_bounds__(kThreads) verify_kernel(VerifyPlan p, int seg_len, int n_local) {
-  extern __shared__ double s_seg[];  // [n_local] sums, then inclusive sums
-  __shared__ double warp_sums[kWarps];
-  __shared__ double s_tot[2][kMaxCluster];
+__global__ void __launch_bounds__(kThreads, 2) verify_kernel(VerifyPlan p, int seg_len, int n_local) {
+  extern __shared__ F2 s_seg[];  // [n_local] sums, then inclusive sums
+  __shared__ F2 warp_sums[kWarps];
+  __shared__ F2 s_tot[2][kMaxCluster];
   __shared__ int s_kept, s_pick, s_last;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = cluster.block_rank(), n_ranks = cluster.num_blocks();
@@ -150,7 +190,8 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(VerifyPlan p, int seg_
     }
     return;
   }
-  if (tid == 0) s_kept = len;
+  const float u_sample = p.u_sample[n];
+  if (tid == 0) s_kept = len, s_pick = 0x7fffffff, s_last = -1;
   __syncthreads();
   for (int j = tid; j < len; j += kThreads) {
     const int x = drafts[j];
@@ -178,44 +219,55 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(VerifyPlan p, int seg_
   }
 
   const int first = rank * n_local;
-  double start = 0., thr = 0.;  // this CTA's first border, the place that is sought
+  F2 start = {0.f, 0.f}, thr = {0.f, 0.f};  // this CTA's first border, the place that is sought
   int owner = -1;
   for (int phase = 0; phase < 2; ++phase) {
     for (int g = tid >> 5; g < n_local; g += kWarps) {
       const int64_t i0 = (int64_t)(first + g) * seg_len;
-      double v = 0.;
-      if (i0 < V) v = segment_sum<T, VECT>(row, (int)i0, (int)min(V, i0 + seg_len));
+      F2 v = {0.f, 0.f};
+      const int a = (int)i0, b = (int)min(V, i0 + seg_len);
+      if (i0 < V)
+        v = row.q ? segment_sum<T, VECT, true>(row, a, b) : segment_sum<T, VECT, false>(row, a, b);
       if ((tid & 31) == 0) s_seg[g] = v;
     }
     __syncthreads();
-    // inclusive sums over the CTA's segments, a run per thread
-    const int run = (n_local + kThreads - 1) / kThreads;
-    const int g0 = min(n_local, tid * run), g1 = min(n_local, g0 + run);
-    double mine = 0.;
-    for (int g = g0; g < g1; ++g) mine += s_seg[g];
-    const double inc = block_scan(mine, warp_sums);
-    double c = inc - mine;
-    if (run == 1) {
-      if (g0 < g1) s_seg[g0] = inc;
+    // inclusive sums over the CTA's segments: a warp's scan where they are few,
+    // else a run of them per thread
+    F2 mine_total;
+    if (n_local <= 32) {
+      if (tid < 32) {
+        const F2 v = warp_scan(tid < n_local ? s_seg[tid] : F2{0.f, 0.f});
+        if (tid < n_local) s_seg[tid] = v;
+      }
     } else {
-      for (int g = g0; g < g1; ++g) c += s_seg[g], s_seg[g] = c;
+      const int run = (n_local + kThreads - 1) / kThreads;
+      const int g0 = min(n_local, tid * run), g1 = min(n_local, g0 + run);
+      F2 c = {0.f, 0.f};
+      for (int g = g0; g < g1; ++g) s_seg[g] = c = add(c, s_seg[g]);
+      const F2 inc = block_scan(c, warp_sums, &mine_total);
+      // what the threads before hold: the neighbour's inclusive sum
+      F2 before = shuffled(inc, [](float x) { return __shfl_up_sync(0xffffffffu, x, 1); });
+      if ((tid & 31) == 0) {
+        before = {0.f, 0.f};
+        for (int w = 0; w < (tid >> 5); ++w) before = add(before, warp_sums[w]);
+      }
+      for (int g = g0; g < g1; ++g) s_seg[g] = add(before, s_seg[g]);
     }
     __syncthreads();
     // every CTA learns every CTA's sum
     if (tid < n_ranks) cluster.map_shared_rank(&s_tot[phase][0], tid)[rank] = s_seg[n_local - 1];
     cluster.sync();
-    double total = 0.;
-    for (int r = 0; r < n_ranks; ++r) total += s_tot[phase][r];
-    if (total > 0.) {
-      thr = (double)p.u_sample[n] * total;
-      double b = 0.;
+    F2 total = {0.f, 0.f};
+    for (int r = 0; r < n_ranks; ++r) total = add(total, s_tot[phase][r]);
+    if (total.hi > 0.f) {
+      thr = times(total, u_sample);
+      F2 b = {0.f, 0.f};
       int last = -1;
       for (int r = 0; r < n_ranks; ++r) {
-        const double v = s_tot[phase][r];
-        if (v > 0.) last = r;
-        if (owner < 0 && b + v > thr) owner = r;
         if (r == rank) start = b;
-        b += v;
+        if (s_tot[phase][r].hi > 0.f) last = r;
+        b = add(b, s_tot[phase][r]);
+        if (owner < 0 && above(b, thr)) owner = r;
       }
       if (owner < 0) owner = last;  // u at its upper end
       break;
@@ -230,30 +282,39 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(VerifyPlan p, int seg_
   if (owner != rank) return;
 
   // the first segment whose border passes thr (or the last one with mass)
-  if (tid == 0) s_pick = n_local, s_last = 0;
-  __syncthreads();
   for (int g = tid; g < n_local; g += kThreads) {
-    if (start + s_seg[g] > thr) atomicMin(&s_pick, g);
-    if (s_seg[g] > (g ? s_seg[g - 1] : 0.)) atomicMax(&s_last, g);
+    if (above(add(start, s_seg[g]), thr)) atomicMin(&s_pick, g);
+    if (above(s_seg[g], g ? s_seg[g - 1] : F2{0.f, 0.f})) atomicMax(&s_last, g);
   }
   __syncthreads();
-  const int g = s_pick < n_local ? s_pick : s_last;
-  double c = start + (g ? s_seg[g - 1] : 0.);
+  const int g = s_pick != 0x7fffffff ? s_pick : max(s_last, 0);
+  F2 c = g ? add(start, s_seg[g - 1]) : start;
   const int64_t i0 = (int64_t)(first + g) * seg_len, i1 = min(V, i0 + seg_len);
   __syncthreads();
   if (tid == 0) s_pick = 0x7fffffff, s_last = -1;
-  for (int64_t base = i0; base < i1; base += kThreads) {
-    const int i = (int)base + tid;
-    float hi = 0.f, lo = 0.f;
-    if (i < i1)
-      mass(row, to_f32<T>(row.p[i]), row.q ? to_f32<T>(row.q[i]) : 0.f, i, hi, lo);
-    const double v = (double)hi + (double)lo;
-    const double inc = c + block_scan(v, warp_sums);
-    if (v > 0.) {
-      atomicMax(&s_last, i);
-      if (inc > thr) atomicMin(&s_pick, i);
+  for (int64_t base = i0; base < i1; base += 2 * kThreads) {
+    const int i = (int)base + 2 * tid;  // two neighbours a thread
+    float hi[2] = {0.f, 0.f}, lo[2] = {0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (i + k < i1) {
+        const float pv = to_f32<T>(row.p[i + k]);
+        if (row.q) mass<true>(pv, to_f32<T>(row.q[i + k]), false, hi[k], lo[k]);
+        else mass<false>(pv, 0.f, i + k == row.gone, hi[k], lo[k]);
+      }
+    const F2 a = {hi[0], lo[0]}, b = {hi[1], lo[1]}, both = add(a, b);
+    F2 total;
+    const F2 inc = block_scan(both, warp_sums, &total);
+    if (both.hi > 0.f) {
+      atomicMax(&s_last, hi[1] > 0.f ? i + 1 : i);
+      if (above(add(c, inc), thr)) {
+        // the border lies in this thread's pair or before it: before its second
+        // token lies what is before the pair and its first token
+        const F2 one = add(add(c, inc), F2{-hi[1], -lo[1]});
+        atomicMin(&s_pick, hi[0] > 0.f && above(one, thr) ? i : hi[1] > 0.f ? i + 1 : i);
+      }
     }
-    for (int w = 0; w < kWarps; ++w) c += warp_sums[w];
+    c = add(c, total);
     __syncthreads();
     if (s_pick != 0x7fffffff) break;
   }
@@ -265,8 +326,15 @@ cudaError_t launch_t(const VerifyPlan &p) {
   // elements of a segment: what a warp sums before one reduction; longer ones
   // for vocabularies that would have more segments than a CTA keeps
   int seg_len = 1024;
-  const int ranks = 1;
   int n_segs = (p.V + seg_len - 1) / seg_len;
+  // CTAs of a sequence: more while all of them run at once (two fit an SM) and
+  // each has a segment for half its warps; eight only while they find an SM
+  // each (38 sequences of 131072 tokens: 16.0 us on four, 19.9 us on eight; 16
+  // sequences: 11.4 and 10.6 us; one: 9.4 and 7.6 us).
+  int ranks = 1;
+  while (ranks < kMaxCluster && n_segs >= ranks * kWarps &&
+         (int64_t)p.N * ranks * 2 <= (ranks < 4 ? 2 : 1) * kPagedMaxCtas)
+    ranks *= 2;
   while (n_segs > ranks * kMaxSegs) {
     seg_len *= 2;
     n_segs = (p.V + seg_len - 1) / seg_len;
@@ -276,7 +344,7 @@ cudaError_t launch_t(const VerifyPlan &p) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.N * ranks);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = (size_t)n_local * sizeof(double);
+  cfg.dynamicSmemBytes = (size_t)n_local * sizeof(F2);
   cfg.stream = p.stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
