@@ -3,13 +3,18 @@
 //
 //     x' = x / sqrt(mean(x^2) + eps) * w,   (a, b) -> (a cos - b sin, a sin + b cos)
 //
-// Bound by HBM: every element is read once and written once, with about six
-// operations between (norm statistics and rotation in fp32, one rounding at
+// Bound by HBM: every element is read once and written once, with about ten
+// instructions between (norm statistics and rotation in fp32, one rounding at
 // the store).  A lane holds 16 bytes of a head, a head takes d * es / 16
-// lanes; the mean is a shuffle tree over them and, with halves rotated, a
-// channel's partner sits in the lane rot / (2 * VEC) away (rot is a multiple
-// of 16, so a lane's channels share one partner lane).  A warp keeps one
-// token's cosines and sines in registers and walks several of its heads.
+// lanes, and the mean is a shuffle tree over them.  Where halves are rotated a
+// lane holds a run of channels and the run rot / 2 behind it, so that both
+// partners of a rotation are in one lane.
+//
+// What a token's row needs first (its slot, its position, then the cosines and
+// sines there) is a chain of two loads.  A warp walks the heads of a token in
+// batches of kBatch passes, the next batch's loads in flight while one is
+// worked on, so that the chain and the load latency are paid once a token; with
+// one batch per warp they were paid six times as often.
 #include "kda_paged.cuh"
 
 namespace kda {
@@ -17,138 +22,169 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kBatch = 4;  // passes (32 lanes' worth of heads) of a batch
 
-template <typename T> struct Vec;
-template <> struct Vec<__nv_bfloat16> { static constexpr int N = 8; };
-template <> struct Vec<float> { static constexpr int N = 4; };
+template <typename T> constexpr int kVec = 16 / (int)sizeof(T);  // channels of a lane
 
 template <typename T>
-__device__ __forceinline__ void unpack(const uint4 &w, float (&x)[Vec<T>::N]) {
+__device__ __forceinline__ void unpack(const uint4 &w, float (&x)[kVec<T>]) {
   const T *t = reinterpret_cast<const T *>(&w);
 #pragma unroll
-  for (int i = 0; i < Vec<T>::N; ++i) x[i] = to_f32<T>(t[i]);
+  for (int i = 0; i < kVec<T>; ++i) x[i] = to_f32<T>(t[i]);
 }
 template <typename T>
-__device__ __forceinline__ uint4 pack(const float (&x)[Vec<T>::N]) {
+__device__ __forceinline__ uint4 pack(const float (&x)[kVec<T>]) {
   uint4 w;
   T *t = reinterpret_cast<T *>(&w);
 #pragma unroll
-  for (int i = 0; i < Vec<T>::N; ++i) t[i] = from_f32<T>(x[i]);
+  for (int i = 0; i < kVec<T>; ++i) t[i] = from_f32<T>(x[i]);
   return w;
 }
 
-// U: passes (32 lanes' worth of heads) a warp walks
-template <typename T, int D, int U>
-__global__ void __launch_bounds__(kThreads) append_kernel(AppendPlan p) {
-  constexpr int N = Vec<T>::N;
-  constexpr int LPH = D / N;         // lanes of a head
-  constexpr int HPP = 32 / LPH;      // heads of a pass
-  const int lane = threadIdx.x & 31;
+// HALVES: the lane's channels are two runs of kVec / 2, at ca and cb; else they
+// are one run at ca.
+template <bool HALVES, typename T>
+__device__ __forceinline__ uint4 load_row(const T *head, int ca, int cb) {
+  if constexpr (HALVES) {
+    const uint2 a = __ldcs(reinterpret_cast<const uint2 *>(head + ca));
+    const uint2 b = __ldcs(reinterpret_cast<const uint2 *>(head + cb));
+    return make_uint4(a.x, a.y, b.x, b.y);
+  } else {
+    return __ldcs(reinterpret_cast<const uint4 *>(head + ca));
+  }
+}
+template <bool HALVES, typename T>
+__device__ __forceinline__ void store_row(T *head, int ca, int cb, uint4 w) {
+  if constexpr (HALVES) {
+    *reinterpret_cast<uint2 *>(head + ca) = make_uint2(w.x, w.y);
+    *reinterpret_cast<uint2 *>(head + cb) = make_uint2(w.z, w.w);
+  } else {
+    *reinterpret_cast<uint4 *>(head + ca) = w;
+  }
+}
+// N / 2 floats at a and at b
+template <int N>
+__device__ __forceinline__ void load_runs(const float *a, const float *b, float (&x)[N]) {
+#pragma unroll
+  for (int i = 0; i < N / 2; i += 2) {
+    const float2 u = *reinterpret_cast<const float2 *>(a + i);
+    const float2 v = *reinterpret_cast<const float2 *>(b + i);
+    x[i] = u.x, x[i + 1] = u.y, x[N / 2 + i] = v.x, x[N / 2 + i + 1] = v.y;
+  }
+}
+
+// A warp takes `share` consecutive passes of a token, `groups` warps a token.
+template <typename T, int D, bool HALVES>
+__global__ void __launch_bounds__(kThreads) append_kernel(AppendPlan p, int share, int groups) {
+  constexpr int N = kVec<T>, M = N / 2;
+  constexpr int LPH = D / N;     // lanes of a head
+  constexpr int HPP = 32 / LPH;  // heads of a pass
+  const int lane = threadIdx.x & 31, l = lane % LPH;
   const int heads = p.Hq + 2 * p.Hkv;
-  const int groups = (heads + HPP * U - 1) / (HPP * U);  // warps of a token
   const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int64_t t = unit / groups;
   if (t >= p.T) return;
-  const int h0 = (int)(unit - t * groups) * (HPP * U) + lane / LPH;
-  const int e0 = (lane % LPH) * N;   // first channel of this lane
+  const int first = (int)(unit - t * groups) * share;
+  const int last = min(first + share, (heads + HPP - 1) / HPP);  // passes [first, last)
 
+  const int half = p.rot / 2;
+  const bool turned = l * N < p.rot;  // (rot is a multiple of 16: whole lanes)
+  const int ca = HALVES && turned ? l * M : l * N;
+  const int cb = HALVES && turned ? half + l * M : l * N + M;
+  const T *src = static_cast<const T *>(p.qkv) + t * heads * D;
+  // the rows do not depend on where the token goes: they are asked for first
+  uint4 raw[kBatch], next[kBatch];
+  auto load = [&](uint4 (&r)[kBatch], int pass) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int h = (pass + u) * HPP + lane / LPH;
+      r[u] = pass + u < last && h < heads ? load_row<HALVES>(src + (int64_t)h * D, ca, cb)
+                                          : make_uint4(0, 0, 0, 0);
+    }
+  };
+  load(raw, first);
   const int64_t slot = p.slots[t];
-  if (slot < 0) return;
   const int64_t pos = p.rot > 0 ? p.positions[t] : 0;
+  if (slot < 0) return;
   if (slot >= p.n_slots || pos < 0 || (p.rot > 0 && pos >= p.max_pos)) {
     if (lane == 0) raise_error(p.err, slot >= p.n_slots ? (uint32_t)ERR_BAD_SLOT : (uint32_t)ERR_BAD_POS);
     return;
   }
-  uint4 raw[U];
-  const T *src = static_cast<const T *>(p.qkv) + t * heads * D + e0;
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int h = h0 + u * HPP;
-    if (h < heads) raw[u] = *reinterpret_cast<const uint4 *>(src + (int64_t)h * D);
-  }
-  // cosines and sines of this lane's channels; channels behind rot pass through
-  float cs[N], sn[N];
-  const int half = p.rot / 2;
-  const bool turned = e0 < p.rot;
+  // cosines and sines of this lane's pairs of channels; channels behind rot pass through
+  float cs[M], sn[M];
   if (turned) {
-    const float *row = p.rope + pos * p.rot;
-    if (p.mode == 0) {
-      const int i = e0 < half ? e0 : e0 - half;
+    const float *row = p.rope + pos * p.rot + l * M;
 #pragma unroll
-      for (int k = 0; k < N; k += 4) {
-        const float4 c = *reinterpret_cast<const float4 *>(row + i + k);
-        const float4 s = *reinterpret_cast<const float4 *>(row + half + i + k);
-        cs[k] = c.x, cs[k + 1] = c.y, cs[k + 2] = c.z, cs[k + 3] = c.w;
-        sn[k] = s.x, sn[k + 1] = s.y, sn[k + 2] = s.z, sn[k + 3] = s.w;
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < N; k += 2) {
-        cs[k] = cs[k + 1] = row[(e0 + k) / 2];
-        sn[k] = sn[k + 1] = row[half + (e0 + k) / 2];
-      }
+    for (int i = 0; i < M; i += 2) {
+      const float2 c = *reinterpret_cast<const float2 *>(row + i);
+      const float2 s = *reinterpret_cast<const float2 *>(row + half + i);
+      cs[i] = c.x, cs[i + 1] = c.y, sn[i] = s.x, sn[i + 1] = s.y;
     }
   }
-  const int hop = half / N;  // lanes to the partner channel (halves)
 
+  for (int pass = first; pass < last; pass += kBatch) {
+    if (pass + kBatch < last) load(next, pass + kBatch);
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int h = h0 + u * HPP;
-    const bool live = h < heads, is_q = h < p.Hq, is_k = !is_q && h < p.Hq + p.Hkv;
-    float x[N];
-    if (!live) raw[u] = make_uint4(0, 0, 0, 0);
-    unpack<T>(raw[u], x);
-    float ss = 0.f;
+    for (int u = 0; u < kBatch; ++u) {
+      const int h = (pass + u) * HPP + lane / LPH;
+      const bool live = pass + u < last && h < heads;
+      const bool is_q = h < p.Hq, is_k = !is_q && h < p.Hq + p.Hkv;
+      float x[N];
+      unpack<T>(raw[u], x);
+      float ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) ss = fmaf(x[i], x[i], ss);
+      for (int i = 0; i < N; ++i) ss = fmaf(x[i], x[i], ss);
 #pragma unroll
-    for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float *w = is_q ? p.q_norm : is_k ? p.k_norm : nullptr;
-    if (w) {
-      const float r = rsqrtf(ss * (1.f / D) + p.eps);
+      for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (!live) continue;
+      uint4 w = raw[u];
+      if (is_q || is_k) {
+        const float *norm = is_q ? p.q_norm : p.k_norm;
+        if (norm) {
+          const float r = rsqrtf(ss * (1.f / D) + p.eps);
+          float g[N];
+          load_runs<N>(norm + ca, norm + cb, g);
 #pragma unroll
-      for (int i = 0; i < N; ++i) x[i] = x[i] * r * w[e0 + i];
-    }
-    float y[N];
-    if (p.mode == 0) {
+          for (int i = 0; i < N; ++i) x[i] = x[i] * r * g[i];
+        }
+        if (turned) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        // every lane takes part; lanes behind rot read their own channel
-        const int from = !turned ? lane : e0 < half ? lane + hop : lane - hop;
-        const float other = __shfl_sync(0xffffffffu, x[i], from);
-        y[i] = !turned ? x[i]
-               : e0 < half ? x[i] * cs[i] - other * sn[i]
-                           : other * sn[i] + x[i] * cs[i];
+          for (int i = 0; i < M; ++i) {
+            const int a = HALVES ? i : 2 * i, b = HALVES ? i + M : 2 * i + 1;
+            const float u0 = x[a], u1 = x[b];
+            x[a] = u0 * cs[i] - u1 * sn[i];
+            x[b] = u0 * sn[i] + u1 * cs[i];
+          }
+        }
+        w = pack<T>(x);
       }
-    } else {
+      T *dst = is_q   ? static_cast<T *>(p.q) + (t * p.Hq + h) * D
+               : is_k ? static_cast<T *>(p.k_pages) + (slot * p.Hkv + (h - p.Hq)) * D
+                      : static_cast<T *>(p.v_pages) + (slot * p.Hkv + (h - p.Hq - p.Hkv)) * D;
+      store_row<HALVES>(dst, ca, cb, w);
+    }
 #pragma unroll
-      for (int i = 0; i < N; i += 2) {
-        y[i] = turned ? x[i] * cs[i] - x[i + 1] * sn[i] : x[i];
-        y[i + 1] = turned ? x[i] * sn[i] + x[i + 1] * cs[i] : x[i + 1];
-      }
-    }
-    if (!live) continue;
-    T *dst;
-    if (is_q) {
-      dst = static_cast<T *>(p.q) + (t * p.Hq + h) * D;
-    } else if (is_k) {
-      dst = static_cast<T *>(p.k_pages) + (slot * p.Hkv + (h - p.Hq)) * D;
-    } else {
-      dst = static_cast<T *>(p.v_pages) + (slot * p.Hkv + (h - p.Hq - p.Hkv)) * D;
-    }
-    *reinterpret_cast<uint4 *>(dst + e0) = is_q || is_k ? pack<T>(y) : raw[u];
+    for (int u = 0; u < kBatch; ++u) raw[u] = next[u];
   }
 }
 
+template <typename T, int D, bool HALVES>
+cudaError_t launch_h(const AppendPlan &p) {
+  constexpr int HPP = 32 / (D / kVec<T>);
+  const int passes = (p.Hq + 2 * p.Hkv + HPP - 1) / HPP;
+  // a whole token a warp, unless that leaves the SMs short of warps (16 each)
+  int groups = (int)((16ll * kPagedMaxCtas + p.T - 1) / p.T);
+  groups = groups < passes ? groups : passes;
+  const int share = (passes + groups - 1) / groups;
+  groups = (passes + share - 1) / share;
+  const int64_t grid = ((int64_t)p.T * groups + kWarps - 1) / kWarps;
+  if (grid >= (1ll << 31)) return cudaErrorInvalidValue;
+  append_kernel<T, D, HALVES><<<(unsigned)grid, kThreads, 0, p.stream>>>(p, share, groups);
+  return cudaGetLastError();
+}
 template <typename T, int D>
 cudaError_t launch_d(const AppendPlan &p) {
-  constexpr int HPP = 32 / (D / Vec<T>::N), U = 4;
-  const int heads = p.Hq + 2 * p.Hkv;
-  const int64_t units = (int64_t)p.T * ((heads + HPP * U - 1) / (HPP * U));
-  const int64_t grid = (units + kWarps - 1) / kWarps;
-  if (grid >= (1ll << 31)) return cudaErrorInvalidValue;
-  append_kernel<T, D, U><<<(unsigned)grid, kThreads, 0, p.stream>>>(p);
-  return cudaGetLastError();
+  return p.mode == 0 && p.rot > 0 ? launch_h<T, D, true>(p) : launch_h<T, D, false>(p);
 }
 
 }  // namespace
