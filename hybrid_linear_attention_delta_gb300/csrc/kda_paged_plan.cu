@@ -7,7 +7,7 @@
 //               = ring[(head + sum_{c<b} need_c + j - held_b) mod n]   else
 //
 // Latency-bound: a few bytes per request and eight per token.  Every CTA scans
-// all requests itself (three words each, from L2) and then fills its own slice
+// all requests itself (three words each, staged in shared memory) and then fills its own slice
 // of tokens and rows, so nothing waits for another CTA: pages are taken from
 // the front of the ring and given back behind its end, which never overlap,
 // and a new page is looked up in the ring, not in the row that another CTA
@@ -53,11 +53,11 @@ struct Ask {
   int cached, len, held, want;
   bool ok;
 };
-__device__ __forceinline__ Ask ask(const PagedPlanArgs &p, int b, int cu0, int cu1) {
+__device__ __forceinline__ Ask ask(const PagedPlanArgs &p, int cached, int held, int len) {
   Ask r;
-  r.cached = p.cached[b];
-  r.held = p.held[b];
-  r.len = cu1 - cu0;
+  r.cached = cached;
+  r.held = held;
+  r.len = len;
   const int64_t total = (int64_t)r.cached + r.len;
   r.ok = r.cached >= 0 && r.held >= 0 && r.held <= p.max_pages &&
          total <= (int64_t)p.max_pages * p.page_size;
@@ -68,7 +68,9 @@ __device__ __forceinline__ Ask ask(const PagedPlanArgs &p, int b, int cu0, int c
 __global__ void __launch_bounds__(kThreads) plan_kernel(PagedPlanArgs p) {
   extern __shared__ int smem[];
   int *s_cu = smem;                // [B + 1]
-  int *s_first = s_cu + p.B + 1;   // [B] pages taken by the requests before
+  int *s_cached = s_cu + p.B + 1;  // [B]
+  int *s_held = s_cached + p.B;    // [B]
+  int *s_first = s_held + p.B;     // [B] pages taken by the requests before
   int *s_back = s_first + p.B;     // [B] pages given back by the requests before
   __shared__ Sums warp_sums[kWarps];
   __shared__ int s_taken;
@@ -76,7 +78,13 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PagedPlanArgs p) {
   const int cta = blockIdx.x, n_ctas = gridDim.x;
 
   if (tid == 0) s_taken = 0;
-  for (int b = tid; b <= B; b += kThreads) s_cu[b] = p.cu[b];
+  // all that is read of a request, in one round of loads
+  for (int b = tid; b < B; b += kThreads) {
+    s_cu[b] = p.cu[b];
+    s_cached[b] = p.cached[b];
+    s_held[b] = p.held[b];
+  }
+  if (tid == 0) s_cu[B] = p.cu[B];
   const int ring_head = p.ring[0], ring_count = p.ring[1];
   __syncthreads();
   int bad = 0;
@@ -95,7 +103,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PagedPlanArgs p) {
   if (bad) {
     for (int t = t_lo + tid; t < t_hi; t += kThreads) p.positions[t] = 0, p.slots[t] = -1;
     if (cta == 0) {
-      for (int b = tid; b < B; b += kThreads) p.kv_lens[b] = 0, p.held_out[b] = p.held[b];
+      for (int b = tid; b < B; b += kThreads) p.kv_lens[b] = 0, p.held_out[b] = s_held[b];
       if (tid == 0) p.ring_out[0] = head, p.ring_out[1] = count;
     }
     return;
@@ -107,14 +115,14 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PagedPlanArgs p) {
   const int b0 = min(B, tid * run), b1 = min(B, b0 + run);
   Sums mine = {0, 0}, total;
   for (int b = b0; b < b1; ++b) {
-    const Ask r = ask(p, b, s_cu[b], s_cu[b + 1]);
+    const Ask r = ask(p, s_cached[b], s_held[b], s_cu[b + 1] - s_cu[b]);
     mine.need += max(0, r.want - r.held);
     mine.back += max(0, r.held - r.want);
   }
   Sums before = block_scan(mine, warp_sums, &total);
   int taken = 0;
   for (int b = b0; b < b1; ++b) {
-    const Ask r = ask(p, b, s_cu[b], s_cu[b + 1]);
+    const Ask r = ask(p, s_cached[b], s_held[b], s_cu[b + 1] - s_cu[b]);
     const int need = max(0, r.want - r.held), back = max(0, r.held - r.want);
     const bool fits = r.ok && (need == 0 || before.need + need <= count);
     // (need == 0: the first page is not used; behind the ring's room: dropped)
@@ -142,7 +150,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PagedPlanArgs p) {
 
   // rows: one warp per request, its new pages and the ones it gives back
   for (int b = cta * kWarps + (tid >> 5); b < B; b += n_ctas * kWarps) {
-    const Ask r = ask(p, b, s_cu[b], s_cu[b + 1]);
+    const Ask r = ask(p, s_cached[b], s_held[b], s_cu[b + 1] - s_cu[b]);
     if (s_first[b] < 0) continue;
     int32_t *row = p.table + (int64_t)b * p.max_pages;
     for (int j = r.held + (tid & 31); j < r.want; j += 32) {
@@ -173,8 +181,8 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PagedPlanArgs p) {
       }
       const int first = s_first[lo];
       if (first >= 0) {
-        const int held = p.held[lo];
-        pos = p.cached[lo] + t - s_cu[lo];
+        const int held = s_held[lo];
+        pos = s_cached[lo] + t - s_cu[lo];
         const int j = pos >> p.page_shift;
         int page;
         if (j < held) {
@@ -196,9 +204,9 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PagedPlanArgs p) {
 }  // namespace
 
 cudaError_t launch_paged_plan(const PagedPlanArgs &p) {
-  const int smem = (3 * p.B + 1) * (int)sizeof(int);
+  const int smem = (5 * p.B + 1) * (int)sizeof(int);
   const cudaError_t e = set_smem_limit_once(reinterpret_cast<const void *>(plan_kernel),
-                                            (3 * kMaxRequests + 1) * (int)sizeof(int));
+                                            (5 * kMaxRequests + 1) * (int)sizeof(int));
   if (e != cudaSuccess) return e;
   // a token a thread, up to a CTA per SM
   int grid = (p.T + kThreads - 1) / kThreads;
