@@ -56,6 +56,7 @@ struct PagedAttnPlan {
   float *part;         // [kPagedMaxCtas][2][part_rows][d] partial outputs
   float *part_ml;      // [kPagedMaxCtas][2][part_rows][2] their maxima and sums
   int32_t part_rows;
+  int32_t min_stretch;  // keys of a CTA's stretch at least
   cudaStream_t stream;
 };
 

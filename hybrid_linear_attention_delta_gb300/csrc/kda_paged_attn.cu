@@ -159,12 +159,12 @@ struct PieceReader {
 };
 
 // ------------------------------------------------------------------ pieces
-__device__ bool sched_role(Ctl &ctl, const AttnArgs &a, PagedSched &sched, const PagedItems &it) {
+__device__ bool sched_role(Ctl &ctl, const AttnArgs &a, PagedSched<kKeys> &sched) {
   const int tpt = kRows / a.p.G;  // tokens of a tile
   for (uint32_t n = 0;; ++n) {
     const uint32_t slot = n % kPieces;
     Work w;
-    w.o = sched.next(a.p, it);
+    w.o = sched.next(a.p);
     w.keys = max(0, a.p.causal ? min(w.o.kv, w.o.seen0 + w.o.n - 1) : w.o.kv);
     w.split = w.o.n <= tpt;
     const int tiles = w.o.tile1 - w.o.tile0;
@@ -412,57 +412,102 @@ __device__ __forceinline__ void store_row(__nv_bfloat16 *dst, const float (&x)[D
   }
 }
 
-// Joins the pieces of an item, first piece first: a warp per row, rows [r0, r1)
-// of the item strided over the calling warps.
+// Counts a piece in: what this CTA's threads wrote before the barrier behind
+// them is visible to whoever finds the count, and the other way round.
+__device__ __forceinline__ uint32_t arrive_acq_rel(uint32_t *count) {
+  uint32_t old;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(count) : "memory");
+  return old;
+}
+
+// A lane's N = D / 32 channels of a partial result.
+template <int N>
+__device__ __forceinline__ void load_part(const float *src, float (&x)[N]) {
+  if constexpr (N == 4) {
+    const float4 f = __ldcg(reinterpret_cast<const float4 *>(src));
+    x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
+  } else {
+    const float2 f = __ldcg(reinterpret_cast<const float2 *>(src));
+    x[0] = f.x, x[1] = f.y;
+  }
+}
+
+// Joins the pieces of an item, first piece first, rows [r0, r1) of the item
+// over the calling warps: a warp takes ROWS rows and PIECES pieces of them at a
+// time, all their loads in flight (four rows of an item cut in a few, as those
+// with many rows are; one row of an item that many SMs share).
+template <int D, int ROWS, int PIECES>
+__device__ void join_rows(const PagedAttnPlan &p, const PagedPiece &o, int r0, int r1, int warp,
+                          int n_warps) {
+  constexpr int N = D / 32;
+  static_assert(ROWS * PIECES <= 32, "a lane per (row, piece)");
+  const int lane = threadIdx.x & 31;
+  const int my_row = lane / PIECES, my_piece = lane % PIECES;  // whose weight this lane keeps
+  for (int r = r0 + warp * ROWS; r < r1; r += n_warps * ROWS) {
+    float m[ROWS], l[ROWS], acc[ROWS][N];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      m[i] = -INFINITY, l[i] = 0.f;
+#pragma unroll
+      for (int j = 0; j < N; ++j) acc[i][j] = 0.f;
+    }
+    for (int k0 = 0; k0 < o.n_pieces; k0 += PIECES) {
+      float x[ROWS][PIECES][N];
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+        for (int k = 0; k < PIECES; ++k) {
+          const int slot = paged_part_slot(o, min(k0 + k, o.n_pieces - 1));
+          load_part<N>(p.part + ((int64_t)slot * p.part_rows + min(r + i, r1 - 1)) * D + lane * N,
+                       x[i][k]);
+        }
+      // maximum and sum of this lane's (row, piece)
+      float mk = -INFINITY, lk = 0.f;
+      if (my_row < ROWS && k0 + my_piece < o.n_pieces) {
+        const int64_t at = (int64_t)paged_part_slot(o, k0 + my_piece) * p.part_rows +
+                           min(r + my_row, r1 - 1);
+        mk = __ldcg(&p.part_ml[at * 2]);
+        lk = __ldcg(&p.part_ml[at * 2 + 1]);
+      }
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i) {
+        float top = m[i];
+#pragma unroll
+        for (int k = 0; k < PIECES; ++k)
+          top = fmaxf(top, __shfl_sync(0xffffffffu, mk, i * PIECES + k));
+        const float ref = top == -INFINITY ? 0.f : top, keep = exp2f(m[i] - ref);
+        m[i] = top;
+        l[i] *= keep;
+#pragma unroll
+        for (int j = 0; j < N; ++j) acc[i][j] *= keep;
+        // (a piece in which the row saw no key left no output)
+        const float w = lk == 0.f ? 0.f : exp2f(mk - ref), wl = w * lk;
+#pragma unroll
+        for (int k = 0; k < PIECES; ++k) {
+          const float wk = __shfl_sync(0xffffffffu, w, i * PIECES + k);
+          l[i] += __shfl_sync(0xffffffffu, wl, i * PIECES + k);
+#pragma unroll
+          for (int j = 0; j < N; ++j) acc[i][j] = wk == 0.f ? acc[i][j] : fmaf(wk, x[i][k][j], acc[i][j]);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      if (r + i >= r1) break;
+      const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+#pragma unroll
+      for (int j = 0; j < N; ++j) acc[i][j] *= inv;
+      store_row<D>(static_cast<__nv_bfloat16 *>(p.out) +
+                       row_offset(p, o, (r + i) / p.G, (r + i) % p.G),
+                   acc[i]);
+    }
+  }
+}
 template <int D>
 __device__ void join_pieces(const PagedAttnPlan &p, const PagedPiece &o, int r0, int r1, int warp,
                             int n_warps) {
-  constexpr int N = D / 32;
-  const int lane = threadIdx.x & 31;
-  for (int r = r0 + warp; r < r1; r += n_warps) {
-    float m = -INFINITY;
-    for (int k = lane; k < o.n_pieces; k += 32)
-      m = fmaxf(m, __ldcg(&p.part_ml[((int64_t)paged_part_slot(o, k) * p.part_rows + r) * 2]));
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-    float l = 0.f, acc[N];
-#pragma unroll
-    for (int j = 0; j < N; ++j) acc[j] = 0.f;
-    for (int k0 = 0; k0 < o.n_pieces; k0 += 32) {
-      float w = 0.f, lk = 0.f;
-      if (k0 + lane < o.n_pieces) {
-        const int64_t at = (int64_t)paged_part_slot(o, k0 + lane) * p.part_rows + r;
-        lk = __ldcg(&p.part_ml[at * 2 + 1]);
-        // a piece in which the row saw no key left no output
-        w = lk == 0.f ? 0.f : exp2f(__ldcg(&p.part_ml[at * 2]) - m);
-      }
-      float wl = w * lk;
-#pragma unroll
-      for (int x = 16; x > 0; x >>= 1) wl += __shfl_xor_sync(0xffffffffu, wl, x);
-      l += wl;
-      const int kn = min(32, o.n_pieces - k0);
-#pragma unroll 4
-      for (int k = 0; k < kn; ++k) {
-        const float wk = __shfl_sync(0xffffffffu, w, k);
-        const float *src =
-            p.part + ((int64_t)paged_part_slot(o, k0 + k) * p.part_rows + r) * D + lane * N;
-        float x[N];
-        if constexpr (N == 4) {
-          const float4 f = __ldcg(reinterpret_cast<const float4 *>(src));
-          x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
-        } else {
-          const float2 f = __ldcg(reinterpret_cast<const float2 *>(src));
-          x[0] = f.x, x[1] = f.y;
-        }
-#pragma unroll
-        for (int j = 0; j < N; ++j) acc[j] = wk == 0.f ? acc[j] : fmaf(wk, x[j], acc[j]);
-      }
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-    for (int j = 0; j < N; ++j) acc[j] *= inv;
-    store_row<D>(static_cast<__nv_bfloat16 *>(p.out) + row_offset(p, o, r / p.G, r % p.G), acc);
-  }
+  if (o.n_pieces <= 4) join_rows<D, 4, 4>(p, o, r0, r1, warp, n_warps);
+  else join_rows<D, 1, 16>(p, o, r0, r1, warp, n_warps);
 }
 
 template <int D>
@@ -659,13 +704,11 @@ __device__ bool softmax_role(Ctl &ctl, const AttnArgs &a, uint32_t tmem, int s) 
         p.part_ml[part_at * 2] = mm;
         p.part_ml[part_at * 2 + 1] = l0;
       }
-      __threadfence();
       named_bar_sync(1 + s, 128);
       if (r == 0) {
         uint32_t *count = p.arrivals + w.o.first_cta * 2 + s;
-        const bool last = atomicAdd(count, 1u) == (uint32_t)w.o.n_pieces - 1;
+        const bool last = arrive_acq_rel(count) == (uint32_t)w.o.n_pieces - 1;
         if (last) *count = 0;  // as it was found
-        __threadfence();
         ctl.last[s] = last;
       }
       named_bar_sync(1 + s, 128);
@@ -690,9 +733,6 @@ attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
     if (tid == 0) raise_error(a.p.err, ERR_TIMEOUT);
     return;
   }
-  const PagedItems items = {2 * (kRows / a.p.G), kKeys};
-  PagedSched sched;
-  if (!sched.init<kThreads>(a.p, items, ctl.scratch)) return;
   if (tid == 0) {
     for (int i = 0; i < Ly::kStages; ++i) {
       mbar_init(smem_u32(&ctl.kv_full[i]), 1);
@@ -721,14 +761,16 @@ attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
   }
   if (warp == kMmaWarp) tmem_alloc(smem_u32(&ctl.tmem), 512);
   tc_fence_before();
-  __syncthreads();
+  PagedSched<kKeys> sched;  // (its barriers are the set-up's too)
+  const bool work = sched.template init<kThreads>(a.p, 2 * (kRows / a.p.G), ctl.scratch);
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&ctl.tmem);
 
   // a softmax thread holds a row of 128 scores: registers go from the last
   // warpgroup to the other two (168 a thread at the launch, 2 * 216 + 72 = 3 * 168)
   bool ok = true;
-  if (warp < kSoftmaxWarps) {
+  if (!work) {  // bad cu_seqlens
+  } else if (warp < kSoftmaxWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     ok = softmax_role<D>(ctl, a, tmem, warp >> 2);
   } else {
@@ -738,7 +780,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
     } else if (warp == kLoadWarp) {
       ok = load_role<D>(sbase, ctl, a, &tq, &tk, &tv);
     } else if (tid == kSchedWarp * 32) {
-      ok = sched_role(ctl, a, sched, items);
+      ok = sched_role(ctl, a, sched);
     }
   }
   if (!ok) raise_error(a.p.err, ERR_TIMEOUT);

@@ -44,14 +44,13 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(PagedAttnPlan p) {
   S &sm = *reinterpret_cast<S *>(raw);
   constexpr int NC = D / 16;  // output channels of a thread, in groups of four
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-  const PagedItems items = {S::kRows / p.G, kKeys};
-  PagedSched sched;
-  if (!sched.init<kThreads>(p, items, sm.scratch)) return;
+  PagedSched<kKeys> sched;
+  if (!sched.init<kThreads>(p, S::kRows / p.G, sm.scratch)) return;
   const float c = p.scale * 1.4426950408889634f;  // scores in powers of two
 
   for (;;) {
     __syncthreads();
-    if (tid == 0) sm.piece = sched.next(p, items);
+    if (tid == 0) sm.piece = sched.next(p);
     __syncthreads();
     const PagedPiece o = sm.piece;
     if (o.n == 0) break;

@@ -18,11 +18,6 @@
 
 namespace kda {
 
-struct PagedItems {
-  int32_t tokens;  // query tokens of an item at most
-  int32_t tile;    // keys of a tile
-};
-
 // Fixed cost of an item, in keys.
 constexpr int kItemCost = 128;
 
@@ -68,7 +63,15 @@ __device__ __forceinline__ PagedReq paged_request(const PagedAttnPlan &p, int b)
   return r;
 }
 
+// Quotient of two non-negative numbers; 64-bit division takes many times as long.
+__device__ __forceinline__ int64_t paged_div(int64_t a, int64_t b) {
+  return ((a | b) >> 31) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// TILE: keys of a tile; tokens: query tokens of an item at most.
+template <int TILE>
 struct PagedSched {
+  int32_t tokens;
   int64_t pos, end, base;  // place on the line, end of the stretch, start of request b
   int64_t per_cta;
   int32_t b;
@@ -77,9 +80,10 @@ struct PagedSched {
   // All threads of the CTA; scratch: THREADS / 32 + 4 words of 64 bits.  False:
   // bad cu_seqlens (nothing is to be done).
   template <int THREADS>
-  __device__ bool init(const PagedAttnPlan &p, const PagedItems &it, int64_t *scratch) {
+  __device__ bool init(const PagedAttnPlan &p, int tokens_per_item, int64_t *scratch) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int W = THREADS / 32;
+    tokens = tokens_per_item;
     const int run = (p.B + THREADS - 1) / THREADS;
     const int b0 = min(p.B, tid * run), b1 = min(p.B, b0 + run);
     int64_t mine = 0;
@@ -90,7 +94,7 @@ struct PagedSched {
       const int kvl = p.kv_lens[i];
       if (blockIdx.x == 0 && (kvl < 0 || (int64_t)kvl > (int64_t)p.max_pages * p.page_size))
         raise_error(p.err, ERR_BAD_LEN);
-      mine += paged_head_cost(q, it.tokens, p.causal) * p.Hkv;
+      mine += paged_head_cost(q, tokens, p.causal) * p.Hkv;
     }
     int64_t inc = mine;
 #pragma unroll
@@ -110,15 +114,15 @@ struct PagedSched {
       if (w < warp) before += scratch[w];
       total += scratch[w];
     }
-    // no stretch shorter than two tiles and an item's fixed cost: a cut costs a
-    // round trip of partials, and a stretch inside an item always has a tile
-    per_cta = max((int64_t)2 * it.tile + kItemCost, (total + gridDim.x - 1) / gridDim.x);
+    // a cut costs a round trip of partials (see min_stretch); two tiles and an
+    // item's fixed cost at least, so that a stretch inside an item has a tile
+    per_cta = max((int64_t)max(p.min_stretch, 2 * TILE + kItemCost), paged_div(total + gridDim.x - 1, gridDim.x));
     pos = blockIdx.x * per_cta;
     end = min(total, pos + per_cta);
     if (pos < end && before <= pos && pos < before + mine) {  // this thread's requests hold it
       int64_t at = before;
       for (int i = b0; i < b1; ++i) {
-        const int64_t c = paged_head_cost(paged_request(p, i), it.tokens, p.causal) * p.Hkv;
+        const int64_t c = paged_head_cost(paged_request(p, i), tokens, p.causal) * p.Hkv;
         if (pos < at + c) {
           scratch[W] = i;
           scratch[W + 1] = at;
@@ -138,21 +142,20 @@ struct PagedSched {
   // The tile that a cut at cost x of the item falls on.  Items of a request
   // that brings more tokens than it has keys (their cost does not follow the
   // keys they see) are left whole.
-  static __device__ __forceinline__ int cut(int64_t x, int64_t cost, int tiles, int tile,
-                                            bool whole) {
+  static __device__ __forceinline__ int cut(int64_t x, int64_t cost, int tiles, bool whole) {
     if (x <= 0) return 0;
     if (x >= cost) return tiles;
     if (whole) return 0;
-    const int64_t k = x - kItemCost + tile / 2;
-    return k <= 0 ? 0 : (int)min((int64_t)tiles, k / tile);
+    const int64_t k = x - kItemCost + TILE / 2;
+    return k <= 0 ? 0 : (int)min((int64_t)tiles, k / TILE);
   }
 
   // The next piece of the stretch (n = 0 when there is none).
-  __device__ PagedPiece next(const PagedAttnPlan &p, const PagedItems &it) {
+  __device__ PagedPiece next(const PagedAttnPlan &p) {
     PagedPiece o;
     o.n = 0;
     while (pos < end) {
-      const int64_t head_cost = paged_head_cost(r, it.tokens, p.causal);
+      const int64_t head_cost = paged_head_cost(r, tokens, p.causal);
       if (pos >= base + head_cost * p.Hkv) {  // on to the next request with work
         base += head_cost * p.Hkv;
         if (++b >= p.B) {
@@ -162,42 +165,44 @@ struct PagedSched {
         r = paged_request(p, b);
         continue;
       }
-      const int head = (int)((pos - base) / head_cost);
+      const int head = (int)paged_div(pos - base, head_cost);
       const int64_t head_base = base + head * head_cost;
-      const int runs = (r.n + it.tokens - 1) / it.tokens;
+      const int runs = (r.n + tokens - 1) / tokens;
       int lo = 0, hi = runs - 1;  // largest run that starts at or before pos
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (head_base + paged_prefix(r, mid, it.tokens, p.causal) <= pos) lo = mid; else hi = mid - 1;
+        if (head_base + paged_prefix(r, mid, tokens, p.causal) <= pos) lo = mid; else hi = mid - 1;
       }
-      const int64_t start = head_base + paged_prefix(r, lo, it.tokens, p.causal);
-      const int64_t cost = head_base + paged_prefix(r, lo + 1, it.tokens, p.causal) - start;
+      const int64_t start = head_base + paged_prefix(r, lo, tokens, p.causal);
+      const int64_t cost = head_base + paged_prefix(r, lo + 1, tokens, p.causal) - start;
       const int64_t stop = min(end, start + cost);
-      o.n = min(it.tokens, r.n - lo * it.tokens);
-      o.tok0 = r.tok0 + lo * it.tokens;
+      o.n = min(tokens, r.n - lo * tokens);
+      o.tok0 = r.tok0 + lo * tokens;
       o.head = head;
       o.req = b;
       o.kv = r.kv;
-      o.seen0 = p.causal ? r.kv - r.n + lo * it.tokens + 1 : r.kv;
+      o.seen0 = p.causal ? r.kv - r.n + lo * tokens + 1 : r.kv;
       const int keys = max(0, p.causal ? min(r.kv, o.seen0 + o.n - 1) : r.kv);
-      const int tiles = (keys + it.tile - 1) / it.tile;
+      const int tiles = (keys + TILE - 1) / TILE;
       const bool whole = p.causal && r.kv < r.n;
       const bool starts = pos == start;
-      o.tile0 = cut(pos - start, cost, tiles, it.tile, whole);
-      o.tile1 = cut(stop - start, cost, tiles, it.tile, whole);
+      o.tile0 = cut(pos - start, cost, tiles, whole);
+      o.tile1 = cut(stop - start, cost, tiles, whole);
       o.n_pieces = o.index = o.first_cta = o.first_slot = 0;
       pos = stop;
-      const int64_t c0 = start / per_cta, c1 = (start + cost - 1) / per_cta;
+      const int64_t cta = blockIdx.x;
+      const int64_t c0 = start >= cta * per_cta ? cta : paged_div(start, per_cta);
+      const int64_t c1 = start + cost <= end ? cta : paged_div(start + cost - 1, per_cta);
       if (c0 != c1) {
         // an item without keys belongs to the CTA it starts in
         if (tiles == 0 ? !starts : o.tile0 == o.tile1) continue;
         // only the first and the last stretch can be left without a tile
-        const bool skip0 = cut((c0 + 1) * per_cta - start, cost, tiles, it.tile, whole) == 0;
-        const bool skip1 = cut(c1 * per_cta - start, cost, tiles, it.tile, whole) == tiles;
+        const bool skip0 = cut((c0 + 1) * per_cta - start, cost, tiles, whole) == 0;
+        const bool skip1 = cut(c1 * per_cta - start, cost, tiles, whole) == tiles;
         const int n = (int)(c1 - c0) + 1 - skip0 - skip1;
         if (tiles > 0 && !whole && n > 1) {
           o.n_pieces = n;
-          o.index = (int)blockIdx.x - (int)c0 - skip0;
+          o.index = (int)(cta - c0) - skip0;
           o.first_cta = (int32_t)c0 + skip0;
           o.first_slot = 2 * o.first_cta + !skip0;
         }
