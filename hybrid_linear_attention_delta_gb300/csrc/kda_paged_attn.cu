@@ -220,7 +220,14 @@ __device__ bool load_role(uint32_t sbase, Ctl &ctl, const AttnArgs &a, const CUt
                       w.o.tok0 + s * tpt, bar);
     }
     ++nq;
+    // The request's row of the block table, 32 pages at a time: lane l keeps page
+    // base + l, and the 32 behind them are on their way.  (A tile has 8, 4, 2 or
+    // 1 pages, or half of one, so its pages are never in two such runs.)
     const int32_t *row = p.table + (int64_t)w.o.req * p.max_pages;
+    const int held = (w.o.kv + p.page_size - 1) >> p.page_shift;
+    auto pages_at = [&](int first) { return first + lane < held ? row[first + lane] : 0; };
+    int base = (w.o.tile0 * kKeys) >> p.page_shift;
+    int here = pages_at(base), ahead = pages_at(base + 32);
     // boxes of tile i (pages that hold a key of the item's request), and this
     // lane's page of it
     auto boxes = [&](int i) {
@@ -228,10 +235,15 @@ __device__ bool load_role(uint32_t sbase, Ctl &ctl, const AttnArgs &a, const CUt
       return (left + rows - 1) / rows;
     };
     auto page_of = [&](int i) {
-      if (box >= boxes(i)) return 0;
+      const int first = ((w.o.tile0 + i) * kKeys) >> p.page_shift;
+      if (first >= base + 32) {
+        base += 32;
+        here = ahead;
+        ahead = pages_at(base + 32);
+      }
       const int key = (w.o.tile0 + i) * kKeys + box * rows;
-      const int page = row[key >> p.page_shift];
-      if (page < 0 || page >= p.n_pages) {
+      const int page = __shfl_sync(0xffffffffu, here, ((key >> p.page_shift) - base) & 31);
+      if (box < boxes(i) && (page < 0 || page >= p.n_pages)) {
         raise_error(p.err, ERR_BAD_PAGE);
         return -1;
       }
