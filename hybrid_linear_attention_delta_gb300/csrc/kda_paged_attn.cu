@@ -51,6 +51,12 @@ struct Layout {
   static constexpr uint32_t kQ = 0;
   static constexpr uint32_t kStage = 2 * kTile;
   static constexpr uint32_t kCtl = kStage + kStages * kTile;
+  // Tensor memory columns.  With 64 channels there is room for P beside S, and
+  // the next scores are made while the softmax works on these; with 128, P lies
+  // over S.
+  static constexpr bool kApart = D == 64;
+  static constexpr uint32_t kO = 256, kP = kApart ? 384 : 0;
+  static constexpr uint32_t kStepP = kApart ? 64 : 128;  // between the streams' P
 };
 
 // A piece as the warps see it.
@@ -64,7 +70,7 @@ struct Work {
 struct Ctl {
   uint64_t kv_full[8], kv_empty[8];
   uint64_t q_full, q_empty;
-  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
+  uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2], o_full[2], o_empty[2];
   uint64_t ml_full;
   uint64_t piece_full[kPieces], piece_empty[kPieces];
   uint64_t drain[2];
@@ -297,10 +303,11 @@ __device__ bool mma_role(uint32_t sbase, Ctl &ctl, const AttnArgs &a, uint32_t t
   const int lane = threadIdx.x & 31;
   const uint32_t idesc_s = idesc_bf16(kRows, kKeys, 0, 0) | (a.neg_q << 13);
   const uint32_t idesc_o = idesc_bf16(kRows, D, 0, 1);
-  const uint32_t ds = uniform(tmem + s * 128), d_o = uniform(tmem + 256 + s * D);
+  const uint32_t ds = uniform(tmem + s * 128), d_o = uniform(tmem + Ly::kO + s * D);
+  const uint32_t dp = uniform(tmem + Ly::kP + s * Ly::kStepP);
   PieceReader pieces;
   uint32_t e = 0, nq = 0;      // ring entries and Q tiles of the pieces before
-  uint32_t n_p = 0, n_o = 0;   // tiles and outputs of the stream so far
+  uint32_t n_s = 0, n_p = 0, n_o = 0;  // scores, weights and outputs of the stream so far
   bool ok = true, any = false;
   int n = 0, tail = 0;         // the piece's key tiles; keys of the last one
   int i_last = 0;              // the stream's last tile
@@ -322,7 +329,42 @@ __device__ bool mma_role(uint32_t sbase, Ctl &ctl, const AttnArgs &a, uint32_t t
   };
   auto take = [&](uint32_t at) { return pass_to(at) && landed(x++); };
 
-  // One turn: O += P V of tile i (the stream's j-th), then S of tile i_next.
+  // O += P V from stage st_v (more: not the stream's first tile of the item, end:
+  // the last) and S from stage st_k (last: the last that reads Q); whole warp.
+  // One elected block for both: a second one costs the chunk workload 7%.
+  auto issue = [&](bool do_o, uint32_t st_v, uint64_t v, uint32_t more, bool end, bool do_s,
+                   uint32_t st_k, uint64_t k, bool last) {
+    if (elect_one()) {
+      tc_fence_after();
+      if (do_o) {
+#pragma unroll
+        for (int kk = 0; kk < kKeys / 16; ++kk)
+          mma_bf16_ts(d_o, dp + kk * 8, v + kk * (2048 >> 4), idesc_o, kk > 0 ? 1 : more);
+        mma_commit(smem_u32(&ctl.kv_empty[st_v]));
+        if constexpr (Ly::kApart) mma_commit(smem_u32(&ctl.p_empty[s]));
+        if (end) mma_commit(smem_u32(&ctl.o_full[s]));
+      }
+      if (do_s) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t step = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+          mma_bf16(ds, q + step, k + step, idesc_s, kk > 0);
+        }
+        mma_commit(smem_u32(&ctl.s_full[s]));
+        mma_commit(smem_u32(&ctl.kv_empty[st_k]));
+        if (last) mma_commit(smem_u32(&ctl.q_empty));
+      }
+    }
+    __syncwarp();
+    any = true;
+    if (do_o) {
+      ++n_p;
+      if (end) ++n_o;
+    }
+    if (do_s) ++n_s;
+  };
+
+  // One turn: O += P V of tile i (the stream's j-th) and S of tile i_next.
   // i < 0: scores only, i_next < 0: no more scores.
   auto turn = [&](int i, int j, int i_next) {
     const uint32_t at_v = e + entry_v(max(i, 0), n), at_k = e + entry_k(max(i_next, 0));
@@ -330,7 +372,14 @@ __device__ bool mma_role(uint32_t sbase, Ctl &ctl, const AttnArgs &a, uint32_t t
     const uint64_t v = sw128_desc(uniform(sbase + Ly::kStage + st_v * Ly::kTile), kHalf, 1024);
     const uint64_t k = sw128_desc(uniform(sbase + Ly::kStage + st_k * Ly::kTile), 16, 1024);
     const uint32_t more = uniform(j > 0);
-    if (i_next >= 0 && (i < 0 || at_k < at_v) && !take(at_k)) return false;
+    const bool k_first = i_next >= 0 && (i < 0 || at_k < at_v);
+    if (k_first) {
+      if (!take(at_k)) return false;
+      if constexpr (Ly::kApart) {
+        if (n_s > 0 && !warp_wait(&ctl.s_empty[s], (n_s - 1) & 1)) return false;
+        issue(false, 0, v, 0, false, true, st_k, k, i_next == i_last);
+      }
+    }
     if (i >= 0) {
       if (!take(at_v)) return false;
       if (i == n - 1 && tail < kKeys) {
@@ -343,35 +392,20 @@ __device__ bool mma_role(uint32_t sbase, Ctl &ctl, const AttnArgs &a, uint32_t t
         fence_async_smem();
         __syncwarp();
       }
-      if (i_next >= 0 && at_k > at_v && !take(at_k)) return false;
+      if (i_next >= 0 && !k_first) {
+        if (!take(at_k)) return false;
+        if constexpr (Ly::kApart) {
+          if (!warp_wait(&ctl.s_empty[s], (n_s - 1) & 1)) return false;
+          issue(false, 0, v, 0, false, true, st_k, k, i_next == i_last);
+        }
+      }
       if (j == 0 && n_o > 0 && !warp_wait(&ctl.o_empty[s], (n_o - 1) & 1)) return false;
       if (!warp_wait(&ctl.p_full[s], n_p & 1)) return false;
     }
-    if (elect_one()) {
-      tc_fence_after();
-      if (i >= 0) {
-#pragma unroll
-        for (int kk = 0; kk < kKeys / 16; ++kk)
-          mma_bf16_ts(d_o, ds + kk * 8, v + kk * (2048 >> 4), idesc_o, kk > 0 ? 1 : more);
-        mma_commit(smem_u32(&ctl.kv_empty[st_v]));
-        if (i_next < 0) mma_commit(smem_u32(&ctl.o_full[s]));
-      }
-      if (i_next >= 0) {
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t step = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
-          mma_bf16(ds, q + step, k + step, idesc_s, kk > 0);
-        }
-        mma_commit(smem_u32(&ctl.s_full[s]));
-        mma_commit(smem_u32(&ctl.kv_empty[st_k]));
-        if (i_next == i_last) mma_commit(smem_u32(&ctl.q_empty));
-      }
-    }
-    __syncwarp();
-    any = true;
-    if (i >= 0) {
-      ++n_p;
-      if (i_next < 0) ++n_o;
+    if constexpr (Ly::kApart) {
+      if (i >= 0) issue(true, st_v, v, more, i_next < 0, false, 0, k, false);
+    } else {
+      issue(i >= 0, st_v, v, more, i_next < 0, i_next >= 0, st_k, k, i_next == i_last);
     }
     return true;
   };
@@ -530,7 +564,9 @@ __device__ bool softmax_role(Ctl &ctl, const AttnArgs &a, uint32_t tmem, int s) 
   const int t = r / p.G, g = r - t * p.G;  // its token and head
   const int tpt = kRows / p.G;
   const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-  const uint32_t ts = tmem + lanes + s * 128, to = tmem + lanes + 256 + s * D;
+  using Ly = Layout<D>;
+  const uint32_t ts = tmem + lanes + s * 128, to = tmem + lanes + Ly::kO + s * D;
+  const uint32_t tp = tmem + lanes + Ly::kP + s * Ly::kStepP;
   const float c = a.c;
   PieceReader pieces;
   uint32_t n_s = 0, n_o[2] = {0, 0}, n_ml = 0;
@@ -559,6 +595,17 @@ __device__ bool softmax_role(Ctl &ctl, const AttnArgs &a, uint32_t tmem, int s) 
         tmem_wait_ld();
 #pragma unroll
         for (int q = 0; q < 4; ++q) reg_fence(x[q]);
+        if constexpr (Ly::kApart) {
+          tc_fence_before();
+          warp_arrive(&ctl.s_empty[s]);
+        }
+        // P and O are this tile's when the products of the tile before have ended
+        // (with P over S they have, or its scores would not be there)
+        bool mine = !Ly::kApart || n_s == 1;
+        auto own = [&] {
+          if (!mine) mine = warp_wait(&ctl.p_empty[s], n_s & 1);
+          return mine;
+        };
         if (__any_sync(0xffffffffu, live && left < kKeys)) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
@@ -592,7 +639,8 @@ __device__ bool softmax_role(Ctl &ctl, const AttnArgs &a, uint32_t tmem, int s) 
               const float keep = move ? ex2_approx(ref - tm) : 1.f;
               if (move) ref = tm;
               l *= keep;
-              // (the products before this tile's scores have ended)
+              if (!own()) return false;
+              tc_fence_after();
 #pragma unroll
               for (int q = 0; q < D / 16; ++q) {
                 uint32_t o[16];
@@ -620,7 +668,8 @@ __device__ bool softmax_role(Ctl &ctl, const AttnArgs &a, uint32_t tmem, int s) 
               sum[i & 1] = add2(sum[i & 1], pair(u, v));
               pk[i] = pack_bf16x2(u, v);
             }
-            tmem_st16(ts + q * 16, pk);
+            if (Ly::kApart && q == 0 && !own()) return false;
+            tmem_st16(tp + q * 16, pk);
           }
           float su, sv;
           unpair(add2(sum[0], sum[1]), su, sv);
@@ -630,6 +679,9 @@ __device__ bool softmax_role(Ctl &ctl, const AttnArgs &a, uint32_t tmem, int s) 
         l += sum_j;
         tmem_wait_st();
         tc_fence_before();
+      } else if constexpr (Ly::kApart) {
+        warp_arrive(&ctl.s_empty[s]);
+        if (n_s > 1 && !warp_wait(&ctl.p_empty[s], n_s & 1)) return false;
       }
       warp_arrive(&ctl.p_full[s]);
     }
@@ -754,7 +806,9 @@ attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
     mbar_init(smem_u32(&ctl.q_empty), 2);
     for (int s = 0; s < 2; ++s) {
       mbar_init(smem_u32(&ctl.s_full[s]), 1);
+      mbar_init(smem_u32(&ctl.s_empty[s]), kStreamWarps);
       mbar_init(smem_u32(&ctl.p_full[s]), kStreamWarps);
+      mbar_init(smem_u32(&ctl.p_empty[s]), 1);
       mbar_init(smem_u32(&ctl.o_full[s]), 1);
       mbar_init(smem_u32(&ctl.o_empty[s]), kStreamWarps);
     }
