@@ -71,7 +71,7 @@ struct Ctl {
   uint64_t kv_full[8], kv_empty[8];
   uint64_t q_full, q_empty;
   uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2], o_full[2], o_empty[2];
-  uint64_t ml_full;
+  uint64_t ml_full, go[2];
   uint64_t piece_full[kPieces], piece_empty[kPieces];
   uint64_t drain[2];
   Work work[kPieces];
@@ -255,20 +255,20 @@ __device__ bool load_role(uint32_t sbase, Ctl &ctl, const AttnArgs &a, const CUt
       }
       return page;
     };
+    // Tile i of the keys or values into the next stage, a box a lane.  What a
+    // request needs is ready before its stage is free: the ring has little slack.
     auto fetch = [&](const CUtensorMap *map, int i, int page) {
       const uint32_t st = e % Ly::kStages, use = e / Ly::kStages;
-      if (use > 0 && !warp_wait(&ctl.kv_empty[st], (use - 1) & 1)) return false;
       const uint32_t bar = smem_u32(&ctl.kv_full[st]);
-      const int nb = boxes(i);
+      const uint32_t dst = sbase + Ly::kStage + st * Ly::kTile + half * kHalf + box * rows * 128;
+      const int nb = boxes(i), key = (w.o.tile0 + i) * kKeys + box * rows;
+      // a page that is none reads as zeros: a head behind the last one
+      const int y = page < 0 ? p.Hkv : w.o.head;
+      const int z = page < 0 ? 0 : (page << p.page_shift) + (key & (p.page_size - 1));
+      if (use > 0 && !warp_wait(&ctl.kv_empty[st], (use - 1) & 1)) return false;
       if (lane == 0) mbar_expect_tx(bar, (uint32_t)(nb * rows * 128 * Ly::kHalves));
       __syncwarp();
-      if (box < nb) {
-        const int key = (w.o.tile0 + i) * kKeys + box * rows;
-        // a page that is none reads as zeros: a head behind the last one
-        const int z = page < 0 ? 0 : (page << p.page_shift) + (key & (p.page_size - 1));
-        tma_load_3d(sbase + Ly::kStage + st * Ly::kTile + half * kHalf + box * rows * 128, map,
-                    half * 64, page < 0 ? p.Hkv : w.o.head, z, bar);
-      }
+      if (box < nb) tma_load_3d(dst, map, half * 64, y, z, bar);
       ++e;
       return true;
     };
@@ -308,6 +308,7 @@ __device__ bool mma_role(uint32_t sbase, Ctl &ctl, const AttnArgs &a, uint32_t t
   PieceReader pieces;
   uint32_t e = 0, nq = 0;      // ring entries and Q tiles of the pieces before
   uint32_t n_s = 0, n_p = 0, n_o = 0;  // scores, weights and outputs of the stream so far
+  uint32_t n_go = 0;                   // rounds so far
   bool ok = true, any = false;
   int n = 0, tail = 0;         // the piece's key tiles; keys of the last one
   int i_last = 0;              // the stream's last tile
@@ -364,6 +365,19 @@ __device__ bool mma_role(uint32_t sbase, Ctl &ctl, const AttnArgs &a, uint32_t t
     if (do_s) ++n_s;
   };
 
+  // With P over S the streams issue in rounds, stream 0 first: left to themselves
+  // the two warps' products mix, end at the same time, and from then on both
+  // softmaxes run at once and the tensor cores wait for them (8k-token chunk: 2.2
+  // ms or 2.6 to 2.8 ms, as the start happened to fall out).
+  auto my_round = [&] {
+    if (Ly::kApart || (s == 0 && n_go == 0)) return true;
+    return warp_wait(&ctl.go[s], (s ? n_go : n_go - 1) & 1);
+  };
+  auto end_round = [&] {
+    if (!Ly::kApart) warp_arrive(&ctl.go[s ^ 1]);
+    ++n_go;
+  };
+
   // One turn: O += P V of tile i (the stream's j-th) and S of tile i_next.
   // i < 0: scores only, i_next < 0: no more scores.
   auto turn = [&](int i, int j, int i_next) {
@@ -405,7 +419,9 @@ __device__ bool mma_role(uint32_t sbase, Ctl &ctl, const AttnArgs &a, uint32_t t
     if constexpr (Ly::kApart) {
       if (i >= 0) issue(true, st_v, v, more, i_next < 0, false, 0, k, false);
     } else {
+      if (!my_round()) return false;
       issue(i >= 0, st_v, v, more, i_next < 0, i_next >= 0, st_k, k, i_next == i_last);
+      end_round();
     }
     return true;
   };
@@ -429,6 +445,11 @@ __device__ bool mma_role(uint32_t sbase, Ctl &ctl, const AttnArgs &a, uint32_t t
     } else {
       warp_arrive(&ctl.q_empty);
     }
+    // rounds in which only the other stream has something to issue
+    for (int j = cnt > 0 ? cnt + 1 : 0; !Ly::kApart && ok && j <= max(w->cnt0, w->cnt1); ++j) {
+      ok = my_round();
+      if (ok) end_round();
+    }
     if (!(ok = ok && pass_to(e + 2 * n))) break;
     e += 2 * n;
   }
@@ -444,6 +465,29 @@ __device__ bool mma_role(uint32_t sbase, Ctl &ctl, const AttnArgs &a, uint32_t t
 __device__ __forceinline__ int64_t row_offset(const PagedAttnPlan &p, const PagedPiece &o, int t,
                                               int g) {
   return ((int64_t)(o.tok0 + t) * p.Hq + o.head * p.G + g) * p.d;
+}
+
+// Transposes 4 x 4 vectors of 16 bytes among the four lanes of a group: lane j
+// of it gives vector k of its own row and gets vector j of row k.  A row's vectors
+// then leave as 64 bytes side by side; stored from the lane that made them, every
+// 16 bytes are a row apart from the next lane's, and the stores of an item of 256
+// rows take 6500 cycles.
+__device__ __forceinline__ void transpose4(uint32_t (&v)[16]) {
+  const int j = threadIdx.x & 3;
+#pragma unroll
+  for (int bit = 1; bit < 4; bit <<= 1) {
+    const bool hi = j & bit;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k & bit) continue;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {  // vector k of the hi lane against k + bit of the lo lane
+        uint32_t &a = v[k * 4 + x], &b = v[(k | bit) * 4 + x];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, hi ? a : b, bit);
+        if (hi) a = got; else b = got;
+      }
+    }
+  }
 }
 
 // One warp writes row x of a result, lane l the channels VEC * l ...
@@ -480,7 +524,7 @@ __device__ __forceinline__ void load_part(const float *src, float (&x)[N]) {
 
 // Joins the pieces of an item, first piece first, rows [r0, r1) of the item
 // over the calling warps: a warp takes ROWS rows and PIECES pieces of them at a
-// time, all their loads in flight (four rows of an item cut in a few, as those
+// time, all their loads in flight (eight rows of an item cut in a few, as those
 // with many rows are; one row of an item that many SMs share).
 template <int D, int ROWS, int PIECES>
 __device__ void join_rows(const PagedAttnPlan &p, const PagedPiece &o, int r0, int r1, int warp,
@@ -552,7 +596,7 @@ __device__ void join_rows(const PagedAttnPlan &p, const PagedPiece &o, int r0, i
 template <int D>
 __device__ void join_pieces(const PagedAttnPlan &p, const PagedPiece &o, int r0, int r1, int warp,
                             int n_warps) {
-  if (o.n_pieces <= 4) join_rows<D, 4, 4>(p, o, r0, r1, warp, n_warps);
+  if (o.n_pieces <= 4 && r1 - r0 > 16) join_rows<D, 8, 2>(p, o, r0, r1, warp, n_warps);
   else join_rows<D, 1, 16>(p, o, r0, r1, warp, n_warps);
 }
 
@@ -724,7 +768,13 @@ __device__ bool softmax_role(Ctl &ctl, const AttnArgs &a, uint32_t tmem, int s) 
         parts ? (int64_t)paged_part_slot(w.o, w.o.index) * p.part_rows + item_row : 0;
     if (warp_live) {
       const float f0 = l == 0.f ? 0.f : f * w0, f1 = f * w1;
+      // where the rows of this lane's group go (-1: nowhere)
+      const int64_t mine = parts ? part_at * D : row_offset(p, w.o, row_tok, g);
+      int64_t to_row[4];
 #pragma unroll
+      for (int k = 0; k < 4; ++k)
+        to_row[k] = __shfl_sync(0xffffffffu, live ? mine : (int64_t)-1, (lane & ~3) + k);
+#pragma unroll 1
       for (int q = 0; q < D / 32; ++q) {
         float y[32];
         uint32_t o[32];
@@ -732,30 +782,42 @@ __device__ bool softmax_role(Ctl &ctl, const AttnArgs &a, uint32_t tmem, int s) 
           tmem_ld32_async(to + q * 32, o);
           tmem_wait_ld();
           reg_fence(o);
-        }
-        // (an output that no key went into is not read: it may hold anything)
 #pragma unroll
-        for (int i = 0; i < 32; ++i) y[i] = f0 == 0.f ? 0.f : __uint_as_float(o[i]) * f0;
+          for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(o[i]) * f0;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) y[i] = 0.f;
+        }
         if (join) {
           tmem_ld32_async(to + D + q * 32, o);
           tmem_wait_ld();
           reg_fence(o);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) y[i] = f1 == 0.f ? y[i] : fmaf(__uint_as_float(o[i]), f1, y[i]);
+          for (int i = 0; i < 32; ++i) y[i] = fmaf(__uint_as_float(o[i]), f1, y[i]);
         }
-        if (live && parts) {
-          float *dst = p.part + part_at * D + q * 32;
+        uint32_t v[16];
+        if (parts) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<float4 *>(dst + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
-        } else if (live) {
-          __nv_bfloat16 *dst =
-              static_cast<__nv_bfloat16 *>(p.out) + row_offset(p, w.o, row_tok, g) + q * 32;
+          for (int h = 0; h < 2; ++h) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 8)
-            *reinterpret_cast<uint4 *>(dst + i) =
-                make_uint4(pack_bf16x2(y[i], y[i + 1]), pack_bf16x2(y[i + 2], y[i + 3]),
-                           pack_bf16x2(y[i + 4], y[i + 5]), pack_bf16x2(y[i + 6], y[i + 7]));
+            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(y[h * 16 + i]);
+            transpose4(v);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (to_row[k] >= 0)
+                *reinterpret_cast<uint4 *>(p.part + to_row[k] + q * 32 + h * 16 + (lane & 3) * 4) =
+                    make_uint4(v[k * 4], v[k * 4 + 1], v[k * 4 + 2], v[k * 4 + 3]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = pack_bf16x2(y[2 * i], y[2 * i + 1]);
+          transpose4(v);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (to_row[k] >= 0)
+              *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + to_row[k] + q * 32 +
+                                         (lane & 3) * 8) =
+                  make_uint4(v[k * 4], v[k * 4 + 1], v[k * 4 + 2], v[k * 4 + 3]);
         }
       }
     }
@@ -813,6 +875,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
       mbar_init(smem_u32(&ctl.o_empty[s]), kStreamWarps);
     }
     mbar_init(smem_u32(&ctl.ml_full), kStreamWarps);
+    for (int s = 0; s < 2; ++s) mbar_init(smem_u32(&ctl.go[s]), 1);
     for (int i = 0; i < kPieces; ++i) {
       mbar_init(smem_u32(&ctl.piece_full[i]), 1);
       mbar_init(smem_u32(&ctl.piece_empty[i]), kPieceReaders);
