@@ -41,8 +41,10 @@ struct AppendPlan {
 
 // Attention work is cut into pieces of equal cost for a fixed grid of CTAs;
 // see PagedSched.
-constexpr int kPagedMaxCtas = 152;
+constexpr int kPagedMaxCtas = 152;  // one per SM
 constexpr int kPagedMaxRows = 256;  // query rows (token, head of the group) of an item at most
+// the fp32 kernel: up to two CTAs per SM, smaller items
+constexpr int kPagedF32Ctas = 2 * kPagedMaxCtas, kPagedF32Rows = 64;
 
 struct PagedAttnPlan {
   const void *q, *k, *v;
@@ -52,26 +54,30 @@ struct PagedAttnPlan {
   int32_t causal;
   int32_t B, T, Hq, Hkv, G, d, page_size, page_shift, n_pages, max_pages, dtype;
   uint32_t *err;
-  uint32_t *arrivals;  // [kPagedMaxCtas][2], zero between calls
-  float *part;         // [kPagedMaxCtas][2][part_rows][d] partial outputs
-  float *part_ml;      // [kPagedMaxCtas][2][part_rows][2] their maxima and sums
+  uint32_t *arrivals;  // [CTAs][2], zero between calls
+  float *part;         // [CTAs][2][part_rows][d] partial outputs
+  float *part_ml;      // [CTAs][2][part_rows][2] their maxima and sums
   int32_t part_rows;
   int32_t min_stretch;  // keys of a CTA's stretch at least
   cudaStream_t stream;
 };
 
 // Rows a partial result holds at most for a batch of T tokens.
-__host__ __device__ inline int32_t paged_part_rows(int64_t T, int64_t G) {
+__host__ __device__ inline int32_t paged_part_rows(int64_t T, int64_t G, int32_t dtype) {
+  const int64_t most = dtype == KDA_F32 ? kPagedF32Rows : kPagedMaxRows;
   const int64_t rows = (T * G + 15) / 16 * 16;
-  return (int32_t)(rows < kPagedMaxRows ? (rows > 16 ? rows : 16) : kPagedMaxRows);
+  return (int32_t)(rows < most ? (rows > 16 ? rows : 16) : most);
 }
 
+// Sized for either type.
 struct PagedWorkspace {
   size_t arrivals_off, part_off, ml_off, total;
   PagedWorkspace(int64_t T, int64_t G, int64_t d) {
-    const size_t rows = (size_t)kPagedMaxCtas * 2 * (size_t)paged_part_rows(T, G);
+    const size_t a = (size_t)kPagedMaxCtas * paged_part_rows(T, G, KDA_BF16);
+    const size_t b = (size_t)kPagedF32Ctas * paged_part_rows(T, G, KDA_F32);
+    const size_t rows = 2 * (a > b ? a : b);
     arrivals_off = 256;
-    part_off = arrivals_off + align256(kPagedMaxCtas * 2 * sizeof(uint32_t));
+    part_off = arrivals_off + align256(kPagedF32Ctas * 2 * sizeof(uint32_t));
     ml_off = part_off + align256(rows * (size_t)d * sizeof(float));
     total = ml_off + align256(rows * 2 * sizeof(float));
   }

@@ -158,7 +158,7 @@ kda_status kda_paged_attn(const void *q, const void *k_pages, const void *v_page
   p.arrivals = reinterpret_cast<uint32_t *>(ws + lay.arrivals_off);
   p.part = reinterpret_cast<float *>(ws + lay.part_off);
   p.part_ml = reinterpret_cast<float *>(ws + lay.ml_off);
-  p.part_rows = kda::paged_part_rows(a->T_total, G);
+  p.part_rows = kda::paged_part_rows(a->T_total, G, a->dtype);
   // Where requests bring a tile of rows and more, joining the pieces of an item
   // costs as much as six of its key tiles; with few rows it costs little.  (200
   // tokens over 500 keys, 32/8 heads: 42 us at 384, 47 us at 768, 55 us at 1152;

@@ -6,8 +6,9 @@
 // tile of keys, P = exp(S - m'), l = l exp(m - m') + sum P, O = O exp(m - m') +
 // P V.  A tile's scores and probabilities stay in registers and shared memory.
 // Thread (ty, tx) of the 16 x 16 holds rows ty * R .. + R - 1 and keys tx + 16 j of
-// the scores, and the same rows with D / 16 channels of the output.  Bound by
-// the fp32 pipes and the shared-memory reads that feed them.
+// the scores, and the same rows with D / 16 channels of the output.  The
+// next tile is copied to shared memory while one is worked on.  Bound by the
+// fp32 pipes and the shared-memory reads that feed them.
 #include "kda_paged_sched.cuh"
 
 namespace kda {
@@ -22,14 +23,26 @@ struct Smem {
   static constexpr int kLd = D + 4;      // floats of a Q / K row
   static constexpr int kLdP = kKeys + 4;
   float q[kRows * kLd];
-  float k[kKeys * kLd];
-  float v[kKeys * D];
+  float k[2][kKeys * kLd];  // a tile and the one on its way
+  float v[2][kKeys * D];
   float p[kRows * kLdP];
-  int page[kKeys];
   PagedPiece piece;
   int64_t scratch[kThreads / 32 + 4];
   int last;
 };
+
+// Copies 16 bytes to shared memory in the background, or zeros.
+__device__ __forceinline__ void copy16(float *dst, const float *src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(dst)),
+               "l"(src), "r"(real ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 // Element offset of row r of an item: token r / G, query head r % G of the group.
 __device__ __forceinline__ int64_t row_offset(const PagedAttnPlan &p, const PagedPiece &o, int r) {
@@ -38,7 +51,7 @@ __device__ __forceinline__ int64_t row_offset(const PagedAttnPlan &p, const Page
 }
 
 template <int D, int R>
-__global__ void __launch_bounds__(kThreads) attn_kernel(PagedAttnPlan p) {
+__global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) attn_kernel(PagedAttnPlan p) {
   extern __shared__ __align__(16) unsigned char raw[];
   using S = Smem<D, R>;
   S &sm = *reinterpret_cast<S *>(raw);
@@ -73,11 +86,12 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(PagedAttnPlan p) {
       for (int j = 0; j < NC; ++j) acc[i][j] = 0.f;
     }
 
-    for (int tile = o.tile0; tile < o.tile1; ++tile) {
-      const int key0 = tile * kKeys;
-      __syncthreads();
-      if (tid < kKeys) {
-        const int key = key0 + tid;
+    // keys and values of a tile into buffer `to`; slots behind the request's
+    // last key and pages that are none become zeros
+    auto fetch = [&](int tile, int to) {
+      for (int i = tid; i < kKeys * (D / 4); i += kThreads) {
+        const int k = i / (D / 4), e = (i % (D / 4)) * 4;
+        const int key = tile * kKeys + k;
         int page = -1;
         if (key < o.kv) {
           page = p.table[(int64_t)o.req * p.max_pages + (key >> p.page_shift)];
@@ -86,22 +100,25 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(PagedAttnPlan p) {
             page = -1;
           }
         }
-        sm.page[tid] = page;
+        const int64_t slot = ((int64_t)max(page, 0) << p.page_shift) + (key & (p.page_size - 1));
+        const int64_t at = page < 0 ? 0 : (slot * p.Hkv + o.head) * D + e;
+        copy16(&sm.k[to][k * S::kLd + e], static_cast<const float *>(p.k) + at, page >= 0);
+        copy16(&sm.v[to][k * D + e], static_cast<const float *>(p.v) + at, page >= 0);
       }
+      copies_commit();
+    };
+    if (o.tile0 < o.tile1) fetch(o.tile0, 0);
+
+    for (int tile = o.tile0; tile < o.tile1; ++tile) {
+      const int key0 = tile * kKeys, buf = (tile - o.tile0) & 1;
+      const float *sk = sm.k[buf], *sv = sm.v[buf];
+      // the tile before has been read by all: its buffer takes the next one
       __syncthreads();
-      for (int i = tid; i < kKeys * (D / 4); i += kThreads) {
-        const int k = i / (D / 4), e = (i % (D / 4)) * 4;
-        const int page = sm.page[k];
-        float4 kx = make_float4(0.f, 0.f, 0.f, 0.f), vx = kx;
-        if (page >= 0) {
-          const int64_t at =
-              ((((int64_t)page << p.page_shift) + ((key0 + k) & (p.page_size - 1))) * p.Hkv +
-               o.head) * D + e;
-          kx = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.k) + at);
-          vx = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.v) + at);
-        }
-        *reinterpret_cast<float4 *>(&sm.k[k * S::kLd + e]) = kx;
-        *reinterpret_cast<float4 *>(&sm.v[k * D + e]) = vx;
+      if (tile + 1 < o.tile1) {
+        fetch(tile + 1, buf ^ 1);
+        copies_wait<1>();
+      } else {
+        copies_wait<0>();
       }
       __syncthreads();
 
@@ -118,7 +135,7 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(PagedAttnPlan p) {
           a[i] = *reinterpret_cast<const float4 *>(&sm.q[(ty * R + i) * S::kLd + e]);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          b[j] = *reinterpret_cast<const float4 *>(&sm.k[(tx + 16 * j) * S::kLd + e]);
+          b[j] = *reinterpret_cast<const float4 *>(&sk[(tx + 16 * j) * S::kLd + e]);
 #pragma unroll
         for (int i = 0; i < R; ++i)
 #pragma unroll
@@ -163,7 +180,7 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(PagedAttnPlan p) {
         for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
           for (int j = 0; j < NC; j += 4) {
-            const float4 x = *reinterpret_cast<const float4 *>(&sm.v[(k + kk) * D + j * 16 + tx * 4]);
+            const float4 x = *reinterpret_cast<const float4 *>(&sv[(k + kk) * D + j * 16 + tx * 4]);
 #pragma unroll
             for (int i = 0; i < R; ++i) {
               const float f = kk == 0 ? w[i].x : kk == 1 ? w[i].y : kk == 2 ? w[i].z : w[i].w;
@@ -249,7 +266,10 @@ cudaError_t launch_r(const PagedAttnPlan &p) {
   const void *f = reinterpret_cast<const void *>(attn_kernel<D, R>);
   const cudaError_t e = set_smem_limit_once(f, sizeof(Smem<D, R>));
   if (e != cudaSuccess) return e;
-  attn_kernel<D, R><<<kPagedMaxCtas, kThreads, sizeof(Smem<D, R>), p.stream>>>(p);
+  static_assert(16 * R <= kPagedF32Rows, "rows of a partial result");
+  // two CTAs fit an SM with 64 channels, one with 128
+  constexpr int kCtas = sizeof(Smem<D, R>) <= 113 * 1024 ? kPagedF32Ctas : kPagedMaxCtas;
+  attn_kernel<D, R><<<kCtas, kThreads, sizeof(Smem<D, R>), p.stream>>>(p);
   return cudaGetLastError();
 }
 
