@@ -38,7 +38,8 @@ kda_status check_heads(const kda_paged_args *a) {
 kda_status check_batch(const kda_paged_args *a) {
   if (a->B < 0 || a->T_total < 0 || a->max_pages <= 0) return KDA_ERR_INVALID_ARG;
   if (a->B > kda::kMaxRequests) return KDA_ERR_UNSUPPORTED;
-  if ((int64_t)a->max_pages * a->page_size >= (1ll << 31)) return KDA_ERR_UNSUPPORTED;
+  // (positions and key counts, rounded up to tiles, stay below 2^31)
+  if ((int64_t)a->max_pages * a->page_size > (1ll << 30)) return KDA_ERR_UNSUPPORTED;
   return KDA_OK;
 }
 

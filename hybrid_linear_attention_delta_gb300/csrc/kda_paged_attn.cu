@@ -664,7 +664,9 @@ __device__ bool softmax_role(Ctl &ctl, const AttnArgs &a, uint32_t tmem, int s) 
         // weights sum to 2^16 at most, which the sum itself tells; else the
         // tile is taken again with its own maximum.  (A row that sees no key in
         // its first tile sees none in the later ones.)
-        float sum_j;
+        // (Each row for itself: what a row comes to does not depend on the rows
+        // that share its warp.)
+        float sum_j = 0.f;
         for (bool again = j == 0;; again = true) {
           if (again) {
             float top[4];
@@ -679,7 +681,7 @@ __device__ bool softmax_role(Ctl &ctl, const AttnArgs &a, uint32_t tmem, int s) 
             if (j == 0) {
               if (live && tm > -INFINITY) ref = tm;
             } else {
-              const bool move = live && tm > ref;
+              const bool move = live && !(sum_j <= 65536.f) && tm > ref;
               const float keep = move ? ex2_approx(ref - tm) : 1.f;
               if (move) ref = tm;
               l *= keep;

@@ -98,8 +98,9 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PagedPlanArgs p) {
     if (bad) raise_error(p.err, ERR_BAD_CU);
     if (!ring_ok) raise_error(p.err, ERR_BAD_PAGE);
   }
-  const int t_per = (p.T + n_ctas - 1) / n_ctas;
-  const int t_lo = min(p.T, cta * t_per), t_hi = min(p.T, t_lo + t_per);
+  const int64_t t_per = ((int64_t)p.T + n_ctas - 1) / n_ctas;
+  const int t_lo = (int)min((int64_t)p.T, cta * t_per);
+  const int t_hi = (int)min((int64_t)p.T, t_lo + t_per);
   if (bad) {
     for (int t = t_lo + tid; t < t_hi; t += kThreads) p.positions[t] = 0, p.slots[t] = -1;
     if (cta == 0) {
@@ -209,9 +210,9 @@ cudaError_t launch_paged_plan(const PagedPlanArgs &p) {
                                             (5 * kMaxRequests + 1) * (int)sizeof(int));
   if (e != cudaSuccess) return e;
   // a token a thread, up to a CTA per SM
-  int grid = (p.T + kThreads - 1) / kThreads;
-  const int rows = (p.B + 4 * kWarps - 1) / (4 * kWarps);
-  grid = max(1, min(kPagedMaxCtas, max(grid, rows)));
+  const int64_t tokens = ((int64_t)p.T + kThreads - 1) / kThreads;
+  const int64_t rows = (p.B + 4 * kWarps - 1) / (4 * kWarps);
+  const int grid = (int)max((int64_t)1, min((int64_t)kPagedMaxCtas, max(tokens, rows)));
   plan_kernel<<<grid, kThreads, smem, p.stream>>>(p);
   return cudaGetLastError();
 }

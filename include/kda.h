@@ -380,7 +380,8 @@ int64_t kda_snapshot_count(const int32_t *cu_seqlens_host, int32_t B, int32_t sn
  * it receives the raw error bits (1 slot out of range, 2 duplicate slot or a
  * source that is another sequence's destination, 4 bad cu_seqlens, 8 snapshot
  * buffer too small, 16 wait timeout, 64 an accepted length of kda_decode_spec
- * outside [0, n_prev]; bit 32 is not used).
+ * outside [0, n_prev]; bit 32 is not used; bits 128 and up belong to the calls
+ * of kda_paged.h, which names them).
  *
  * Only a->stream and a->workspace are read.  (The status word lives in the
  * workspace, so the call takes the kda_args that name it rather than only a

@@ -43,13 +43,14 @@ typedef struct {
   int32_t d;          /* head dim: 64 or 128 */
   int32_t page_size;  /* tokens of a page: 16, 32, 64, 128 or 256 */
   int32_t n_pages;    /* pages of the pool; n_pages * page_size < 2^31 */
-  int32_t max_pages;  /* columns of the block table; max_pages * page_size < 2^31 */
+  int32_t max_pages;  /* columns of the block table; max_pages * page_size <= 2^30 */
   int32_t dtype;      /* kda_dtype of q, k, v, out and the pages */
   int32_t reserved;   /* 0 */
   void *stream;       /* cudaStream_t */
   void *workspace;    /* device scratch, 256-byte aligned, ZERO-FILLED ONCE after allocation;
                          reusable across calls (and graphs) that are ordered on one stream;
-                         never shared by calls that may overlap */
+                         never shared by calls that may overlap, nor with the calls of kda.h;
+                         to be zero-filled again after KDA_ERR_TIMEOUT */
   size_t workspace_bytes;
   void *ev_begin, *ev_end;  /* optional cudaEvent_t around the call's main kernel */
 } kda_paged_args;

@@ -211,6 +211,59 @@ def test_another_stream():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_many_short_requests(dtype):
+    """More requests than threads of a CTA, most of them a token, some of them
+    without one."""
+    g = torch.Generator().manual_seed(31)
+    new = torch.randint(0, 3, (1500,), generator=g).tolist()
+    total = [n + c for n, c in zip(new, torch.randint(0, 40, (1500,), generator=g).tolist())]
+    _check(AttnCase(new, total, Hq=2, Hkv=1, d=64, page=16, dtype=dtype, seed=32, pad=5))
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, each with a workspace of its own, in flight together."""
+    cases = [AttnCase([1, 40], [3000, 700], Hq=8, Hkv=2, d=d, page=16, dtype="bf16", seed=d)
+             for d in (64, 128)]
+    devs = [c.cuda() for c in cases]
+    outs = [torch.zeros_like(t["q"]) for t in devs]
+    wss = [kda.paged_workspace_for(41, 8, 2, c.d) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, t, o, ws, s in zip(cases, devs, outs, wss, streams):
+            kda.kda_paged_attn(t["q"], t["k"], t["v"], t["table"], t["cu"], t["kv"], o,
+                               workspace=ws, stream=s)
+    torch.cuda.synchronize()
+    for c, o, ws in zip(cases, outs, wss):
+        ref, size, top = c.reference()
+        assert ((o.double().cpu() - ref).abs() <= c.bound(ref, size, top)).all()
+        assert kda.kda_device_status(ws) == (kda.KDA_OK, 0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_shared_pages(dtype):
+    """Requests whose rows name the same pages (a shared prompt), and one row
+    that names a page twice."""
+    case = AttnCase([5, 7], [64, 64], Hq=4, Hkv=2, d=64, page=16, dtype=dtype, seed=6)
+    case.table[1, :3] = case.table[0, :3]
+    case.table[0, 2] = case.table[0, 0]
+    _check(case)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_nan_stays_in_its_row(dtype):
+    """A query that holds a NaN gives NaNs, and nothing else does."""
+    case = AttnCase([70], [300], Hq=2, Hkv=1, d=64, page=16, dtype=dtype, seed=8)
+    clean, _ = _run(case)
+    case.q[33, 1, 5] = float("nan")
+    out, _ = _run(case)
+    assert out[33, 1].isnan().all()
+    keep = torch.ones(70, 2, dtype=torch.bool)
+    keep[33, 1] = False
+    assert torch.equal(out[keep], clean[keep])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_bad_lengths_tables_and_pages(dtype):
     """Inputs that the device checks refuse: an error bit, and nothing else."""
     mk = lambda: AttnCase([3, 5], [40, 60], Hq=4, Hkv=2, d=64, page=16, dtype=dtype)

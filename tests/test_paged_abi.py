@@ -45,7 +45,8 @@ def test_workspace_grows_with_the_batch_up_to_a_bound(lib):
     (dict(d=96), UNSUP), (dict(d=256), UNSUP), (dict(Hq=130, Hkv=2), UNSUP),
     (dict(page_size=0), BAD), (dict(page_size=48), UNSUP), (dict(page_size=8), UNSUP),
     (dict(page_size=512), UNSUP), (dict(n_pages=0), BAD), (dict(n_pages=1 << 27), UNSUP),
-    (dict(max_pages=0), BAD), (dict(max_pages=1 << 27), UNSUP), (dict(B=-1), BAD),
+    (dict(max_pages=0), BAD), (dict(max_pages=1 << 27), UNSUP),
+    (dict(max_pages=(1 << 26) + 1), UNSUP), (dict(B=-1), BAD),
     (dict(B=8193), UNSUP), (dict(T_total=-1), BAD), (dict(workspace=None), BAD),
     (dict(workspace=V(1 << 20 | 16)), BAD), (dict(workspace_bytes=4096), BAD)])
 def test_attention_refuses(lib, kw, want):
