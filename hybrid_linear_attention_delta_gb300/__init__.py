@@ -387,22 +387,26 @@ def kda_decode_fused(xq, xk, xv, g, beta, gate, conv_w, norm_w, slot_ids, state_
 # A decode step makes these calls once per layer, so what they cost on the host
 # is kept small: a device is its index, a check is four comparisons.
 def _check(name, t, shape, dtype, dev):
-    """A tensor argument of the calls below: its shape (None: any extent), dtype
-    and device index are what the library would otherwise take on trust.
-    Returns its address."""
-    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
-        have = t.shape
-        if have == shape or (len(have) == len(shape) and
-                             all(w is None or w == h for w, h in zip(shape, have))):
-            return t.data_ptr()
+    """A tensor argument of the calls below: its shape, dtype and device index
+    are what the library would otherwise take on trust.  Returns its address."""
+    if (t.dtype is dtype and t.shape == shape and t.get_device() == dev
+            and t.is_contiguous()):
+        return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, wanted {tuple(shape)}")
     if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}: every tensor of a call is on one CUDA device")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    raise ValueError(f"{name} has shape {tuple(t.shape)}, wanted "
-                     f"{tuple('any' if s is None else s for s in shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _shape(name, t, n):
+    """The shape of a tensor of n dimensions that the other arguments follow."""
+    shape = t.shape
+    if len(shape) != n:
+        raise ValueError(f"{name} has shape {tuple(shape)}, wanted {n} dimensions")
+    return shape
 
 
 def _launch(what, fn, args, a, dev, workspace, stream, events):
@@ -411,8 +415,9 @@ def _launch(what, fn, args, a, dev, workspace, stream, events):
     torch = _torch
     if dev < 0:
         raise ValueError(f"{what} takes tensors on a CUDA device")
-    a.workspace = _check("workspace", workspace, (None,), torch.uint8, dev)
-    a.workspace_bytes = workspace.numel()
+    size = _shape("workspace", workspace, 1)
+    a.workspace = _check("workspace", workspace, size, torch.uint8, dev)
+    a.workspace_bytes = size[0]
     if events is not None:
         a.ev_begin = events[0].cuda_event
         a.ev_end = events[1].cuda_event
@@ -465,18 +470,20 @@ def kda_paged_plan(cu_seqlens, cached_lens, block_table, held, free_ring, ring, 
     i32, dev = _get_torch().int32, free_ring.get_device()
     B, T = held.numel(), slot_map.numel()
     per_req, per_tok = (B,), (T,)
+    width = _shape("block_table", block_table, 2)[1]
+    n_pages = free_ring.numel()
     args = (_check("cu_seqlens", cu_seqlens, (B + 1,), i32, dev),
             _check("cached_lens", cached_lens, per_req, i32, dev),
-            _check("block_table", block_table, (B, None), i32, dev),
+            _check("block_table", block_table, (B, width), i32, dev),
             _check("held", held, per_req, i32, dev),
-            _check("free_ring", free_ring, (None,), i32, dev),
+            _check("free_ring", free_ring, (n_pages,), i32, dev),
             _check("ring", ring, (2,), i32, dev),
             _check("held_out", held_out, per_req, i32, dev),
             _check("ring_out", ring_out, (2,), i32, dev),
             _check("kv_lens", kv_lens, per_req, i32, dev),
             _check("positions", positions, per_tok, i32, dev),
             _check("slot_map", slot_map, per_tok, i32, dev))
-    a = KdaPagedArgs(B, T, 0, 0, 0, page_size, free_ring.numel(), block_table.shape[1])
+    a = KdaPagedArgs(B, T, 0, 0, 0, page_size, n_pages, width)
     _launch("kda_paged_plan", lib().kda_paged_plan, args, a, dev, workspace, stream, events)
 
 
@@ -491,10 +498,8 @@ def kda_paged_append(qkv, q_norm, k_norm, rope, positions, slot_map, q_out, k_pa
     torch = _get_torch()
     dt, dev, i32, f32 = qkv.dtype, qkv.get_device(), torch.int32, torch.float32
     code = _dtype_code(qkv)
-    pk = _check("k_pages", k_pages, (None,) * 4, dt, dev)
-    n_pages, page_size, Hkv, d = k_pages.shape
-    pq = _check("q_out", q_out, (None, None, d), dt, dev)
-    T, Hq, _ = q_out.shape
+    pages = n_pages, page_size, Hkv, d = _shape("k_pages", k_pages, 4)
+    T, Hq, _ = _shape("q_out", q_out, 3)
     f = KdaAppendArgs(None, None, None, 0, 0, ROPE_MODE[rope_mode], norm_eps)
     if q_norm is not None:
         f.q_norm = _check("q_norm", q_norm, (d,), f32, dev)
@@ -502,12 +507,13 @@ def kda_paged_append(qkv, q_norm, k_norm, rope, positions, slot_map, q_out, k_pa
         f.k_norm = _check("k_norm", k_norm, (d,), f32, dev)
     pos = None
     if rope is not None:
-        f.rope = _check("rope", rope, (None, None), f32, dev)
-        f.max_pos, f.rot_dim = rope.shape
+        f.max_pos, f.rot_dim = _shape("rope", rope, 2)
+        f.rope = _check("rope", rope, rope.shape, f32, dev)
         pos = _check("positions", positions, (T,), i32, dev)
     args = (_check("qkv", qkv, (T, Hq + 2 * Hkv, d), dt, dev), pos,
-            _check("slot_map", slot_map, (T,), i32, dev), pq, pk,
-            _check("v_pages", v_pages, k_pages.shape, dt, dev), ctypes.byref(f))
+            _check("slot_map", slot_map, (T,), i32, dev),
+            _check("q_out", q_out, (T, Hq, d), dt, dev), _check("k_pages", k_pages, pages, dt, dev),
+            _check("v_pages", v_pages, pages, dt, dev), ctypes.byref(f))
     a = KdaPagedArgs(0, T, Hq, Hkv, d, page_size, n_pages, 0, code)
     _launch("kda_paged_append", lib().kda_paged_append, args, a, dev, workspace, stream, events)
 
@@ -521,18 +527,17 @@ def kda_paged_attn(q, k_pages, v_pages, block_table, cu_seqlens, kv_lens, out, *
     kv_lens [B] int32.  scale: 1 / sqrt(d) when not given."""
     i32, dt, dev = _get_torch().int32, q.dtype, q.get_device()
     code = _dtype_code(q)
-    pk = _check("k_pages", k_pages, (None,) * 4, dt, dev)
-    n_pages, page_size, Hkv, d = k_pages.shape
-    pq = _check("q", q, (None, None, d), dt, dev)
-    T, Hq, _ = q.shape
-    B = kv_lens.numel()
-    args = (pq, pk, _check("v_pages", v_pages, k_pages.shape, dt, dev),
-            _check("block_table", block_table, (B, None), i32, dev),
+    pages = n_pages, page_size, Hkv, d = _shape("k_pages", k_pages, 4)
+    T, Hq, _ = _shape("q", q, 3)
+    rows = (T, Hq, d)
+    B, width = _shape("block_table", block_table, 2)
+    args = (_check("q", q, rows, dt, dev), _check("k_pages", k_pages, pages, dt, dev),
+            _check("v_pages", v_pages, pages, dt, dev),
+            _check("block_table", block_table, (B, width), i32, dev),
             _check("cu_seqlens", cu_seqlens, (B + 1,), i32, dev),
-            _check("kv_lens", kv_lens, (B,), i32, dev),
-            _check("out", out, q.shape, dt, dev),
+            _check("kv_lens", kv_lens, (B,), i32, dev), _check("out", out, rows, dt, dev),
             d ** -0.5 if scale is None else scale, 1 if causal else 0)
-    a = KdaPagedArgs(B, T, Hq, Hkv, d, page_size, n_pages, block_table.shape[1], code)
+    a = KdaPagedArgs(B, T, Hq, Hkv, d, page_size, n_pages, width, code)
     _launch("kda_paged_attn", lib().kda_paged_attn, args, a, dev, workspace, stream, events)
 
 
@@ -547,12 +552,11 @@ def kda_verify_drafts(target_probs, draft_probs, draft_tokens, u_accept, u_sampl
     i32, f32 = torch.int32, torch.float32
     dt, dev = target_probs.dtype, target_probs.get_device()
     code = _dtype_code(target_probs)
-    pp = _check("target_probs", target_probs, (None,) * 3, dt, dev)
-    N, n1, V = target_probs.shape
+    N, n1, V = _shape("target_probs", target_probs, 3)
     n = n1 - 1
     if n < 0:
         raise ValueError("target_probs has n_draft + 1 >= 1 rows per sequence")
-    args = (pp,
+    args = (_check("target_probs", target_probs, (N, n1, V), dt, dev),
             None if draft_probs is None else _check("draft_probs", draft_probs, (N, n, V), dt, dev),
             _check("draft_tokens", draft_tokens, (N, n), i32, dev),
             None if draft_lens is None else _check("draft_lens", draft_lens, (N,), i32, dev),
