@@ -76,7 +76,7 @@ struct Ctl {
   uint64_t drain[2];
   Work work[kPieces];
   float ml[kRows][2];    // stream 1's references and sums when the streams are joined
-  int64_t scratch[kThreads / 32 + 4];
+  int64_t scratch[kThreads / 16 + 4];
   uint32_t tmem;
   int32_t last[2];
 };

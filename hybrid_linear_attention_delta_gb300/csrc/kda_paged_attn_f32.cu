@@ -27,7 +27,7 @@ struct Smem {
   float v[2][kKeys * D];
   float p[kRows * kLdP];
   PagedPiece piece;
-  int64_t scratch[kThreads / 32 + 4];
+  int64_t scratch[kThreads / 16 + 4];
   int last;
 };
 

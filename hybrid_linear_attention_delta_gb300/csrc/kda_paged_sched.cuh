@@ -10,6 +10,10 @@
 // short ones.  The pieces of a cut item leave partial results (output, maximum
 // and sum of each row) and the last one to arrive joins them, in order.
 //
+// A batch of few short items (decodes) leaves most of the grid idle at the
+// shortest stretch.  Then every item starts a stretch of its own, so that no
+// CTA works on the end of one item and the start of another.
+//
 // Every CTA finds its stretch itself from cu_seqlens and kv_lens (a block scan
 // of one number per request), so no plan is stored and nothing is cleared.
 #pragma once
@@ -72,12 +76,18 @@ __device__ __forceinline__ int64_t paged_div(int64_t a, int64_t b) {
 template <int TILE>
 struct PagedSched {
   int32_t tokens;
+  bool apart;              // every item starts a stretch
   int64_t pos, end, base;  // place on the line, end of the stretch, start of request b
   int64_t per_cta;
   int32_t b;
   PagedReq r;
 
-  // All threads of the CTA; scratch: THREADS / 32 + 4 words of 64 bits.  False:
+  // What an item of the request and one head takes of the line.
+  __device__ __forceinline__ int64_t stride(int64_t cost) const {
+    return apart ? paged_div(cost + per_cta - 1, per_cta) * per_cta : cost;
+  }
+
+  // All threads of the CTA; scratch: THREADS / 16 + 4 words of 64 bits.  False:
   // bad cu_seqlens (nothing is to be done).
   template <int THREADS>
   __device__ bool init(const PagedAttnPlan &p, int tokens_per_item, int64_t *scratch) {
@@ -86,7 +96,10 @@ struct PagedSched {
     tokens = tokens_per_item;
     const int run = (p.B + THREADS - 1) / THREADS;
     const int b0 = min(p.B, tid * run), b1 = min(p.B, b0 + run);
-    int64_t mine = 0;
+    // a cut costs a round trip of partials (see min_stretch); two tiles and an
+    // item's fixed cost at least, so that a stretch inside an item has a tile
+    per_cta = max(p.min_stretch, 2 * TILE + kItemCost);
+    int64_t mine = 0, mine_s = 0;  // this thread's requests: cost, and stretches of per_cta
     bool bad = tid == 0 && (p.cu[0] != 0 || p.cu[p.B] > p.T);
     for (int i = b0; i < b1; ++i) {
       bad |= p.cu[i + 1] < p.cu[i];
@@ -94,46 +107,53 @@ struct PagedSched {
       const int kvl = p.kv_lens[i];
       if (blockIdx.x == 0 && (kvl < 0 || (int64_t)kvl > (int64_t)p.max_pages * p.page_size))
         raise_error(p.err, ERR_BAD_LEN);
-      mine += paged_head_cost(q, tokens, p.causal) * p.Hkv;
+      const int64_t c = paged_head_cost(q, tokens, p.causal);
+      mine += c * p.Hkv;
+      mine_s += q.n > tokens ? 1ll << 32  // several items: not apart
+                             : paged_div(c + per_cta - 1, per_cta) * p.Hkv;
     }
-    int64_t inc = mine;
+    int64_t inc = mine, inc_s = mine_s;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += x;
+      const int64_t y = __shfl_up_sync(0xffffffffu, inc_s, o);
+      if (lane >= o) inc += x, inc_s += y;
     }
-    if (lane == 31) scratch[warp] = inc;
-    if (tid == 0) scratch[W] = -1;
+    if (lane == 31) scratch[warp] = inc, scratch[W + warp] = inc_s;
+    if (tid == 0) scratch[2 * W] = -1;
     if (__syncthreads_or(bad)) {
       if (blockIdx.x == 0 && tid == 0) raise_error(p.err, ERR_BAD_CU);
       return false;
     }
-    int64_t before = inc - mine, total = 0;
+    int64_t before = inc - mine, total = 0, before_s = inc_s - mine_s, total_s = 0;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-      if (w < warp) before += scratch[w];
-      total += scratch[w];
+      if (w < warp) before += scratch[w], before_s += scratch[W + w];
+      total += scratch[w], total_s += scratch[W + w];
     }
-    // a cut costs a round trip of partials (see min_stretch); two tiles and an
-    // item's fixed cost at least, so that a stretch inside an item has a tile
-    per_cta = max((int64_t)max(p.min_stretch, 2 * TILE + kItemCost), paged_div(total + gridDim.x - 1, gridDim.x));
+    apart = total_s <= gridDim.x;
+    if (apart) {
+      before = before_s * per_cta, mine = mine_s * per_cta, total = total_s * per_cta;
+    } else {
+      per_cta = max(per_cta, paged_div(total + gridDim.x - 1, gridDim.x));
+    }
     pos = blockIdx.x * per_cta;
     end = min(total, pos + per_cta);
     if (pos < end && before <= pos && pos < before + mine) {  // this thread's requests hold it
       int64_t at = before;
       for (int i = b0; i < b1; ++i) {
-        const int64_t c = paged_head_cost(paged_request(p, i), tokens, p.causal) * p.Hkv;
+        const int64_t c = stride(paged_head_cost(paged_request(p, i), tokens, p.causal)) * p.Hkv;
         if (pos < at + c) {
-          scratch[W] = i;
-          scratch[W + 1] = at;
+          scratch[2 * W] = i;
+          scratch[2 * W + 1] = at;
           break;
         }
         at += c;
       }
     }
     __syncthreads();
-    b = (int32_t)scratch[W];
-    base = scratch[W + 1];
+    b = (int32_t)scratch[2 * W];
+    base = scratch[2 * W + 1];
     if (b < 0) pos = end = 0;
     else r = paged_request(p, b);
     return true;
@@ -155,7 +175,7 @@ struct PagedSched {
     PagedPiece o;
     o.n = 0;
     while (pos < end) {
-      const int64_t head_cost = paged_head_cost(r, tokens, p.causal);
+      const int64_t head_cost = stride(paged_head_cost(r, tokens, p.causal));
       if (pos >= base + head_cost * p.Hkv) {  // on to the next request with work
         base += head_cost * p.Hkv;
         if (++b >= p.B) {
@@ -189,7 +209,7 @@ struct PagedSched {
       o.tile0 = cut(pos - start, cost, tiles, whole);
       o.tile1 = cut(stop - start, cost, tiles, whole);
       o.n_pieces = o.index = o.first_cta = o.first_slot = 0;
-      pos = stop;
+      pos = apart ? end : stop;
       const int64_t cta = blockIdx.x;
       const int64_t c0 = start >= cta * per_cta ? cta : paged_div(start, per_cta);
       const int64_t c1 = start + cost <= end ? cta : paged_div(start + cost - 1, per_cta);
