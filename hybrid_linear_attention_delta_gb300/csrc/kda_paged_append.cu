@@ -14,7 +14,9 @@
 // sines there) is a chain of two loads.  A warp walks the heads of a token in
 // batches of kBatch passes, the next batch's loads in flight while one is
 // worked on, so that the chain and the load latency are paid once a token; with
-// one batch per warp they were paid six times as often.
+// one batch per warp they were paid six times as often (32767 tokens of 32 + 16
+// heads of 128 channels: 198 us then, 145 us, 5.6 TB/s, now; the same loads and
+// stores without norm and rotation: 118 us).
 #include "kda_paged.cuh"
 
 namespace kda {

@@ -19,6 +19,19 @@
 // Warps 0-3 and 4-7: the softmax and the outputs of stream 0 and 1; warps 8 and
 // 9 issue the streams' products; warp 10 loads Q and the K / V tiles, page by
 // page, into a ring of stages; warp 11 cuts the work into pieces (PagedSched).
+//
+// Roundings: scores, sums and outputs are fp32; the weights are rounded to bf16
+// for the product with V (half a step, 2^-8 relative, which averages out over the
+// keys: 2.3e-3 relative error of the outputs in all, where rounding them alone
+// costs 1.7e-3), the outputs to bf16 at the end.
+//
+// Bound and measured (GB300): a chunk of 8192 tokens over 32768 keys, 32 / 8 heads
+// of 128 channels, by the tensor cores and the chain of a tile (scores, softmax,
+// outputs): 2.27 ms, 1.70 PFLOP/s (cuBLAS: 1.87), 2.54 ms in a loop at the power
+// limit.  Decode of 256 requests over 511 to 8191 keys: HBM, 0.72 ms, 6.7 TB/s
+// (99% of a copy); 64 x 8 tokens over 1000 to 32760 keys, 32 / 4 heads: 0.347 ms,
+// 6.4 TB/s.  64 channels: the softmax, 1.0 PFLOP/s.  One token over 777 keys:
+// latency, 14.8 us, of which 6 are spent before the first scores.
 #include <cuda.h>
 
 #include <cstring>

@@ -12,7 +12,8 @@
 // sums are therefore carried as pairs of floats (the rounding error of every
 // addition is kept, about 46 bits); doubles would do, but a GB300 SM adds two
 // of them per cycle, and the joins of a row's partial sums alone then take
-// longer than its loads (64 x 7 drafts, V = 131072: 38.9 us with doubles).
+// longer than its loads (64 x 7 drafts, V = 131072: 38.9 us with doubles, 18 us,
+// 3.7 TB/s, with pairs: 8 us of latency and the loads; one sequence: 7.5 us).
 #include <cooperative_groups.h>
 
 #include "kda_paged.cuh"
