@@ -288,36 +288,43 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(VerifyPlan p, int s
     if (above(s_seg[g], g ? s_seg[g - 1] : F2{0.f, 0.f})) atomicMax(&s_last, g);
   }
   __syncthreads();
-  const int g = s_pick != 0x7fffffff ? s_pick : max(s_last, 0);
-  F2 c = g ? add(start, s_seg[g - 1]) : start;
-  const int64_t i0 = (int64_t)(first + g) * seg_len, i1 = min(V, i0 + seg_len);
-  __syncthreads();
-  if (tid == 0) s_pick = 0x7fffffff, s_last = -1;
-  for (int64_t base = i0; base < i1; base += 2 * kThreads) {
-    const int i = (int)base + 2 * tid;  // two neighbours a thread
-    float hi[2] = {0.f, 0.f}, lo[2] = {0.f, 0.f};
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-      if (i + k < i1) {
-        const float pv = to_f32<T>(row.p[i + k]);
-        if (row.q) mass<true>(pv, to_f32<T>(row.q[i + k]), false, hi[k], lo[k]);
-        else mass<false>(pv, 0.f, i + k == row.gone, hi[k], lo[k]);
-      }
-    const F2 a = {hi[0], lo[0]}, b = {hi[1], lo[1]}, both = add(a, b);
-    F2 total;
-    const F2 inc = block_scan(both, warp_sums, &total);
-    if (both.hi > 0.f) {
-      atomicMax(&s_last, hi[1] > 0.f ? i + 1 : i);
-      if (above(add(c, inc), thr)) {
-        // the border lies in this thread's pair or before it: before its second
-        // token lies what is before the pair and its first token
-        const F2 one = add(add(c, inc), F2{-hi[1], -lo[1]});
-        atomicMin(&s_pick, hi[0] > 0.f && above(one, thr) ? i : hi[1] > 0.f ? i + 1 : i);
-      }
-    }
-    c = add(c, total);
+  int g = s_pick != 0x7fffffff ? s_pick : max(s_last, 0);
+  // Sums of the same tokens in two orders differ in their last bits, so thr may
+  // lie between two values of the border of a segment without mass; the token is
+  // then the last one with mass before it.
+  for (;; --g) {
+    F2 c = g ? add(start, s_seg[g - 1]) : start;
+    const int64_t i0 = (int64_t)(first + g) * seg_len, i1 = min(V, i0 + seg_len);
     __syncthreads();
-    if (s_pick != 0x7fffffff) break;
+    if (tid == 0) s_pick = 0x7fffffff, s_last = -1;
+    __syncthreads();
+    for (int64_t base = i0; base < i1; base += 2 * kThreads) {
+      const int i = (int)base + 2 * tid;  // two neighbours a thread
+      float hi[2] = {0.f, 0.f}, lo[2] = {0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (i + k < i1) {
+          const float pv = to_f32<T>(row.p[i + k]);
+          if (row.q) mass<true>(pv, to_f32<T>(row.q[i + k]), false, hi[k], lo[k]);
+          else mass<false>(pv, 0.f, i + k == row.gone, hi[k], lo[k]);
+        }
+      const F2 a = {hi[0], lo[0]}, b = {hi[1], lo[1]}, both = add(a, b);
+      F2 total;
+      const F2 inc = block_scan(both, warp_sums, &total);
+      if (both.hi > 0.f) {
+        atomicMax(&s_last, hi[1] > 0.f ? i + 1 : i);
+        if (above(add(c, inc), thr)) {
+          // the border lies in this thread's pair or before it: before its second
+          // token lies what is before the pair and its first token
+          const F2 one = add(add(c, inc), F2{-hi[1], -lo[1]});
+          atomicMin(&s_pick, hi[0] > 0.f && above(one, thr) ? i : hi[1] > 0.f ? i + 1 : i);
+        }
+      }
+      c = add(c, total);
+      __syncthreads();
+      if (s_pick != 0x7fffffff) break;
+    }
+    if (s_last >= 0 || g == 0) break;
   }
   if (tid == 0) tokens[kept] = s_pick != 0x7fffffff ? s_pick : s_last;
 }

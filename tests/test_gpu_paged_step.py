@@ -335,6 +335,47 @@ def test_verify_far_tokens_are_not_lost():
     assert bits == 0 and torch.equal(acc, racc) and torch.equal(tok, rtok)
 
 
+# Four rows, found by search: the mass of segments 0, 2, ... 30 of 1024 tokens, that
+# of segment 40, and u, for which u times the sum lies between two values that
+# sums in different orders give the border behind a segment with mass.
+GAPS = [
+    (16, "0x1.b0a24ep-1", "0x1.07cbeap-2",
+     "0x1.c13056p-1 0x1.d602ap-2 0x1.e2c394p-1 0x1.5f382cp-13 0x1.43a47cp-5 0x1.031cacp-2 "
+     "0x1.bea34ap-18 0x1.7167b4p-9 0x1.f0c782p-24 0x1.74fc3cp-5 0x1.a0d156p-6 "
+     "0x1.58fdeep-6 0x1.96894ep-19 0x1.f5f8cap-4 0x1.0beea4p-14 0x1.3778fcp-14"),
+    (20, "0x1.4c4b14p-1", "0x1.30c7ccp+0",
+     "0x1.b0790cp-1 0x1.dbd38p-11 0x1.c92292p-16 0x1.5179cep-7 0x1.71fb98p-19 "
+     "0x1.e560d2p-4 0x1.54b324p-2 0x1.ef3a5ap-24 0x1.067714p-14 0x1.c9e13p-1 0x1.7151ecp-9 "
+     "0x1.142b9cp-17 0x1.2a259ap-12 0x1.49f1dep-10 0x1.a8f24ap-23 0x1.9a34a2p-19"),
+    (22, "0x1.f3f3a2p-1", "0x1.358824p-4",
+     "0x1.d0629ep-1 0x1.f7410cp-1 0x1.db59ecp-13 0x1.69015p-8 0x1.1946ep-16 0x1.1a5edp-8 "
+     "0x1.64aceep-23 0x1.6ac5e2p-1 0x1.6a6194p-5 0x1.a9e0a6p-17 0x1.5ce42ep-1 "
+     "0x1.c845bcp-1 0x1.ef19a6p-8 0x1.db0904p-10 0x1.1420c6p-6 0x1.3720dp-15"),
+    (30, "0x1.70a224p-1", "0x1.d84e8ep-1",
+     "0x1.ba60a2p-14 0x1.232738p-8 0x1.5db0b4p-8 0x1.26c9d6p-19 0x1.96e8a2p-17 "
+     "0x1.eae3bp-21 0x1.eb71acp-1 0x1.f941f8p-16 0x1.d365fcp-4 0x1.d2371cp-21 "
+     "0x1.fc6992p-24 0x1.11fdbcp-23 0x1.14bfa2p-1 0x1.b358ecp-15 0x1.7ea80cp-1 "
+     "0x1.4b6b6ap-14"),
+]
+
+
+def test_verify_border_between_two_roundings():
+    """The draw finds a token with mass although the place that it seeks falls on
+    a border whose two roundings enclose it, with segments without mass behind."""
+    V, N = 65536, 160
+    p, us = torch.zeros((N, 1, V)), torch.zeros((N,))
+    for n in range(N):
+        _, u, last, m = GAPS[n % len(GAPS)]
+        p[n, 0, 5:32 * 1024:2048] = torch.tensor([float.fromhex(x) / 4 for x in m.split()])
+        p[n, 0, 40 * 1024 + 5] = float.fromhex(last) / 4
+        us[n] = float.fromhex(u)
+    acc, tok, bits = _verify([p, None, torch.zeros((N, 0), dtype=I32), torch.zeros((N, 0)), us])
+    assert bits == 0 and (acc == 1).all()
+    for n in range(N):
+        seg = GAPS[n % len(GAPS)][0]  # either side of the border is a fair draw
+        assert tok[n, 0] in (seg * 1024 + 5, (seg + 2 if seg < 30 else 40) * 1024 + 5)
+
+
 def test_verify_bad_inputs_on_the_device():
     p, q, x, ua, us = _verify_case(4, 2, 300, "f32", seed=4, noise=0.0)
     x[0, 0], x[1, 1] = 300, -1
