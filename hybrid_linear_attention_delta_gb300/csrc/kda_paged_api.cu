@@ -2,6 +2,7 @@
 // host-side argument checks and the stream-ordered launches.  No device memory
 // is allocated here.
 #include <cmath>
+#include <initializer_list>
 
 #include "kda_paged.cuh"
 
@@ -43,6 +44,17 @@ kda_status check_batch(const kda_paged_args *a) {
   return KDA_OK;
 }
 
+// Whether an output (the first n_out of the arrays) is another array too; NULL and
+// empty arrays aside.  CTAs read inputs at different times, so a call in place
+// would race.
+bool shared(std::initializer_list<const void *> arrays, size_t n_out) {
+  const void *const *v = arrays.begin();
+  for (size_t i = 0; i < n_out; ++i)
+    for (size_t j = i + 1; j < arrays.size(); ++j)
+      if (v[i] && v[i] == v[j]) return true;
+  return false;
+}
+
 // Runs one launch with the caller's events around it.
 template <typename Launch>
 kda_status launch(void *stream, void *ev_begin, void *ev_end, Launch f) {
@@ -77,12 +89,17 @@ kda_status kda_paged_plan(const int32_t *cu_seqlens, const int32_t *cached_lens,
   if (st == KDA_OK) st = check_workspace(a->workspace, a->workspace_bytes, 256);
   if (st != KDA_OK) return st;
   if (!aligned(cu_seqlens, 4) || !aligned(free_ring, 4) || !aligned(ring, 4) ||
-      !aligned(ring_out, 4) || ring == ring_out)
+      !aligned(ring_out, 4))
     return KDA_ERR_INVALID_ARG;
   if (a->B > 0 && (!aligned(cached_lens, 4) || !aligned(block_table, 4) || !aligned(held, 4) ||
-                   !aligned(held_out, 4) || !aligned(kv_lens, 4) || held == held_out))
+                   !aligned(held_out, 4) || !aligned(kv_lens, 4)))
     return KDA_ERR_INVALID_ARG;
   if (a->T_total > 0 && (!aligned(positions, 4) || !aligned(slot_map, 4))) return KDA_ERR_INVALID_ARG;
+  const bool any = a->B > 0, tok = a->T_total > 0;
+  if (shared({any ? block_table : nullptr, free_ring, any ? held_out : nullptr, ring_out,
+              any ? kv_lens : nullptr, tok ? positions : nullptr, tok ? slot_map : nullptr,
+              cu_seqlens, any ? cached_lens : nullptr, any ? held : nullptr, ring}, 7))
+    return KDA_ERR_INVALID_ARG;
   kda::PagedPlanArgs p = {};
   p.cu = cu_seqlens; p.cached = cached_lens; p.held = held; p.ring = ring;
   p.table = block_table; p.free_ring = free_ring; p.held_out = held_out; p.ring_out = ring_out;
@@ -115,6 +132,7 @@ kda_status kda_paged_append(const void *qkv, const int32_t *positions, const int
   if (!aligned(qkv, 16) || !aligned(q_out, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) ||
       !aligned(slot_map, 4) || (f->rot_dim > 0 && !aligned(positions, 4)))
     return KDA_ERR_INVALID_ARG;
+  if (shared({q_out, k_pages, v_pages, qkv}, 3)) return KDA_ERR_INVALID_ARG;
   kda::AppendPlan p = {};
   p.qkv = qkv; p.positions = positions; p.slots = slot_map;
   p.q = q_out; p.k_pages = k_pages; p.v_pages = v_pages;
@@ -188,6 +206,8 @@ kda_status kda_verify_drafts(const void *target_probs, const void *draft_probs,
       (draft_lens && !aligned(draft_lens, 4)))
     return KDA_ERR_INVALID_ARG;
   if (a->n_draft > 0 && (!aligned(draft_tokens, 4) || !aligned(u_accept, 4)))
+    return KDA_ERR_INVALID_ARG;
+  if (shared({accepted, tokens, draft_lens, a->n_draft > 0 ? draft_tokens : nullptr}, 2))
     return KDA_ERR_INVALID_ARG;
   kda::VerifyPlan p = {};
   p.p = target_probs; p.q = a->n_draft > 0 ? draft_probs : nullptr;

@@ -86,8 +86,9 @@ size_t kda_paged_workspace_bytes(const kda_paged_args *a);
  * positions   [T_total] int32  position of each new token (0 for rows >= cu[B])
  * slot_map    [T_total] int32  cache slot, page * page_size + offset (-1 for rows >= cu[B])
  *
- * held_out and ring_out may not be held and ring: the call changes none of its
- * inputs but the entries named above, so it can be repeated.
+ * No output may be another array of the call (held_out and held, ring_out and
+ * ring, kv_lens and cached_lens are different ones): the call changes none of
+ * its inputs but the entries named above, so it can be repeated.
  *
  * Refused requests keep held_out = held, write nothing, get kv_lens = 0 (their
  * rows of kda_paged_attn become zeros) and slot -1 for their tokens:
@@ -96,7 +97,7 @@ size_t kda_paged_workspace_bytes(const kda_paged_args *a);
  *   - a length that is negative or beyond max_pages pages, held outside
  *     [0, max_pages] (bit 128).
  * A page number outside [0, n_pages) raises bit 512 and its tokens get slot
- * -1; a ring state outside its range, or more pages given back than the ring
+ * -1 (given back, it goes into the ring as it is); a ring state outside its range, or more pages given back than the ring
  * has room for, raises bit 512 too (the ring then counts as empty, or the
  * surplus is dropped).  With bad cu_seqlens (bit 4) every request is refused.
  * Uses B, T_total, page_size, n_pages, max_pages of a.
@@ -125,8 +126,8 @@ kda_status kda_paged_plan(const int32_t *cu_seqlens, const int32_t *cached_lens,
  *                              negative slot is skipped: nothing of it is written
  * q_out      [T_total][Hq][d] dtype
  * k_pages, v_pages [n_pages][page_size][Hkv][d] dtype
- * A slot beyond the pool (bit 1) or a position beyond the table (bit 1024)
- * skips the token.  Uses T_total, Hq, Hkv, d, page_size, n_pages, dtype of a.
+ * q_out, k_pages, v_pages and qkv are different arrays.  A slot beyond the pool
+ * (bit 1) or a position beyond the table (bit 1024) skips the token.  Uses T_total, Hq, Hkv, d, page_size, n_pages, dtype of a.
  */
 typedef struct {
   const float *q_norm, *k_norm;  /* [d] fp32 weights; NULL: that norm is left out */
@@ -199,6 +200,7 @@ kda_status kda_paged_attn(const void *q, const void *k_pages, const void *v_page
  * accepted     [N] int32     1 + the drafts that stand (the verified tokens that are kept,
  *                            the step's first included): accepted_prev of kda_decode_spec
  * tokens       [N][n_draft+1] int32  the drafts that stand, the drawn token, then -1
+ * (accepted and tokens are arrays of their own, not draft_lens or draft_tokens)
  *
  * A draft token outside [0, V) does not stand (bit 2048).  draft_lens outside
  * its range (bit 128): accepted 0, tokens -1.  A row without mass (bit 4096):

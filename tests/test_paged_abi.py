@@ -142,6 +142,30 @@ def test_verify_refuses(lib):
     assert lib.kda_last_launch_count() == 0
 
 
+def test_outputs_are_arrays_of_their_own(lib):
+    """CTAs read inputs at different times: an output over another array is
+    refused before a launch."""
+    ptr = lambda n: [V(4096 + 4096 * i) for i in range(n)]
+
+    def pairs(call, n, outs, others):
+        for i in outs:
+            for j in list(outs) + list(others):
+                if i != j:
+                    ptrs = ptr(n)
+                    ptrs[i] = ptrs[j]
+                    assert call(ptrs) == BAD, (i, j)
+
+    a = _args()
+    # block_table, free_ring, held_out, ring_out, kv_lens, positions, slot_map
+    pairs(lambda p: lib.kda_paged_plan(*p, ctypes.byref(a)), 11, (2, 4, 6, 7, 8, 9, 10),
+          (0, 1, 3, 5))
+    f = kda.KdaAppendArgs(None, None, FAKE, 10, 32, 0, 1e-6)
+    pairs(lambda p: lib.kda_paged_append(*p, ctypes.byref(f), ctypes.byref(a)), 6, (3, 4, 5), (0,))
+    v = kda.KdaVerifyArgs(2, 3, 100, kda.KDA_F32, None, WS, 256)
+    pairs(lambda p: lib.kda_verify_drafts(*p, ctypes.byref(v)), 8, (6, 7), (2, 3))
+    assert lib.kda_last_launch_count() == 0
+
+
 def test_binding_refuses_host_tensors_types_and_shapes():
     """Tensors off the GPU never reach the library (it would read them there)."""
     kda.build()
