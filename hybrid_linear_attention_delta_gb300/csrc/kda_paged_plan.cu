@@ -167,7 +167,9 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PagedPlanArgs p) {
       if (behind >= p.n_pages) break;
       long long at = head + behind;
       if (at >= p.n_pages) at -= p.n_pages;
-      p.free_ring[at] = row[j];
+      const int page = row[j];
+      if (page < 0 || page >= p.n_pages) raise_error(p.err, ERR_BAD_PAGE);
+      p.free_ring[at] = page;
     }
   }
 

@@ -150,6 +150,13 @@ def test_plan_bad_inputs_on_the_device():
     t = c.run()
     assert kda.kda_device_status(c.ws)[1] == 512
     assert t["slots"].tolist()[3:] == [-1] * 5 and min(t["slots"].tolist()[:3]) >= 0
+    # a page that is none is given back: it is told
+    c = PlanCase([0, 5], [0, 20], [2, 2], 16, 6, 1)
+    c.table[0][1] = -3
+    t = c.run()
+    assert kda.kda_device_status(c.ws)[1] == 512
+    assert t["kv"].tolist() == [0, 25] and t["ring_out"].tolist() == [c.head, 8]
+    assert t["ring"].tolist()[(c.head + 7) % 10] == -3
     # more pages given back than the ring has room for
     c = PlanCase([0, 0], [0, 0], [3, 3], 16, 2, 1)
     c.count = 5
