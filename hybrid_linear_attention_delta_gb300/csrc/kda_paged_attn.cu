@@ -164,6 +164,7 @@ struct AttnArgs {
   PagedAttnPlan p;
   float c;         // |scale| log2(e)
   uint32_t neg_q;  // scale < 0: Q is negated by the product
+  int32_t tpt;     // tokens of a tile: kRows / G
 };
 
 // Reads the published pieces; a piece stays where it is until it is released.
@@ -179,7 +180,7 @@ struct PieceReader {
 
 // ------------------------------------------------------------------ pieces
 __device__ bool sched_role(Ctl &ctl, const AttnArgs &a, PagedSched<kKeys> &sched) {
-  const int tpt = kRows / a.p.G;  // tokens of a tile
+  const int tpt = a.tpt;
   for (uint32_t n = 0;; ++n) {
     const uint32_t slot = n % kPieces;
     Work w;
@@ -216,7 +217,7 @@ __device__ bool load_role(uint32_t sbase, Ctl &ctl, const AttnArgs &a, const CUt
   const PagedAttnPlan &p = a.p;
   const int lane = threadIdx.x & 31;
   const int rs = min(p.page_shift, 7), rows = 1 << rs;  // key rows of a box
-  const int tpt = kRows / p.G;
+  const int tpt = a.tpt;
   const uint32_t q_bytes = (uint32_t)(tpt * p.G * 128 * Ly::kHalves);
   // lane l fetches half l % kHalves of page l / kHalves of a tile
   const int half = lane % Ly::kHalves, box = lane / Ly::kHalves;
@@ -623,7 +624,7 @@ __device__ bool softmax_role(Ctl &ctl, const AttnArgs &a, uint32_t tmem, int s) 
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
   const int r = warp * 32 + lane;          // this thread's row of the tile
   const int t = r / p.G, g = r - t * p.G;  // its token and head
-  const int tpt = kRows / p.G;
+  const int tpt = a.tpt;
   const uint32_t lanes = (uint32_t)(warp * 32) << 16;
   using Ly = Layout<D>;
   const uint32_t ts = tmem + lanes + s * 128, to = tmem + lanes + Ly::kO + s * D;
@@ -917,7 +918,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
   if (warp == kMmaWarp) tmem_alloc(smem_u32(&ctl.tmem), 512);
   tc_fence_before();
   PagedSched<kKeys> sched;  // (its barriers are the set-up's too)
-  const bool work = sched.template init<kThreads>(a.p, 2 * (kRows / a.p.G), ctl.scratch);
+  const bool work = sched.template init<kThreads>(a.p, 2 * a.tpt, ctl.scratch);
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&ctl.tmem);
 
@@ -995,6 +996,7 @@ cudaError_t launch_d(const PagedAttnPlan &p) {
   // 10^22 times 10^-30 are 0 to any rounding)
   a.c = fmaxf(fabsf(p.scale) * 1.4426950408889634f, 1e-30f);
   a.neg_q = p.scale < 0.f;
+  a.tpt = kRows / p.G;
   attn_kernel<D><<<kPagedMaxCtas, kThreads, smem_bytes<D>(), p.stream>>>(tq, tk, tv, a);
   return cudaGetLastError();
 }

@@ -25,9 +25,9 @@ namespace kda {
 // Fixed cost of an item, in keys.
 constexpr int kItemCost = 128;
 
-// A request as the line sees it; n = 0 for one that is skipped.
-struct PagedReq {
-  int32_t tok0, n, kv;
+// A request as the line sees it; n = runs = 0 for one that is skipped.
+struct alignas(8) PagedReq {
+  int32_t tok0, n, kv, runs;
 };
 
 struct PagedPiece {
@@ -45,25 +45,25 @@ struct PagedPiece {
                        // 2 * (first_cta + k)
 };
 
+// Cost of the request's first i runs of one head.
 __device__ __forceinline__ int64_t paged_prefix(const PagedReq &r, int64_t i, int tokens,
                                                 bool causal) {
-  // cost of the request's first i runs of one head
-  const int64_t n = (r.n + tokens - 1) / tokens;
   if (!causal || r.kv < r.n) return i * (r.kv + kItemCost);
   int64_t c = i * (r.kv - r.n + kItemCost) + (int64_t)tokens * (i * (i + 1) / 2);
-  if (i == n) c += r.n - n * tokens;  // the last run is shorter
+  if (i == r.runs) c += r.n - (int64_t)r.runs * tokens;  // the last run is shorter
   return c;
 }
 __device__ __forceinline__ int64_t paged_head_cost(const PagedReq &r, int tokens, bool causal) {
-  return r.n == 0 ? 0 : paged_prefix(r, (r.n + tokens - 1) / tokens, tokens, causal);
+  return paged_prefix(r, r.runs, tokens, causal);
 }
 
-__device__ __forceinline__ PagedReq paged_request(const PagedAttnPlan &p, int b) {
+__device__ __forceinline__ PagedReq paged_request(const PagedAttnPlan &p, int b, int tokens) {
   PagedReq r;
   r.tok0 = p.cu[b];
   r.n = p.cu[b + 1] - r.tok0;
   r.kv = p.kv_lens[b];
   if (r.n <= 0 || r.kv < 0 || (int64_t)r.kv > (int64_t)p.max_pages * p.page_size) r.n = 0;
+  r.runs = (int32_t)(((uint32_t)r.n + tokens - 1) / (uint32_t)tokens);
   return r;
 }
 
@@ -100,10 +100,12 @@ struct PagedSched {
     // item's fixed cost at least, so that a stretch inside an item has a tile
     per_cta = max(p.min_stretch, 2 * TILE + kItemCost);
     int64_t mine = 0, mine_s = 0;  // this thread's requests: cost, and stretches of per_cta
-    bool bad = tid == 0 && (p.cu[0] != 0 || p.cu[p.B] > p.T);
+    // (both asked for at once)
+    const int cu0 = tid == 0 ? p.cu[0] : 0, cuB = tid == 0 ? p.cu[p.B] : 0;
+    bool bad = false;
     for (int i = b0; i < b1; ++i) {
       bad |= p.cu[i + 1] < p.cu[i];
-      const PagedReq q = paged_request(p, i);
+      const PagedReq q = paged_request(p, i, tokens);
       const int kvl = p.kv_lens[i];
       if (blockIdx.x == 0 && (kvl < 0 || (int64_t)kvl > (int64_t)p.max_pages * p.page_size))
         raise_error(p.err, ERR_BAD_LEN);
@@ -112,6 +114,7 @@ struct PagedSched {
       mine_s += q.n > tokens ? 1ll << 32  // several items: not apart
                              : paged_div(c + per_cta - 1, per_cta) * p.Hkv;
     }
+    bad |= cu0 != 0 || cuB > p.T;
     int64_t inc = mine, inc_s = mine_s;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -142,10 +145,12 @@ struct PagedSched {
     if (pos < end && before <= pos && pos < before + mine) {  // this thread's requests hold it
       int64_t at = before;
       for (int i = b0; i < b1; ++i) {
-        const int64_t c = stride(paged_head_cost(paged_request(p, i), tokens, p.causal)) * p.Hkv;
+        const PagedReq q = paged_request(p, i, tokens);
+        const int64_t c = stride(paged_head_cost(q, tokens, p.causal)) * p.Hkv;
         if (pos < at + c) {
           scratch[2 * W] = i;
           scratch[2 * W + 1] = at;
+          reinterpret_cast<PagedReq *>(scratch)[W + 1] = q;
           break;
         }
         at += c;
@@ -155,7 +160,7 @@ struct PagedSched {
     b = (int32_t)scratch[2 * W];
     base = scratch[2 * W + 1];
     if (b < 0) pos = end = 0;
-    else r = paged_request(p, b);
+    else r = reinterpret_cast<PagedReq *>(scratch)[W + 1];
     return true;
   }
 
@@ -182,13 +187,12 @@ struct PagedSched {
           pos = end;
           break;
         }
-        r = paged_request(p, b);
+        r = paged_request(p, b, tokens);
         continue;
       }
       const int head = (int)paged_div(pos - base, head_cost);
       const int64_t head_base = base + head * head_cost;
-      const int runs = (r.n + tokens - 1) / tokens;
-      int lo = 0, hi = runs - 1;  // largest run that starts at or before pos
+      int lo = 0, hi = r.runs - 1;  // largest run that starts at or before pos
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (head_base + paged_prefix(r, mid, tokens, p.causal) <= pos) lo = mid; else hi = mid - 1;
