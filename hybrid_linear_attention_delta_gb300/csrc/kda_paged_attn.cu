@@ -233,6 +233,15 @@ __device__ bool load_role(uint32_t sbase, Ctl &ctl, const AttnArgs &a, const CUt
     const Work &w = *wp;
     const int n = w.o.tile1 - w.o.tile0;
     if (n == 0) continue;
+    // The request's row of the block table, 32 pages at a time: lane l keeps page
+    // base + l, and the 32 behind them are on their way.  (A tile has 8, 4, 2 or
+    // 1 pages, or half of one, so its pages are never in two such runs.)
+    const int32_t *row = p.table + (int64_t)w.o.req * p.max_pages;
+    const int held = (w.o.kv + p.page_size - 1) >> p.page_shift;
+    auto pages_at = [&](int first) { return first + lane < held ? row[first + lane] : 0; };
+    int key = w.o.tile0 * kKeys;  // the next tile's first key
+    int base = key >> p.page_shift;
+    int here = pages_at(base), ahead = pages_at(base + 32);
     if (nq > 0 && !(ok = warp_wait(&ctl.q_empty, (nq - 1) & 1))) break;
     if (lane == 0) {
       const uint32_t bar = smem_u32(&ctl.q_full);
@@ -244,18 +253,9 @@ __device__ bool load_role(uint32_t sbase, Ctl &ctl, const AttnArgs &a, const CUt
     }
     ++nq;
     // What follows is done for every tile, and a warp's instructions take long
-    // beside two softmax warps on the same scheduler: no divisions here, no
-    // address made twice (8k-token chunk: 2.26 -> 2.23 ms).
+    // beside two softmax warps on the same scheduler: no divisions, no address
+    // made twice (8k-token chunk: 2.26 -> 2.23 ms).
     //
-    // The request's row of the block table, 32 pages at a time: lane l keeps page
-    // base + l, and the 32 behind them are on their way.  (A tile has 8, 4, 2 or
-    // 1 pages, or half of one, so its pages are never in two such runs.)
-    const int32_t *row = p.table + (int64_t)w.o.req * p.max_pages;
-    const int held = (w.o.kv + p.page_size - 1) >> p.page_shift;
-    auto pages_at = [&](int first) { return first + lane < held ? row[first + lane] : 0; };
-    int key = w.o.tile0 * kKeys;  // the next tile's first key
-    int base = key >> p.page_shift;
-    int here = pages_at(base), ahead = pages_at(base + 32);
     // boxes of the piece's last tile: pages that hold a key of the request
     const int last = (min(kKeys, w.o.kv - (w.o.tile1 - 1) * kKeys) + rows - 1) >> rs;
     const int heads = p.Hkv, head = w.o.head;
@@ -886,7 +886,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
     if (tid == 0) raise_error(a.p.err, ERR_TIMEOUT);
     return;
   }
-  if (tid == 0) {
+  if (tid == kSchedWarp * 32) {  // (the first warp has requests to look at)
     for (int i = 0; i < Ly::kStages; ++i) {
       mbar_init(smem_u32(&ctl.kv_full[i]), 1);
       mbar_init(smem_u32(&ctl.kv_empty[i]), 2);

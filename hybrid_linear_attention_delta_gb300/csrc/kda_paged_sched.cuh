@@ -103,9 +103,10 @@ struct PagedSched {
     // (both asked for at once)
     const int cu0 = tid == 0 ? p.cu[0] : 0, cuB = tid == 0 ? p.cu[p.B] : 0;
     bool bad = false;
+    PagedReq q = {0, 0, 0, 0};
     for (int i = b0; i < b1; ++i) {
       bad |= p.cu[i + 1] < p.cu[i];
-      const PagedReq q = paged_request(p, i, tokens);
+      q = paged_request(p, i, tokens);
       const int kvl = p.kv_lens[i];
       if (blockIdx.x == 0 && (kvl < 0 || (int64_t)kvl > (int64_t)p.max_pages * p.page_size))
         raise_error(p.err, ERR_BAD_LEN);
@@ -128,11 +129,15 @@ struct PagedSched {
       if (blockIdx.x == 0 && tid == 0) raise_error(p.err, ERR_BAD_CU);
       return false;
     }
-    int64_t before = inc - mine, total = 0, before_s = inc_s - mine_s, total_s = 0;
+    int64_t before = inc - mine, before_s = inc_s - mine_s;
+    int64_t total = scratch[0], total_s = scratch[W];
+    if (p.B > 32) {  // (else the first warp has them all)
+      if (warp > 0) before += total, before_s += total_s;
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
-      if (w < warp) before += scratch[w], before_s += scratch[W + w];
-      total += scratch[w], total_s += scratch[W + w];
+      for (int w = 1; w < W; ++w) {
+        if (w < warp) before += scratch[w], before_s += scratch[W + w];
+        total += scratch[w], total_s += scratch[W + w];
+      }
     }
     apart = total_s <= gridDim.x;
     if (apart) {
@@ -144,17 +149,19 @@ struct PagedSched {
     end = min(total, pos + per_cta);
     if (pos < end && before <= pos && pos < before + mine) {  // this thread's requests hold it
       int64_t at = before;
-      for (int i = b0; i < b1; ++i) {
-        const PagedReq q = paged_request(p, i, tokens);
-        const int64_t c = stride(paged_head_cost(q, tokens, p.causal)) * p.Hkv;
+      int i = b0;
+      for (; i + 1 < b1; ++i) {  // (the last one is at hand)
+        const PagedReq x = paged_request(p, i, tokens);
+        const int64_t c = stride(paged_head_cost(x, tokens, p.causal)) * p.Hkv;
         if (pos < at + c) {
-          scratch[2 * W] = i;
-          scratch[2 * W + 1] = at;
-          reinterpret_cast<PagedReq *>(scratch)[W + 1] = q;
+          q = x;
           break;
         }
         at += c;
       }
+      scratch[2 * W] = i;
+      scratch[2 * W + 1] = at;
+      reinterpret_cast<PagedReq *>(scratch)[W + 1] = q;
     }
     __syncthreads();
     b = (int32_t)scratch[2 * W];
