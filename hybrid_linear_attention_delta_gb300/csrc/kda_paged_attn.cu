@@ -797,6 +797,7 @@ __device__ bool softmax_role(Ctl &ctl, const AttnArgs &a, uint32_t tmem, int s) 
       const float f0 = l == 0.f ? 0.f : f * w0, f1 = f * w1;
       // where the rows of this lane's group go (-1: nowhere)
       const int64_t mine = parts ? part_at * D : row_offset(p, w.o, row_tok, g);
+      const bool few = __popc(__ballot_sync(0xffffffffu, live)) <= 8;
       int64_t to_row[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k)
@@ -823,7 +824,14 @@ __device__ bool softmax_role(Ctl &ctl, const AttnArgs &a, uint32_t tmem, int s) 
           for (int i = 0; i < 32; ++i) y[i] = fmaf(__uint_as_float(o[i]), f1, y[i]);
         }
         uint32_t v[16];
-        if (parts) {
+        if (parts && few) {  // (transposing takes longer than a few rows' stores)
+          if (live) {
+            float *dst = p.part + part_at * D + q * 32;
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              *reinterpret_cast<float4 *>(dst + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+          }
+        } else if (parts) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
 #pragma unroll
