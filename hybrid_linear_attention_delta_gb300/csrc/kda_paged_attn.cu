@@ -540,18 +540,22 @@ __device__ __forceinline__ void load_part(const float *src, float (&x)[N]) {
   }
 }
 
-// Joins the pieces of an item, first piece first, rows [r0, r1) of the item
-// over the calling warps: a warp takes ROWS rows and PIECES pieces of them at a
-// time, all their loads in flight (eight rows of an item cut in a few, as those
-// with many rows are; one row of an item that many SMs share).
+// Joins the pieces of an item, in a fixed order, rows [r0, r1) of the item over
+// the calling warps: a warp takes ROWS rows and PIECES pieces of them at a time,
+// all their loads in flight (eight rows and two pieces where there are many rows,
+// two and eight where there are few).  fold: not ROWS rows but one, its pieces in
+// ROWS runs of PIECES, joined at the end (no more rows than warps).
 template <int D, int ROWS, int PIECES>
 __device__ void join_rows(const PagedAttnPlan &p, const PagedPiece &o, int r0, int r1, int warp,
-                          int n_warps) {
+                          int n_warps, bool fold) {
   constexpr int N = D / 32;
   static_assert(ROWS * PIECES <= 32, "a lane per (row, piece)");
   const int lane = threadIdx.x & 31;
-  const int my_row = lane / PIECES, my_piece = lane % PIECES;  // whose weight this lane keeps
-  for (int r = r0 + warp * ROWS; r < r1; r += n_warps * ROWS) {
+  const int my_row = lane / PIECES;  // whose weight this lane keeps
+  const int step = fold ? 1 : ROWS;  // rows of a warp at a time
+  const int up = fold ? 0 : 1, on = fold ? PIECES : 0;  // row i: r + i * up, from piece i * on
+  const int my_piece = lane % PIECES + my_row * on;
+  for (int r = r0 + warp * step; r < r1; r += n_warps * step) {
     float m[ROWS], l[ROWS], acc[ROWS][N];
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
@@ -559,21 +563,21 @@ __device__ void join_rows(const PagedAttnPlan &p, const PagedPiece &o, int r0, i
 #pragma unroll
       for (int j = 0; j < N; ++j) acc[i][j] = 0.f;
     }
-    for (int k0 = 0; k0 < o.n_pieces; k0 += PIECES) {
+    for (int k0 = 0; k0 < o.n_pieces; k0 += fold ? ROWS * PIECES : PIECES) {
       float x[ROWS][PIECES][N];
 #pragma unroll
       for (int i = 0; i < ROWS; ++i)
 #pragma unroll
         for (int k = 0; k < PIECES; ++k) {
-          const int slot = paged_part_slot(o, min(k0 + k, o.n_pieces - 1));
-          load_part<N>(p.part + ((int64_t)slot * p.part_rows + min(r + i, r1 - 1)) * D + lane * N,
+          const int slot = paged_part_slot(o, min(k0 + k + i * on, o.n_pieces - 1));
+          load_part<N>(p.part + ((int64_t)slot * p.part_rows + min(r + i * up, r1 - 1)) * D + lane * N,
                        x[i][k]);
         }
       // maximum and sum of this lane's (row, piece)
       float mk = -INFINITY, lk = 0.f;
       if (my_row < ROWS && k0 + my_piece < o.n_pieces) {
         const int64_t at = (int64_t)paged_part_slot(o, k0 + my_piece) * p.part_rows +
-                           min(r + my_row, r1 - 1);
+                           min(r + my_row * up, r1 - 1);
         mk = __ldcg(&p.part_ml[at * 2]);
         lk = __ldcg(&p.part_ml[at * 2 + 1]);
       }
@@ -599,9 +603,18 @@ __device__ void join_rows(const PagedAttnPlan &p, const PagedPiece &o, int r0, i
         }
       }
     }
+    if constexpr (ROWS == 2) {
+      if (fold) {
+        const float top = fmaxf(m[0], m[1]), ref = top == -INFINITY ? 0.f : top;
+        const float w0 = exp2f(m[0] - ref), w1 = exp2f(m[1] - ref);
+        l[0] = w0 * l[0] + w1 * l[1];
+#pragma unroll
+        for (int j = 0; j < N; ++j) acc[0][j] = w0 * acc[0][j] + w1 * acc[1][j];
+      }
+    }
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
-      if (r + i >= r1) break;
+      if (i >= step || r + i >= r1) break;
       const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
 #pragma unroll
       for (int j = 0; j < N; ++j) acc[i][j] *= inv;
@@ -614,8 +627,8 @@ __device__ void join_rows(const PagedAttnPlan &p, const PagedPiece &o, int r0, i
 template <int D>
 __device__ void join_pieces(const PagedAttnPlan &p, const PagedPiece &o, int r0, int r1, int warp,
                             int n_warps) {
-  if (o.n_pieces <= 4 && r1 - r0 > 16) join_rows<D, 8, 2>(p, o, r0, r1, warp, n_warps);
-  else join_rows<D, 1, 16>(p, o, r0, r1, warp, n_warps);
+  if (r1 - r0 > 16) join_rows<D, 8, 2>(p, o, r0, r1, warp, n_warps, false);
+  else join_rows<D, 2, 8>(p, o, r0, r1, warp, n_warps, r1 - r0 <= n_warps);
 }
 
 template <int D>
