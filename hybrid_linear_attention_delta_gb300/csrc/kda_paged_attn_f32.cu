@@ -5,24 +5,28 @@
 // One pass over the keys with a running maximum m and sum l per row: for each
 // tile of keys, P = exp(S - m'), l = l exp(m - m') + sum P, O = O exp(m - m') +
 // P V.  A tile's scores and probabilities stay in registers and shared memory.
-// Thread (ty, tx) of the 16 x 16 holds rows ty * R .. + R - 1 and keys tx + 16 j of
-// the scores, and the same rows with D / 16 channels of the output.  The
-// next tile is copied to shared memory while one is worked on.  Bound by the
-// fp32 pipes and the shared-memory reads that feed them (8 requests of up to 301
-// tokens over up to 2800 keys, 8 / 2 heads of 64 channels: 121 us, 28 TFLOP/s).
+// Thread (ty, tx) holds rows ty + TY i and keys tx + 16 j of the scores, and the
+// same rows with D / 16 channels of the output: eight rows a thread with 64
+// channels, where two CTAs share an SM (four rows and twice the threads read shared
+// memory half as often again: 8 x 1000 tokens over 1089 to 3208 keys, 8 / 2 heads,
+// 0.89 against 0.82 ms), four with 128, whose tiles leave room for one.  The next
+// tile is copied to shared memory while one is worked on.  Bound by the fp32 pipes
+// and the shared-memory reads that feed them, and where items are short by their
+// start and their joining (8 requests of up to 301 tokens over up to 2800 keys: 122
+// us, 28 TFLOP/s; 1000 tokens each: 39 TFLOP/s).
 #include "kda_paged_sched.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kKeys = 64;  // keys of a tile
 
-template <int D, int R>
+// R: rows of a thread, TY: threads along the rows
+template <int D, int R, int TY>
 struct Smem {
-  static constexpr int kRows = 16 * R;
+  static constexpr int kRows = TY * R, kThreads = TY * 16;
   static constexpr int kLd = D + 4;      // floats of a Q / K row
-  static constexpr int kLdP = kKeys + 4;
+  static constexpr int kLdP = kKeys + 16;  // two rows side by side: other banks
   float q[kRows * kLd];
   float k[2][kKeys * kLd];  // a tile and the one on its way
   float v[2][kKeys * D];
@@ -51,10 +55,11 @@ __device__ __forceinline__ int64_t row_offset(const PagedAttnPlan &p, const Page
   return ((int64_t)(o.tok0 + t) * p.Hq + o.head * p.G + (r - t * p.G)) * p.d;
 }
 
-template <int D, int R>
-__global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) attn_kernel(PagedAttnPlan p) {
+template <int D, int R, int TY>
+__global__ void __launch_bounds__(TY * 16, D == 64 ? 2 : 1) attn_kernel(PagedAttnPlan p) {
   extern __shared__ __align__(16) unsigned char raw[];
-  using S = Smem<D, R>;
+  using S = Smem<D, R, TY>;
+  constexpr int kThreads = S::kThreads;
   S &sm = *reinterpret_cast<S *>(raw);
   constexpr int NC = D / 16;  // output channels of a thread, in groups of four
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
@@ -80,7 +85,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) attn_kernel(PagedAt
     float m[R], l[R], acc[R][NC];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      const int r = ty * R + i;
+      const int r = ty + TY * i;
       lim[i] = r < rows ? min(o.kv, p.causal ? o.seen0 + r / p.G : o.kv) : 0;
       m[i] = -INFINITY, l[i] = 0.f;
 #pragma unroll
@@ -133,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) attn_kernel(PagedAt
         float4 a[R], b[4];
 #pragma unroll
         for (int i = 0; i < R; ++i)
-          a[i] = *reinterpret_cast<const float4 *>(&sm.q[(ty * R + i) * S::kLd + e]);
+          a[i] = *reinterpret_cast<const float4 *>(&sm.q[(ty + TY * i) * S::kLd + e]);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           b[j] = *reinterpret_cast<const float4 *>(&sk[(tx + 16 * j) * S::kLd + e]);
@@ -165,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) attn_kernel(PagedAt
         for (int j = 0; j < 4; ++j) {
           const float e = exp2f(s[i][j] - ref);
           l[i] += e;  // this thread's keys only; joined at the end
-          sm.p[(ty * R + i) * S::kLdP + tx + 16 * j] = e;
+          sm.p[(ty + TY * i) * S::kLdP + tx + 16 * j] = e;
         }
 #pragma unroll
         for (int j = 0; j < NC; ++j) acc[i][j] *= keep;
@@ -176,19 +181,18 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) attn_kernel(PagedAt
         float4 w[R];
 #pragma unroll
         for (int i = 0; i < R; ++i)
-          w[i] = *reinterpret_cast<const float4 *>(&sm.p[(ty * R + i) * S::kLdP + k]);
+          w[i] = *reinterpret_cast<const float4 *>(&sm.p[(ty + TY * i) * S::kLdP + k]);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
           for (int j = 0; j < NC; j += 4) {
-            const float4 x = *reinterpret_cast<const float4 *>(&sv[(k + kk) * D + j * 16 + tx * 4]);
+            const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(&sv[(k + kk) * D + j * 16 + tx * 4]);
 #pragma unroll
             for (int i = 0; i < R; ++i) {
               const float f = kk == 0 ? w[i].x : kk == 1 ? w[i].y : kk == 2 ? w[i].z : w[i].w;
-              acc[i][j] = fmaf(f, x.x, acc[i][j]);
-              acc[i][j + 1] = fmaf(f, x.y, acc[i][j + 1]);
-              acc[i][j + 2] = fmaf(f, x.z, acc[i][j + 2]);
-              acc[i][j + 3] = fmaf(f, x.w, acc[i][j + 3]);
+              const uint64_t ff = pair(f, f);
+              unpair(fma2(ff, x.x, pair(acc[i][j], acc[i][j + 1])), acc[i][j], acc[i][j + 1]);
+              unpair(fma2(ff, x.y, pair(acc[i][j + 2], acc[i][j + 3])), acc[i][j + 2], acc[i][j + 3]);
             }
           }
       }
@@ -203,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) attn_kernel(PagedAt
       const int64_t slot = paged_part_slot(o, o.index);
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        const int r = ty * R + i;
+        const int r = ty + TY * i;
         if (r >= rows) continue;
         const int64_t at = slot * p.part_rows + r;
         if (tx == 0) p.part_ml[at * 2] = m[i], p.part_ml[at * 2 + 1] = l[i];
@@ -225,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) attn_kernel(PagedAt
       // the last piece to arrive joins them all, first piece first
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        const int r = ty * R + i;
+        const int r = ty + TY * i;
         m[i] = -INFINITY, l[i] = 0.f;
 #pragma unroll
         for (int j = 0; j < NC; ++j) acc[i][j] = 0.f;
@@ -250,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) attn_kernel(PagedAt
     }
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      const int r = ty * R + i;
+      const int r = ty + TY * i;
       if (r >= rows) continue;
       const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];  // a row without keys: zeros
       float *out = static_cast<float *>(p.out) + row_offset(p, o, r);
@@ -262,22 +266,23 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) attn_kernel(PagedAt
   }
 }
 
-template <int D, int R>
+template <int D, int R, int TY>
 cudaError_t launch_r(const PagedAttnPlan &p) {
-  const void *f = reinterpret_cast<const void *>(attn_kernel<D, R>);
-  const cudaError_t e = set_smem_limit_once(f, sizeof(Smem<D, R>));
+  using S = Smem<D, R, TY>;
+  const void *f = reinterpret_cast<const void *>(attn_kernel<D, R, TY>);
+  const cudaError_t e = set_smem_limit_once(f, sizeof(S));
   if (e != cudaSuccess) return e;
-  static_assert(16 * R <= kPagedF32Rows, "rows of a partial result");
+  static_assert(S::kRows <= kPagedF32Rows, "rows of a partial result");
   // two CTAs fit an SM with 64 channels, one with 128
-  constexpr int kCtas = sizeof(Smem<D, R>) <= 113 * 1024 ? kPagedF32Ctas : kPagedMaxCtas;
-  attn_kernel<D, R><<<kCtas, kThreads, sizeof(Smem<D, R>), p.stream>>>(p);
+  constexpr int kCtas = sizeof(S) <= 113 * 1024 ? kPagedF32Ctas : kPagedMaxCtas;
+  attn_kernel<D, R, TY><<<kCtas, S::kThreads, sizeof(S), p.stream>>>(p);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_paged_attn_f32(const PagedAttnPlan &p) {
-  return p.d == 128 ? launch_r<128, 4>(p) : launch_r<64, 4>(p);
+  return p.d == 128 ? launch_r<128, 4, 16>(p) : launch_r<64, 8, 8>(p);
 }
 
 }  // namespace kda
