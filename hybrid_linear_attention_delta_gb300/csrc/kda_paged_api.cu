@@ -179,10 +179,10 @@ kda_status kda_paged_attn(const void *q, const void *k_pages, const void *v_page
   p.part_ml = reinterpret_cast<float *>(ws + lay.ml_off);
   p.part_rows = kda::paged_part_rows(a->T_total, G, a->dtype);
   // Where requests bring a tile of rows and more, joining the pieces of an item
-  // costs as much as six of its key tiles; with few rows it costs little.  (200
-  // tokens over 500 keys, 32/8 heads: 42 us at 384, 47 us at 768, 55 us at 1152;
-  // 100 tokens over 8000 keys, 8/1 heads: 97, 71 and 74 us; 300 over 2000, 16/2
-  // heads: 66, 49 and 54 us.)
+  // costs as much as six of its key tiles; with few rows it costs little.  (With
+  // 512, 768 and 1024: 200 tokens over 500 keys, 32/8 heads, 35.1, 34.4 and 39.0 us;
+  // 1000 over 10 47, 40.6 and 43.5; 300 over 2000, 16/2 heads, 40.6, 37.9 and 41.4;
+  // 100 over 8000, 8/1 heads, 57, 53 and 45.  One token: the same from 256 to 384.)
   p.min_stretch = (int64_t)a->T_total * G >= 128ll * a->B ? 768 : 384;
   p.stream = static_cast<cudaStream_t>(a->stream);
   return launch(a->stream, a->ev_begin, a->ev_end, [&] {
