@@ -27,11 +27,11 @@
 //
 // Bound and measured (GB300): a chunk of 8192 tokens over 32768 keys, 32 / 8 heads
 // of 128 channels, by the tensor cores and the chain of a tile (scores, softmax,
-// outputs): 2.27 ms, 1.70 PFLOP/s (cuBLAS: 1.87), 2.54 ms in a loop at the power
+// outputs): 2.25 ms, 1.71 PFLOP/s (cuBLAS: 1.87), 2.5 ms in a loop at the power
 // limit.  Decode of 256 requests over 511 to 8191 keys: HBM, 0.72 ms, 6.7 TB/s
-// (99% of a copy); 64 x 8 tokens over 1000 to 32760 keys, 32 / 4 heads: 0.347 ms,
+// (99% of a copy); 64 x 8 tokens over 1000 to 32760 keys, 32 / 4 heads: 0.343 ms,
 // 6.4 TB/s.  64 channels: the softmax, 1.0 PFLOP/s.  One token over 777 keys:
-// latency, 14.8 us, of which 6 are spent before the first scores.
+// latency, 12.3 us, of which 5 are spent before the first scores.
 #include <cuda.h>
 
 #include <cstring>
