@@ -111,6 +111,15 @@ def test_long_context_is_split_and_joined(dtype, Hq, Hkv, d):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G,new", [(3, 1), (4, 1), (5, 1), (8, 2), (17, 1), (64, 2), (7, 30)])
+def test_pieces_are_joined_whatever_the_rows(dtype, d, G, new):
+    """One item over some twenty CTAs: no more rows than a warp each, a few, a
+    tile of them, two tiles; and two heads, so that pieces of both are about."""
+    _check(AttnCase([new, 1], [9001, 130], Hq=2 * G, Hkv=2, d=d, page=64, dtype=dtype, seed=G))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_large_scores(dtype):
     """Scores that differ by hundreds: the running maximum moves often and a few
     keys carry all the weight.  (A score of 300 is summed to 300 half steps of
