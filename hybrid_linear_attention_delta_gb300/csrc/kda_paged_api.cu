@@ -163,6 +163,7 @@ kda_status kda_paged_attn(const void *q, const void *k_pages, const void *v_page
   if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(out, 16) ||
       !aligned(block_table, 4) || !aligned(cu_seqlens, 4) || !aligned(kv_lens, 4))
     return KDA_ERR_INVALID_ARG;
+  if (shared({out, k_pages, v_pages}, 1)) return KDA_ERR_INVALID_ARG;
   const int G = a->Hq / a->Hkv;
   const kda::PagedWorkspace lay(a->T_total, G, a->d);
   char *ws = static_cast<char *>(a->workspace);

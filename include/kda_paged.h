@@ -157,7 +157,7 @@ kda_status kda_paged_append(const void *qkv, const int32_t *positions, const int
  * result, whatever they hold; a key that the mask hides has weight zero, and
  * its value must be finite where other rows of the request see it.
  *
- * q, out     [T_total][Hq][d] dtype
+ * q, out     [T_total][Hq][d] dtype; out may be q
  * k_pages, v_pages [n_pages][page_size][Hkv][d] dtype
  * block_table [B][max_pages] int32
  * cu_seqlens [B+1] int32     cu[0] = 0, non-decreasing, cu[B] <= T_total

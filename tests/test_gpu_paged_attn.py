@@ -250,6 +250,21 @@ def test_two_calls_at_once():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("G,d", [(8, 128), (3, 64)])
+def test_out_over_q(dtype, G, d):
+    """The outputs take the queries' place: whole items, two tiles of rows, and
+    items whose pieces lie on many CTAs."""
+    case = AttnCase([1, 90, 0, 301, 2], [9000, 700, 5, 301, 4000], Hq=2 * G, Hkv=2, d=d, page=32,
+                    dtype=dtype, seed=G)
+    apart, _ = _run(case)
+    t = case.cuda()
+    ws = kda.paged_workspace_for(t["q"].shape[0], 2 * G, 2, d)
+    kda.kda_paged_attn(t["q"], t["k"], t["v"], t["table"], t["cu"], t["kv"], t["q"], workspace=ws)
+    assert kda.kda_device_status(ws) == (kda.KDA_OK, 0)
+    assert torch.equal(t["q"], apart)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_shared_pages(dtype):
     """Requests whose rows name the same pages (a shared prompt), and one row
     that names a page twice."""

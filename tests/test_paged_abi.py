@@ -159,6 +159,7 @@ def test_outputs_are_arrays_of_their_own(lib):
     # block_table, free_ring, held_out, ring_out, kv_lens, positions, slot_map
     pairs(lambda p: lib.kda_paged_plan(*p, ctypes.byref(a)), 11, (2, 4, 6, 7, 8, 9, 10),
           (0, 1, 3, 5))
+    pairs(lambda p: _attn(lib, a, p), 7, (6,), (1, 2))
     f = kda.KdaAppendArgs(None, None, FAKE, 10, 32, 0, 1e-6)
     pairs(lambda p: lib.kda_paged_append(*p, ctypes.byref(f), ctypes.byref(a)), 6, (3, 4, 5), (0,))
     v = kda.KdaVerifyArgs(2, 3, 100, kda.KDA_F32, None, WS, 256)
