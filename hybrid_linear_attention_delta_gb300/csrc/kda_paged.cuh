@@ -59,6 +59,7 @@ struct PagedAttnPlan {
   float *part_ml;      // [CTAs][2][part_rows][2] their maxima and sums
   int32_t part_rows;
   int32_t min_stretch;  // keys of a CTA's stretch at least
+  int32_t item_cost;    // fixed cost of an item, in keys
   cudaStream_t stream;
 };
 

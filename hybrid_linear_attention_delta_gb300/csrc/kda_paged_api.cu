@@ -179,12 +179,17 @@ kda_status kda_paged_attn(const void *q, const void *k_pages, const void *v_page
   p.part = reinterpret_cast<float *>(ws + lay.part_off);
   p.part_ml = reinterpret_cast<float *>(ws + lay.ml_off);
   p.part_rows = kda::paged_part_rows(a->T_total, G, a->dtype);
-  // Where requests bring a tile of rows and more, joining the pieces of an item
-  // costs as much as six of its key tiles; with few rows it costs little.  (With
-  // 512, 768 and 1024: 200 tokens over 500 keys, 32/8 heads, 35.1, 34.4 and 39.0 us;
-  // 1000 over 10 47, 40.6 and 43.5; 300 over 2000, 16/2 heads, 40.6, 37.9 and 41.4;
-  // 100 over 8000, 8/1 heads, 57, 53 and 45.  One token: the same from 256 to 384.)
-  p.min_stretch = (int64_t)a->T_total * G >= 128ll * a->B ? 768 : 384;
+  // What an item's start and end cost, and the shortest stretch worth a join, in
+  // keys.  Where requests bring a tile of rows and more, both are longer.  (bf16,
+  // item cost 128, 192, 256, 320, 384: mixed batch of 24, 64 channels, 910, 875,
+  // 854, 855, 858 us; 128 channels 1244, 1192, 1168, 1171, 1154; 100 decodes of up
+  // to 1000 keys with 64, 128, 192, 256: 101, 90, 82, 78 us.  Shortest stretch 768,
+  // 896, 1024: a prompt of 1000 tokens, 32/8 heads, 46.7, 37.1, 38.2 us; 200 tokens
+  // over 500 keys 31.9, 32.8, 33.9; one token: the same from 256 to 384.  fp32, item
+  // cost 32, 64, 128, 256: 8 requests of up to 301 tokens 148, 134, 129, 140 us.)
+  const bool wide = (int64_t)a->T_total * G >= 128ll * a->B, bf16 = a->dtype == KDA_BF16;
+  p.min_stretch = !wide ? 384 : bf16 ? 896 : 768;
+  p.item_cost = !bf16 ? 128 : wide ? 320 : 256;
   p.stream = static_cast<cudaStream_t>(a->stream);
   return launch(a->stream, a->ev_begin, a->ev_end, [&] {
     return a->dtype == KDA_BF16 ? kda::launch_paged_attn_bf16(p) : kda::launch_paged_attn_f32(p);

@@ -2,7 +2,7 @@
 //
 // An item is (request, key/value head, run of query tokens) with all query
 // heads of the group: its rows share every key.  It costs the keys it sees
-// plus kItemCost keys for its start and end.  All items in a row (request,
+// plus item_cost keys for its start and end.  All items in a row (request,
 // head, run) make one long line of cost; CTA c of the grid takes the stretch
 // [c * per_cta, (c + 1) * per_cta).  A stretch cuts at most its first and its
 // last item; cuts fall on key tiles.  Long contexts of few rows are so spread
@@ -12,7 +12,8 @@
 //
 // A batch of few short items (decodes) leaves most of the grid idle at the
 // shortest stretch.  Then every item starts a stretch of its own, so that no
-// CTA works on the end of one item and the start of another.
+// CTA works on the end of one item and the start of another; the fixed cost
+// counts as less there (kApartCost), as it is nobody else's time.
 //
 // Every CTA finds its stretch itself from cu_seqlens and kv_lens (a block scan
 // of one number per request), so no plan is stored and nothing is cleared.
@@ -22,8 +23,8 @@
 
 namespace kda {
 
-// Fixed cost of an item, in keys.
-constexpr int kItemCost = 128;
+// (One token over 777 keys: 12.2 us, with an item cost of 256 there too 12.7.)
+constexpr int kApartCost = 128;
 
 // A request as the line sees it; n = runs = 0 for one that is skipped.
 struct alignas(8) PagedReq {
@@ -47,14 +48,15 @@ struct PagedPiece {
 
 // Cost of the request's first i runs of one head.
 __device__ __forceinline__ int64_t paged_prefix(const PagedReq &r, int64_t i, int tokens,
-                                                bool causal) {
-  if (!causal || r.kv < r.n) return i * (r.kv + kItemCost);
-  int64_t c = i * (r.kv - r.n + kItemCost) + (int64_t)tokens * (i * (i + 1) / 2);
+                                                bool causal, int item_cost) {
+  if (!causal || r.kv < r.n) return i * (r.kv + item_cost);
+  int64_t c = i * (r.kv - r.n + item_cost) + (int64_t)tokens * (i * (i + 1) / 2);
   if (i == r.runs) c += r.n - (int64_t)r.runs * tokens;  // the last run is shorter
   return c;
 }
-__device__ __forceinline__ int64_t paged_head_cost(const PagedReq &r, int tokens, bool causal) {
-  return paged_prefix(r, r.runs, tokens, causal);
+__device__ __forceinline__ int64_t paged_head_cost(const PagedReq &r, int tokens, bool causal,
+                                                   int item_cost) {
+  return paged_prefix(r, r.runs, tokens, causal, item_cost);
 }
 
 __device__ __forceinline__ PagedReq paged_request(const PagedAttnPlan &p, int b, int tokens) {
@@ -75,7 +77,7 @@ __device__ __forceinline__ int64_t paged_div(int64_t a, int64_t b) {
 // TILE: keys of a tile; tokens: query tokens of an item at most.
 template <int TILE>
 struct PagedSched {
-  int32_t tokens;
+  int32_t tokens, item_cost;
   bool apart;              // every item starts a stretch
   int64_t pos, end, base;  // place on the line, end of the stretch, start of request b
   int64_t per_cta;
@@ -94,11 +96,13 @@ struct PagedSched {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int W = THREADS / 32;
     tokens = tokens_per_item;
+    item_cost = p.item_cost;
     const int run = (p.B + THREADS - 1) / THREADS;
     const int b0 = min(p.B, tid * run), b1 = min(p.B, b0 + run);
     // a cut costs a round trip of partials (see min_stretch); two tiles and an
     // item's fixed cost at least, so that a stretch inside an item has a tile
-    per_cta = max(p.min_stretch, 2 * TILE + kItemCost);
+    const int less = max(0, item_cost - kApartCost);
+    per_cta = max(p.min_stretch, 2 * TILE + item_cost - less);
     int64_t mine = 0, mine_s = 0;  // this thread's requests: cost, and stretches of per_cta
     // (both asked for at once)
     const int cu0 = tid == 0 ? p.cu[0] : 0, cuB = tid == 0 ? p.cu[p.B] : 0;
@@ -110,10 +114,10 @@ struct PagedSched {
       const int kvl = p.kv_lens[i];
       if (blockIdx.x == 0 && (kvl < 0 || (int64_t)kvl > (int64_t)p.max_pages * p.page_size))
         raise_error(p.err, ERR_BAD_LEN);
-      const int64_t c = paged_head_cost(q, tokens, p.causal);
+      const int64_t c = paged_head_cost(q, tokens, p.causal, item_cost);
       mine += c * p.Hkv;
       mine_s += q.n > tokens ? 1ll << 32  // several items: not apart
-                             : paged_div(c + per_cta - 1, per_cta) * p.Hkv;
+                             : paged_div(c - less + per_cta - 1, per_cta) * p.Hkv;
     }
     bad |= cu0 != 0 || cuB > p.T;
     int64_t inc = mine, inc_s = mine_s;
@@ -141,9 +145,11 @@ struct PagedSched {
     }
     apart = total_s <= gridDim.x;
     if (apart) {
+      item_cost -= less;
       before = before_s * per_cta, mine = mine_s * per_cta, total = total_s * per_cta;
     } else {
-      per_cta = max(per_cta, paged_div(total + gridDim.x - 1, gridDim.x));
+      per_cta = max(max(per_cta, (int64_t)2 * TILE + item_cost),
+                    paged_div(total + gridDim.x - 1, gridDim.x));
     }
     pos = blockIdx.x * per_cta;
     end = min(total, pos + per_cta);
@@ -152,7 +158,7 @@ struct PagedSched {
       int i = b0;
       for (; i + 1 < b1; ++i) {  // (the last one is at hand)
         const PagedReq x = paged_request(p, i, tokens);
-        const int64_t c = stride(paged_head_cost(x, tokens, p.causal)) * p.Hkv;
+        const int64_t c = stride(paged_head_cost(x, tokens, p.causal, item_cost)) * p.Hkv;
         if (pos < at + c) {
           q = x;
           break;
@@ -174,11 +180,12 @@ struct PagedSched {
   // The tile that a cut at cost x of the item falls on.  Items of a request
   // that brings more tokens than it has keys (their cost does not follow the
   // keys they see) are left whole.
-  static __device__ __forceinline__ int cut(int64_t x, int64_t cost, int tiles, bool whole) {
+  static __device__ __forceinline__ int cut(int64_t x, int64_t cost, int tiles, bool whole,
+                                            int item_cost) {
     if (x <= 0) return 0;
     if (x >= cost) return tiles;
     if (whole) return 0;
-    const int64_t k = x - kItemCost + TILE / 2;
+    const int64_t k = x - item_cost + TILE / 2;
     return k <= 0 ? 0 : (int)min((int64_t)tiles, k / TILE);
   }
 
@@ -187,7 +194,7 @@ struct PagedSched {
     PagedPiece o;
     o.n = 0;
     while (pos < end) {
-      const int64_t head_cost = stride(paged_head_cost(r, tokens, p.causal));
+      const int64_t head_cost = stride(paged_head_cost(r, tokens, p.causal, item_cost));
       if (pos >= base + head_cost * p.Hkv) {  // on to the next request with work
         base += head_cost * p.Hkv;
         if (++b >= p.B) {
@@ -202,10 +209,10 @@ struct PagedSched {
       int lo = 0, hi = r.runs - 1;  // largest run that starts at or before pos
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (head_base + paged_prefix(r, mid, tokens, p.causal) <= pos) lo = mid; else hi = mid - 1;
+        if (head_base + paged_prefix(r, mid, tokens, p.causal, item_cost) <= pos) lo = mid; else hi = mid - 1;
       }
-      const int64_t start = head_base + paged_prefix(r, lo, tokens, p.causal);
-      const int64_t cost = head_base + paged_prefix(r, lo + 1, tokens, p.causal) - start;
+      const int64_t start = head_base + paged_prefix(r, lo, tokens, p.causal, item_cost);
+      const int64_t cost = head_base + paged_prefix(r, lo + 1, tokens, p.causal, item_cost) - start;
       const int64_t stop = min(end, start + cost);
       o.n = min(tokens, r.n - lo * tokens);
       o.tok0 = r.tok0 + lo * tokens;
@@ -217,8 +224,8 @@ struct PagedSched {
       const int tiles = (keys + TILE - 1) / TILE;
       const bool whole = p.causal && r.kv < r.n;
       const bool starts = pos == start;
-      o.tile0 = cut(pos - start, cost, tiles, whole);
-      o.tile1 = cut(stop - start, cost, tiles, whole);
+      o.tile0 = cut(pos - start, cost, tiles, whole, item_cost);
+      o.tile1 = cut(stop - start, cost, tiles, whole, item_cost);
       o.n_pieces = o.index = o.first_cta = o.first_slot = 0;
       pos = apart ? end : stop;
       const int64_t cta = blockIdx.x;
@@ -228,8 +235,8 @@ struct PagedSched {
         // an item without keys belongs to the CTA it starts in
         if (tiles == 0 ? !starts : o.tile0 == o.tile1) continue;
         // only the first and the last stretch can be left without a tile
-        const bool skip0 = cut((c0 + 1) * per_cta - start, cost, tiles, whole) == 0;
-        const bool skip1 = cut(c1 * per_cta - start, cost, tiles, whole) == tiles;
+        const bool skip0 = cut((c0 + 1) * per_cta - start, cost, tiles, whole, item_cost) == 0;
+        const bool skip1 = cut(c1 * per_cta - start, cost, tiles, whole, item_cost) == tiles;
         const int n = (int)(c1 - c0) + 1 - skip0 - skip1;
         if (tiles > 0 && !whole && n > 1) {
           o.n_pieces = n;
