@@ -55,14 +55,213 @@ __device__ __forceinline__ int64_t row_offset(const PagedAttnPlan &p, const Page
   return ((int64_t)(o.tok0 + t) * p.Hq + o.head * p.G + (r - t * p.G)) * p.d;
 }
 
+// A piece, RA rows a thread (rows ty + TY i of the item, i < RA).
+template <int D, int R, int TY, int RA>
+__device__ __forceinline__ void run_piece(const PagedAttnPlan &p, Smem<D, R, TY> &sm,
+                                          const PagedPiece &o, float c) {
+  using S = Smem<D, R, TY>;
+  constexpr int kThreads = S::kThreads, kRows = TY * RA;
+  constexpr int NC = D / 16;  // output channels of a thread, in groups of four
+  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+  const int rows = o.n * p.G;
+  const float *q = static_cast<const float *>(p.q);
+  for (int i = tid; i < kRows * (D / 4); i += kThreads) {
+    const int r = i / (D / 4), e = (i % (D / 4)) * 4;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < rows) x = *reinterpret_cast<const float4 *>(q + row_offset(p, o, r) + e);
+    *reinterpret_cast<float4 *>(&sm.q[r * S::kLd + e]) = x;
+  }
+  int lim[RA];  // keys that each row sees
+  float m[RA], l[RA], acc[RA][NC];
+#pragma unroll
+  for (int i = 0; i < RA; ++i) {
+    const int r = ty + TY * i;
+    lim[i] = r < rows ? min(o.kv, p.causal ? o.seen0 + r / p.G : o.kv) : 0;
+    m[i] = -INFINITY, l[i] = 0.f;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) acc[i][j] = 0.f;
+  }
+
+  // keys and values of a tile into buffer `to`; slots behind the request's
+  // last key and pages that are none become zeros
+  auto fetch = [&](int tile, int to) {
+    for (int i = tid; i < kKeys * (D / 4); i += kThreads) {
+      const int k = i / (D / 4), e = (i % (D / 4)) * 4;
+      const int key = tile * kKeys + k;
+      int page = -1;
+      if (key < o.kv) {
+        page = p.table[(int64_t)o.req * p.max_pages + (key >> p.page_shift)];
+        if (page < 0 || page >= p.n_pages) {
+          raise_error(p.err, ERR_BAD_PAGE);
+          page = -1;
+        }
+      }
+      const int64_t slot = ((int64_t)max(page, 0) << p.page_shift) + (key & (p.page_size - 1));
+      const int64_t at = page < 0 ? 0 : (slot * p.Hkv + o.head) * D + e;
+      copy16(&sm.k[to][k * S::kLd + e], static_cast<const float *>(p.k) + at, page >= 0);
+      copy16(&sm.v[to][k * D + e], static_cast<const float *>(p.v) + at, page >= 0);
+    }
+    copies_commit();
+  };
+  if (o.tile0 < o.tile1) fetch(o.tile0, 0);
+
+  for (int tile = o.tile0; tile < o.tile1; ++tile) {
+    const int key0 = tile * kKeys, buf = (tile - o.tile0) & 1;
+    const float *sk = sm.k[buf], *sv = sm.v[buf];
+    // the tile before has been read by all: its buffer takes the next one
+    __syncthreads();
+    if (tile + 1 < o.tile1) {
+      fetch(tile + 1, buf ^ 1);
+      copies_wait<1>();
+    } else {
+      copies_wait<0>();
+    }
+    __syncthreads();
+
+    float s[RA][4];
+#pragma unroll
+    for (int i = 0; i < RA; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 4
+    for (int e = 0; e < D; e += 4) {
+      float4 a[RA], b[4];
+#pragma unroll
+      for (int i = 0; i < RA; ++i)
+        a[i] = *reinterpret_cast<const float4 *>(&sm.q[(ty + TY * i) * S::kLd + e]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        b[j] = *reinterpret_cast<const float4 *>(&sk[(tx + 16 * j) * S::kLd + e]);
+#pragma unroll
+      for (int i = 0; i < RA; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s[i][j] = fmaf(a[i].x, b[j].x, s[i][j]);
+          s[i][j] = fmaf(a[i].y, b[j].y, s[i][j]);
+          s[i][j] = fmaf(a[i].z, b[j].z, s[i][j]);
+          s[i][j] = fmaf(a[i].w, b[j].w, s[i][j]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < RA; ++i) {
+      float top = m[i];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[i][j] = key0 + tx + 16 * j < lim[i] ? s[i][j] * c : -INFINITY;
+        top = fmaxf(top, s[i][j]);
+      }
+#pragma unroll
+      for (int x = 8; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+      const float ref = top == -INFINITY ? 0.f : top;  // a row that has seen no key yet
+      const float keep = exp2f(m[i] - ref);
+      m[i] = top;
+      l[i] *= keep;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float e = exp2f(s[i][j] - ref);
+        l[i] += e;  // this thread's keys only; joined at the end
+        sm.p[(ty + TY * i) * S::kLdP + tx + 16 * j] = e;
+      }
+#pragma unroll
+      for (int j = 0; j < NC; ++j) acc[i][j] *= keep;
+    }
+    __syncwarp();  // a row's sixteen threads are in one warp
+#pragma unroll 4
+    for (int k = 0; k < kKeys; k += 4) {
+      float4 w[RA];
+#pragma unroll
+      for (int i = 0; i < RA; ++i)
+        w[i] = *reinterpret_cast<const float4 *>(&sm.p[(ty + TY * i) * S::kLdP + k]);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+        for (int j = 0; j < NC; j += 4) {
+          const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(&sv[(k + kk) * D + j * 16 + tx * 4]);
+#pragma unroll
+          for (int i = 0; i < RA; ++i) {
+            const float f = kk == 0 ? w[i].x : kk == 1 ? w[i].y : kk == 2 ? w[i].z : w[i].w;
+            const uint64_t ff = pair(f, f);
+            unpair(fma2(ff, x.x, pair(acc[i][j], acc[i][j + 1])), acc[i][j], acc[i][j + 1]);
+            unpair(fma2(ff, x.y, pair(acc[i][j + 2], acc[i][j + 3])), acc[i][j + 2], acc[i][j + 3]);
+          }
+        }
+    }
+  }
+
+#pragma unroll
+  for (int i = 0; i < RA; ++i)
+#pragma unroll
+    for (int x = 8; x > 0; x >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
+
+  if (o.n_pieces > 0) {
+    const int64_t slot = paged_part_slot(o, o.index);
+#pragma unroll
+    for (int i = 0; i < RA; ++i) {
+      const int r = ty + TY * i;
+      if (r >= rows) continue;
+      const int64_t at = slot * p.part_rows + r;
+      if (tx == 0) p.part_ml[at * 2] = m[i], p.part_ml[at * 2 + 1] = l[i];
+#pragma unroll
+      for (int j = 0; j < NC; j += 4)
+        *reinterpret_cast<float4 *>(&p.part[at * D + j * 16 + tx * 4]) =
+            make_float4(acc[i][j], acc[i][j + 1], acc[i][j + 2], acc[i][j + 3]);
+    }
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) {
+      uint32_t *count = p.arrivals + o.first_cta * 2;
+      sm.last = atomicAdd(count, 1u) == (uint32_t)o.n_pieces - 1;
+      if (sm.last) *count = 0;  // as it was found
+      __threadfence();
+    }
+    __syncthreads();
+    if (!sm.last) return;
+    // the last piece to arrive joins them all, first piece first
+#pragma unroll
+    for (int i = 0; i < RA; ++i) {
+      const int r = ty + TY * i;
+      m[i] = -INFINITY, l[i] = 0.f;
+#pragma unroll
+      for (int j = 0; j < NC; ++j) acc[i][j] = 0.f;
+      if (r >= rows) continue;
+      for (int k = 0; k < o.n_pieces; ++k)
+        m[i] = fmaxf(m[i], __ldcg(&p.part_ml[((int64_t)paged_part_slot(o, k) * p.part_rows + r) * 2]));
+      const float ref = m[i] == -INFINITY ? 0.f : m[i];
+      for (int k = 0; k < o.n_pieces; ++k) {
+        const int64_t at = (int64_t)paged_part_slot(o, k) * p.part_rows + r;
+        const float w = exp2f(__ldcg(&p.part_ml[at * 2]) - ref);
+        l[i] = fmaf(w, __ldcg(&p.part_ml[at * 2 + 1]), l[i]);
+#pragma unroll
+        for (int j = 0; j < NC; j += 4) {
+          const float4 x = __ldcg(reinterpret_cast<const float4 *>(&p.part[at * D + j * 16 + tx * 4]));
+          acc[i][j] = fmaf(w, x.x, acc[i][j]);
+          acc[i][j + 1] = fmaf(w, x.y, acc[i][j + 1]);
+          acc[i][j + 2] = fmaf(w, x.z, acc[i][j + 2]);
+          acc[i][j + 3] = fmaf(w, x.w, acc[i][j + 3]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < RA; ++i) {
+    const int r = ty + TY * i;
+    if (r >= rows) continue;
+    const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];  // a row without keys: zeros
+    float *out = static_cast<float *>(p.out) + row_offset(p, o, r);
+#pragma unroll
+    for (int j = 0; j < NC; j += 4)
+      *reinterpret_cast<float4 *>(out + j * 16 + tx * 4) = make_float4(
+          acc[i][j] * inv, acc[i][j + 1] * inv, acc[i][j + 2] * inv, acc[i][j + 3] * inv);
+  }
+}
+
 template <int D, int R, int TY>
 __global__ void __launch_bounds__(TY * 16, D == 64 ? 2 : 1) attn_kernel(PagedAttnPlan p) {
   extern __shared__ __align__(16) unsigned char raw[];
   using S = Smem<D, R, TY>;
   constexpr int kThreads = S::kThreads;
   S &sm = *reinterpret_cast<S *>(raw);
-  constexpr int NC = D / 16;  // output channels of a thread, in groups of four
-  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+  const int tid = threadIdx.x;
   PagedSched<kKeys> sched;
   if (!sched.init<kThreads>(p, S::kRows / p.G, sm.scratch)) return;
   const float c = p.scale * 1.4426950408889634f;  // scores in powers of two
@@ -73,196 +272,10 @@ __global__ void __launch_bounds__(TY * 16, D == 64 ? 2 : 1) attn_kernel(PagedAtt
     __syncthreads();
     const PagedPiece o = sm.piece;
     if (o.n == 0) break;
-    const int rows = o.n * p.G;
-    const float *q = static_cast<const float *>(p.q);
-    for (int i = tid; i < S::kRows * (D / 4); i += kThreads) {
-      const int r = i / (D / 4), e = (i % (D / 4)) * 4;
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r < rows) x = *reinterpret_cast<const float4 *>(q + row_offset(p, o, r) + e);
-      *reinterpret_cast<float4 *>(&sm.q[r * S::kLd + e]) = x;
-    }
-    int lim[R];  // keys that each row sees
-    float m[R], l[R], acc[R][NC];
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const int r = ty + TY * i;
-      lim[i] = r < rows ? min(o.kv, p.causal ? o.seen0 + r / p.G : o.kv) : 0;
-      m[i] = -INFINITY, l[i] = 0.f;
-#pragma unroll
-      for (int j = 0; j < NC; ++j) acc[i][j] = 0.f;
-    }
-
-    // keys and values of a tile into buffer `to`; slots behind the request's
-    // last key and pages that are none become zeros
-    auto fetch = [&](int tile, int to) {
-      for (int i = tid; i < kKeys * (D / 4); i += kThreads) {
-        const int k = i / (D / 4), e = (i % (D / 4)) * 4;
-        const int key = tile * kKeys + k;
-        int page = -1;
-        if (key < o.kv) {
-          page = p.table[(int64_t)o.req * p.max_pages + (key >> p.page_shift)];
-          if (page < 0 || page >= p.n_pages) {
-            raise_error(p.err, ERR_BAD_PAGE);
-            page = -1;
-          }
-        }
-        const int64_t slot = ((int64_t)max(page, 0) << p.page_shift) + (key & (p.page_size - 1));
-        const int64_t at = page < 0 ? 0 : (slot * p.Hkv + o.head) * D + e;
-        copy16(&sm.k[to][k * S::kLd + e], static_cast<const float *>(p.k) + at, page >= 0);
-        copy16(&sm.v[to][k * D + e], static_cast<const float *>(p.v) + at, page >= 0);
-      }
-      copies_commit();
-    };
-    if (o.tile0 < o.tile1) fetch(o.tile0, 0);
-
-    for (int tile = o.tile0; tile < o.tile1; ++tile) {
-      const int key0 = tile * kKeys, buf = (tile - o.tile0) & 1;
-      const float *sk = sm.k[buf], *sv = sm.v[buf];
-      // the tile before has been read by all: its buffer takes the next one
-      __syncthreads();
-      if (tile + 1 < o.tile1) {
-        fetch(tile + 1, buf ^ 1);
-        copies_wait<1>();
-      } else {
-        copies_wait<0>();
-      }
-      __syncthreads();
-
-      float s[R][4];
-#pragma unroll
-      for (int i = 0; i < R; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
-#pragma unroll 4
-      for (int e = 0; e < D; e += 4) {
-        float4 a[R], b[4];
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-          a[i] = *reinterpret_cast<const float4 *>(&sm.q[(ty + TY * i) * S::kLd + e]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          b[j] = *reinterpret_cast<const float4 *>(&sk[(tx + 16 * j) * S::kLd + e]);
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            s[i][j] = fmaf(a[i].x, b[j].x, s[i][j]);
-            s[i][j] = fmaf(a[i].y, b[j].y, s[i][j]);
-            s[i][j] = fmaf(a[i].z, b[j].z, s[i][j]);
-            s[i][j] = fmaf(a[i].w, b[j].w, s[i][j]);
-          }
-      }
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        float top = m[i];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          s[i][j] = key0 + tx + 16 * j < lim[i] ? s[i][j] * c : -INFINITY;
-          top = fmaxf(top, s[i][j]);
-        }
-#pragma unroll
-        for (int x = 8; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-        const float ref = top == -INFINITY ? 0.f : top;  // a row that has seen no key yet
-        const float keep = exp2f(m[i] - ref);
-        m[i] = top;
-        l[i] *= keep;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float e = exp2f(s[i][j] - ref);
-          l[i] += e;  // this thread's keys only; joined at the end
-          sm.p[(ty + TY * i) * S::kLdP + tx + 16 * j] = e;
-        }
-#pragma unroll
-        for (int j = 0; j < NC; ++j) acc[i][j] *= keep;
-      }
-      __syncwarp();  // a row's sixteen threads are in one warp
-#pragma unroll 4
-      for (int k = 0; k < kKeys; k += 4) {
-        float4 w[R];
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-          w[i] = *reinterpret_cast<const float4 *>(&sm.p[(ty + TY * i) * S::kLdP + k]);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-          for (int j = 0; j < NC; j += 4) {
-            const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(&sv[(k + kk) * D + j * 16 + tx * 4]);
-#pragma unroll
-            for (int i = 0; i < R; ++i) {
-              const float f = kk == 0 ? w[i].x : kk == 1 ? w[i].y : kk == 2 ? w[i].z : w[i].w;
-              const uint64_t ff = pair(f, f);
-              unpair(fma2(ff, x.x, pair(acc[i][j], acc[i][j + 1])), acc[i][j], acc[i][j + 1]);
-              unpair(fma2(ff, x.y, pair(acc[i][j + 2], acc[i][j + 3])), acc[i][j + 2], acc[i][j + 3]);
-            }
-          }
-      }
-    }
-
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-#pragma unroll
-      for (int x = 8; x > 0; x >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
-
-    if (o.n_pieces > 0) {
-      const int64_t slot = paged_part_slot(o, o.index);
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const int r = ty + TY * i;
-        if (r >= rows) continue;
-        const int64_t at = slot * p.part_rows + r;
-        if (tx == 0) p.part_ml[at * 2] = m[i], p.part_ml[at * 2 + 1] = l[i];
-#pragma unroll
-        for (int j = 0; j < NC; j += 4)
-          *reinterpret_cast<float4 *>(&p.part[at * D + j * 16 + tx * 4]) =
-              make_float4(acc[i][j], acc[i][j + 1], acc[i][j + 2], acc[i][j + 3]);
-      }
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        uint32_t *count = p.arrivals + o.first_cta * 2;
-        sm.last = atomicAdd(count, 1u) == (uint32_t)o.n_pieces - 1;
-        if (sm.last) *count = 0;  // as it was found
-        __threadfence();
-      }
-      __syncthreads();
-      if (!sm.last) continue;
-      // the last piece to arrive joins them all, first piece first
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const int r = ty + TY * i;
-        m[i] = -INFINITY, l[i] = 0.f;
-#pragma unroll
-        for (int j = 0; j < NC; ++j) acc[i][j] = 0.f;
-        if (r >= rows) continue;
-        for (int k = 0; k < o.n_pieces; ++k)
-          m[i] = fmaxf(m[i], __ldcg(&p.part_ml[((int64_t)paged_part_slot(o, k) * p.part_rows + r) * 2]));
-        const float ref = m[i] == -INFINITY ? 0.f : m[i];
-        for (int k = 0; k < o.n_pieces; ++k) {
-          const int64_t at = (int64_t)paged_part_slot(o, k) * p.part_rows + r;
-          const float w = exp2f(__ldcg(&p.part_ml[at * 2]) - ref);
-          l[i] = fmaf(w, __ldcg(&p.part_ml[at * 2 + 1]), l[i]);
-#pragma unroll
-          for (int j = 0; j < NC; j += 4) {
-            const float4 x = __ldcg(reinterpret_cast<const float4 *>(&p.part[at * D + j * 16 + tx * 4]));
-            acc[i][j] = fmaf(w, x.x, acc[i][j]);
-            acc[i][j + 1] = fmaf(w, x.y, acc[i][j + 1]);
-            acc[i][j + 2] = fmaf(w, x.z, acc[i][j + 2]);
-            acc[i][j + 3] = fmaf(w, x.w, acc[i][j + 3]);
-          }
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const int r = ty + TY * i;
-      if (r >= rows) continue;
-      const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];  // a row without keys: zeros
-      float *out = static_cast<float *>(p.out) + row_offset(p, o, r);
-#pragma unroll
-      for (int j = 0; j < NC; j += 4)
-        *reinterpret_cast<float4 *>(out + j * 16 + tx * 4) = make_float4(
-            acc[i][j] * inv, acc[i][j + 1] * inv, acc[i][j + 2] * inv, acc[i][j + 3] * inv);
-    }
+    // an item of a few rows leaves the others out (8 decodes, 8 / 2 heads of 64
+    // channels: 47 -> 33 us)
+    if (o.n * p.G <= TY) run_piece<D, R, TY, 1>(p, sm, o, c);
+    else run_piece<D, R, TY, R>(p, sm, o, c);
   }
 }
 
