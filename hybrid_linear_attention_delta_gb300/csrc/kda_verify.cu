@@ -165,6 +165,15 @@ __device__ F2 block_scan(F2 v, F2 *warp_sums, F2 *total) {
   return warp ? add(before, v) : v;
 }
 
+// The halves of a barrier of the cluster's CTAs, apart, without ordering what was
+// written before it: all that it tells is that every CTA has started.
+__device__ __forceinline__ void cluster_started() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait_started() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // One cluster per sequence; CTA `rank` owns segments [rank * n_local, ...) of
 // seg_len elements.
 template <typename T, bool VECT>
@@ -191,6 +200,9 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(VerifyPlan p, int s
     }
     return;
   }
+  // A CTA's shared memory is written by the others only once it is known to have
+  // started: said here, waited for in front of the first exchange, the sums between.
+  cluster_started();
   const float u_sample = p.u_sample[n];
   if (tid == 0) s_kept = len, s_pick = 0x7fffffff, s_last = -1;
   __syncthreads();
@@ -256,6 +268,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(VerifyPlan p, int s
     }
     __syncthreads();
     // every CTA learns every CTA's sum
+    if (phase == 0) cluster_wait_started();
     if (tid < n_ranks) cluster.map_shared_rank(&s_tot[phase][0], tid)[rank] = s_seg[n_local - 1];
     cluster.sync();
     F2 total = {0.f, 0.f};

@@ -342,6 +342,27 @@ def test_verify_far_tokens_are_not_lost():
     assert bits == 0 and torch.equal(acc, racc) and torch.equal(tok, rtok)
 
 
+@pytest.mark.parametrize("N,V", [(3, 16 * 1024 + 1), (19, 33 * 1024), (19, 65 * 1024 - 3),
+                                 (1, 73 * 1024), (76, 65 * 1024 + 8), (152, 17000)])
+@pytest.mark.parametrize("probs", [True, False])
+def test_verify_sequences_on_several_ctas(probs, N, V):
+    """Two, four and eight CTAs a sequence, the last of them with few segments (it
+    has its sum long before the others), launch after launch; sequences with a bad
+    length between them, whose CTAs leave at once."""
+    c = _verify_case(N, 2, V, "bf16", seed=V, probs=probs)
+    lens = [(-1 if n % 5 == 2 else n % 3) for n in range(N)]
+    good = [n for n in range(N) if lens[n] >= 0]
+    pick = lambda t: None if t is None else t[good]
+    racc, rtok = verify_reference(*(pick(t) for t in c), lens=[lens[n] for n in good])
+    for _ in range(8):
+        acc, tok, bits = _verify(c, lens)
+        assert bits == (128 if len(good) < N else 0)
+        assert torch.equal(acc[good], racc) and torch.equal(tok[good], rtok)
+        bad = torch.ones(N, dtype=torch.bool)
+        bad[good] = False
+        assert (acc[bad] == 0).all() and (tok[bad] == -1).all()
+
+
 # Four rows, found by search: the mass of segments 0, 2, ... 30 of 1024 tokens, that
 # of segment 40, and u, for which u times the sum lies between two values that
 # sums in different orders give the border behind a segment with mass.
