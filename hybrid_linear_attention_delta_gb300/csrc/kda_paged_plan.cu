@@ -22,7 +22,7 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 
 // Pages taken and given back, summed over requests.  One request may ask for
-// 2^27 pages (max_pages * page_size < 2^31), so the sums have 64 bits.
+// 2^26 pages (max_pages * page_size <= 2^30), so the sums have 64 bits.
 struct Sums {
   long long need, back;
 };
@@ -100,10 +100,11 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PagedPlanArgs p) {
     if (!ring_ok) raise_error(p.err, ERR_BAD_PAGE);
   }
   const int64_t t_per = ((int64_t)p.T + n_ctas - 1) / n_ctas;
-  const int t_lo = (int)min((int64_t)p.T, cta * t_per);
-  const int t_hi = (int)min((int64_t)p.T, t_lo + t_per);
+  // (64 bits: a step of the loops over them passes 2^31 at the end of the longest batches)
+  const int64_t t_lo = min((int64_t)p.T, cta * t_per);
+  const int64_t t_hi = min((int64_t)p.T, t_lo + t_per);
   if (bad) {
-    for (int t = t_lo + tid; t < t_hi; t += kThreads) p.positions[t] = 0, p.slots[t] = -1;
+    for (int64_t t = t_lo + tid; t < t_hi; t += kThreads) p.positions[t] = 0, p.slots[t] = -1;
     if (cta == 0) {
       for (int b = tid; b < B; b += kThreads) p.kv_lens[b] = 0, p.held_out[b] = s_held[b];
       if (tid == 0) p.ring_out[0] = head, p.ring_out[1] = count;
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PagedPlanArgs p) {
 
   // tokens
   const int T_used = s_cu[B];
-  for (int t = t_lo + tid; t < t_hi; t += kThreads) {
+  for (int64_t t = t_lo + tid; t < t_hi; t += kThreads) {
     int pos = 0, slot = -1;
     if (t < T_used) {
       int lo = 0, hi = B - 1;  // largest b with cu[b] <= t; its range holds t
@@ -186,7 +187,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PagedPlanArgs p) {
       const int first = s_first[lo];
       if (first >= 0) {
         const int held = s_held[lo];
-        pos = s_cached[lo] + t - s_cu[lo];
+        pos = s_cached[lo] + (int)(t - s_cu[lo]);
         const int j = pos >> p.page_shift;
         int page;
         if (j < held) {

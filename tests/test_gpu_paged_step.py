@@ -165,6 +165,48 @@ def test_plan_bad_inputs_on_the_device():
     assert t["ring_out"].tolist() == [c.head, 8]
 
 
+def test_plan_token_counts_near_the_end_of_32_bits():
+    """The longest batch that T_total can name: positions, slots and padding up to
+    row 2^31 - 2, a request whose last rows lie there and whose cache is at its
+    longest."""
+    page, width = 256, 1 << 22                  # width * page = 2^30
+    T = (1 << 31) - 1
+    new = [1 << 30, (1 << 30) - 4096, 300]      # ends 3797 rows before T
+    cached = [0, 0, (1 << 30) - 300]
+    n_pages = (1 << 23) - 1
+    cu = [0, new[0], new[0] + new[1], sum(new)]
+    table = torch.full((3, width), 5, dtype=I32, device="cuda")
+    ring = torch.arange(n_pages, dtype=I32, device="cuda").flip(0).contiguous()
+    head = 1000
+    held, kv, held_out = _i32([0, 0, width]), _i32([0] * 3), _i32([0] * 3)
+    pos = torch.full((T,), -3, dtype=I32, device="cuda")
+    slot = torch.full((T,), -3, dtype=I32, device="cuda")
+    state = _i32([0, 0])
+    ws = kda.paged_workspace_for()
+
+    def plan():
+        kda.kda_paged_plan(_i32(cu), _i32(cached), table, held, ring, _i32([head, n_pages]),
+                           held_out, state, kv, pos, slot, page_size=page, workspace=ws)
+    plan()
+    assert kda.kda_device_status(ws) == (kda.KDA_OK, 0)
+    assert kv.tolist() == [new[0], new[1], 1 << 30]
+    first = [0, width, None]
+    step = 1 << 27
+    for b in range(3):
+        for a in range(cu[b], cu[b + 1], step):
+            e = min(cu[b + 1], a + step)
+            want = cached[b] + torch.arange(a - cu[b], e - cu[b], device="cuda")
+            assert torch.equal(pos[a:e].long(), want)
+            pages = (n_pages - 1 - (head + first[b] + want // page) % n_pages) if b < 2 else 5
+            assert torch.equal(slot[a:e].long(), pages * page + want % page)
+    assert (pos[cu[3]:] == 0).all() and (slot[cu[3]:] == -1).all()
+    cu[2] = -1                                   # bad: every row is marked
+    plan()
+    assert kda.kda_device_status(ws) == (kda.KDA_ERR_DEVICE_CHECK, 4)
+    assert all((slot[a:a + step] == -1).all() and (pos[a:a + step] == 0).all()
+               for a in range(0, T, step))
+
+
 # ---------------------------------------------------------------------- append
 
 def _append_case(T, Hq, Hkv, d, rot, page, dtype, norm, max_pos, seed, pad=0):
