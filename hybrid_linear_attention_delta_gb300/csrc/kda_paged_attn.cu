@@ -760,6 +760,9 @@ __device__ bool softmax_role(Ctl &ctl, const AttnArgs &a, uint32_t tmem, int s) 
               if (move) ref = tm;
               l *= keep;
               if (!own()) return false;
+              // the weights of the pass before lie where this one's go: stores to
+              // tensor memory are in order only across a wait
+              tmem_wait_st();
               tc_fence_after();
 #pragma unroll
               for (int q = 0; q < D / 16; ++q) {

@@ -143,6 +143,36 @@ def test_rising_scores_move_the_maximum_every_tile():
         _check(case, norm_bar=False)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv,new,total", [
+    (2, 1, [130], [1500]),            # two tiles of rows
+    (4, 2, [300, 1, 0, 9], [900, 2900, 5, 640]),  # both forms of item, ragged ends
+    (8, 1, [1], [20011]),             # one item over many CTAs
+    (64, 1, [5], [6000]),             # both tiles of rows over many CTAs
+])
+@pytest.mark.parametrize("kind", ["rising", "falling", "steps", "large"])
+def test_references_move(d, Hq, Hkv, new, total, kind):
+    """Scores that pass a row's reference: from tile to tile, in jumps that are
+    apart from one row to the next, or anywhere (sums and outputs are rescaled, the
+    tile's weights made again), and scores that fall, where nothing moves."""
+    case = AttnCase(new, total, Hq=Hq, Hkv=Hkv, d=d, page=16, dtype="bf16", seed=d + Hq,
+                    scale_q=30.0 if kind == "large" else 1.0)
+    for b, t in enumerate(total if kind != "large" else []):
+        if t == 0:
+            continue
+        at = torch.arange(t, dtype=torch.float64)
+        ramp = {"rising": -40 + 80 * at / t, "falling": 40 - 80 * at / t,
+                "steps": 10.0 * (at // 200)}[kind]
+        ids = case.table[b, :-(-t // 16)].long()
+        k = case.k[ids].reshape(-1, Hkv, d)
+        k[:t, :, 0] = ramp[:, None].to(torch.bfloat16)
+        case.k[ids] = k.reshape(-1, 16, Hkv, d)
+    if kind != "large":
+        rows = torch.arange(case.q.shape[0])[:, None] % 3
+        case.q[..., 0] = (torch.tensor([6.0, 0.5, 20.0])[rows]).to(torch.bfloat16)
+    _check(case, norm_bar=False)
+
+
 def test_mixed_batch_of_many_requests():
     g = torch.Generator().manual_seed(11)
     new = torch.randint(0, 60, (90,), generator=g).tolist()
