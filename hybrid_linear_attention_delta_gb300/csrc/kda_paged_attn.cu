@@ -92,6 +92,7 @@ struct Ctl {
   int64_t scratch[kThreads / 16 + 4];
   uint32_t tmem;
   int32_t last[2];
+  int32_t gave_up[2];  // a warp of the stream gave up a wait
 };
 
 template <int D>
@@ -925,6 +926,7 @@ __device__ bool softmax_role(Ctl &ctl, const AttnArgs &a, uint32_t tmem, int s) 
         p.part_ml[part_at * 2 + 1] = l0;
       }
       named_bar_sync(1 + s, 128);
+      if (ctl.gave_up[s]) return false;
       if (r == 0) {
         uint32_t *count = p.arrivals + w.o.first_cta * 2 + s;
         const bool last = arrive_acq_rel(count) == (uint32_t)w.o.n_pieces - 1;
@@ -975,6 +977,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
       mbar_init(smem_u32(&ctl.piece_empty[i]), kPieceReaders);
     }
     for (int s = 0; s < 2; ++s) mbar_init(smem_u32(&ctl.drain[s]), 1);
+    ctl.gave_up[0] = ctl.gave_up[1] = 0;
     fence_mbar_init();
   }
   if (warp == kLoadWarp && (tid & 31) == 0) {
@@ -996,6 +999,15 @@ attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
   } else if (warp < kSoftmaxWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     ok = softmax_role<D>(ctl, a, tmem, warp >> 2);
+    if (!ok) {
+      // The barriers of a stream's warps have no time limit: one that gave up a wait
+      // is counted in at the next one, the first of a cut piece, where the others
+      // find its flag and leave too.  (Nobody gives up between that barrier and the
+      // piece's second one, so they all read the same.)
+      if ((tid & 31) == 0) ctl.gave_up[warp >> 2] = 1;
+      __syncwarp();
+      named_bar_arrive(1 + (warp >> 2), 128);
+    }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp < kLoadWarp) {
