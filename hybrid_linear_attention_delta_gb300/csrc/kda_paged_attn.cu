@@ -48,6 +48,12 @@ constexpr int kThreads = 384;
 constexpr int kRows = 128;  // query rows of a stream's tile
 constexpr int kKeys = 128;  // keys of a tile
 constexpr int kPieces = 4;  // pieces published ahead
+// Key tiles that are added up in tensor memory before the sum is put aside, in fp32
+// (LONG, the kernels of wide block tables).  The tensor cores cut each product off
+// some 26 bits below the sum that it is added to, which takes up to 6e-9 of the sum
+// per key: 8e-4 of the outputs with these 131072 keys at a time, whatever their
+// number (values of one sign; 1.4e-4 for any); without end it was 1.8e-2 at 4 million.
+constexpr int kLongRun = 1024;
 constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kLoadWarp = 10, kSchedWarp = 11;
 constexpr int kStreamWarps = kSoftmaxWarps / 2;
 // readers of a published piece: the softmax, the MMA and the load warps
@@ -75,9 +81,11 @@ struct Layout {
 // A piece as the warps see it.
 struct Work {
   PagedPiece o;
-  int32_t keys;   // 1 + last key that the item sees
   int32_t split;  // 1: one tile of rows, key tiles in turn over the streams
   int32_t cnt0, cnt1;  // key tiles of the streams
+  // LONG: a piece goes over in runs of kLongRun tiles.  1: runs before this one have
+  // left their sums in the piece's slot, 2: so does this one, for those behind it.
+  int32_t runs;
 };
 
 struct Ctl {
@@ -180,13 +188,27 @@ struct PieceReader {
 };
 
 // ------------------------------------------------------------------ pieces
+template <bool LONG>
 __device__ bool sched_role(Ctl &ctl, const AttnArgs &a, PagedSched<kKeys> &sched) {
   const int tpt = a.tpt;
+  int at = 0, end = 0;  // LONG: the piece's next tile, and its end
+  PagedPiece o;
   for (uint32_t n = 0;; ++n) {
     const uint32_t slot = n % kPieces;
     Work w;
-    w.o = sched.next(a.p);
-    w.keys = max(0, a.p.causal ? min(w.o.kv, w.o.seen0 + w.o.n - 1) : w.o.kv);
+    if constexpr (LONG) {
+      w.runs = at < end;
+      if (at == end) {
+        o = sched.next(a.p);
+        at = o.tile0, end = o.n == 0 ? at : o.tile1;
+      }
+      w.o = o;
+      w.o.tile0 = at;
+      w.o.tile1 = at = min(end, at + kLongRun);
+      w.runs |= at < end ? 2 : 0;
+    } else {
+      w.o = sched.next(a.p);
+    }
     w.split = w.o.n <= tpt;
     const int tiles = w.o.tile1 - w.o.tile0;
     if (w.split) {
@@ -675,7 +697,7 @@ __device__ void join_pieces(const PagedAttnPlan &p, const PagedPiece &o, int r0,
   else join_rows<D, 2, 8>(p, o, r0, r1, warp, n_warps, r1 - r0 <= n_warps);
 }
 
-template <int D>
+template <int D, bool LONG>
 __device__ bool softmax_role(Ctl &ctl, const AttnArgs &a, uint32_t tmem, int s) {
   const PagedAttnPlan &p = a.p;
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
@@ -848,13 +870,28 @@ __device__ bool softmax_role(Ctl &ctl, const AttnArgs &a, uint32_t tmem, int s) 
       l0 = w0 * l + w1 * l1;
     }
     tc_fence_after();
-    const bool parts = w.o.n_pieces > 0;
-    const float f = parts ? 1.f : l0 == 0.f ? 0.f : 1.f / l0;
+    const bool parts = w.o.n_pieces > 0 || (LONG && (w.runs & 2));  // a partial result
     const int item_row = row_tok * p.G + g;
-    const int64_t part_at =
-        parts ? (int64_t)paged_part_slot(w.o, w.o.index) * p.part_rows + item_row : 0;
+    int64_t part_at =
+        w.o.n_pieces > 0 ? (int64_t)paged_part_slot(w.o, w.o.index) * p.part_rows + item_row : 0;
+    float w2 = 0.f;  // weight of what the runs before left
+    if constexpr (LONG) {
+      // (an item that is not cut keeps its runs in the slot of the CTA's last item)
+      if (w.o.n_pieces == 0) part_at = (2 * (int64_t)blockIdx.x + 1) * p.part_rows + item_row;
+      if ((w.runs & 1) && live) {
+        const float m2 = __ldcg(&p.part_ml[part_at * 2]), l2 = __ldcg(&p.part_ml[part_at * 2 + 1]);
+        const float top = fmaxf(mm, m2), zero = top == -INFINITY ? 0.f : top;
+        const float w01 = l0 == 0.f ? 0.f : exp2f(mm - zero);
+        w2 = l2 == 0.f ? 0.f : exp2f(m2 - zero);
+        w0 *= w01;
+        w1 *= w01;
+        l0 = w01 * l0 + w2 * l2;
+        mm = top;
+      }
+    }
+    const float f = parts ? 1.f : l0 == 0.f ? 0.f : 1.f / l0;
     if (warp_live) {
-      const float f0 = l == 0.f ? 0.f : f * w0, f1 = f * w1;
+      const float f0 = l == 0.f ? 0.f : f * w0, f1 = f * w1, f2 = f * w2;
       // where the rows of this lane's group go (-1: nowhere)
       const int64_t mine = parts ? part_at * D : row_offset(p, w.o, row_tok, g);
       const bool few = __popc(__ballot_sync(0xffffffffu, live)) <= 8;
@@ -882,6 +919,20 @@ __device__ bool softmax_role(Ctl &ctl, const AttnArgs &a, uint32_t tmem, int s) 
           reg_fence(o);
 #pragma unroll
           for (int i = 0; i < 32; ++i) y[i] = fmaf(__uint_as_float(o[i]), f1, y[i]);
+        }
+        if constexpr (LONG) {
+          if (w2 != 0.f) {
+            const float *src = p.part + part_at * D + q * 32;
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const float4 x = __ldcg(reinterpret_cast<const float4 *>(src + i));
+              y[i] = fmaf(x.x, f2, y[i]);
+              y[i + 1] = fmaf(x.y, f2, y[i + 1]);
+              y[i + 2] = fmaf(x.z, f2, y[i + 2]);
+              y[i + 3] = fmaf(x.w, f2, y[i + 3]);
+            }
+          }
+          __syncwarp();  // other lanes write this row's new sums
         }
         uint32_t v[16];
         if (parts && few) {  // (transposing takes longer than a few rows' stores)
@@ -925,6 +976,7 @@ __device__ bool softmax_role(Ctl &ctl, const AttnArgs &a, uint32_t tmem, int s) 
         p.part_ml[part_at * 2] = mm;
         p.part_ml[part_at * 2 + 1] = l0;
       }
+      if (LONG && (w.runs & 2)) continue;
       named_bar_sync(1 + s, 128);
       if (ctl.gave_up[s]) return false;
       if (r == 0) {
@@ -942,7 +994,7 @@ __device__ bool softmax_role(Ctl &ctl, const AttnArgs &a, uint32_t tmem, int s) 
 }
 
 // ------------------------------------------------------------------ kernel
-template <int D>
+template <int D, bool LONG>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
             const __grid_constant__ CUtensorMap tv, const AttnArgs a) {
@@ -998,7 +1050,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
   if (!work) {  // bad cu_seqlens
   } else if (warp < kSoftmaxWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-    ok = softmax_role<D>(ctl, a, tmem, warp >> 2);
+    ok = softmax_role<D, LONG>(ctl, a, tmem, warp >> 2);
     if (!ok) {
       // The barriers of a stream's warps have no time limit: one that gave up a wait
       // is counted in at the next one, the first of a cut piece, where the others
@@ -1015,7 +1067,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
     } else if (warp == kLoadWarp) {
       ok = load_role<D>(sbase, ctl, a, &tq, &tk, &tv);
     } else if (tid == kSchedWarp * 32) {
-      ok = sched_role(ctl, a, sched);
+      ok = sched_role<LONG>(ctl, a, sched);
     }
   }
   if (!ok) raise_error(a.p.err, ERR_TIMEOUT);
@@ -1057,10 +1109,10 @@ bool make_map(CUtensorMap *map, const void *base, uint64_t d, uint64_t heads, ui
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
+template <int D, bool LONG>
 cudaError_t launch_d(const PagedAttnPlan &p) {
   static_assert(smem_bytes<D>() <= 232448, "shared memory of one CTA");
-  const void *f = reinterpret_cast<const void *>(attn_kernel<D>);
+  const void *f = reinterpret_cast<const void *>(attn_kernel<D, LONG>);
   const cudaError_t e = set_smem_limit_once(f, smem_bytes<D>());
   if (e != cudaSuccess) return e;
   CUtensorMap tq, tk, tv;
@@ -1076,14 +1128,19 @@ cudaError_t launch_d(const PagedAttnPlan &p) {
   a.c = fmaxf(fabsf(p.scale) * 1.4426950408889634f, 1e-30f);
   a.neg_q = p.scale < 0.f;
   a.tpt = kRows / p.G;
-  attn_kernel<D><<<kPagedMaxCtas, kThreads, smem_bytes<D>(), p.stream>>>(tq, tk, tv, a);
+  attn_kernel<D, LONG><<<kPagedMaxCtas, kThreads, smem_bytes<D>(), p.stream>>>(tq, tk, tv, a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_paged_attn_bf16(const PagedAttnPlan &p) {
-  return p.d == 128 ? launch_d<128>(p) : launch_d<64>(p);
+  // Only a table of more pages can name a piece of more than one run.  (One token over
+  // 777 keys: 12.2 us, with a wide table 12.6; over 30000: 24.8 and 26.0; the cases of a
+  // millisecond: the same.)
+  const bool wide = (int64_t)p.max_pages * p.page_size > (int64_t)kLongRun * kKeys;
+  if (p.d == 128) return wide ? launch_d<128, true>(p) : launch_d<128, false>(p);
+  return wide ? launch_d<64, true>(p) : launch_d<64, false>(p);
 }
 
 }  // namespace kda

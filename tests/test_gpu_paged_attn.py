@@ -203,6 +203,67 @@ def test_values_beyond_32_bit_offsets(dtype):
     assert ((out.double().cpu() - ref).abs() <= case.bound(ref, size, top)).all()
 
 
+@pytest.mark.parametrize("d,Hkv,G,B,T,lg", [
+    (128, 16, 2, 1, 1280, 22),   # items of whole tiles of rows, each on one CTA
+    (64, 16, 3, 1, 1000, 22),
+    (128, 4, 4, 40, 1, 24),      # decodes: an item and a part of one on a CTA
+    (64, 4, 4, 40, 1, 24),
+    (128, 2, 8, 1, 2, 26),       # an item over many CTAs, several runs on each
+])
+@pytest.mark.parametrize("causal", [True, False])
+def test_sums_over_millions_of_keys(d, Hkv, G, B, T, lg, causal):
+    """Values of one sign, whose sums in tensor memory would lose 1e-2 and more to
+    the products that are cut off.  The pages of a request are the same sixteen over
+    and over, less the last slot: every distinct key then weighs as often, but
+    for the few at the end (2^-10 of all)."""
+    g = torch.Generator(device="cuda").manual_seed(lg + d)
+    page, n_pages, kv = 256, 16, (1 << lg) - (3 if causal else 0)
+    k = torch.randn((n_pages, page, Hkv, d), generator=g, device="cuda").bfloat16()
+    v = (torch.randn((n_pages, page, Hkv, d), generator=g, device="cuda").abs() + 0.5).bfloat16()
+    q = torch.randn((B * T, Hkv * G, d), generator=g, device="cuda").bfloat16()
+    table = (torch.arange(1 << lg - 8, device="cuda") % n_pages).int().repeat(B, 1)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    ws = kda.paged_workspace_for(B * T, Hkv * G, Hkv, d)
+    outs = []
+    for _ in range(2):
+        out = torch.zeros_like(q)
+        kda.kda_paged_attn(q, k, v, table, i32([T * b for b in range(B + 1)]), i32([kv] * B), out,
+                           causal=causal, workspace=ws)
+        assert kda.kda_device_status(ws) == (kda.KDA_OK, 0)
+        outs.append(out)
+    assert torch.equal(*outs)
+    ref = torch.empty(q.shape, dtype=torch.float64, device="cuda")
+    for h in range(Hkv * G):
+        K, V = (x[:, :, h // G].flatten(0, 1).double() for x in (k, v))
+        ref[:, h] = torch.softmax(q[:, h].double() @ K.T * d ** -0.5, -1) @ V
+    # weights and outputs are rounded to bf16; a run of 2^17 keys loses at most 2^-26
+    # of its sum per key, on average over the run half of that: 2^-10; the last up
+    # to 1003 keys that a row does not see are 2^-12 of 2^22, and weigh up to e^5 times
+    # the mean in a row (|q k| d^-1/2 < 5): they move it by less than 2^-5 of |v|'s
+    # spread, so the rows of the causal forms are compared by their norm alone
+    err = outs[0].double() - ref
+    if not causal:
+        assert (err.abs() <= ref.abs() * (2 * 2.0 ** -8 * 1.01 + 2.0 ** -10)).all()
+    assert float(err.norm() / ref.norm()) <= TOL["bf16"]
+
+
+def test_exact_sums_over_2_to_27_keys():
+    """Keys of zeros weigh the same and values are powers of two, so that every sum
+    is exact as long as it is kept: the outputs are the values."""
+    Hq, d, page, kv, T = 64, 64, 256, 1 << 27, 640
+    q = torch.ones((T, Hq, d), dtype=torch.bfloat16, device="cuda")
+    k = torch.zeros((1, page, 1, d), dtype=torch.bfloat16, device="cuda")
+    value = 2.0 ** (torch.arange(d, device="cuda") % 5)
+    v = value.to(torch.bfloat16).expand(1, page, 1, d).contiguous()
+    table = torch.zeros((1, kv // page), dtype=torch.int32, device="cuda")
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    ws = kda.paged_workspace_for(T, Hq, 1, d)
+    out = torch.zeros_like(q)
+    kda.kda_paged_attn(q, k, v, table, i32([0, T]), i32([kv]), out, causal=False, workspace=ws)
+    assert kda.kda_device_status(ws) == (kda.KDA_OK, 0)
+    assert (out.float() == value).all()
+
+
 def test_captured_graphs_share_a_workspace_and_follow_the_lengths():
     """Two graphs over one workspace, replayed in turn with other lengths."""
     cases = [AttnCase([1, 1], [900, 300], Hq=8, Hkv=2, d=128, page=16, dtype="bf16", seed=1),
