@@ -10,6 +10,8 @@ namespace {
 
 bool aligned(const void *p, uintptr_t n) { return p && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+int64_t elem_bytes(int32_t dtype) { return dtype == KDA_F32 ? 4 : 2; }
+
 kda_status check_workspace(const void *ws, size_t bytes, size_t need) {
   return aligned(ws, 256) && bytes >= need ? KDA_OK : KDA_ERR_INVALID_ARG;
 }
@@ -44,14 +46,23 @@ kda_status check_batch(const kda_paged_args *a) {
   return KDA_OK;
 }
 
-// Whether an output (the first n_out of the arrays) is another array too; NULL and
-// empty arrays aside.  CTAs read inputs at different times, so a call in place
-// would race.
-bool shared(std::initializer_list<const void *> arrays, size_t n_out) {
-  const void *const *v = arrays.begin();
+struct Span {
+  const void *p;
+  int64_t bytes;
+};
+
+// Whether an output (the first n_out of the arrays) lies over a part of another
+// array of the call; NULL and empty arrays aside.  CTAs read inputs at different
+// times, so such a call would race.
+bool overlap(std::initializer_list<Span> arrays, size_t n_out) {
+  const Span *v = arrays.begin();
   for (size_t i = 0; i < n_out; ++i)
-    for (size_t j = i + 1; j < arrays.size(); ++j)
-      if (v[i] && v[i] == v[j]) return true;
+    for (size_t j = i + 1; j < arrays.size(); ++j) {
+      const uintptr_t a = reinterpret_cast<uintptr_t>(v[i].p), b = reinterpret_cast<uintptr_t>(v[j].p);
+      if (a && b && v[i].bytes > 0 && v[j].bytes > 0 &&
+          (a < b ? b - a < (uintptr_t)v[i].bytes : a - b < (uintptr_t)v[j].bytes))
+        return true;
+    }
   return false;
 }
 
@@ -95,10 +106,11 @@ kda_status kda_paged_plan(const int32_t *cu_seqlens, const int32_t *cached_lens,
                    !aligned(held_out, 4) || !aligned(kv_lens, 4)))
     return KDA_ERR_INVALID_ARG;
   if (a->T_total > 0 && (!aligned(positions, 4) || !aligned(slot_map, 4))) return KDA_ERR_INVALID_ARG;
-  const bool any = a->B > 0, tok = a->T_total > 0;
-  if (shared({any ? block_table : nullptr, free_ring, any ? held_out : nullptr, ring_out,
-              any ? kv_lens : nullptr, tok ? positions : nullptr, tok ? slot_map : nullptr,
-              cu_seqlens, any ? cached_lens : nullptr, any ? held : nullptr, ring}, 7))
+  const int64_t per_req = 4ll * a->B, per_tok = 4ll * a->T_total;
+  if (overlap({{block_table, per_req * a->max_pages}, {free_ring, 4ll * a->n_pages},
+               {held_out, per_req}, {ring_out, 8}, {kv_lens, per_req}, {positions, per_tok},
+               {slot_map, per_tok}, {a->workspace, 256}, {cu_seqlens, per_req + 4},
+               {cached_lens, per_req}, {held, per_req}, {ring, 8}}, 8))
     return KDA_ERR_INVALID_ARG;
   kda::PagedPlanArgs p = {};
   p.cu = cu_seqlens; p.cached = cached_lens; p.held = held; p.ring = ring;
@@ -132,7 +144,13 @@ kda_status kda_paged_append(const void *qkv, const int32_t *positions, const int
   if (!aligned(qkv, 16) || !aligned(q_out, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) ||
       !aligned(slot_map, 4) || (f->rot_dim > 0 && !aligned(positions, 4)))
     return KDA_ERR_INVALID_ARG;
-  if (shared({q_out, k_pages, v_pages, qkv}, 3)) return KDA_ERR_INVALID_ARG;
+  const int64_t row = (int64_t)a->d * elem_bytes(a->dtype), T = a->T_total;
+  const int64_t pool = (int64_t)a->n_pages * a->page_size * a->Hkv * row;
+  if (overlap({{q_out, T * a->Hq * row}, {k_pages, pool}, {v_pages, pool}, {a->workspace, 256},
+               {qkv, T * (a->Hq + 2 * a->Hkv) * row}, {slot_map, T * 4},
+               {positions, f->rot_dim > 0 ? T * 4 : 0}, {f->q_norm, a->d * 4}, {f->k_norm, a->d * 4},
+               {f->rope, 4ll * f->max_pos * f->rot_dim}}, 4))
+    return KDA_ERR_INVALID_ARG;
   kda::AppendPlan p = {};
   p.qkv = qkv; p.positions = positions; p.slots = slot_map;
   p.q = q_out; p.k_pages = k_pages; p.v_pages = v_pages;
@@ -163,9 +181,14 @@ kda_status kda_paged_attn(const void *q, const void *k_pages, const void *v_page
   if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(out, 16) ||
       !aligned(block_table, 4) || !aligned(cu_seqlens, 4) || !aligned(kv_lens, 4))
     return KDA_ERR_INVALID_ARG;
-  if (shared({out, k_pages, v_pages}, 1)) return KDA_ERR_INVALID_ARG;
   const int G = a->Hq / a->Hkv;
   const kda::PagedWorkspace lay(a->T_total, G, a->d);
+  const int64_t row = (int64_t)a->d * elem_bytes(a->dtype), rows = row * a->T_total * a->Hq;
+  const int64_t pool = (int64_t)a->n_pages * a->page_size * a->Hkv * row;
+  if (overlap({{out, rows}, {a->workspace, (int64_t)lay.total}, {q, q == out ? 0 : rows},
+               {k_pages, pool}, {v_pages, pool}, {block_table, 4ll * a->B * a->max_pages},
+               {cu_seqlens, 4ll * a->B + 4}, {kv_lens, 4ll * a->B}}, 2))
+    return KDA_ERR_INVALID_ARG;
   char *ws = static_cast<char *>(a->workspace);
   kda::PagedAttnPlan p = {};
   p.q = q; p.k = k_pages; p.v = v_pages;
@@ -213,7 +236,11 @@ kda_status kda_verify_drafts(const void *target_probs, const void *draft_probs,
     return KDA_ERR_INVALID_ARG;
   if (a->n_draft > 0 && (!aligned(draft_tokens, 4) || !aligned(u_accept, 4)))
     return KDA_ERR_INVALID_ARG;
-  if (shared({accepted, tokens, draft_lens, a->n_draft > 0 ? draft_tokens : nullptr}, 2))
+  const int64_t N = a->N, n = a->n_draft, row = (int64_t)a->V * elem_bytes(a->dtype);
+  if (overlap({{accepted, N * 4}, {tokens, N * (n + 1) * 4}, {a->workspace, 256},
+               {target_probs, N * (n + 1) * row}, {draft_probs, N * n * row},
+               {draft_tokens, N * n * 4}, {draft_lens, N * 4}, {u_accept, N * n * 4},
+               {u_sample, N * 4}}, 3))
     return KDA_ERR_INVALID_ARG;
   kda::VerifyPlan p = {};
   p.p = target_probs; p.q = a->n_draft > 0 ? draft_probs : nullptr;

@@ -21,7 +21,9 @@
  * errors returned before anything is launched, device-visible errors recorded
  * in the workspace's sticky word (kda_device_status), deterministic results,
  * no device memory allocated.  The calls can be captured into CUDA graphs;
- * lengths, tables and page counts are read on the device at every replay.
+ * lengths, tables and page counts are read on the device at every replay.  No
+ * output of a call, its workspace included, may lie over any part of another of
+ * its arrays (KDA_ERR_INVALID_ARG), but for the exceptions named below.
  *
  * Padded batches: cu_seqlens[B] may be smaller than T_total; token rows behind
  * it belong to no request and are left as they were (kda_paged_plan marks them
@@ -86,9 +88,9 @@ size_t kda_paged_workspace_bytes(const kda_paged_args *a);
  * positions   [T_total] int32  position of each new token (0 for rows >= cu[B])
  * slot_map    [T_total] int32  cache slot, page * page_size + offset (-1 for rows >= cu[B])
  *
- * No output may be another array of the call (held_out and held, ring_out and
- * ring, kv_lens and cached_lens are different ones): the call changes none of
- * its inputs but the entries named above, so it can be repeated.
+ * (held_out and held, ring_out and ring, kv_lens and cached_lens are different
+ * arrays: the call changes none of its inputs but the entries named above, so it
+ * can be repeated.)
  *
  * Refused requests keep held_out = held, write nothing, get kv_lens = 0 (their
  * rows of kda_paged_attn become zeros) and slot -1 for their tokens:
@@ -126,8 +128,8 @@ kda_status kda_paged_plan(const int32_t *cu_seqlens, const int32_t *cached_lens,
  *                              negative slot is skipped: nothing of it is written
  * q_out      [T_total][Hq][d] dtype
  * k_pages, v_pages [n_pages][page_size][Hkv][d] dtype
- * q_out, k_pages, v_pages and qkv are different arrays.  A slot beyond the pool
- * (bit 1) or a position beyond the table (bit 1024) skips the token.  Uses T_total, Hq, Hkv, d, page_size, n_pages, dtype of a.
+ * A slot beyond the pool (bit 1) or a position beyond the table (bit 1024) skips
+ * the token.  Uses T_total, Hq, Hkv, d, page_size, n_pages, dtype of a.
  */
 typedef struct {
   const float *q_norm, *k_norm;  /* [d] fp32 weights; NULL: that norm is left out */
@@ -157,7 +159,7 @@ kda_status kda_paged_append(const void *qkv, const int32_t *positions, const int
  * result, whatever they hold; a key that the mask hides has weight zero, and
  * its value must be finite where other rows of the request see it.
  *
- * q, out     [T_total][Hq][d] dtype; out may be q
+ * q, out     [T_total][Hq][d] dtype; out may be q itself
  * k_pages, v_pages [n_pages][page_size][Hkv][d] dtype
  * block_table [B][max_pages] int32
  * cu_seqlens [B+1] int32     cu[0] = 0, non-decreasing, cu[B] <= T_total
@@ -200,7 +202,6 @@ kda_status kda_paged_attn(const void *q, const void *k_pages, const void *v_page
  * accepted     [N] int32     1 + the drafts that stand (the verified tokens that are kept,
  *                            the step's first included): accepted_prev of kda_decode_spec
  * tokens       [N][n_draft+1] int32  the drafts that stand, the drawn token, then -1
- * (accepted and tokens are arrays of their own, not draft_lens or draft_tokens)
  *
  * A draft token outside [0, V) does not stand (bit 2048).  draft_lens outside
  * its range (bit 128): accepted 0, tokens -1.  A row without mass (bit 4096):

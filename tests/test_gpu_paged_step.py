@@ -462,6 +462,34 @@ def test_verify_bad_inputs_on_the_device():
     assert bits == 4096 and tok[2, 0] == -1 and tok[3, 0] == -1
 
 
+def test_arrays_side_by_side_in_one_buffer():
+    """A plan and a verification whose arrays touch each other in one allocation."""
+    c = PlanCase([20, 0, 33, 1], [0, 0, 5, 16], [0, 4, 1, 1], 16, 8, 3, seed=2)
+    B, width, n_pages, T = 4, len(c.table[0]), len(c.ring), c.T
+    ref = plan_reference(c.cu, c.cached, c.table, c.held, c.ring, c.head, c.count, c.page, T)
+    fill = dict(cu=c.cu, cached=c.cached, table=sum(c.table, []), held=c.held, ring=c.ring,
+                state=[c.head, c.count], held_out=[-1] * B, ring_out=[-1, -1], kv=[-1] * B,
+                positions=[-1] * T, slots=[-2] * T)
+    buf, t, at = _i32(sum(fill.values(), [])), {}, 0
+    for name, x in fill.items():
+        t[name] = buf[at:at + len(x)]
+        at += len(x)
+    t["table"] = t["table"].view(B, width)
+    ws = kda.paged_workspace_for()
+    kda.kda_paged_plan(*t.values(), page_size=c.page, workspace=ws)
+    assert kda.kda_device_status(ws) == (kda.KDA_OK, 0)
+    for name, want in ref.items():
+        assert t[name].tolist() == want, name
+    c = _verify_case(5, 3, 700, "f32", seed=3)
+    x, lens, acc = c[2], [3, 0, 2, 1, 3], [0] * 5
+    buf = _i32(x.flatten().tolist() + lens + acc + [0] * 20)
+    draft, n_draft, accepted, tokens = buf[:15].view(5, 3), buf[15:20], buf[20:25], buf[25:].view(5, 4)
+    kda.kda_verify_drafts(c[0].cuda(), c[1].cuda(), draft, c[3].cuda(), c[4].cuda(), accepted, tokens,
+                          n_draft, workspace=ws)
+    racc, rtok = verify_reference(*c, lens=lens)
+    assert torch.equal(accepted.cpu(), racc) and torch.equal(tokens.cpu(), rtok)
+
+
 # ------------------------------------------------------------------- a whole step
 
 def test_serving_steps_together():

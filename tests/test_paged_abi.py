@@ -167,6 +167,63 @@ def test_outputs_are_arrays_of_their_own(lib):
     assert lib.kda_last_launch_count() == 0
 
 
+def test_outputs_lie_over_no_part_of_another_array(lib):
+    """An output that begins or ends inside another array of the call, or inside the
+    workspace, is refused like one at its address."""
+    def pairs(call, sizes, outs, free=()):
+        # arrays of `sizes` bytes, 2^20 apart from address 2^24 on; the last is the workspace
+        for i in outs:
+            for j in range(len(sizes)):
+                if i == j or (i, j) in free or (j, i) in free:
+                    continue
+                for into in (0, sizes[j] - 16, 16 - sizes[i]):
+                    if into % 16 == 0 and -sizes[i] < into < sizes[j] and call.aligned(i, into):
+                        at = [(1 << 24) + (k << 20) for k in range(len(sizes))]
+                        at[i] = at[j] + into
+                        assert call([V(x) for x in at]) == BAD, (i, j, into)
+
+    class Call:
+        def __init__(self, fn, n):
+            self.fn, self.n = fn, n
+
+        def __call__(self, at):
+            return self.fn(at[:-1], at[-1])
+
+        def aligned(self, i, into):     # the workspace stays where it may lie
+            return i != self.n or into % 256 == 0
+
+    def plan(p, ws):
+        return lib.kda_paged_plan(*p, ctypes.byref(_args(B=8, T_total=64, n_pages=64, max_pages=8,
+                                                         workspace=ws)))
+    # cu, cached, table, held, ring, state, held_out, state_out, kv, positions, slots
+    pairs(Call(plan, 11), [48, 32, 256, 32, 256, 16, 32, 16, 32, 256, 256, 256],
+          (2, 4, 6, 7, 8, 9, 10, 11))
+
+    def attn(p, ws):
+        return lib.kda_paged_attn(*p, 0.1, 1, ctypes.byref(_args(workspace=ws)))
+    # q, k, v, table, cu, kv, out
+    sizes = [8 * 4 * 128, 8 * 16 * 2 * 128, 8 * 16 * 2 * 128, 32, 16, 16, 8 * 4 * 128, 1 << 16]
+    pairs(Call(attn, 7), sizes, (6, 7), free=((6, 0),))
+    p = [V((1 << 24) + (k << 20)) for k in range(7)]
+    for into in (16, 8 * 4 * 128 - 16, -16):      # out may be q, but not lie across it
+        p[6] = V((1 << 24) + into)
+        assert attn(p, V(1 << 20)) == BAD
+
+    def append(p, ws):
+        f = kda.KdaAppendArgs(p[6], p[7], p[8], 16, 32, 0, 1e-6)
+        return lib.kda_paged_append(*p[:6], ctypes.byref(f), ctypes.byref(_args(workspace=ws)))
+    # qkv, positions, slots, q, k, v, q_norm, k_norm, rope
+    pairs(Call(append, 9), [8 * 8 * 128, 32, 32, 8 * 4 * 128, 8 * 16 * 2 * 128, 8 * 16 * 2 * 128,
+                            256, 256, 2048, 256], (3, 4, 5, 9))
+
+    def verify(p, ws):
+        a = kda.KdaVerifyArgs(8, 3, 128, kda.KDA_F32, None, ws, 256)
+        return lib.kda_verify_drafts(*p, ctypes.byref(a))
+    # p, q, drafts, lens, u_accept, u_sample, accepted, tokens
+    pairs(Call(verify, 8), [8 * 4 * 512, 8 * 3 * 512, 96, 32, 96, 32, 32, 128, 256], (6, 7, 8))
+    assert lib.kda_last_launch_count() == 0
+
+
 def test_binding_refuses_host_tensors_types_and_shapes():
     """Tensors off the GPU never reach the library (it would read them there)."""
     kda.build()
