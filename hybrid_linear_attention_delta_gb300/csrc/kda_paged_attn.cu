@@ -34,6 +34,7 @@
 // latency, 12.3 us, of which 5 are spent before the first scores.
 #include <cuda.h>
 
+#include <cfloat>
 #include <cstring>
 
 #include "kda_paged_sched.cuh"
@@ -776,7 +777,9 @@ __device__ bool softmax_role(Ctl &ctl, const AttnArgs &a, uint32_t tmem, int s) 
             }
             const float tm = fmaxf(max3(top[0], top[1], top[2]), top[3]) * c;
             if (j == 0) {
-              if (live && tm > -INFINITY) ref = tm;
+              // (a row whose scores are all -inf so far takes the next tile's maximum,
+              // whatever that is: its weights then sum to more than 2^16)
+              if (live) ref = tm > -INFINITY ? tm : -FLT_MAX;
             } else {
               const bool move = live && !(sum_j <= 65536.f) && tm > ref;
               const float keep = move ? ex2_approx(ref - tm) : 1.f;

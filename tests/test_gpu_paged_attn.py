@@ -173,6 +173,35 @@ def test_references_move(d, Hq, Hkv, new, total, kind):
     _check(case, norm_bar=False)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new,total,hidden", [
+    ([3, 1], [700, 300], 300), ([1], [9000], 4097),   # few rows, cut items
+    ([1] * 40, [1000] * 40, 500),                     # few rows, key tiles in turn
+    ([300, 70], [1500, 900], 600),                    # two tiles of rows
+])
+def test_scores_of_minus_infinity_before_others(dtype, d, new, total, hidden):
+    """Keys that a row scores -inf fill its first tiles; the others' scores are far
+    below zero and carry all the weight."""
+    Hkv = 8 if len(new) > 2 else 2
+    case = AttnCase(new, total, Hq=8, Hkv=Hkv, d=d, page=16, dtype=dtype, seed=hidden + d)
+    for b, t in enumerate(total):
+        ids = case.table[b, :-(-t // 16)].long()
+        k = case.k[ids].reshape(-1, Hkv, d)
+        k[:t, :, 0] = 0.0
+        k[:t, :, 1] = -40.0
+        k[:min(hidden, t - 1), :, 0] = -float("inf")
+        case.k[ids] = k.reshape(-1, 16, Hkv, d)
+    case.q[..., 0], case.q[..., 1] = 1.0, 6.0 * d ** 0.5
+    ref, size, _ = case.reference()
+    out, ws = _run(case)
+    assert kda.kda_device_status(ws) == (kda.KDA_OK, 0)
+    case.k = torch.where(case.k == -float("inf"), torch.zeros_like(case.k), case.k)
+    _, _, top = case.reference()            # sum |q k| of the keys with finite scores
+    got = out.double().cpu()
+    assert ((got - ref).abs() <= case.bound(ref, size, top)).all(), float((got - ref).abs().max())
+
+
 def test_mixed_batch_of_many_requests():
     g = torch.Generator().manual_seed(11)
     new = torch.randint(0, 60, (90,), generator=g).tolist()
