@@ -174,7 +174,9 @@ kda_status kda_paged_attn(const void *q, const void *k_pages, const void *v_page
   if (st == KDA_OK) st = check_heads(a);
   if (st == KDA_OK) st = check_batch(a);
   if (st != KDA_OK) return st;
-  if (!std::isfinite(scale) || (causal != 0 && causal != 1)) return KDA_ERR_INVALID_ARG;
+  // (the kernels' scale: scores in powers of two)
+  if (!std::isfinite(scale * 1.4426950408889634f) || (causal != 0 && causal != 1))
+    return KDA_ERR_INVALID_ARG;
   st = check_workspace(a->workspace, a->workspace_bytes, kda_paged_workspace_bytes(a));
   if (st != KDA_OK) return st;
   if (a->B == 0 || a->T_total == 0) return KDA_OK;

@@ -1126,9 +1126,9 @@ cudaError_t launch_d(const PagedAttnPlan &p) {
     return cudaErrorInvalidValue;
   AttnArgs a;
   a.p = p;
-  // (never 0: a masked score stays -inf in powers of two, and scores below
-  // 10^22 times 10^-30 are 0 to any rounding)
-  a.c = fmaxf(fabsf(p.scale) * 1.4426950408889634f, 1e-30f);
+  // (never 0, so that a masked score stays -inf in powers of two; the smallest float
+  // times any finite score is 0 to any rounding of its power)
+  a.c = fmaxf(fabsf(p.scale) * 1.4426950408889634f, FLT_TRUE_MIN);
   a.neg_q = p.scale < 0.f;
   a.tpt = kRows / p.G;
   attn_kernel<D, LONG><<<kPagedMaxCtas, kThreads, smem_bytes<D>(), p.stream>>>(tq, tk, tv, a);

@@ -164,7 +164,7 @@ kda_status kda_paged_append(const void *qkv, const int32_t *positions, const int
  * block_table [B][max_pages] int32
  * cu_seqlens [B+1] int32     cu[0] = 0, non-decreasing, cu[B] <= T_total
  * kv_lens    [B] int32       keys of the request, the new tokens' own included
- * scale      finite
+ * scale      finite, as scale * log2(e) is too
  *
  * bf16 runs on the tensor cores (fp32 scores, sums and accumulators; the
  * weights are rounded to bf16 for the product with v), fp32 in fp32

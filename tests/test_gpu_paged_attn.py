@@ -101,6 +101,17 @@ def test_not_causal_and_scale(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_smallest_scales(dtype):
+    """Queries and keys so large that their products need a scale of 10^-34, and a
+    scale of zero whatever the products."""
+    case = AttnCase([40, 1], [500, 77], Hq=4, Hkv=1, d=64, page=64, dtype=dtype, seed=2)
+    case.q, case.k = (x.double().mul(2.0 ** 56).to(case.dtype) for x in (case.q, case.k))
+    _check(case, scale=2.0 ** -115)
+    _check(case, scale=-2.0 ** -115)
+    _check(case, scale=0.0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("Hq,Hkv,d", [(1, 1, 128), (8, 1, 128), (16, 8, 64)])
 def test_long_context_is_split_and_joined(dtype, Hq, Hkv, d):
     """Few rows over many keys: pieces on every SM, joined in order."""

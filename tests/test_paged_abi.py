@@ -167,6 +167,12 @@ def test_outputs_are_arrays_of_their_own(lib):
     assert lib.kda_last_launch_count() == 0
 
 
+def test_attention_refuses_scales_that_overflow_in_powers_of_two(lib):
+    for scale in (2.4e38, -3.4e38):
+        assert _attn(lib, _args(), [V((1 << 24) + (k << 20)) for k in range(7)], scale=scale) == BAD
+    assert lib.kda_last_launch_count() == 0
+
+
 def test_outputs_lie_over_no_part_of_another_array(lib):
     """An output that begins or ends inside another array of the call, or inside the
     workspace, is refused like one at its address."""
