@@ -360,6 +360,23 @@ def test_many_short_requests(dtype):
     _check(AttnCase(new, total, Hq=2, Hkv=1, d=64, page=16, dtype=dtype, seed=32, pad=5))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_f32_counters_of_every_cta_are_left_at_zero(d):
+    """Cut items all over the line: the counters of all CTAs, 304 of them with 64
+    channels, are as they were found, and the next call joins as this one did."""
+    case = AttnCase([1, 3, 1, 40] * 5, [9000, 4000, 2500, 3100] * 5, Hq=16, Hkv=8, d=d, page=32,
+                    dtype="f32", seed=d)
+    t = case.cuda()
+    first, ws = _run(case, dev=t)
+    assert int(ws[256:256 + 8 * 304].sum()) == 0
+    ref, size, top = case.reference()
+    assert ((first.double().cpu() - ref).abs() <= case.bound(ref, size, top)).all()
+    for _ in range(3):
+        again, _ = _run(case, dev=t, ws=ws)
+        assert torch.equal(again, first)
+    assert kda.kda_device_status(ws) == (kda.KDA_OK, 0)
+
+
 def test_two_calls_at_once():
     """Calls on two streams, each with a workspace of its own, in flight together."""
     cases = [AttnCase([1, 40], [3000, 700], Hq=8, Hkv=2, d=d, page=16, dtype="bf16", seed=d)

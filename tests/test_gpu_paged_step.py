@@ -291,6 +291,39 @@ def test_append_skips_padding_and_bad_tokens():
     _check_append(c, 4, 2, 64, 16, "half", skipped=1 | 1024)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("mode", ["half", "interleaved"])
+def test_append_beyond_32_bit_offsets(dtype, mode):
+    """More than 2^31 elements in the projection, the queries and the pages."""
+    T, Hq, Hkv, d, page = 176000, 96, 16, 128, 64
+    n_pages = (1 << 31) // (page * Hkv * d) + 300
+    dt = DT[dtype]
+    g = torch.Generator(device="cuda").manual_seed(7)
+    qkv = torch.zeros((T, Hq + 2 * Hkv, d), dtype=dt, device="cuda")
+    rows = torch.cat([torch.arange(64), torch.arange(T // 2, T // 2 + 64), torch.arange(T - 64, T)]).cuda()
+    qkv[rows] = torch.randn((192, Hq + 2 * Hkv, d), generator=g, device="cuda").to(dt)
+    slot = torch.randperm(n_pages * page, generator=g, device="cuda")[:T].to(I32)
+    slot[rows[-64:]] = torch.arange(n_pages * page - 64, n_pages * page, device="cuda").to(I32)
+    taken = (slot[:-64] >= n_pages * page - 64).nonzero()[:, 0]
+    slot[taken] = -1                      # (slots are distinct)
+    pos = torch.arange(T, device="cuda").to(I32)
+    wq, wk = (1 + 0.2 * torch.randn(d, generator=g, device="cuda") for _ in range(2))
+    rope = kda.rope_table(T, d)
+    q = torch.zeros((T, Hq, d), dtype=dt, device="cuda")
+    k, v = (torch.zeros((n_pages, page, Hkv, d), dtype=dt, device="cuda") for _ in range(2))
+    ws = kda.paged_workspace_for()
+    kda.kda_paged_append(qkv, wq, wk, rope, pos, slot, q, k, v, rope_mode=mode, workspace=ws)
+    assert kda.kda_device_status(ws) == (kda.KDA_OK, 0)
+    rows = rows[slot[rows] >= 0]
+    (rq, sq), (rk, sk), rv = append_reference(qkv[rows].cpu(), wq.cpu(), wk.cpu(), rope.cpu(),
+                                              pos[rows].cpu(), Hq, Hkv, mode, 1e-6)
+    at = slot[rows].long()
+    for got, ref, size in ((q[rows], rq, sq), (k.view(-1, Hkv, d)[at], rk, sk)):
+        tol = half_step(dt) * ref.abs() * 1.01 + (d / 2 + 16) * half_step(torch.float32) * size + 1e-30
+        assert ((got.double().cpu() - ref).abs() <= tol).all()
+    assert torch.equal(v.view(-1, Hkv, d)[at], qkv[rows][:, Hq + Hkv:])
+
+
 def test_append_zero_tokens():
     ws = kda.paged_workspace_for()
     e = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")
@@ -337,6 +370,36 @@ def test_verify_matches_plain_form(dtype, probs, N, n, V):
         racc, rtok = verify_reference(*c)
         assert bits == 0
         assert torch.equal(acc, racc) and torch.equal(tok, rtok)
+
+
+# More segments of 1024 tokens to a CTA than a warp has lanes,
+# with aligned rows and others; more than it has threads; so many that
+# they are longer; the largest vocabulary; the most drafts.
+@pytest.mark.parametrize("N,n,V,dtype", [
+    (64, 1, 151936, "bf16"), (128, 1, 128256, "f32"), (160, 1, 40009, "bf16"), (160, 1, 600000, "f32"),
+    (160, 0, 600001, "bf16"), (8, 1, (1 << 23) + 5, "f32"), (160, 1, 5000000, "bf16"),
+    (154, 0, 4194305, "f32"), (2, 1, 1 << 24, "f32"), (1, 1024, 257, "f32"), (3, 1000, 5000, "bf16")])
+@pytest.mark.parametrize("probs", [True, False])
+def test_verify_sizes_up_to_the_limits(probs, N, n, V, dtype):
+    g = torch.Generator(device="cuda").manual_seed(V + n)
+    dt = DT[dtype]
+    p = torch.empty((N, n + 1, V), dtype=dt, device="cuda")
+    q = torch.empty((N, n, V), dtype=dt, device="cuda")
+    x = torch.zeros((N, n), dtype=I32, device="cuda")
+    for i in range(N):
+        logits = 3 * torch.randn((n + 1, V), generator=g, device="cuda")
+        p[i] = torch.softmax(logits, -1).to(dt)
+        # few of the drafts stand, or nearly all of them where there are many
+        noise = 0.02 if n > 8 else 0.6
+        q[i] = torch.softmax(logits[:n] + noise * torch.randn((n, V), generator=g, device="cuda"), -1).to(dt)
+        if n:
+            x[i] = torch.multinomial(q[i].float(), 1, generator=g)[:, 0].to(I32)
+    ua = torch.rand((N, n), generator=g, device="cuda") * (0.2 if n > 8 else 1.0)
+    c = [p, q if probs else None, x, ua, torch.rand((N,), generator=g, device="cuda")]
+    acc, tok, bits = _verify(c)
+    racc, rtok = verify_reference(*c)
+    assert bits == 0
+    assert torch.equal(acc, racc) and torch.equal(tok, rtok)
 
 
 def test_verify_ragged_drafts():
