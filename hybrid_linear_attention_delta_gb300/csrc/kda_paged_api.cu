@@ -205,15 +205,18 @@ kda_status kda_paged_attn(const void *q, const void *k_pages, const void *v_page
   p.part_ml = reinterpret_cast<float *>(ws + lay.ml_off);
   p.part_rows = kda::paged_part_rows(a->T_total, G, a->dtype);
   // What an item's start and end cost, and the shortest stretch worth a join, in
-  // keys.  Where requests bring a tile of rows and more, both are longer.  (bf16,
+  // keys.  In bf16 both are longer where requests bring a tile of rows and more.  (bf16,
   // item cost 128, 192, 256, 320, 384: mixed batch of 24, 64 channels, 910, 875,
   // 854, 855, 858 us; 128 channels 1244, 1192, 1168, 1171, 1154; 100 decodes of up
   // to 1000 keys with 64, 128, 192, 256: 101, 90, 82, 78 us.  Shortest stretch 768,
   // 896, 1024: a prompt of 1000 tokens, 32/8 heads, 46.7, 37.1, 38.2 us; 200 tokens
   // over 500 keys 31.9, 32.8, 33.9; one token: the same from 256 to 384.  fp32, item
-  // cost 32, 64, 128, 256: 8 requests of up to 301 tokens 148, 134, 129, 140 us.)
+  // cost 32, 64, 128, 256: 8 requests of up to 301 tokens 148, 134, 129, 140 us; shortest
+  // stretch 384, 512, 768, 1024: a prompt of 1000 tokens, 8/2 heads of 64 channels, 66, 71,
+  // 78, 96; 200 tokens over 500 keys, 128 channels, 63, 85, 107, 137; 100 over 8000 90, 91,
+  // 118, 97; 8 requests of up to 301 120, 120, 120, 142; 8 x 1000 tokens the same.)
   const bool wide = (int64_t)a->T_total * G >= 128ll * a->B, bf16 = a->dtype == KDA_BF16;
-  p.min_stretch = !wide ? 384 : bf16 ? 896 : 768;
+  p.min_stretch = bf16 && wide ? 896 : 384;
   p.item_cost = !bf16 ? 128 : wide ? 320 : 256;
   p.stream = static_cast<cudaStream_t>(a->stream);
   return launch(a->stream, a->ev_begin, a->ev_end, [&] {
