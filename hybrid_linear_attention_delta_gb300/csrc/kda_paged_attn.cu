@@ -804,7 +804,6 @@ __device__ bool softmax_role(Ctl &ctl, const AttnArgs &a, uint32_t tmem, int s) 
           }
           const uint64_t c2 = pair(c, c), ref2 = pair(-ref, -ref);
           uint64_t sum[2] = {0ull, 0ull};
-          uint32_t pk0[16];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             uint32_t pk[16];
@@ -818,14 +817,8 @@ __device__ bool softmax_role(Ctl &ctl, const AttnArgs &a, uint32_t tmem, int s) 
               sum[i & 1] = add2(sum[i & 1], pair(u, v));
               pk[i] = pack_bf16x2(u, v);
             }
-            // (the products that read the P before are given the time of two
-            // quarters to end)
-            if (q == 1 && !own()) return false;
-            if (q == 1) tmem_st16(tp, pk0);
-            if (q > 0) tmem_st16(tp + q * 16, pk);
-            else
-#pragma unroll
-              for (int i = 0; i < 16; ++i) pk0[i] = pk[i];
+            if (q == 0 && !own()) return false;
+            tmem_st16(tp + q * 16, pk);
           }
           float su, sv;
           unpair(add2(sum[0], sum[1]), su, sv);
