@@ -30,8 +30,11 @@
 // outputs): 2.25 ms, 1.71 PFLOP/s (cuBLAS: 1.87), 2.5 ms in a loop at the power
 // limit.  Decode of 256 requests over 511 to 8191 keys: HBM, 0.72 ms, 6.7 TB/s
 // (99% of a copy); 64 x 8 tokens over 1000 to 32760 keys, 32 / 4 heads: 0.343 ms,
-// 6.4 TB/s.  64 channels: the softmax, 1.0 PFLOP/s.  One token over 777 keys:
-// latency, 12.3 us, of which 5 are spent before the first scores.
+// 6.4 TB/s.  64 channels: the same chunk 1.84 ms, 1.04 PFLOP/s, a mixed batch of 24
+// requests 0.84 to 0.90 ms, by no pipe (tensor 39 to 43% busy, issue 47%) but by the
+// waits of a stream's softmax and products for each other; the same decode 0.53 ms,
+// 4.5 TB/s, and 1.45 times its bytes are read.  One token over 777 keys: latency,
+// 12.3 us, of which 5 are spent before the first scores.
 #include <cuda.h>
 
 #include <cfloat>

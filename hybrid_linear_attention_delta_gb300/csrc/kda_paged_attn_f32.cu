@@ -12,8 +12,10 @@
 // 0.89 against 0.82 ms), four with 128, whose tiles leave room for one.  The next
 // tile is copied to shared memory while one is worked on.  Bound by the fp32 pipes
 // and the shared-memory reads that feed them, and where items are short by their
-// start and their joining (8 requests of up to 301 tokens over up to 2800 keys: 122
-// us, 28 TFLOP/s; 1000 tokens each: 39 TFLOP/s).
+// start and their joining (8 requests of up to 301 tokens over up to 2800 keys: 120
+// us, 28 TFLOP/s; 1000 tokens each: 39 TFLOP/s).  Decode of 64 requests over 511 to 8191
+// keys, 32 / 8 heads: 0.41 ms, 2.7 TB/s, with 64 channels, 1.34 ms, 1.6 TB/s, with 128,
+// where the scores and outputs of 8 and 16 rows are made for the 4 that there are.
 #include "kda_paged_sched.cuh"
 
 namespace kda {

@@ -6,8 +6,8 @@
 //   page j of b = block_table[b][j]                          j < held_b
 //               = ring[(head + sum_{c<b} need_c + j - held_b) mod n]   else
 //
-// Latency-bound: a few bytes per request and eight per token (64 requests: 3.9
-// us, 2048 requests with 60000 tokens: 9 us).  Every CTA scans
+// Latency-bound: a few bytes per request and eight per token (64 requests: 4.0
+// us, 2048 requests with 60000 tokens: 9.7 us).  Every CTA scans
 // all requests itself (three words each, staged in shared memory) and then fills its own slice
 // of tokens and rows, so nothing waits for another CTA: pages are taken from
 // the front of the ring and given back behind its end, which never overlap,

@@ -120,7 +120,8 @@ kda_status kda_paged_plan(const int32_t *cu_seqlens, const int32_t *cached_lens,
  *
  * with pairs (a, b) = (x'[i], x'[i + rot_dim/2]) (rope_mode 0) or (x'[2i],
  * x'[2i + 1]) (rope_mode 1), i < rot_dim / 2; cos = rope[pos][i], sin =
- * rope[pos][rot_dim/2 + i].  Computed in fp32, rounded once.
+ * rope[pos][rot_dim/2 + i].  Computed in fp32, rounded once (the sum of a head's squares
+ * must not overflow: channels below 10^18 in magnitude).
  *
  * qkv        [T_total][Hq + 2 Hkv][d] dtype   q heads, k heads, v heads
  * positions  [T_total] int32   in [0, max_pos) (read when rot_dim > 0)
@@ -169,7 +170,8 @@ kda_status kda_paged_append(const void *qkv, const int32_t *positions, const int
  * bf16 runs on the tensor cores (fp32 scores, sums and accumulators; the
  * weights are rounded to bf16 for the product with v), fp32 in fp32
  * arithmetic.  Long key ranges are split over the SMs and joined in a fixed
- * order, so results do not change from run to run.
+ * order, so results do not change from run to run.  Sums of weighted values do not
+ * overflow while the values are below 10^24 in magnitude.
  * Bad cu_seqlens (bit 4): nothing is written.  kv_lens[b] negative or beyond
  * max_pages pages (bit 128): the request's rows are left as they were.  A page
  * number outside [0, n_pages) (bit 512): that page reads as zeros.
@@ -190,8 +192,8 @@ kda_status kda_paged_attn(const void *q, const void *k_pages, const void *v_page
  * probabilities (looked-up drafts) q is 1 at the drafted token and 0
  * elsewhere.  n_draft = 0 is plain sampling.
  *
- * The comparisons and cumulative sums are carried to about 48 bits, so that a
- * far token of a large vocabulary is not lost to rounding.
+ * The comparisons are exact and the cumulative sums carried to about 46 bits, so
+ * that a far token of a large vocabulary is not lost to rounding.
  *
  * target_probs [N][n_draft+1][V] dtype, draft_probs [N][n_draft][V] dtype or NULL:
  *              finite, >= 0, rows sum to about 1
