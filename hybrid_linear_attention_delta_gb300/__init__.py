@@ -28,7 +28,8 @@ EXPORTS = ("kda_prefill_varlen", "kda_prefill_varlen_retain", "kda_decode", "kda
            "kda_snapshot_count", "kda_device_status", "kda_status_string",
            "kda_last_launch_count",
            "kda_paged_plan", "kda_paged_append", "kda_paged_attn", "kda_verify_drafts",
-           "kda_paged_workspace_bytes")
+           "kda_paged_workspace_bytes",
+           "kda_paged_append_q8", "kda_paged_attn_q8", "kda_token_logprobs")
 
 
 class KdaArgs(ctypes.Structure):
@@ -75,6 +76,15 @@ class KdaVerifyArgs(ctypes.Structure):
     """Mirror of ``kda_verify_args`` in include/kda_paged.h."""
     _fields_ = [("N", ctypes.c_int32), ("n_draft", ctypes.c_int32), ("V", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("stream", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+                ("ev_begin", ctypes.c_void_p), ("ev_end", ctypes.c_void_p)]
+
+
+class KdaLogprobsArgs(ctypes.Structure):
+    """Mirror of ``kda_logprobs_args`` in include/kda_paged.h."""
+    _fields_ = [("N", ctypes.c_int32), ("V", ctypes.c_int32), ("n_top", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("stride", ctypes.c_int64), ("scale", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("stream", ctypes.c_void_p),
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
                 ("ev_begin", ctypes.c_void_p), ("ev_end", ctypes.c_void_p)]
 
@@ -139,6 +149,12 @@ def lib(path: Optional[str] = None) -> ctypes.CDLL:
         L.kda_paged_append.restype = ctypes.c_int
         L.kda_paged_attn.argtypes = [V] * 7 + [ctypes.c_float, I32, P]
         L.kda_paged_attn.restype = ctypes.c_int
+        L.kda_paged_append_q8.argtypes = [V] * 8 + [ctypes.POINTER(KdaAppendArgs), P]
+        L.kda_paged_append_q8.restype = ctypes.c_int
+        L.kda_paged_attn_q8.argtypes = [V] * 9 + [ctypes.c_float, I32, P]
+        L.kda_paged_attn_q8.restype = ctypes.c_int
+        L.kda_token_logprobs.argtypes = [V] * 7 + [ctypes.POINTER(KdaLogprobsArgs)]
+        L.kda_token_logprobs.restype = ctypes.c_int
         L.kda_verify_drafts.argtypes = [V] * 8 + [ctypes.POINTER(KdaVerifyArgs)]
         L.kda_verify_drafts.restype = ctypes.c_int
         if path:
@@ -487,14 +503,8 @@ def kda_paged_plan(cu_seqlens, cached_lens, block_table, held, free_ring, ring, 
     _launch("kda_paged_plan", lib().kda_paged_plan, args, a, dev, workspace, stream, events)
 
 
-def kda_paged_append(qkv, q_norm, k_norm, rope, positions, slot_map, q_out, k_pages, v_pages, *,
-                     workspace, rope_mode: str = "half", norm_eps: float = 1e-6, stream=None,
-                     events=None) -> None:
-    """Per-head RMSNorm and rotation of q and k, q out, k and v into their cache
-    slots (see kda_paged_append in include/kda_paged.h).  qkv [T, Hq + 2 Hkv, d];
-    q_norm, k_norm [d] fp32 or None; rope [max_pos, rot_dim] fp32 or None (see
-    rope_table; without it positions are not read and may be None); pages
-    [n_pages, page_size, Hkv, d]."""
+def _append(what, qkv, q_norm, k_norm, rope, positions, slot_map, q_out, k_pages, v_pages, scales,
+            workspace, rope_mode, norm_eps, stream, events):
     torch = _get_torch()
     dt, dev, i32, f32 = qkv.dtype, qkv.get_device(), torch.int32, torch.float32
     code = _dtype_code(qkv)
@@ -510,12 +520,66 @@ def kda_paged_append(qkv, q_norm, k_norm, rope, positions, slot_map, q_out, k_pa
         f.max_pos, f.rot_dim = _shape("rope", rope, 2)
         f.rope = _check("rope", rope, rope.shape, f32, dev)
         pos = _check("positions", positions, (T,), i32, dev)
+    kv_dt, ps, fn = (dt, (), lib().kda_paged_append) if scales is None else (
+        torch.float8_e4m3fn, _scales(scales, pages, dev), lib().kda_paged_append_q8)
     args = (_check("qkv", qkv, (T, Hq + 2 * Hkv, d), dt, dev), pos,
             _check("slot_map", slot_map, (T,), i32, dev),
-            _check("q_out", q_out, (T, Hq, d), dt, dev), _check("k_pages", k_pages, pages, dt, dev),
-            _check("v_pages", v_pages, pages, dt, dev), ctypes.byref(f))
+            _check("q_out", q_out, (T, Hq, d), dt, dev),
+            _check("k_pages", k_pages, pages, kv_dt, dev),
+            _check("v_pages", v_pages, pages, kv_dt, dev), *ps, ctypes.byref(f))
     a = KdaPagedArgs(0, T, Hq, Hkv, d, page_size, n_pages, 0, code)
-    _launch("kda_paged_append", lib().kda_paged_append, args, a, dev, workspace, stream, events)
+    _launch(what, fn, args, a, dev, workspace, stream, events)
+
+
+def _scales(scales, pages, dev):
+    """Addresses of an 8-bit cache's scales of keys and values."""
+    n_pages, page_size, Hkv, _ = pages
+    shape, f32 = (n_pages, page_size // 16, Hkv), _torch.float32
+    return (_check("k_scales", scales[0], shape, f32, dev),
+            _check("v_scales", scales[1], shape, f32, dev))
+
+
+def kda_paged_append(qkv, q_norm, k_norm, rope, positions, slot_map, q_out, k_pages, v_pages, *,
+                     workspace, rope_mode: str = "half", norm_eps: float = 1e-6, stream=None,
+                     events=None) -> None:
+    """Per-head RMSNorm and rotation of q and k, q out, k and v into their cache
+    slots (see kda_paged_append in include/kda_paged.h).  qkv [T, Hq + 2 Hkv, d];
+    q_norm, k_norm [d] fp32 or None; rope [max_pos, rot_dim] fp32 or None (see
+    rope_table; without it positions are not read and may be None); pages
+    [n_pages, page_size, Hkv, d]."""
+    _append("kda_paged_append", qkv, q_norm, k_norm, rope, positions, slot_map, q_out, k_pages,
+            v_pages, None, workspace, rope_mode, norm_eps, stream, events)
+
+
+def kda_paged_append_q8(qkv, q_norm, k_norm, rope, positions, slot_map, q_out, k_pages, v_pages,
+                        k_scales, v_scales, *, workspace, rope_mode: str = "half",
+                        norm_eps: float = 1e-6, stream=None, events=None) -> None:
+    """kda_paged_append into an 8-bit cache (see kda_paged_append_q8 in
+    include/kda_paged.h): pages of torch.float8_e4m3fn, scales [n_pages,
+    page_size / 16, Hkv] fp32, which grow with what comes into their blocks."""
+    _append("kda_paged_append_q8", qkv, q_norm, k_norm, rope, positions, slot_map, q_out, k_pages,
+            v_pages, (k_scales, v_scales), workspace, rope_mode, norm_eps, stream, events)
+
+
+def _attn(what, q, k_pages, v_pages, scales, block_table, cu_seqlens, kv_lens, out, workspace,
+          scale, causal, stream, events):
+    torch = _get_torch()
+    i32, dt, dev = torch.int32, q.dtype, q.get_device()
+    code = _dtype_code(q)
+    pages = n_pages, page_size, Hkv, d = _shape("k_pages", k_pages, 4)
+    T, Hq, _ = _shape("q", q, 3)
+    rows = (T, Hq, d)
+    B, width = _shape("block_table", block_table, 2)
+    kv_dt, ps, fn = (dt, (), lib().kda_paged_attn) if scales is None else (
+        torch.float8_e4m3fn, _scales(scales, pages, dev), lib().kda_paged_attn_q8)
+    args = (_check("q", q, rows, dt, dev), _check("k_pages", k_pages, pages, kv_dt, dev),
+            _check("v_pages", v_pages, pages, kv_dt, dev), *ps,
+            _check("block_table", block_table, (B, width), i32, dev),
+            _check("cu_seqlens", cu_seqlens, (B + 1,), i32, dev),
+            _check("kv_lens", kv_lens, (B,), i32, dev), _check("out", out, rows, dt, dev),
+            d ** -0.5 if scale is None else scale, 1 if causal else 0)
+    a = KdaPagedArgs(B, T, Hq, Hkv, d, page_size, n_pages, width, code)
+    _launch(what, fn, args, a, dev, workspace, stream, events)
 
 
 def kda_paged_attn(q, k_pages, v_pages, block_table, cu_seqlens, kv_lens, out, *, workspace,
@@ -525,20 +589,18 @@ def kda_paged_attn(q, k_pages, v_pages, block_table, cu_seqlens, kv_lens, out, *
     kda_paged_attn in include/kda_paged.h).  q, out [T, Hq, d]; pages [n_pages,
     page_size, Hkv, d]; block_table [B, max_pages], cu_seqlens [B + 1] and
     kv_lens [B] int32.  scale: 1 / sqrt(d) when not given."""
-    i32, dt, dev = _get_torch().int32, q.dtype, q.get_device()
-    code = _dtype_code(q)
-    pages = n_pages, page_size, Hkv, d = _shape("k_pages", k_pages, 4)
-    T, Hq, _ = _shape("q", q, 3)
-    rows = (T, Hq, d)
-    B, width = _shape("block_table", block_table, 2)
-    args = (_check("q", q, rows, dt, dev), _check("k_pages", k_pages, pages, dt, dev),
-            _check("v_pages", v_pages, pages, dt, dev),
-            _check("block_table", block_table, (B, width), i32, dev),
-            _check("cu_seqlens", cu_seqlens, (B + 1,), i32, dev),
-            _check("kv_lens", kv_lens, (B,), i32, dev), _check("out", out, rows, dt, dev),
-            d ** -0.5 if scale is None else scale, 1 if causal else 0)
-    a = KdaPagedArgs(B, T, Hq, Hkv, d, page_size, n_pages, width, code)
-    _launch("kda_paged_attn", lib().kda_paged_attn, args, a, dev, workspace, stream, events)
+    _attn("kda_paged_attn", q, k_pages, v_pages, None, block_table, cu_seqlens, kv_lens, out,
+          workspace, scale, causal, stream, events)
+
+
+def kda_paged_attn_q8(q, k_pages, v_pages, k_scales, v_scales, block_table, cu_seqlens, kv_lens,
+                      out, *, workspace, scale: Optional[float] = None, causal: bool = True,
+                      stream=None, events=None) -> None:
+    """kda_paged_attn over an 8-bit cache (see kda_paged_attn_q8 in
+    include/kda_paged.h): pages of torch.float8_e4m3fn and their scales [n_pages,
+    page_size / 16, Hkv] fp32; q and out bf16 or fp32."""
+    _attn("kda_paged_attn_q8", q, k_pages, v_pages, (k_scales, v_scales), block_table, cu_seqlens,
+          kv_lens, out, workspace, scale, causal, stream, events)
 
 
 def kda_verify_drafts(target_probs, draft_probs, draft_tokens, u_accept, u_sample, accepted,
@@ -566,6 +628,33 @@ def kda_verify_drafts(target_probs, draft_probs, draft_tokens, u_accept, u_sampl
             _check("tokens", tokens, (N, n1), i32, dev))
     a = KdaVerifyArgs(N, n, V, code)
     _launch("kda_verify_drafts", lib().kda_verify_drafts, args, a, dev, workspace, stream, events)
+
+
+def kda_token_logprobs(logits, tokens, logprobs, entropy, ranks, top_ids=None, top_logprobs=None, *,
+                       workspace, scale: float = 1.0, stream=None, events=None) -> None:
+    """Log probabilities and ranks of a token a row, the rows' entropies and their
+    most likely tokens (see kda_token_logprobs in include/kda_paged.h).  logits
+    [N, V], rows any stride apart; tokens, ranks [N] int32, logprobs, entropy [N]
+    fp32, each or None (without tokens no logprobs and ranks); top_ids int32 and
+    top_logprobs fp32 [N, n_top], or None.  scale: one over the temperature."""
+    torch = _get_torch()
+    i32, f32, dev = torch.int32, torch.float32, logits.get_device()
+    code = _dtype_code(logits)
+    N, V = _shape("logits", logits, 2)
+    stride = logits.stride(0) if N > 1 else V
+    if logits.stride(1) != 1 and V > 1 or stride < V:
+        raise ValueError("logits has its rows' elements side by side, row behind row")
+    K = 0 if top_ids is None else _shape("top_ids", top_ids, 2)[1]
+    if (top_ids is None) != (top_logprobs is None):
+        raise ValueError("top_ids and top_logprobs come together")
+    per_row = (N,)
+    opt = lambda name, t, shape, dt: None if t is None else _check(name, t, shape, dt, dev)
+    args = (logits.data_ptr(), opt("tokens", tokens, per_row, i32),
+            opt("logprobs", logprobs, per_row, f32), opt("entropy", entropy, per_row, f32),
+            opt("ranks", ranks, per_row, i32), opt("top_ids", top_ids, (N, K), i32),
+            opt("top_logprobs", top_logprobs, (N, K), f32))
+    a = KdaLogprobsArgs(N, V, K, code, stride, scale)
+    _launch("kda_token_logprobs", lib().kda_token_logprobs, args, a, dev, workspace, stream, events)
 
 
 def kda_device_status(workspace, stream=None):

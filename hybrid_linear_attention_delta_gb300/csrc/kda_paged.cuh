@@ -15,6 +15,8 @@ enum PagedErrBits : uint32_t {
   ERR_BAD_POS = 1024u,
   ERR_BAD_TOKEN = 2048u,
   ERR_NO_MASS = 4096u,
+  ERR_BAD_SCALE = 8192u,
+  ERR_BAD_LOGIT = 16384u,
 };
 
 constexpr int kMaxRequests = 8192;
@@ -31,6 +33,7 @@ struct AppendPlan {
   const void *qkv;
   const int32_t *positions, *slots;
   void *q, *k_pages, *v_pages;
+  float *k_scales, *v_scales;  // the 8-bit cache's
   const float *q_norm, *k_norm, *rope;
   int32_t T, Hq, Hkv, d, dtype, max_pos, rot, mode;
   int64_t n_slots;
@@ -48,6 +51,7 @@ constexpr int kPagedF32Ctas = 2 * kPagedMaxCtas, kPagedF32Rows = 64;
 
 struct PagedAttnPlan {
   const void *q, *k, *v;
+  const float *k_scales, *v_scales;  // the 8-bit cache's
   const int32_t *table, *cu, *kv_lens;
   void *out;
   float scale;
@@ -94,6 +98,18 @@ struct VerifyPlan {
   cudaStream_t stream;
 };
 
+struct LogprobsPlan {
+  const void *logits;
+  const int32_t *tokens;
+  float *logprobs, *entropy, *top_logprobs;
+  int32_t *ranks, *top_ids;
+  int64_t stride;  // elements between rows
+  int32_t N, V, n_top, dtype;
+  float scale;
+  uint32_t *err;
+  cudaStream_t stream;
+};
+
 // Two fp32 values in one 64-bit register and the operations on both at once.
 __device__ __forceinline__ uint64_t pair(float lo, float hi) {
   uint64_t r;
@@ -124,6 +140,10 @@ cudaError_t launch_paged_append(const AppendPlan &p);
 cudaError_t launch_paged_attn_bf16(const PagedAttnPlan &p);
 cudaError_t launch_paged_attn_f32(const PagedAttnPlan &p);
 cudaError_t launch_verify(const VerifyPlan &p);
+cudaError_t launch_paged_append_q8(const AppendPlan &p);
+cudaError_t launch_paged_attn_q8_f32(const PagedAttnPlan &p);
+cudaError_t launch_paged_attn_q8_bf16(const PagedAttnPlan &p);
+cudaError_t launch_logprobs(const LogprobsPlan &p);
 
 // launches of the last successful call on this host thread (kda_api.cu)
 void set_last_launches(int32_t n);

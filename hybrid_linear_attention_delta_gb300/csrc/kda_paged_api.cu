@@ -12,6 +12,8 @@ bool aligned(const void *p, uintptr_t n) { return p && (reinterpret_cast<uintptr
 
 int64_t elem_bytes(int32_t dtype) { return dtype == KDA_F32 ? 4 : 2; }
 
+constexpr int kScaleTokens = 16;  // tokens of a scale of the 8-bit cache
+
 kda_status check_workspace(const void *ws, size_t bytes, size_t need) {
   return aligned(ws, 256) && bytes >= need ? KDA_OK : KDA_ERR_INVALID_ARG;
 }
@@ -78,6 +80,124 @@ kda_status launch(void *stream, void *ev_begin, void *ev_end, Launch f) {
   return KDA_OK;
 }
 
+// kda_paged_append, and kda_paged_append_q8 with scales.
+kda_status append(const void *qkv, const int32_t *positions, const int32_t *slot_map, void *q_out,
+                  void *k_pages, void *v_pages, float *k_scales, float *v_scales, bool q8,
+                  const kda_append_args *f, const kda_paged_args *a) {
+  kda::set_last_launches(0);
+  if (!a || !f) return KDA_ERR_INVALID_ARG;
+  kda_status st = check_pages(a);
+  if (st == KDA_OK) st = check_heads(a);
+  if (st == KDA_OK) st = check_workspace(a->workspace, a->workspace_bytes, 256);
+  if (st != KDA_OK) return st;
+  if (a->T_total < 0 || f->rot_dim < 0 || f->rot_dim > a->d || !(f->norm_eps >= 0.f) ||
+      (f->rope_mode != 0 && f->rope_mode != 1))
+    return KDA_ERR_INVALID_ARG;
+  if (f->rot_dim % 16 != 0) return KDA_ERR_UNSUPPORTED;
+  if (f->rot_dim > 0 && (!aligned(f->rope, 16) || f->max_pos <= 0)) return KDA_ERR_INVALID_ARG;
+  if ((f->q_norm && !aligned(f->q_norm, 16)) || (f->k_norm && !aligned(f->k_norm, 16)))
+    return KDA_ERR_INVALID_ARG;
+  if (a->T_total == 0) return KDA_OK;
+  if (!aligned(qkv, 16) || !aligned(q_out, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) ||
+      !aligned(slot_map, 4) || (f->rot_dim > 0 && !aligned(positions, 4)) ||
+      (q8 && (!aligned(k_scales, 4) || !aligned(v_scales, 4))))
+    return KDA_ERR_INVALID_ARG;
+  const int64_t row = (int64_t)a->d * elem_bytes(a->dtype), T = a->T_total;
+  const int64_t slots = (int64_t)a->n_pages * a->page_size;
+  const int64_t pool = slots * a->Hkv * (q8 ? a->d : row);
+  const int64_t scales = q8 ? slots / kScaleTokens * a->Hkv * 4 : 0;
+  if (overlap({{q_out, T * a->Hq * row}, {k_pages, pool}, {v_pages, pool}, {a->workspace, 256},
+               {k_scales, scales}, {v_scales, scales},
+               {qkv, T * (a->Hq + 2 * a->Hkv) * row}, {slot_map, T * 4},
+               {positions, f->rot_dim > 0 ? T * 4 : 0}, {f->q_norm, a->d * 4}, {f->k_norm, a->d * 4},
+               {f->rope, 4ll * f->max_pos * f->rot_dim}}, 6))
+    return KDA_ERR_INVALID_ARG;
+  kda::AppendPlan p = {};
+  p.qkv = qkv; p.positions = positions; p.slots = slot_map;
+  p.q = q_out; p.k_pages = k_pages; p.v_pages = v_pages;
+  p.k_scales = k_scales; p.v_scales = v_scales;
+  p.q_norm = f->q_norm; p.k_norm = f->k_norm; p.rope = f->rope;
+  p.T = a->T_total; p.Hq = a->Hq; p.Hkv = a->Hkv; p.d = a->d; p.dtype = a->dtype;
+  p.max_pos = f->max_pos; p.rot = f->rot_dim; p.mode = f->rope_mode;
+  p.n_slots = slots;
+  p.eps = f->norm_eps;
+  p.err = static_cast<uint32_t *>(a->workspace);
+  p.stream = static_cast<cudaStream_t>(a->stream);
+  return launch(a->stream, a->ev_begin, a->ev_end, [&] {
+    return q8 ? kda::launch_paged_append_q8(p) : kda::launch_paged_append(p);
+  });
+}
+
+
+// kda_paged_attn, and kda_paged_attn_q8 with scales.
+kda_status attn(const void *q, const void *k_pages, const void *v_pages, const float *k_scales,
+                const float *v_scales, bool q8, const int32_t *block_table,
+                const int32_t *cu_seqlens, const int32_t *kv_lens, void *out, float scale,
+                int32_t causal, const kda_paged_args *a) {
+  kda::set_last_launches(0);
+  if (!a) return KDA_ERR_INVALID_ARG;
+  kda_status st = check_pages(a);
+  if (st == KDA_OK) st = check_heads(a);
+  if (st == KDA_OK) st = check_batch(a);
+  if (st != KDA_OK) return st;
+  // (the kernels' scale: scores in powers of two)
+  if (!std::isfinite(scale * 1.4426950408889634f) || (causal != 0 && causal != 1))
+    return KDA_ERR_INVALID_ARG;
+  st = check_workspace(a->workspace, a->workspace_bytes, kda_paged_workspace_bytes(a));
+  if (st != KDA_OK) return st;
+  if (a->B == 0 || a->T_total == 0) return KDA_OK;
+  if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(out, 16) ||
+      !aligned(block_table, 4) || !aligned(cu_seqlens, 4) || !aligned(kv_lens, 4) ||
+      (q8 && (!aligned(k_scales, 4) || !aligned(v_scales, 4))))
+    return KDA_ERR_INVALID_ARG;
+  const int G = a->Hq / a->Hkv;
+  const kda::PagedWorkspace lay(a->T_total, G, a->d);
+  const int64_t row = (int64_t)a->d * elem_bytes(a->dtype), rows = row * a->T_total * a->Hq;
+  const int64_t slots = (int64_t)a->n_pages * a->page_size;
+  const int64_t pool = slots * a->Hkv * (q8 ? a->d : row);
+  const int64_t scales = q8 ? slots / kScaleTokens * a->Hkv * 4 : 0;
+  if (overlap({{out, rows}, {a->workspace, (int64_t)lay.total}, {q, q == out ? 0 : rows},
+               {k_pages, pool}, {v_pages, pool}, {block_table, 4ll * a->B * a->max_pages},
+               {cu_seqlens, 4ll * a->B + 4}, {kv_lens, 4ll * a->B}, {k_scales, scales},
+               {v_scales, scales}}, 2))
+    return KDA_ERR_INVALID_ARG;
+  char *ws = static_cast<char *>(a->workspace);
+  kda::PagedAttnPlan p = {};
+  p.q = q; p.k = k_pages; p.v = v_pages;
+  p.k_scales = k_scales; p.v_scales = v_scales;
+  p.table = block_table; p.cu = cu_seqlens; p.kv_lens = kv_lens;
+  p.out = out; p.scale = scale; p.causal = causal;
+  p.B = a->B; p.T = a->T_total; p.Hq = a->Hq; p.Hkv = a->Hkv; p.G = G; p.d = a->d;
+  p.page_size = a->page_size; p.page_shift = page_shift(a->page_size);
+  p.n_pages = a->n_pages; p.max_pages = a->max_pages; p.dtype = a->dtype;
+  p.err = reinterpret_cast<uint32_t *>(ws);
+  p.arrivals = reinterpret_cast<uint32_t *>(ws + lay.arrivals_off);
+  p.part = reinterpret_cast<float *>(ws + lay.part_off);
+  p.part_ml = reinterpret_cast<float *>(ws + lay.ml_off);
+  // (the kernel of the 8-bit cache works in fp32 whatever the type)
+  p.part_rows = kda::paged_part_rows(a->T_total, G, q8 ? (int32_t)KDA_F32 : a->dtype);
+  // What an item's start and end cost, and the shortest stretch worth a join, in
+  // keys.  In bf16 both are longer where requests bring a tile of rows and more.  (bf16,
+  // item cost 128, 192, 256, 320, 384: mixed batch of 24, 64 channels, 910, 875,
+  // 854, 855, 858 us; 128 channels 1244, 1192, 1168, 1171, 1154; 100 decodes of up
+  // to 1000 keys with 64, 128, 192, 256: 101, 90, 82, 78 us.  Shortest stretch 768,
+  // 896, 1024: a prompt of 1000 tokens, 32/8 heads, 46.7, 37.1, 38.2 us; 200 tokens
+  // over 500 keys 31.9, 32.8, 33.9; one token: the same from 256 to 384.  fp32, item
+  // cost 32, 64, 128, 256: 8 requests of up to 301 tokens 148, 134, 129, 140 us; shortest
+  // stretch 384, 512, 768, 1024: a prompt of 1000 tokens, 8/2 heads of 64 channels, 66, 71,
+  // 78, 96; 200 tokens over 500 keys, 128 channels, 63, 85, 107, 137; 100 over 8000 90, 91,
+  // 118, 97; 8 requests of up to 301 120, 120, 120, 142; 8 x 1000 tokens the same.)
+  const bool wide = (int64_t)a->T_total * G >= 128ll * a->B, bf16 = a->dtype == KDA_BF16 && !q8;
+  p.min_stretch = bf16 && wide ? 896 : 384;
+  p.item_cost = !bf16 ? 128 : wide ? 320 : 256;
+  p.stream = static_cast<cudaStream_t>(a->stream);
+  return launch(a->stream, a->ev_begin, a->ev_end, [&] {
+    if (q8)
+      return a->dtype == KDA_BF16 ? kda::launch_paged_attn_q8_bf16(p) : kda::launch_paged_attn_q8_f32(p);
+    return bf16 ? kda::launch_paged_attn_bf16(p) : kda::launch_paged_attn_f32(p);
+  });
+}
+
 }  // namespace
 
 extern "C" {
@@ -127,101 +247,31 @@ kda_status kda_paged_plan(const int32_t *cu_seqlens, const int32_t *cached_lens,
 kda_status kda_paged_append(const void *qkv, const int32_t *positions, const int32_t *slot_map,
                             void *q_out, void *k_pages, void *v_pages, const kda_append_args *f,
                             const kda_paged_args *a) {
-  kda::set_last_launches(0);
-  if (!a || !f) return KDA_ERR_INVALID_ARG;
-  kda_status st = check_pages(a);
-  if (st == KDA_OK) st = check_heads(a);
-  if (st == KDA_OK) st = check_workspace(a->workspace, a->workspace_bytes, 256);
-  if (st != KDA_OK) return st;
-  if (a->T_total < 0 || f->rot_dim < 0 || f->rot_dim > a->d || !(f->norm_eps >= 0.f) ||
-      (f->rope_mode != 0 && f->rope_mode != 1))
-    return KDA_ERR_INVALID_ARG;
-  if (f->rot_dim % 16 != 0) return KDA_ERR_UNSUPPORTED;
-  if (f->rot_dim > 0 && (!aligned(f->rope, 16) || f->max_pos <= 0)) return KDA_ERR_INVALID_ARG;
-  if ((f->q_norm && !aligned(f->q_norm, 16)) || (f->k_norm && !aligned(f->k_norm, 16)))
-    return KDA_ERR_INVALID_ARG;
-  if (a->T_total == 0) return KDA_OK;
-  if (!aligned(qkv, 16) || !aligned(q_out, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) ||
-      !aligned(slot_map, 4) || (f->rot_dim > 0 && !aligned(positions, 4)))
-    return KDA_ERR_INVALID_ARG;
-  const int64_t row = (int64_t)a->d * elem_bytes(a->dtype), T = a->T_total;
-  const int64_t pool = (int64_t)a->n_pages * a->page_size * a->Hkv * row;
-  if (overlap({{q_out, T * a->Hq * row}, {k_pages, pool}, {v_pages, pool}, {a->workspace, 256},
-               {qkv, T * (a->Hq + 2 * a->Hkv) * row}, {slot_map, T * 4},
-               {positions, f->rot_dim > 0 ? T * 4 : 0}, {f->q_norm, a->d * 4}, {f->k_norm, a->d * 4},
-               {f->rope, 4ll * f->max_pos * f->rot_dim}}, 4))
-    return KDA_ERR_INVALID_ARG;
-  kda::AppendPlan p = {};
-  p.qkv = qkv; p.positions = positions; p.slots = slot_map;
-  p.q = q_out; p.k_pages = k_pages; p.v_pages = v_pages;
-  p.q_norm = f->q_norm; p.k_norm = f->k_norm; p.rope = f->rope;
-  p.T = a->T_total; p.Hq = a->Hq; p.Hkv = a->Hkv; p.d = a->d; p.dtype = a->dtype;
-  p.max_pos = f->max_pos; p.rot = f->rot_dim; p.mode = f->rope_mode;
-  p.n_slots = (int64_t)a->n_pages * a->page_size;
-  p.eps = f->norm_eps;
-  p.err = static_cast<uint32_t *>(a->workspace);
-  p.stream = static_cast<cudaStream_t>(a->stream);
-  return launch(a->stream, a->ev_begin, a->ev_end, [&] { return kda::launch_paged_append(p); });
+  return append(qkv, positions, slot_map, q_out, k_pages, v_pages, nullptr, nullptr, false, f, a);
+}
+
+kda_status kda_paged_append_q8(const void *qkv, const int32_t *positions, const int32_t *slot_map,
+                               void *q_out, void *k_pages, void *v_pages, float *k_scales,
+                               float *v_scales, const kda_append_args *f,
+                               const kda_paged_args *a) {
+  return append(qkv, positions, slot_map, q_out, k_pages, v_pages, k_scales, v_scales, true, f, a);
 }
 
 kda_status kda_paged_attn(const void *q, const void *k_pages, const void *v_pages,
                           const int32_t *block_table, const int32_t *cu_seqlens,
                           const int32_t *kv_lens, void *out, float scale, int32_t causal,
                           const kda_paged_args *a) {
-  kda::set_last_launches(0);
-  if (!a) return KDA_ERR_INVALID_ARG;
-  kda_status st = check_pages(a);
-  if (st == KDA_OK) st = check_heads(a);
-  if (st == KDA_OK) st = check_batch(a);
-  if (st != KDA_OK) return st;
-  // (the kernels' scale: scores in powers of two)
-  if (!std::isfinite(scale * 1.4426950408889634f) || (causal != 0 && causal != 1))
-    return KDA_ERR_INVALID_ARG;
-  st = check_workspace(a->workspace, a->workspace_bytes, kda_paged_workspace_bytes(a));
-  if (st != KDA_OK) return st;
-  if (a->B == 0 || a->T_total == 0) return KDA_OK;
-  if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(out, 16) ||
-      !aligned(block_table, 4) || !aligned(cu_seqlens, 4) || !aligned(kv_lens, 4))
-    return KDA_ERR_INVALID_ARG;
-  const int G = a->Hq / a->Hkv;
-  const kda::PagedWorkspace lay(a->T_total, G, a->d);
-  const int64_t row = (int64_t)a->d * elem_bytes(a->dtype), rows = row * a->T_total * a->Hq;
-  const int64_t pool = (int64_t)a->n_pages * a->page_size * a->Hkv * row;
-  if (overlap({{out, rows}, {a->workspace, (int64_t)lay.total}, {q, q == out ? 0 : rows},
-               {k_pages, pool}, {v_pages, pool}, {block_table, 4ll * a->B * a->max_pages},
-               {cu_seqlens, 4ll * a->B + 4}, {kv_lens, 4ll * a->B}}, 2))
-    return KDA_ERR_INVALID_ARG;
-  char *ws = static_cast<char *>(a->workspace);
-  kda::PagedAttnPlan p = {};
-  p.q = q; p.k = k_pages; p.v = v_pages;
-  p.table = block_table; p.cu = cu_seqlens; p.kv_lens = kv_lens;
-  p.out = out; p.scale = scale; p.causal = causal;
-  p.B = a->B; p.T = a->T_total; p.Hq = a->Hq; p.Hkv = a->Hkv; p.G = G; p.d = a->d;
-  p.page_size = a->page_size; p.page_shift = page_shift(a->page_size);
-  p.n_pages = a->n_pages; p.max_pages = a->max_pages; p.dtype = a->dtype;
-  p.err = reinterpret_cast<uint32_t *>(ws);
-  p.arrivals = reinterpret_cast<uint32_t *>(ws + lay.arrivals_off);
-  p.part = reinterpret_cast<float *>(ws + lay.part_off);
-  p.part_ml = reinterpret_cast<float *>(ws + lay.ml_off);
-  p.part_rows = kda::paged_part_rows(a->T_total, G, a->dtype);
-  // What an item's start and end cost, and the shortest stretch worth a join, in
-  // keys.  In bf16 both are longer where requests bring a tile of rows and more.  (bf16,
-  // item cost 128, 192, 256, 320, 384: mixed batch of 24, 64 channels, 910, 875,
-  // 854, 855, 858 us; 128 channels 1244, 1192, 1168, 1171, 1154; 100 decodes of up
-  // to 1000 keys with 64, 128, 192, 256: 101, 90, 82, 78 us.  Shortest stretch 768,
-  // 896, 1024: a prompt of 1000 tokens, 32/8 heads, 46.7, 37.1, 38.2 us; 200 tokens
-  // over 500 keys 31.9, 32.8, 33.9; one token: the same from 256 to 384.  fp32, item
-  // cost 32, 64, 128, 256: 8 requests of up to 301 tokens 148, 134, 129, 140 us; shortest
-  // stretch 384, 512, 768, 1024: a prompt of 1000 tokens, 8/2 heads of 64 channels, 66, 71,
-  // 78, 96; 200 tokens over 500 keys, 128 channels, 63, 85, 107, 137; 100 over 8000 90, 91,
-  // 118, 97; 8 requests of up to 301 120, 120, 120, 142; 8 x 1000 tokens the same.)
-  const bool wide = (int64_t)a->T_total * G >= 128ll * a->B, bf16 = a->dtype == KDA_BF16;
-  p.min_stretch = bf16 && wide ? 896 : 384;
-  p.item_cost = !bf16 ? 128 : wide ? 320 : 256;
-  p.stream = static_cast<cudaStream_t>(a->stream);
-  return launch(a->stream, a->ev_begin, a->ev_end, [&] {
-    return a->dtype == KDA_BF16 ? kda::launch_paged_attn_bf16(p) : kda::launch_paged_attn_f32(p);
-  });
+  return attn(q, k_pages, v_pages, nullptr, nullptr, false, block_table, cu_seqlens, kv_lens, out,
+              scale, causal, a);
+}
+
+kda_status kda_paged_attn_q8(const void *q, const void *k_pages, const void *v_pages,
+                             const float *k_scales, const float *v_scales,
+                             const int32_t *block_table, const int32_t *cu_seqlens,
+                             const int32_t *kv_lens, void *out, float scale, int32_t causal,
+                             const kda_paged_args *a) {
+  return attn(q, k_pages, v_pages, k_scales, v_scales, true, block_table, cu_seqlens, kv_lens, out,
+              scale, causal, a);
 }
 
 kda_status kda_verify_drafts(const void *target_probs, const void *draft_probs,
@@ -255,6 +305,39 @@ kda_status kda_verify_drafts(const void *target_probs, const void *draft_probs,
   p.err = static_cast<uint32_t *>(a->workspace);
   p.stream = static_cast<cudaStream_t>(a->stream);
   return launch(a->stream, a->ev_begin, a->ev_end, [&] { return kda::launch_verify(p); });
+}
+
+kda_status kda_token_logprobs(const void *logits, const int32_t *tokens, float *logprobs,
+                              float *entropy, int32_t *ranks, int32_t *top_ids,
+                              float *top_logprobs, const kda_logprobs_args *a) {
+  kda::set_last_launches(0);
+  if (!a || (a->dtype != KDA_F32 && a->dtype != KDA_BF16)) return KDA_ERR_INVALID_ARG;
+  if (a->N < 0 || a->V <= 0 || a->n_top < 0 || a->stride < a->V) return KDA_ERR_INVALID_ARG;
+  if (!(a->scale > 0.f) || !std::isfinite(a->scale * 1.4426950408889634f)) return KDA_ERR_INVALID_ARG;
+  if (a->V > (1 << 24) || a->N > (1 << 20) || a->n_top > 64) return KDA_ERR_UNSUPPORTED;
+  const kda_status st = check_workspace(a->workspace, a->workspace_bytes, 256);
+  if (st != KDA_OK) return st;
+  if (a->N == 0) return KDA_OK;
+  const int64_t N = a->N, K = a->n_top, es = elem_bytes(a->dtype);
+  if (!aligned(logits, es) || (tokens && !aligned(tokens, 4)) || (entropy && !aligned(entropy, 4)) ||
+      (logprobs && !aligned(logprobs, 4)) || (ranks && !aligned(ranks, 4)) ||
+      (K > 0 && (!aligned(top_ids, 4) || !aligned(top_logprobs, 4))))
+    return KDA_ERR_INVALID_ARG;
+  if (!tokens && (logprobs || ranks)) return KDA_ERR_INVALID_ARG;
+  // (the stride times rows of 2^24 and 2^20 at most; a stride beyond that holds no rows)
+  if (N > 1 && a->stride > (1ll << 40) / N) return KDA_ERR_UNSUPPORTED;
+  const int64_t span = N > 1 ? ((N - 1) * a->stride + a->V) * es : a->V * es;
+  if (overlap({{logprobs, N * 4}, {entropy, N * 4}, {ranks, N * 4}, {top_ids, N * K * 4},
+               {top_logprobs, N * K * 4}, {a->workspace, 256}, {logits, span}, {tokens, N * 4}}, 6))
+    return KDA_ERR_INVALID_ARG;
+  kda::LogprobsPlan p = {};
+  p.logits = logits; p.tokens = tokens; p.logprobs = logprobs; p.entropy = entropy;
+  p.ranks = ranks; p.top_ids = top_ids; p.top_logprobs = top_logprobs;
+  p.stride = a->stride; p.N = a->N; p.V = a->V; p.n_top = a->n_top; p.dtype = a->dtype;
+  p.scale = a->scale;
+  p.err = static_cast<uint32_t *>(a->workspace);
+  p.stream = static_cast<cudaStream_t>(a->stream);
+  return launch(a->stream, a->ev_begin, a->ev_end, [&] { return kda::launch_logprobs(p); });
 }
 
 }  // extern "C"

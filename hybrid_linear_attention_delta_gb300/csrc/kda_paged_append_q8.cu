@@ -1,0 +1,294 @@
+// kda_paged_append_q8.cu -- per-head RMSNorm and position rotation of the packed
+// projection's q and k heads, q out, k and v into an 8-bit cache.
+//
+//     y = e4m3(x / s),   s = max(old, p),   p the smallest power of two with max|x| <= 448 p
+//
+// for every block of 16 tokens and head, x the block's new keys or values and old
+// its scale so far (none when the block's first slot is among the new tokens).
+// Where s grows, what the block held before is rounded again, e4m3(y old / s).
+// e4m3 is a floating-point type, so with scales that are powers of two that loses
+// nothing but the lowest bits of values below 2^-6 s, and a scale that is twice as
+// large as it need be costs none of the others.
+//
+// A run is the new tokens of one block, which lie within 16 rows of one another.  One
+// warp holds a run's rows of one head in registers (up to 16 rows, 8 channels of
+// 16-bit inputs a lane), so that every element is read once and written once.  A CTA
+// owns the runs whose first row is among its rows, and the q heads of its rows.
+#include "kda_paged_e4m3.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxRows = 16;  // rows of a CTA at most
+
+template <typename T> constexpr int kVec = 16 / (int)sizeof(T);  // channels of a lane
+
+// Where a lane's channels lie: HALVES: two runs of kVec / 2, at a and b; else one
+// run at a.
+struct Place {
+  int a, b;
+  bool turned;  // its channels are rotated
+};
+template <typename T, bool HALVES>
+__device__ __forceinline__ Place place(int l, int rot) {
+  constexpr int N = kVec<T>, M = N / 2;
+  Place c;
+  c.turned = l * N < rot;  // (rot is a multiple of 16: whole lanes)
+  c.a = HALVES && c.turned ? l * M : l * N;
+  c.b = HALVES && c.turned ? rot / 2 + l * M : l * N + M;
+  return c;
+}
+
+template <typename T, bool HALVES>
+__device__ __forceinline__ uint4 load_row(const T *head, const Place &c) {
+  if constexpr (HALVES) {
+    const T *a = head + c.a, *b = head + c.b;
+    if constexpr (sizeof(T) == 2) {
+      const uint2 u = __ldcs(reinterpret_cast<const uint2 *>(a));
+      const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(b));
+      return make_uint4(u.x, u.y, v.x, v.y);
+    } else {
+      const uint2 u = __ldcs(reinterpret_cast<const uint2 *>(a));
+      const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(b));
+      return make_uint4(u.x, u.y, v.x, v.y);
+    }
+  } else {
+    return __ldcs(reinterpret_cast<const uint4 *>(head + c.a));
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4 &w, float (&x)[kVec<T>]) {
+  const T *t = reinterpret_cast<const T *>(&w);
+#pragma unroll
+  for (int i = 0; i < kVec<T>; ++i) x[i] = to_f32<T>(t[i]);
+}
+
+// RMSNorm and rotation of a lane's channels.  All lanes of a head call this.
+template <typename T, int D, bool HALVES>
+__device__ __forceinline__ void turn(float (&x)[kVec<T>], const Place &c, const float *norm,
+                                     float eps, const float *rope_row, int l, int rot) {
+  constexpr int N = kVec<T>, M = N / 2, LPH = D / N;
+  if (norm) {
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+    for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const float r = rsqrtf(ss * (1.f / D) + eps);
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = x[i] * r * __ldg(norm + (i < M ? c.a + i : c.b + i - M));
+  }
+  if (c.turned && rope_row) {
+    const float *cs = rope_row + l * M;
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+      const float co = __ldg(cs + i), si = __ldg(cs + rot / 2 + i);
+      float &a = x[HALVES ? i : 2 * i], &b = x[HALVES ? i + M : 2 * i + 1];
+      const float a0 = a, b0 = b;
+      a = a0 * co - b0 * si;
+      b = a0 * si + b0 * co;
+    }
+  }
+}
+
+template <typename T, bool HALVES>
+__device__ __forceinline__ void store_q(T *head, const Place &c, const float (&x)[kVec<T>]) {
+  constexpr int N = kVec<T>, M = N / 2;
+  T y[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if constexpr (sizeof(T) == 2) y[i] = __float2bfloat16_rn(x[i]);
+    else y[i] = x[i];
+  }
+  const uint2 *w = reinterpret_cast<const uint2 *>(y);
+  if constexpr (HALVES) {
+    *reinterpret_cast<uint2 *>(head + c.a) = w[0];
+    *reinterpret_cast<uint2 *>(head + c.b) = w[1];
+  } else {
+    *reinterpret_cast<uint4 *>(head + c.a) = make_uint4(w[0].x, w[0].y, w[1].x, w[1].y);
+  }
+  static_assert(M * sizeof(T) == 8, "a run is 8 bytes");
+}
+
+// kVec / 2 bytes at each of the two runs.
+template <typename T, bool HALVES>
+__device__ __forceinline__ void store_e4m3(uint8_t *head, const Place &c, const float (&x)[kVec<T>],
+                                           float inv) {
+  if constexpr (sizeof(T) == 2) {
+    const uint32_t u = f32_to_e4m3(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+    const uint32_t v = f32_to_e4m3(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv);
+    if constexpr (HALVES) {
+      *reinterpret_cast<uint32_t *>(head + c.a) = u;
+      *reinterpret_cast<uint32_t *>(head + c.b) = v;
+    } else {
+      *reinterpret_cast<uint2 *>(head + c.a) = make_uint2(u, v);
+    }
+  } else {
+    const uint32_t u = f32_to_e4m3(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+    if constexpr (HALVES) {
+      *reinterpret_cast<uint16_t *>(head + c.a) = (uint16_t)u;
+      *reinterpret_cast<uint16_t *>(head + c.b) = (uint16_t)(u >> 16);
+    } else {
+      *reinterpret_cast<uint32_t *>(head + c.a) = u;
+    }
+  }
+}
+
+// rows: rows of a CTA (at most kMaxRows); grid y shares out their units.
+template <typename T, int D, bool HALVES>
+__global__ void __launch_bounds__(kThreads) append_kernel(AppendPlan p, int rows) {
+  constexpr int N = kVec<T>;
+  constexpr int LPH = D / N;     // lanes of a head
+  constexpr int HPP = 32 / LPH;  // rows (or heads) of a pass
+  constexpr int P = kScaleTokens / HPP;  // passes of a run
+  constexpr int kNear = kScaleTokens - 1;
+  // slot (-1: none) and position of this CTA's rows, the 15 before and the 15 behind
+  __shared__ int32_t s_slot[64], s_pos[64];
+  __shared__ int32_t s_start[kMaxRows], s_live[kMaxRows];  // first rows of runs, rows with a slot
+  __shared__ int32_t s_n[2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int l = lane % LPH, sub = lane / LPH;
+  const int64_t t0 = (int64_t)blockIdx.x * rows - kNear;  // row of index 0
+  if (tid < 64) {
+    const int64_t t = t0 + tid;
+    int slot = -1, pos = 0;
+    if (t >= 0 && t < p.T && tid < rows + 2 * kNear) {
+      slot = p.slots[t];
+      if (p.rot > 0) pos = p.positions[t];
+      const bool mine = tid >= kNear && tid < kNear + rows && blockIdx.y == 0;
+      if (slot >= p.n_slots) {
+        if (mine) raise_error(p.err, ERR_BAD_SLOT);
+        slot = -1;
+      } else if (slot >= 0 && p.rot > 0 && (pos < 0 || pos >= p.max_pos)) {
+        if (mine) raise_error(p.err, ERR_BAD_POS);
+        slot = -1;
+      }
+    }
+    s_slot[tid] = max(slot, -1);
+    s_pos[tid] = pos;
+  }
+  __syncthreads();
+  if (tid < 32) {
+    const int i = kNear + lane;
+    const int slot = lane < rows ? s_slot[i] : -1;
+    bool start = slot >= 0;
+#pragma unroll
+    for (int k = 1; k <= kNear; ++k) {
+      const int s = s_slot[i - k];
+      start &= s < 0 || (s ^ slot) >= kScaleTokens;  // not in this block
+    }
+    const uint32_t starts = __ballot_sync(0xffffffffu, start);
+    const uint32_t live = __ballot_sync(0xffffffffu, slot >= 0);
+    const uint32_t below = (1u << lane) - 1u;
+    if (start) s_start[__popc(starts & below)] = i;
+    if (slot >= 0) s_live[__popc(live & below)] = i;
+    if (lane == 0) s_n[0] = __popc(starts), s_n[1] = __popc(live);
+  }
+  __syncthreads();
+  const Place c = place<T, HALVES>(l, p.rot);
+  const int64_t row = (int64_t)(p.Hq + 2 * p.Hkv) * D;
+  const T *qkv = static_cast<const T *>(p.qkv) + t0 * row;
+  const int n_kv = s_n[0] * 2 * p.Hkv, nq = (p.Hq + HPP - 1) / HPP;
+  const int units = n_kv + s_n[1] * nq;
+  for (int u = blockIdx.y * kWarps + warp; u < units; u += gridDim.y * kWarps) {
+    if (u < n_kv) {  // a run's keys or values of one head
+      const int i = s_start[u / (2 * p.Hkv)], h = u % (2 * p.Hkv);
+      const bool is_v = h >= p.Hkv;
+      const int head = is_v ? h - p.Hkv : h;
+      const int block = s_slot[i] / kScaleTokens;
+      // the run's rows among the 16 from its first on, and the lowest slot of them
+      const int near = lane < kScaleTokens ? s_slot[i + lane] : -1;
+      const bool in_run = near >= 0 && near / kScaleTokens == block;
+      const uint32_t run = __ballot_sync(0xffffffffu, in_run);
+      const int off = __reduce_min_sync(0xffffffffu, in_run ? near % kScaleTokens : kScaleTokens);
+      const T *src = qkv + i * row + (int64_t)(p.Hq + h) * D;
+      uint4 raw[P];
+#pragma unroll
+      for (int x = 0; x < P; ++x) {
+        const int r = x * HPP + sub;
+        raw[x] = run >> r & 1 ? load_row<T, HALVES>(src + r * row, c) : make_uint4(0, 0, 0, 0);
+      }
+      float *scale = (is_v ? p.v_scales : p.k_scales) + (int64_t)block * p.Hkv + head;
+      float held = 0.f, old = 0.f;
+      if (off > 0) {
+        old = held = *scale;
+        if (!good_scale(old)) {
+          if (lane == 0) raise_error(p.err, ERR_BAD_SCALE);
+          old = kMinScale;
+        }
+      }
+      float y[P][N];
+      float amax = 0.f;
+#pragma unroll
+      for (int x = 0; x < P; ++x) {
+        unpack<T>(raw[x], y[x]);
+        if (!(run >> (x * HPP) & ((1u << HPP) - 1u))) continue;
+        if (!is_v) {
+          const float *rope =
+              p.rot > 0 && run >> (x * HPP + sub) & 1 ? p.rope + (int64_t)s_pos[i + x * HPP + sub] * p.rot : nullptr;
+          turn<T, D, HALVES>(y[x], c, p.k_norm, p.eps, rope, l, p.rot);
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j) amax = fmaxf(amax, fabsf(y[x][j]));
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      const float s = fmaxf(old, scale_for(amax)), inv = 1.f / s;
+      uint8_t *dst = static_cast<uint8_t *>(is_v ? p.v_pages : p.k_pages) +
+                     ((int64_t)block * kScaleTokens * p.Hkv + head) * D;
+      const int64_t step = (int64_t)p.Hkv * D;
+      if (off > 0 && s > old) {  // what the block holds, rounded again: 4 bytes a lane
+        const float ratio = old / s;
+        for (int e = lane; e < off * (D / 4); e += 32) {
+          uint32_t *w = reinterpret_cast<uint32_t *>(dst + e / (D / 4) * step + e % (D / 4) * 4);
+          float z[16];
+          e4m3_to_f32(make_uint4(*w, 0, 0, 0), z);
+          *w = f32_to_e4m3(z[0] * ratio, z[1] * ratio, z[2] * ratio, z[3] * ratio);
+        }
+      }
+      if (lane == 0 && (off == 0 || s != held)) *scale = s;
+#pragma unroll
+      for (int x = 0; x < P; ++x) {
+        const int r = x * HPP + sub;
+        if (run >> r & 1)
+          store_e4m3<T, HALVES>(dst + s_slot[i + r] % kScaleTokens * step, c, y[x], inv);
+      }
+    } else {  // HPP q heads of a row
+      const int v = u - n_kv, i = s_live[v / nq], h = v % nq * HPP + sub;
+      const T *src = qkv + i * row + (int64_t)h * D;
+      float y[N];
+      unpack<T>(h < p.Hq ? load_row<T, HALVES>(src, c) : make_uint4(0, 0, 0, 0), y);
+      const float *rope = p.rot > 0 ? p.rope + (int64_t)s_pos[i] * p.rot : nullptr;
+      turn<T, D, HALVES>(y, c, p.q_norm, p.eps, rope, l, p.rot);
+      if (h < p.Hq)
+        store_q<T, HALVES>(static_cast<T *>(p.q) + ((t0 + i) * p.Hq + h) * D, c, y);
+    }
+  }
+}
+
+template <typename T, int D, bool HALVES>
+cudaError_t launch_h(const AppendPlan &p) {
+  int rows = kMaxRows;
+  while (rows > 1 && (int64_t)p.T < (int64_t)rows * 2 * kPagedMaxCtas) rows /= 2;
+  const unsigned grid = (unsigned)((p.T + rows - 1) / rows);
+  const unsigned share = grid < 4 * kPagedMaxCtas ? 4 : 1;
+  append_kernel<T, D, HALVES><<<dim3(grid, share), kThreads, 0, p.stream>>>(p, rows);
+  return cudaGetLastError();
+}
+template <typename T, int D>
+cudaError_t launch_d(const AppendPlan &p) {
+  return p.mode == 0 && p.rot > 0 ? launch_h<T, D, true>(p) : launch_h<T, D, false>(p);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_append_q8(const AppendPlan &p) {
+  if (p.dtype == KDA_BF16)
+    return p.d == 128 ? launch_d<__nv_bfloat16, 128>(p) : launch_d<__nv_bfloat16, 64>(p);
+  return p.d == 128 ? launch_d<float, 128>(p) : launch_d<float, 64>(p);
+}
+
+}  // namespace kda

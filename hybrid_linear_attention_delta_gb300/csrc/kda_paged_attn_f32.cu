@@ -16,6 +16,11 @@
 // us, 28 TFLOP/s; 1000 tokens each: 39 TFLOP/s).  Decode of 64 requests over 511 to 8191
 // keys, 32 / 8 heads: 0.41 ms, 2.7 TB/s, with 64 channels, 1.34 ms, 1.6 TB/s, with 128,
 // where the scores and outputs of 8 and 16 rows are made for the 4 that there are.
+//
+// The 8-bit cache (e4m3 with a scale for 16 tokens and head) is turned into fp32 on
+// its way to shared memory, the values times their scales: the next tile waits in
+// registers instead of a second buffer.
+#include "kda_paged_e4m3.cuh"
 #include "kda_paged_sched.cuh"
 
 namespace kda {
@@ -23,16 +28,17 @@ namespace {
 
 constexpr int kKeys = 64;  // keys of a tile
 
-// R: rows of a thread, TY: threads along the rows
-template <int D, int R, int TY>
+// R: rows of a thread, TY: threads along the rows; Q8: an 8-bit cache
+template <int D, int R, int TY, bool Q8>
 struct Smem {
-  static constexpr int kRows = TY * R, kThreads = TY * 16;
+  static constexpr int kRows = TY * R, kThreads = TY * 16, kBufs = Q8 ? 1 : 2;
   static constexpr int kLd = D + 4;      // floats of a Q / K row
   static constexpr int kLdP = kKeys + 16;  // two rows side by side: other banks
   float q[kRows * kLd];
-  float k[2][kKeys * kLd];  // a tile and the one on its way
-  float v[2][kKeys * D];
+  float k[kBufs][kKeys * kLd];  // a tile and the one on its way
+  float v[kBufs][kKeys * D];
   float p[kRows * kLdP];
+  float c[kKeys / kScaleTokens];  // Q8: 0, or -inf for blocks that are left out
   PagedPiece piece;
   int64_t scratch[kThreads / 16 + 4];
   int last;
@@ -57,20 +63,34 @@ __device__ __forceinline__ int64_t row_offset(const PagedAttnPlan &p, const Page
   return ((int64_t)(o.tok0 + t) * p.Hq + o.head * p.G + (r - t * p.G)) * p.d;
 }
 
+__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
+  const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(p);
+  const float2 a = __bfloat1622float2(h[0]), b = __bfloat1622float2(h[1]);
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, float a, float b, float c, float d) {
+  reinterpret_cast<__nv_bfloat162 *>(p)[0] = __floats2bfloat162_rn(a, b);
+  reinterpret_cast<__nv_bfloat162 *>(p)[1] = __floats2bfloat162_rn(c, d);
+}
+__device__ __forceinline__ void store4(float *p, float a, float b, float c, float d) {
+  *reinterpret_cast<float4 *>(p) = make_float4(a, b, c, d);
+}
+
 // A piece, RA rows a thread (rows ty + TY i of the item, i < RA).
-template <int D, int R, int TY, int RA>
-__device__ __forceinline__ void run_piece(const PagedAttnPlan &p, Smem<D, R, TY> &sm,
+template <typename T, int D, int R, int TY, int RA, bool Q8>
+__device__ __forceinline__ void run_piece(const PagedAttnPlan &p, Smem<D, R, TY, Q8> &sm,
                                           const PagedPiece &o, float c) {
-  using S = Smem<D, R, TY>;
+  using S = Smem<D, R, TY, Q8>;
   constexpr int kThreads = S::kThreads, kRows = TY * RA;
   constexpr int NC = D / 16;  // output channels of a thread, in groups of four
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
   const int rows = o.n * p.G;
-  const float *q = static_cast<const float *>(p.q);
+  const T *q = static_cast<const T *>(p.q);
   for (int i = tid; i < kRows * (D / 4); i += kThreads) {
     const int r = i / (D / 4), e = (i % (D / 4)) * 4;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r < rows) x = *reinterpret_cast<const float4 *>(q + row_offset(p, o, r) + e);
+    if (r < rows) x = load4(q + row_offset(p, o, r) + e);
     *reinterpret_cast<float4 *>(&sm.q[r * S::kLd + e]) = x;
   }
   int lim[RA];  // keys that each row sees
@@ -105,14 +125,67 @@ __device__ __forceinline__ void run_piece(const PagedAttnPlan &p, Smem<D, R, TY>
     }
     copies_commit();
   };
-  if (o.tile0 < o.tile1) fetch(o.tile0, 0);
+  // Q8: the same, 16 channels of a key or a value at a time, through registers.  A
+  // block whose scale of keys or values is none is left out.
+  constexpr int kChunks = Q8 ? 2 * kKeys * (D / 16) / kThreads : 1;  // of a thread and tile
+  static_assert(!Q8 || kChunks * kThreads == 2 * kKeys * (D / 16), "whole chunks");
+  uint4 raw[kChunks];
+  float by[kChunks];
+  auto ask = [&](int tile) {
+#pragma unroll
+    for (int x = 0; x < kChunks; ++x) {
+      const int i = tid + x * kThreads, is_v = i / (kKeys * (D / 16));
+      const int k = i / (D / 16) % kKeys, e = (i % (D / 16)) * 16;
+      const int key = tile * kKeys + k;
+      raw[x] = make_uint4(0, 0, 0, 0);
+      by[x] = 1.f;
+      if (key >= o.kv) continue;
+      const int page = p.table[(int64_t)o.req * p.max_pages + (key >> p.page_shift)];
+      if (page < 0 || page >= p.n_pages) {
+        raise_error(p.err, ERR_BAD_PAGE);
+        continue;
+      }
+      const int64_t slot = ((int64_t)page << p.page_shift) + (key & (p.page_size - 1));
+      raw[x] = __ldg(reinterpret_cast<const uint4 *>(
+          static_cast<const uint8_t *>(is_v ? p.v : p.k) + (slot * p.Hkv + o.head) * D + e));
+      by[x] = (is_v ? p.v_scales : p.k_scales)[slot / kScaleTokens * p.Hkv + o.head];
+    }
+  };
+  auto give = [&] {
+    if (tid < kKeys / kScaleTokens) sm.c[tid] = 0.f;
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < kChunks; ++x) {
+      const int i = tid + x * kThreads, is_v = i / (kKeys * (D / 16));
+      const int k = i / (D / 16) % kKeys, e = (i % (D / 16)) * 16;
+      float y[16];
+      e4m3_to_f32(raw[x], y);
+      float f = by[x];
+      if (!good_scale(f)) {
+        raise_error(p.err, ERR_BAD_SCALE);
+        sm.c[k / kScaleTokens] = -INFINITY;
+        f = 0.f;
+      }
+      float *dst = is_v ? &sm.v[0][k * D + e] : &sm.k[0][k * S::kLd + e];
+#pragma unroll
+      for (int j = 0; j < 16; j += 4)
+        store4(dst + j, f == 0.f ? 0.f : y[j] * f, f == 0.f ? 0.f : y[j + 1] * f,
+               f == 0.f ? 0.f : y[j + 2] * f, f == 0.f ? 0.f : y[j + 3] * f);
+    }
+  };
+  if (o.tile0 < o.tile1) {
+    if constexpr (Q8) ask(o.tile0); else fetch(o.tile0, 0);
+  }
 
   for (int tile = o.tile0; tile < o.tile1; ++tile) {
-    const int key0 = tile * kKeys, buf = (tile - o.tile0) & 1;
+    const int key0 = tile * kKeys, buf = Q8 ? 0 : (tile - o.tile0) & 1;
     const float *sk = sm.k[buf], *sv = sm.v[buf];
     // the tile before has been read by all: its buffer takes the next one
     __syncthreads();
-    if (tile + 1 < o.tile1) {
+    if constexpr (Q8) {
+      give();
+      if (tile + 1 < o.tile1) ask(tile + 1);
+    } else if (tile + 1 < o.tile1) {
       fetch(tile + 1, buf ^ 1);
       copies_wait<1>();
     } else {
@@ -150,6 +223,8 @@ __device__ __forceinline__ void run_piece(const PagedAttnPlan &p, Smem<D, R, TY>
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         s[i][j] = key0 + tx + 16 * j < lim[i] ? s[i][j] * c : -INFINITY;
+        // (key tx + 16 j is in block j)
+        if constexpr (Q8) s[i][j] = sm.c[j] == 0.f ? s[i][j] : -INFINITY;
         top = fmaxf(top, s[i][j]);
       }
 #pragma unroll
@@ -249,18 +324,18 @@ __device__ __forceinline__ void run_piece(const PagedAttnPlan &p, Smem<D, R, TY>
     const int r = ty + TY * i;
     if (r >= rows) continue;
     const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];  // a row without keys: zeros
-    float *out = static_cast<float *>(p.out) + row_offset(p, o, r);
+    T *out = static_cast<T *>(p.out) + row_offset(p, o, r);
 #pragma unroll
     for (int j = 0; j < NC; j += 4)
-      *reinterpret_cast<float4 *>(out + j * 16 + tx * 4) = make_float4(
-          acc[i][j] * inv, acc[i][j + 1] * inv, acc[i][j + 2] * inv, acc[i][j + 3] * inv);
+      store4(out + j * 16 + tx * 4, acc[i][j] * inv, acc[i][j + 1] * inv, acc[i][j + 2] * inv,
+             acc[i][j + 3] * inv);
   }
 }
 
-template <int D, int R, int TY>
+template <typename T, int D, int R, int TY, bool Q8>
 __global__ void __launch_bounds__(TY * 16, D == 64 ? 2 : 1) attn_kernel(PagedAttnPlan p) {
   extern __shared__ __align__(16) unsigned char raw[];
-  using S = Smem<D, R, TY>;
+  using S = Smem<D, R, TY, Q8>;
   constexpr int kThreads = S::kThreads;
   S &sm = *reinterpret_cast<S *>(raw);
   const int tid = threadIdx.x;
@@ -276,28 +351,36 @@ __global__ void __launch_bounds__(TY * 16, D == 64 ? 2 : 1) attn_kernel(PagedAtt
     if (o.n == 0) break;
     // an item of a few rows leaves the others out (8 decodes, 8 / 2 heads of 64
     // channels: 47 -> 33 us)
-    if (o.n * p.G <= TY) run_piece<D, R, TY, 1>(p, sm, o, c);
-    else run_piece<D, R, TY, R>(p, sm, o, c);
+    if (o.n * p.G <= TY) run_piece<T, D, R, TY, 1, Q8>(p, sm, o, c);
+    else run_piece<T, D, R, TY, R, Q8>(p, sm, o, c);
   }
 }
 
-template <int D, int R, int TY>
+template <typename T, int D, int R, int TY, bool Q8>
 cudaError_t launch_r(const PagedAttnPlan &p) {
-  using S = Smem<D, R, TY>;
-  const void *f = reinterpret_cast<const void *>(attn_kernel<D, R, TY>);
+  using S = Smem<D, R, TY, Q8>;
+  const void *f = reinterpret_cast<const void *>(attn_kernel<T, D, R, TY, Q8>);
   const cudaError_t e = set_smem_limit_once(f, sizeof(S));
   if (e != cudaSuccess) return e;
   static_assert(S::kRows <= kPagedF32Rows, "rows of a partial result");
+  static_assert(sizeof(S) <= (D == 64 ? 113 : 227) * 1024, "shared memory");
   // two CTAs fit an SM with 64 channels, one with 128
-  constexpr int kCtas = sizeof(S) <= 113 * 1024 ? kPagedF32Ctas : kPagedMaxCtas;
-  attn_kernel<D, R, TY><<<kCtas, S::kThreads, sizeof(S), p.stream>>>(p);
+  constexpr int kCtas = D == 64 ? kPagedF32Ctas : kPagedMaxCtas;
+  attn_kernel<T, D, R, TY, Q8><<<kCtas, S::kThreads, sizeof(S), p.stream>>>(p);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_paged_attn_f32(const PagedAttnPlan &p) {
-  return p.d == 128 ? launch_r<128, 4, 16>(p) : launch_r<64, 8, 8>(p);
+  return p.d == 128 ? launch_r<float, 128, 4, 16, false>(p) : launch_r<float, 64, 8, 8, false>(p);
+}
+cudaError_t launch_paged_attn_q8_bf16(const PagedAttnPlan &p) {
+  return p.d == 128 ? launch_r<__nv_bfloat16, 128, 4, 16, true>(p)
+                    : launch_r<__nv_bfloat16, 64, 8, 8, true>(p);
+}
+cudaError_t launch_paged_attn_q8_f32(const PagedAttnPlan &p) {
+  return p.d == 128 ? launch_r<float, 128, 4, 16, true>(p) : launch_r<float, 64, 8, 8, true>(p);
 }
 
 }  // namespace kda

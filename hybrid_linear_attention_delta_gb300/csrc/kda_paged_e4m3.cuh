@@ -1,0 +1,45 @@
+// kda_paged_e4m3.cuh -- the 8-bit cache of the paged calls: e4m3 values with a
+// scale for every 16 tokens and head.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "kda_paged.cuh"
+
+namespace kda {
+
+constexpr int kScaleTokens = 16;  // tokens of a scale
+// Scales.  Within these bounds the largest ratio of two, 2^100, times any weight that
+// counts (2^-24 of the row's largest) is a normal float.
+constexpr float kMinScale = 0x1p-50f, kMaxScale = 0x1p50f;
+constexpr float kMaxE4m3 = 448.f;
+
+__device__ __forceinline__ bool good_scale(float s) { return s >= kMinScale && s <= kMaxScale; }
+
+// 16 values; every e4m3 value is an fp16 value.
+__device__ __forceinline__ void e4m3_to_f32(const uint4 &w, float (&x)[16]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+        (__nv_fp8x2_storage_t)(u[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+    x[2 * i] = f.x, x[2 * i + 1] = f.y;
+  }
+}
+// Four values, rounded to nearest; beyond 448 they become 448.
+__device__ __forceinline__ uint32_t f32_to_e4m3(float a, float b, float c, float d) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return lo | hi << 16;
+}
+
+// The smallest power of two p with amax <= 448 p (448 = 1.75 * 2^8), within the
+// scales' bounds.
+__device__ __forceinline__ float scale_for(float amax) {
+  const uint32_t b = __float_as_uint(amax);
+  const int e = (int)(b >> 23) - 8 + ((b & 0x7fffffu) > 0x600000u);
+  return __uint_as_float((uint32_t)min(max(e, 127 - 50), 127 + 50) << 23);
+}
+
+}  // namespace kda

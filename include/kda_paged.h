@@ -14,6 +14,9 @@
  *   kda_paged_attn     (per layer) attention of the new tokens over the pages
  *   kda_verify_drafts  which drafted tokens stand, and the token after them;
  *                      its accepted[] is the accepted_prev[] of kda_decode_spec
+ *   kda_token_logprobs log probabilities, ranks and alternatives of the step's tokens
+ *
+ * or, with a cache in 8 bits, kda_paged_append_q8 and kda_paged_attn_q8 per layer.
  *
  * The conventions of kda.h hold: caller-owned device pointers, dense row-major
  * arrays with 16-byte aligned bases (8-byte and smaller integer arrays: their
@@ -224,6 +227,96 @@ kda_status kda_verify_drafts(const void *target_probs, const void *draft_probs,
                              const int32_t *draft_tokens, const int32_t *draft_lens,
                              const float *u_accept, const float *u_sample, int32_t *accepted,
                              int32_t *tokens, const kda_verify_args *a);
+
+/*
+ * The same cache in 8 bits: pages of e4m3 values (4 exponent and 3 mantissa bits, up
+ * to 448) with an fp32 scale for every block of 16 tokens and head,
+ *
+ *     key = k_pages[page][i][head][:] * k_scales[page][i / 16][head]
+ *
+ * and values likewise; half the memory and half the traffic of a 16-bit cache.
+ * kda_paged_plan serves it as it is.  Scales are in [2^-50, 2^50]; where a call
+ * needs one that is not, bit 8192 is raised.
+ *
+ * kda_paged_append with an 8-bit cache.  Norm, rotation and q_out are those of
+ * kda_paged_append.  A block's scale is
+ *
+ *     s = max(old, p),  p the smallest power of two in [2^-50, 2^50] with max|x| <= 448 p
+ *
+ * over the block's new values x of that head, old its scale so far, or none when the
+ * block's first slot is among the new tokens.  The values are stored as e4m3(x / s)
+ * (to nearest, ties to even; at most 448 s in magnitude); where s > old, what the
+ * block holds in front of the first of them is rounded again, e4m3(y old / s).  Slots
+ * behind it that are not among the new tokens keep their bytes.  (With scales that are
+ * powers of two rounding again changes only values below 2^-6 s.)
+ *
+ * k_pages, v_pages   [n_pages][page_size][Hkv][d] e4m3
+ * k_scales, v_scales [n_pages][page_size / 16][Hkv] fp32, in/out: read for blocks that
+ *                    are continued, written where they change
+ * slot_map           as for kda_paged_append, and the new tokens of a block lie within
+ *                    16 rows of one another (those of kda_paged_plan are neighbours)
+ * An old scale outside its bounds (bit 8192) counts as 2^-50.  A NaN is stored as a NaN
+ * and does not count for the scale.
+ */
+kda_status kda_paged_append_q8(const void *qkv, const int32_t *positions, const int32_t *slot_map,
+                               void *q_out, void *k_pages, void *v_pages, float *k_scales,
+                               float *v_scales, const kda_append_args *f, const kda_paged_args *a);
+
+/*
+ * kda_paged_attn over an 8-bit cache: the same arguments, and results for the keys and
+ * values that the cache stands for.  a->dtype is the type of q and out.
+ *
+ * k_scales, v_scales [n_pages][page_size / 16][Hkv] fp32; read for blocks that hold a
+ *                    key of the request
+ * Workspace: as for kda_paged_attn.  A block whose scale of keys or of values is outside
+ * its bounds (bit 8192) is left out of the requests that hold it.
+ */
+kda_status kda_paged_attn_q8(const void *q, const void *k_pages, const void *v_pages,
+                             const float *k_scales, const float *v_scales,
+                             const int32_t *block_table, const int32_t *cu_seqlens,
+                             const int32_t *kv_lens, void *out, float scale, int32_t causal,
+                             const kda_paged_args *a);
+
+/*
+ * What a server answers with beside a token: its log probability, its rank, the
+ * entropy of the distribution and the most likely tokens.  With y = scale * logits[n],
+ *
+ *     lp(i) = y_i - log sum_j exp(y_j),   H = -sum_j exp(lp(j)) lp(j)
+ *
+ * logits       [N][stride] dtype, aligned as its type is: V logits a row, any stride >= V
+ *              between rows (what lies between them is not read).  -inf: a masked token
+ * tokens       [N] int32 or NULL (then logprobs and ranks are NULL too): a token a row; a
+ *              negative one asks for nothing and gets logprob 0 and rank -1
+ * logprobs     [N] fp32 or NULL  lp of the token
+ * entropy      [N] fp32 or NULL  H, in nats
+ * ranks        [N] int32 or NULL tokens that stand before the given one, by their
+ *              logits, equal ones by the lower index: 0 for the most likely token
+ * top_ids      [N][n_top] int32  the most likely tokens in that order (-1: there are fewer
+ *              that are not masked)
+ * top_logprobs [N][n_top] fp32   their lp (-inf for -1)
+ *
+ * Sums are fp32 in a fixed order.  A row without a finite logit (bit 4096): logprobs
+ * -inf, entropy 0, top_ids -1.  A row with a NaN or +inf, or whose largest scaled logit
+ * overflows (bit 16384): logprobs, entropy and top_logprobs NaN, ranks and top_ids -1.  A
+ * token beyond V (bit 2048) counts as negative.
+ */
+typedef struct {
+  int32_t N;          /* rows, up to 2^20 */
+  int32_t V;          /* vocabulary, 1 .. 2^24 */
+  int32_t n_top;      /* 0 .. 64 */
+  int32_t dtype;      /* kda_dtype of the logits */
+  int64_t stride;     /* elements between rows, >= V */
+  float scale;        /* > 0: one over the temperature; finite, as scale * log2(e) is too */
+  int32_t reserved;   /* 0 */
+  void *stream;       /* cudaStream_t */
+  void *workspace;    /* >= 256 bytes, zero-filled once (the error word) */
+  size_t workspace_bytes;
+  void *ev_begin, *ev_end;
+} kda_logprobs_args;
+
+kda_status kda_token_logprobs(const void *logits, const int32_t *tokens, float *logprobs,
+                              float *entropy, int32_t *ranks, int32_t *top_ids,
+                              float *top_logprobs, const kda_logprobs_args *a);
 
 #ifdef __cplusplus
 }
