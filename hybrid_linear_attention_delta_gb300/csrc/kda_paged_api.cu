@@ -174,8 +174,7 @@ kda_status attn(const void *q, const void *k_pages, const void *v_pages, const f
   p.arrivals = reinterpret_cast<uint32_t *>(ws + lay.arrivals_off);
   p.part = reinterpret_cast<float *>(ws + lay.part_off);
   p.part_ml = reinterpret_cast<float *>(ws + lay.ml_off);
-  // (the kernel of the 8-bit cache works in fp32 whatever the type)
-  p.part_rows = kda::paged_part_rows(a->T_total, G, q8 ? (int32_t)KDA_F32 : a->dtype);
+  p.part_rows = kda::paged_part_rows(a->T_total, G, a->dtype);
   // What an item's start and end cost, and the shortest stretch worth a join, in
   // keys.  In bf16 both are longer where requests bring a tile of rows and more.  (bf16,
   // item cost 128, 192, 256, 320, 384: mixed batch of 24, 64 channels, 910, 875,
@@ -187,13 +186,13 @@ kda_status attn(const void *q, const void *k_pages, const void *v_pages, const f
   // stretch 384, 512, 768, 1024: a prompt of 1000 tokens, 8/2 heads of 64 channels, 66, 71,
   // 78, 96; 200 tokens over 500 keys, 128 channels, 63, 85, 107, 137; 100 over 8000 90, 91,
   // 118, 97; 8 requests of up to 301 120, 120, 120, 142; 8 x 1000 tokens the same.)
-  const bool wide = (int64_t)a->T_total * G >= 128ll * a->B, bf16 = a->dtype == KDA_BF16 && !q8;
+  const bool wide = (int64_t)a->T_total * G >= 128ll * a->B, bf16 = a->dtype == KDA_BF16;
   p.min_stretch = bf16 && wide ? 896 : 384;
   p.item_cost = !bf16 ? 128 : wide ? 320 : 256;
   p.stream = static_cast<cudaStream_t>(a->stream);
   return launch(a->stream, a->ev_begin, a->ev_end, [&] {
     if (q8)
-      return a->dtype == KDA_BF16 ? kda::launch_paged_attn_q8_bf16(p) : kda::launch_paged_attn_q8_f32(p);
+      return bf16 ? kda::launch_paged_attn_q8_bf16(p) : kda::launch_paged_attn_q8_f32(p);
     return bf16 ? kda::launch_paged_attn_bf16(p) : kda::launch_paged_attn_f32(p);
   });
 }

@@ -375,10 +375,6 @@ cudaError_t launch_r(const PagedAttnPlan &p) {
 cudaError_t launch_paged_attn_f32(const PagedAttnPlan &p) {
   return p.d == 128 ? launch_r<float, 128, 4, 16, false>(p) : launch_r<float, 64, 8, 8, false>(p);
 }
-cudaError_t launch_paged_attn_q8_bf16(const PagedAttnPlan &p) {
-  return p.d == 128 ? launch_r<__nv_bfloat16, 128, 4, 16, true>(p)
-                    : launch_r<__nv_bfloat16, 64, 8, 8, true>(p);
-}
 cudaError_t launch_paged_attn_q8_f32(const PagedAttnPlan &p) {
   return p.d == 128 ? launch_r<float, 128, 4, 16, true>(p) : launch_r<float, 64, 8, 8, true>(p);
 }

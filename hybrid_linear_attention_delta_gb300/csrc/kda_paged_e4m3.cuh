@@ -27,10 +27,20 @@ __device__ __forceinline__ void e4m3_to_f32(const uint4 &w, float (&x)[16]) {
     x[2 * i] = f.x, x[2 * i + 1] = f.y;
   }
 }
-// Four values, rounded to nearest; beyond 448 they become 448.
+__device__ __forceinline__ void e4m3_to_f16(const uint4 &w, uint32_t (&x)[8]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+        (__nv_fp8x2_storage_t)(u[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
+    x[i] = (uint32_t)h.x | (uint32_t)h.y << 16;
+  }
+}
+// Four values, rounded to nearest; beyond 448 they become 448 (NOSAT: NaN).
+template <__nv_saturation_t SAT = __NV_SATFINITE>
 __device__ __forceinline__ uint32_t f32_to_e4m3(float a, float b, float c, float d) {
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), SAT, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), SAT, __NV_E4M3);
   return lo | hi << 16;
 }
 
