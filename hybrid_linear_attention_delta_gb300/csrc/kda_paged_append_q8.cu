@@ -244,8 +244,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendPlan p, int rows
         const float ratio = old / s;
         for (int e = lane; e < off * (D / 4); e += 32) {
           uint32_t *w = reinterpret_cast<uint32_t *>(dst + e / (D / 4) * step + e % (D / 4) * 4);
-          float z[16];
-          e4m3_to_f32(make_uint4(*w, 0, 0, 0), z);
+          float z[4];
+          e4m3_to_f32(*w, z);
           *w = f32_to_e4m3(z[0] * ratio, z[1] * ratio, z[2] * ratio, z[3] * ratio);
         }
       }

@@ -96,7 +96,7 @@ struct Layout {
   static constexpr uint32_t kTile = Q8 ? kTile16 / 2 : kTile16;  // K or V tile of the cache
   static constexpr int kStages = D == 128 ? 5 : 8;
   static constexpr int kWide = !Q8 ? 0 : D == 128 ? 2 : 4;   // fp16 tiles of values
-  static constexpr uint32_t kQ = 0;  // two tiles; Q8: the high and then the low parts of each
+  static constexpr uint32_t kQ = 0;  // two tiles
   static constexpr uint32_t kStage = 2 * kTile16;
   static constexpr uint32_t kV16 = kStage + kStages * kTile;
   static constexpr uint32_t kCtl = kV16 + kWide * kTile16;
@@ -126,6 +126,7 @@ struct Ctl {
   uint64_t piece_full[kPieces], piece_empty[kPieces];
   uint64_t drain[2];
   uint64_t v_full[4], v_empty[4];  // Q8: the fp16 tiles of values
+  uint64_t q_raw;                  // Q8: the queries before they are converted
   Work work[kPieces];
   float ml[kRows][2];    // stream 1's references and sums when the streams are joined
   int64_t scratch[kThreads<true> / 16 + 4];
@@ -136,8 +137,8 @@ struct Ctl {
 
 // What the 8-bit cache needs beside.
 struct CtlQ8 : Ctl {
-  alignas(16) float scales[kScaleSlots][2][kTileBlocks];  // of keys, of values
-  float use[kSoftmaxWarps][3][kTileBlocks];  // a warp's: of keys, log2 and inverse of those of values
+  // a tile's: the keys', and log2 and inverse of the values' (-inf and 0: block left out)
+  alignas(16) float scales[kScaleSlots][3][kTileBlocks];
   float q_scale[2][2 * kRows];               // of the rows of an item and the next
 };
 template <bool Q8> using CtlOf = std::conditional_t<Q8, CtlQ8, Ctl>;
@@ -307,18 +308,16 @@ __device__ bool load_role(uint32_t sbase, CtlOf<Q8> &ctl, const AttnArgs &a, con
     int key = w.o.tile0 * kKeys;  // the next tile's first key
     int base = key >> p.page_shift;
     int here = pages_at(base), ahead = pages_at(base + 32);
-    if constexpr (!Q8) {
-      if (nq > 0 && !(ok = warp_wait(&ctl.q_empty, (nq - 1) & 1))) break;
-      if (lane == 0) {
-        const uint32_t bar = smem_u32(&ctl.q_full);
-        mbar_expect_tx(bar, w.split ? q_bytes : 2 * q_bytes);
-        for (int s = 0; s < (w.split ? 1 : 2); ++s)
-          for (int h = 0; h < Ly::kHalves; ++h)
-            tma_load_3d(sbase + Ly::kQ + s * Ly::kTile + h * kHalf, tq, h * 64, w.o.head * p.G,
-                        w.o.tok0 + s * tpt, bar);
-      }
-      ++nq;
+    if (nq > 0 && !(ok = warp_wait(&ctl.q_empty, (nq - 1) & 1))) break;
+    if (lane == 0) {
+      const uint32_t bar = smem_u32(Q8 ? &ctl.q_raw : &ctl.q_full);
+      mbar_expect_tx(bar, w.split ? q_bytes : 2 * q_bytes);
+      for (int s = 0; s < (w.split ? 1 : 2); ++s)
+        for (int h = 0; h < Ly::kHalves; ++h)
+          tma_load_3d(sbase + Ly::kQ + s * Ly::kTile16 + h * kHalf, tq, h * 64, w.o.head * p.G,
+                      w.o.tok0 + s * tpt, bar);
     }
+    ++nq;
     // What follows is done for every tile, and a warp's instructions take long
     // beside two softmax warps on the same scheduler: no divisions, no address
     // made twice (8k-token chunk: 2.26 -> 2.23 ms).
@@ -370,8 +369,16 @@ __device__ bool load_role(uint32_t sbase, CtlOf<Q8> &ctl, const AttnArgs &a, con
         // (the barrier's phase ends with the arrival, whatever has landed before it)
         if (box < t.nb) tma_load_3d(dst, map, 0, t.y, t.z, bar);
         if (keys) {
-          if (lane < 2 * kTileBlocks) (&ctl.scales[tiles % kScaleSlots][0][0])[lane] = t.scale;
-          ++tiles;
+          float(*to)[kTileBlocks] = ctl.scales[tiles++ % kScaleSlots];
+          const uint32_t good = __ballot_sync(0xffffffffu, good_scale(t.scale));
+          const bool both = good >> (lane & 7) & good >> ((lane & 7) + 8) & 1;
+          if (!both && lane < kTileBlocks) raise_error(p.err, ERR_BAD_SCALE);
+          if (lane < kTileBlocks) {
+            to[0][lane] = both ? t.scale : 1.f;
+          } else if (lane < 2 * kTileBlocks) {
+            to[1][lane - kTileBlocks] = both ? log2f(t.scale) : -INFINITY;
+            to[2][lane - kTileBlocks] = both ? 1.f / t.scale : 0.f;
+          }
         }
         __syncwarp();
         if (lane == 0) mbar_expect_tx(bar, (uint32_t)(t.nb << rs) * kRowBytes);
@@ -384,19 +391,25 @@ __device__ bool load_role(uint32_t sbase, CtlOf<Q8> &ctl, const AttnArgs &a, con
       if (++st == Ly::kStages) st = 0, flip ^= 1;
       return true;
     };
-    At now = place(n == 1);
+    // (Q8: placed a tile earlier, for the scales' way from memory)
+    constexpr int kEarly = Q8 ? 2 : 1;
+    At now = place(n == 1), next = now;
+    if (Q8 && n > 1) next = place(n == 2);
     if (!(ok = fetch(tk, now, true))) break;
     for (int i = 1; i < n && ok; ++i) {
-      const At next = place(i == n - 1);
+      At after = next;
+      if (i + kEarly <= n) after = place(i + kEarly == n);
+      if (!Q8) next = after;
       ok = fetch(tk, next, true) && fetch(tv, now, false);
       now = next;
+      if (Q8) next = after;
     }
     if (!(ok = ok && fetch(tv, now, false))) break;
   }
   if (!ok) {  // copies in flight land before the CTA leaves
     for (uint32_t i = e > Ly::kStages ? e - Ly::kStages : 0; i < e; ++i)
       warp_wait(&ctl.kv_full[i % Ly::kStages], (i / Ly::kStages) & 1);
-    if (nq > 0) warp_wait(&ctl.q_full, (nq - 1) & 1);
+    if (nq > 0) warp_wait(Q8 ? &ctl.q_raw : &ctl.q_full, (nq - 1) & 1);
   }
   return ok;
 }
@@ -618,7 +631,9 @@ __device__ bool mma_role(uint32_t sbase, Ctl &ctl, const AttnArgs &a, uint32_t t
 template <int D>
 __device__ bool mma_role_q8(uint32_t sbase, CtlQ8 &ctl, uint32_t tmem, int s) {
   using Ly = Layout<D, true>;
-  constexpr uint32_t kQTile = Ly::kTile16, kPart = kQTile / 2;
+  // Of a query tile, which takes the place of its 16-bit channels: with 128 channels the
+  // high parts and then the low ones, with 64 rows of 128 bytes that hold both.
+  constexpr uint32_t kPart = D == 128 ? Ly::kTile16 / 2 : 64;
   const uint32_t idesc_s = idesc_e4m3(kRows, kKeys), idesc_o = idesc_f16(kRows, D, 0, 1);
   const uint32_t ds = uniform(tmem + s * 128), d_o = uniform(tmem + Ly::kO + s * D);
   const uint32_t dp = uniform(tmem + Ly::kP + s * Ly::kStepP);
@@ -630,9 +645,6 @@ __device__ bool mma_role_q8(uint32_t sbase, CtlQ8 &ctl, uint32_t tmem, int s) {
   int i_last = 0;                      // the stream's last tile
   int xk = 0, xv = 0;                  // tiles of the piece that are behind this stream
   uint64_t q = 0;
-  auto rows_desc = [](uint32_t addr) {
-    return D == 128 ? sw128_desc(uniform(addr), 16, 1024) : sw64_desc(uniform(addr), 16, 512);
-  };
 
   auto key_landed = [&](int i) {
     const uint32_t at = e + entry_k(i);
@@ -665,7 +677,8 @@ __device__ bool mma_role_q8(uint32_t sbase, CtlQ8 &ctl, uint32_t tmem, int s) {
   // and S from stage sk (last: the last that reads Q).
   auto issue = [&](bool do_o, uint32_t sv, uint32_t more, bool end, bool do_s, uint32_t sk, bool last) {
     const uint64_t v = sw128_desc(uniform(sbase + Ly::kV16 + sv * Ly::kTile16), kHalf, 1024);
-    const uint64_t k = rows_desc(sbase + Ly::kStage + sk * Ly::kTile);
+    const uint32_t k_at = uniform(sbase + Ly::kStage + sk * Ly::kTile);
+    const uint64_t k = D == 128 ? sw128_desc(k_at, 16, 1024) : sw64_desc(k_at, 16, 512);
     if (elect_one()) {
       tc_fence_after();
       if (do_o) {
@@ -741,7 +754,7 @@ __device__ bool mma_role_q8(uint32_t sbase, CtlQ8 &ctl, uint32_t tmem, int s) {
     const int cnt = s ? w->cnt1 : w->cnt0;
     if (!(ok = warp_wait(&ctl.q_full, nq++ & 1))) break;
     if (cnt > 0) {
-      q = rows_desc(sbase + Ly::kQ + (split ? 0 : s) * kQTile);
+      q = sw128_desc(uniform(sbase + Ly::kQ + (split ? 0 : s) * Ly::kTile16), 16, 1024);
       const int i0 = split ? s : 0, step = split ? 2 : 1;  // tiles i0, i0 + step, ...
       i_last = i0 + (cnt - 1) * step;
       ok = turn(-1, 0, i0);
@@ -785,51 +798,45 @@ __device__ bool convert_role(uint32_t sbase, CtlQ8 &ctl, const AttnArgs &a) {
     if (w.o.n == 0) return true;
     const int n = w.o.tile1 - w.o.tile0;
     if (n == 0) continue;
-    if (nq > 0 && !warp_wait(&ctl.q_empty, (nq - 1) & 1)) return false;
+    // Queries: the lanes that hold a row read all of it, then write its parts over it.
+    if (!warp_wait(&ctl.q_raw, nq & 1)) return false;
     for (int s = 0; s < (w.split ? 1 : 2); ++s) {
       const int rows = min(a.tpt, w.o.n - s * a.tpt) * p.G;
-      const uint32_t tile = sbase + Ly::kQ + s * Ly::kTile16;
+      const int l = lane % kLanesQ, sub = lane / kLanesQ;  // channels 8 l ...
+#pragma unroll 2
       for (int r0 = warp * kRowsQ; r0 < rows; r0 += kConvertWarps * kRowsQ) {
-        const int r = r0 + lane / kLanesQ, ch = lane % kLanesQ * 8;
-        const int t = r / p.G;
-        const bool live = r < rows;
-        uint4 raw = make_uint4(0, 0, 0, 0);
-        if (live)
-          raw = __ldg(reinterpret_cast<const uint4 *>(
-              static_cast<const __nv_bfloat16 *>(p.q) +
-              ((int64_t)(w.o.tok0 + s * a.tpt + t) * p.Hq + w.o.head * p.G + (r - t * p.G)) * D + ch));
-        const __nv_bfloat16 *h = reinterpret_cast<const __nv_bfloat16 *>(&raw);
-        float x[8], amax = 0.f;
+        const int r = r0 + sub;  // (rows behind the last are of no use, and of no harm)
+        const uint32_t tile = sbase + Ly::kQ + s * Ly::kTile16;
+        const uint4 raw = ld_shared_v4(tile + l / 8 * kHalf + sw128_chunk(r, l % 8));
+        const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&raw);
+        __nv_bfloat162 top = __hmax2(__hmax2(__habs2(h[0]), __habs2(h[1])),
+                                     __hmax2(__habs2(h[2]), __habs2(h[3])));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[i] = __bfloat162float(h[i]);
-          amax = fmaxf(amax, fabsf(x[i]));
-        }
-#pragma unroll
-        for (int o = kLanesQ / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        // amax in [2^E, 2^(E+1)) goes to [2^7, 2^8); in two steps, as 2^(7 - E) may overflow
-        const int E = amax > 0.f ? max((int)(__float_as_uint(amax) >> 23), 1) - 127 : 7;
-        const int up = (7 - E) / 2;
-        const float f0 = __uint_as_float((uint32_t)(127 + up) << 23) * (a.neg_q ? -1.f : 1.f);
-        const float f1 = __uint_as_float((uint32_t)(127 + 7 - E - up) << 23);
+        for (int o = kLanesQ / 2; o > 0; o >>= 1) top = __hmax2(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float amax = fmaxf(__low2float(top), __high2float(top));
+        // amax in [2^E, 2^(E+1)) goes to [2^7, 2^8).  (Below 2^-119 to less: 2^(7 - E) has
+        // to be a float.)  e4m3 has no infinities: a row with one becomes NaN, as its
+        // scores would.
+        const int E = amax > 0.f ? max((int)(__float_as_uint(amax) >> 23) - 127, -119) : 7;
+        float f = __uint_as_float((uint32_t)(127 + 7 - E) << 23);
+        if (!(amax < INFINITY)) f = NAN;
+        if (a.neg_q) f = -f;
         uint32_t hi[2], lo[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float y[4], z[16];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) y[j] = x[4 * i + j] * f0 * f1;
-          // (an infinite channel becomes a NaN, as its scores would)
-          hi[i] = f32_to_e4m3<__NV_NOSAT>(y[0], y[1], y[2], y[3]);
-          e4m3_to_f32(make_uint4(hi[i], 0, 0, 0), z);
-          lo[i] = f32_to_e4m3<__NV_NOSAT>(y[0] - z[0], y[1] - z[1], y[2] - z[2], y[3] - z[3]);
+        for (int i = 0; i < 4; ++i) {
+          const float2 x = __bfloat1622float2(h[i]);
+          // fp16 holds the scaled channels down to 2^-24 and what the first part leaves
+          const __half2 y = __floats2half2_rn(x.x * f, x.y * f);
+          const uint32_t a8 = f16_to_e4m3(y);
+          const uint32_t b8 = f16_to_e4m3(__hsub2(y, e4m3_to_f16(a8)));
+          hi[i / 2] = i % 2 ? hi[i / 2] | a8 << 16 : a8;
+          lo[i / 2] = i % 2 ? lo[i / 2] | b8 << 16 : b8;
         }
-        if (live) {
-          const uint32_t at = tile + r * D + (D == 128 ? (((ch >> 4) ^ (r & 7)) << 4)
-                                                       : (((ch >> 4) ^ ((r >> 1) & 3)) << 4)) + (ch & 15);
-          st_shared_v2(at, hi[0], hi[1]);
-          st_shared_v2(at + Ly::kTile16 / 2, lo[0], lo[1]);
-          if (lane % kLanesQ == 0) ctl.q_scale[nq & 1][s * kRows + r] = ldexpf(1.f, E - 7);
-        }
+        const uint32_t to = tile + sw128_chunk(r, l / 2) + l % 2 * 8;
+        st_shared_v2(to, hi[0], hi[1]);
+        if constexpr (D == 128) st_shared_v2(to + Ly::kTile16 / 2, lo[0], lo[1]);
+        else st_shared_v2(tile + sw128_chunk(r, 4 + l / 2) + l % 2 * 8, lo[0], lo[1]);
+        if (l == 0) ctl.q_scale[nq & 1][s * kRows + r] = ldexpf(1.f, E - 7);
       }
     }
     fence_async_smem();
@@ -1054,30 +1061,27 @@ __device__ bool softmax_role(CtlOf<Q8> &ctl, const AttnArgs &a, uint32_t tmem, i
         tc_fence_after();
         const int tile = w.o.tile0 + (w.split ? 2 * j + s : j);
         const int left = seen - tile * kKeys;  // keys of the tile that the row sees
-        [[maybe_unused]] const float *use = nullptr;  // Q8: this warp's view of the tile's scales
-        [[maybe_unused]] bool left_out = false;       // ... of blocks that have none
-        if constexpr (Q8) {
-          if (j == 0) c = a.c * ctl.q_scale[n_item & 1][(w.split ? 0 : s * kRows) + r];
-          float *mine = &ctl.use[threadIdx.x >> 5][0][0];
-          const float(*sc)[kTileBlocks] = ctl.scales[(tiles + tile - w.o.tile0) % kScaleSlots];
-          bool good = true;
-          if (lane < kTileBlocks) {
-            const float ks = sc[0][lane], vs = sc[1][lane];
-            good = good_scale(ks) && good_scale(vs);
-            if (!good) raise_error(p.err, ERR_BAD_SCALE);
-            mine[lane] = good ? ks : 1.f;
-            mine[kTileBlocks + lane] = good ? log2f(vs) : -INFINITY;
-            mine[2 * kTileBlocks + lane] = good ? 1.f / vs : 0.f;
-          }
-          left_out = !__all_sync(0xffffffffu, good);
-          __syncwarp();
-          use = mine;
-        }
-        // (never 0, so that a masked score stays -inf in powers of two)
-        auto k_scale = [&](int b) { return fmaxf(c * use[b], FLT_TRUE_MIN); };
         uint32_t x[4][32];
 #pragma unroll
         for (int q = 0; q < 4; ++q) tmem_ld32_async(ts + q * 32, x[q]);
+        // Q8: the scales of blocks 2q and 2q + 1: of the keys, with the row's, and the rest
+        [[maybe_unused]] const float(*sc)[kTileBlocks] = nullptr;
+        if constexpr (Q8) {
+          // (not below 2^-99: times a scale it is never 0, so that a masked score stays -inf
+          // in powers of two)
+          if (j == 0) c = fmaxf(a.c * ctl.q_scale[n_item & 1][(w.split ? 0 : s * kRows) + r], 0x1p-99f);
+          sc = ctl.scales[(tiles + tile - w.o.tile0) % kScaleSlots];
+        }
+        struct Two {
+          float k[2], v[2];
+        };
+        auto scales_of = [&](int q) {
+          const float2 k = *reinterpret_cast<const float2 *>(&sc[0][2 * q]);
+          const float2 v = *reinterpret_cast<const float2 *>(&sc[1][2 * q]);
+          return Two{{c * k.x, c * k.y}, {v.x, v.y}};
+        };
+        [[maybe_unused]] Two now;
+        if constexpr (Q8) now = scales_of(0);
         tmem_wait_ld();
 #pragma unroll
         for (int q = 0; q < 4; ++q) reg_fence(x[q]);
@@ -1102,14 +1106,6 @@ __device__ bool softmax_role(CtlOf<Q8> &ctl, const AttnArgs &a, uint32_t tmem, i
               if (!(bits >> i & 1u)) x[q][i] = 0xff800000u;  // -inf
           }
         }
-        if constexpr (Q8) {
-          if (left_out)
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (use[kTileBlocks + 2 * q + i / 16] == -INFINITY) x[q][i] = 0xff800000u;
-        }
         // The first tile's maximum is the reference.  It holds while a tile's
         // weights sum to 2^16 at most, which the sum itself tells; else the
         // tile is taken again with its own maximum.  (A row that sees no key in
@@ -1125,6 +1121,7 @@ __device__ bool softmax_role(CtlOf<Q8> &ctl, const AttnArgs &a, uint32_t tmem, i
             for (int q = 0; q < 4; ++q) {
               if constexpr (Q8) {
                 float half[2];
+                const Two two = scales_of(q);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                   half[h] = fmaxf(__uint_as_float(x[q][16 * h]), __uint_as_float(x[q][16 * h + 1]));
@@ -1132,7 +1129,7 @@ __device__ bool softmax_role(CtlOf<Q8> &ctl, const AttnArgs &a, uint32_t tmem, i
                   for (int i = 2; i < 16; i += 2)
                     half[h] = max3(half[h], __uint_as_float(x[q][16 * h + i]),
                                    __uint_as_float(x[q][16 * h + i + 1]));
-                  half[h] = fmaf(half[h], k_scale(2 * q + h), use[kTileBlocks + 2 * q + h]);
+                  half[h] = fmaf(half[h], two.k[h], two.v[h]);
                 }
                 top[q] = fmaxf(half[0], half[1]);
               } else {
@@ -1176,31 +1173,39 @@ __device__ bool softmax_role(CtlOf<Q8> &ctl, const AttnArgs &a, uint32_t tmem, i
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             uint32_t pk[16];
+            [[maybe_unused]] Two next = now;
+            [[maybe_unused]] float2 inv;
+            if constexpr (Q8) {
+              next = scales_of((q + 1) & 3);  // (q = 3: for the pass after this one)
+              inv = *reinterpret_cast<const float2 *>(&sc[2][2 * q]);
+            }
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               float u, v;
               if constexpr (Q8) {
                 if (i % 8 == 0) {  // a block
-                  const float kc = k_scale(2 * q + i / 8), by = use[kTileBlocks + 2 * q + i / 8] - ref;
-                  c2 = pair(kc, kc), ref2 = pair(by, by);
-                  sum[0] = sum[1] = 0ull;
+                  const float by = now.v[i / 8] - ref;
+                  c2 = pair(now.k[i / 8], now.k[i / 8]), ref2 = pair(by, by);
+                  sum[0] = 0ull;
                 }
               }
               unpair(fma2(pair(__uint_as_float(x[q][2 * i]), __uint_as_float(x[q][2 * i + 1])), c2,
                           ref2), u, v);
               u = ex2_approx(u);
               v = ex2_approx(v);
-              sum[i & 1] = add2(sum[i & 1], pair(u, v));
+              uint64_t &to = sum[Q8 ? 0 : i & 1];
+              to = add2(to, pair(u, v));
               pk[i] = Q8 ? pack_f16x2(u, v) : pack_bf16x2(u, v);
               if constexpr (Q8) {
                 if (i % 8 == 7) {
                   float su, sv;
-                  unpair(add2(sum[0], sum[1]), su, sv);
+                  unpair(sum[0], su, sv);
                   sum_j += su + sv;
-                  l_j = fmaf(su + sv, use[2 * kTileBlocks + 2 * q + i / 8], l_j);
+                  l_j = fmaf(su + sv, i < 8 ? inv.x : inv.y, l_j);
                 }
               }
             }
+            if constexpr (Q8) now = next;
             if (q == 0 && !own()) return false;
             tmem_st16(tp + q * 16, pk);
           }
@@ -1400,6 +1405,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
       mbar_init(smem_u32(&ctl.v_full[i]), kConvertWarps);
       mbar_init(smem_u32(&ctl.v_empty[i]), 2);
     }
+    mbar_init(smem_u32(&ctl.q_raw), 1);
     mbar_init(smem_u32(&ctl.q_full), Q8 ? kConvertWarps : 1);
     mbar_init(smem_u32(&ctl.q_empty), 2);
     for (int s = 0; s < 2; ++s) {
@@ -1421,7 +1427,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
     fence_mbar_init();
   }
   if (warp == kLoadWarp && (tid & 31) == 0) {
-    if constexpr (!Q8) prefetch_tmap(&tq);
+    prefetch_tmap(&tq);
     prefetch_tmap(&tk);
     prefetch_tmap(&tv);
   }
@@ -1434,11 +1440,11 @@ attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
 
   // a softmax thread holds a row of 128 scores: registers go from the last
   // warpgroup to the other two (168 a thread at the launch, 2 * 216 + 72 = 3 * 168; Q8:
-  // 128, 2 * 184 + 2 * 72 = 4 * 128)
+  // 128, 2 * 192 + 72 + 56 = 4 * 128)
   bool ok = true;
   if (!work) {  // bad cu_seqlens
   } else if (warp < kSoftmaxWarps) {
-    if constexpr (Q8) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    if constexpr (Q8) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     ok = softmax_role<D, LONG, Q8>(ctl, a, tmem, warp >> 2);
     if (!ok) {
@@ -1451,7 +1457,8 @@ attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
       named_bar_arrive(1 + (warp >> 2), 128);
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (Q8 && warp >= kConvertWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp < kLoadWarp) {
       if constexpr (Q8) ok = mma_role_q8<D>(sbase, ctl, tmem, warp - kMmaWarp);
       else ok = mma_role<D>(sbase, ctl, a, tmem, warp - kMmaWarp);
@@ -1517,19 +1524,14 @@ cudaError_t launch_d(const PagedAttnPlan &p) {
   CUtensorMap tq, tk, tv;
   const uint64_t slots = (uint64_t)p.n_pages * p.page_size;
   const uint32_t box = p.page_size < kKeys ? p.page_size : kKeys;
-  if constexpr (Q8) {
-    // keys as the products read them, values as they lie
-    if (!make_map(&tk, p.k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, D, p.Hkv, slots, D, 1, box,
-                  D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B) ||
-        !make_map(&tv, p.v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, D, p.Hkv, slots, D, 1, box,
-                  CU_TENSOR_MAP_SWIZZLE_NONE))
-      return cudaErrorInvalidValue;
-    tq = tk;  // (not used)
-  } else if (!make_map(&tq, p.q, D, p.Hq, p.T, p.G, kRows / p.G) ||
-             !make_map(&tk, p.k, D, p.Hkv, slots, 1, box) ||
-             !make_map(&tv, p.v, D, p.Hkv, slots, 1, box)) {
+  if (!make_map(&tq, p.q, D, p.Hq, p.T, p.G, kRows / p.G)) return cudaErrorInvalidValue;
+  if (!(Q8 ? make_map(&tk, p.k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, D, p.Hkv, slots, D, 1, box,
+                      D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B) &&
+                 make_map(&tv, p.v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, D, p.Hkv, slots, D, 1, box,
+                          CU_TENSOR_MAP_SWIZZLE_NONE)  // keys as the products read them
+           : make_map(&tk, p.k, D, p.Hkv, slots, 1, box) &&
+                 make_map(&tv, p.v, D, p.Hkv, slots, 1, box)))
     return cudaErrorInvalidValue;
-  }
   AttnArgs a;
   a.p = p;
   // (never 0, so that a masked score stays -inf in powers of two; the smallest float

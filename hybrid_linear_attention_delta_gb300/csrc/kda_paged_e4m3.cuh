@@ -16,31 +16,46 @@ constexpr float kMaxE4m3 = 448.f;
 
 __device__ __forceinline__ bool good_scale(float s) { return s >= kMinScale && s <= kMaxScale; }
 
-// 16 values; every e4m3 value is an fp16 value.
-__device__ __forceinline__ void e4m3_to_f32(const uint4 &w, float (&x)[16]) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+// Four and 16 values; every e4m3 value is an fp16 value.
+__device__ __forceinline__ void e4m3_to_f32(uint32_t w, float (&x)[4]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
-        (__nv_fp8x2_storage_t)(u[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
+  for (int i = 0; i < 2; ++i) {
+    const __half2_raw h =
+        __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> (16 * i)), __NV_E4M3);
     const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
     x[2 * i] = f.x, x[2 * i + 1] = f.y;
   }
+}
+__device__ __forceinline__ void e4m3_to_f32(const uint4 &w, float (&x)[16]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float y[4];
+    e4m3_to_f32(u[i], y);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[4 * i + j] = y[j];
+  }
+}
+// Two values (the low 16 bits of w), and back, rounded to nearest.
+__device__ __forceinline__ __half2 e4m3_to_f16(uint32_t w) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)w, __NV_E4M3);
+  return *reinterpret_cast<const __half2 *>(&h);
+}
+__device__ __forceinline__ uint32_t f16_to_e4m3(__half2 x) {
+  return __nv_cvt_halfraw2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
 }
 __device__ __forceinline__ void e4m3_to_f16(const uint4 &w, uint32_t (&x)[8]) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
-        (__nv_fp8x2_storage_t)(u[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
-    x[i] = (uint32_t)h.x | (uint32_t)h.y << 16;
+    const __half2 h = e4m3_to_f16(u[i >> 1] >> (16 * (i & 1)));
+    x[i] = *reinterpret_cast<const uint32_t *>(&h);
   }
 }
-// Four values, rounded to nearest; beyond 448 they become 448 (NOSAT: NaN).
-template <__nv_saturation_t SAT = __NV_SATFINITE>
+// Four values, rounded to nearest; beyond 448 they become 448.
 __device__ __forceinline__ uint32_t f32_to_e4m3(float a, float b, float c, float d) {
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), SAT, __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), SAT, __NV_E4M3);
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
   return lo | hi << 16;
 }
 
