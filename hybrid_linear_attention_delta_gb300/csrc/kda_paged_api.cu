@@ -192,7 +192,9 @@ kda_status attn(const void *q, const void *k_pages, const void *v_pages, const f
   p.stream = static_cast<cudaStream_t>(a->stream);
   return launch(a->stream, a->ev_begin, a->ev_end, [&] {
     if (q8)
-      return bf16 ? kda::launch_paged_attn_q8_bf16(p) : kda::launch_paged_attn_q8_f32(p);
+      return !bf16  ? kda::launch_paged_attn_q8_f32(p)
+             : wide ? kda::launch_paged_attn_q8_wide(p)
+                    : kda::launch_paged_attn_q8_few(p);
     return bf16 ? kda::launch_paged_attn_bf16(p) : kda::launch_paged_attn_f32(p);
   });
 }

@@ -140,6 +140,8 @@ struct CtlQ8 : Ctl {
   // a tile's: the keys', and log2 and inverse of the values' (-inf and 0: block left out)
   alignas(16) float scales[kScaleSlots][3][kTileBlocks];
   float q_scale[2][2 * kRows];               // of the rows of an item and the next
+  float copy_ml[kRows][2];                   // references and sums of the copies of rows
+  float copies[3][32][32];                   // 32 channels of the copies but the first
 };
 template <bool Q8> using CtlOf = std::conditional_t<Q8, CtlQ8, Ctl>;
 
@@ -780,15 +782,30 @@ __device__ bool mma_role_q8(uint32_t sbase, CtlQ8 &ctl, uint32_t tmem, int s) {
   return ok;
 }
 
+// FEW: how often the rows of an item are in its tile (see softmax_role).
+template <bool FEW>
+__device__ __forceinline__ int copies(const Work &w, int G) {
+  const int rows = w.o.n * G;
+  return !FEW || !w.split || rows > kRows / 2 ? 1 : rows > kRows / 4 ? 2 : 4;
+}
+
 // ------------------------------------------------------------------ conversions
 // Q8: the queries of an item into two e4m3 parts, the values of a tile into fp16.
-template <int D>
+template <int D, bool FEW>
 __device__ bool convert_role(uint32_t sbase, CtlQ8 &ctl, const AttnArgs &a) {
   using Ly = Layout<D, true>;
   const PagedAttnPlan &p = a.p;
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
   constexpr int kLanesQ = D / 8, kRowsQ = 32 / kLanesQ;   // of a query row; rows a warp at a time
   constexpr int kLanesV = D / 16, kRowsV = 32 / kLanesV;  // of a row of values
+  // A lane's part of the values: 16 channels, chunks 2c and 2c + 1 of a half, of every
+  // kRowsV-th row from v_row on.  Eight lanes read 128 bytes side by side; with 128
+  // channels half of them take the next row's, so that what they write, even or odd
+  // chunks by the row, lies in all banks.
+  const int c = lane % kLanesV;
+  const int v_row = warp * (kKeys / kConvertWarps) + (D == 128 ? lane / kLanesV ^ c / 4 : lane / kLanesV);
+  const uint32_t v_src = v_row * D + c * 16;
+  const uint32_t v_dst = c / 4 * kHalf + sw128_chunk(v_row, c % 4 * 2);
   PieceReader pieces;
   uint32_t e = 0, v0 = 0, nq = 0;
   for (;; pieces.release(ctl)) {
@@ -800,43 +817,61 @@ __device__ bool convert_role(uint32_t sbase, CtlQ8 &ctl, const AttnArgs &a) {
     if (n == 0) continue;
     // Queries: the lanes that hold a row read all of it, then write its parts over it.
     if (!warp_wait(&ctl.q_raw, nq & 1)) return false;
+    const int reps = copies<FEW>(w, p.G);
     for (int s = 0; s < (w.split ? 1 : 2); ++s) {
       const int rows = min(a.tpt, w.o.n - s * a.tpt) * p.G;
       const int l = lane % kLanesQ, sub = lane / kLanesQ;  // channels 8 l ...
-#pragma unroll 2
-      for (int r0 = warp * kRowsQ; r0 < rows; r0 += kConvertWarps * kRowsQ) {
-        const int r = r0 + sub;  // (rows behind the last are of no use, and of no harm)
-        const uint32_t tile = sbase + Ly::kQ + s * Ly::kTile16;
-        const uint4 raw = ld_shared_v4(tile + l / 8 * kHalf + sw128_chunk(r, l % 8));
-        const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&raw);
-        __nv_bfloat162 top = __hmax2(__hmax2(__habs2(h[0]), __habs2(h[1])),
-                                     __hmax2(__habs2(h[2]), __habs2(h[3])));
+      constexpr int kStep = kConvertWarps * kRowsQ, kBatch = 4;  // (rows of a batch together:
+      // one at a time, a row's way through the shuffles and conversions is 600 cycles)
+      const uint32_t tile = sbase + Ly::kQ + s * Ly::kTile16;
+      for (int r0 = warp * kRowsQ + sub; r0 - sub < rows; r0 += kBatch * kStep) {
+        // (rows behind the last are of no use, and of no harm)
+        uint4 raw[kBatch];
+        __nv_bfloat162 top[kBatch];
 #pragma unroll
-        for (int o = kLanesQ / 2; o > 0; o >>= 1) top = __hmax2(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float amax = fmaxf(__low2float(top), __high2float(top));
-        // amax in [2^E, 2^(E+1)) goes to [2^7, 2^8).  (Below 2^-119 to less: 2^(7 - E) has
-        // to be a float.)  e4m3 has no infinities: a row with one becomes NaN, as its
-        // scores would.
-        const int E = amax > 0.f ? max((int)(__float_as_uint(amax) >> 23) - 127, -119) : 7;
-        float f = __uint_as_float((uint32_t)(127 + 7 - E) << 23);
-        if (!(amax < INFINITY)) f = NAN;
-        if (a.neg_q) f = -f;
-        uint32_t hi[2], lo[2];
+        for (int u = 0; u < kBatch; ++u)
+          raw[u] = ld_shared_v4(tile + l / 8 * kHalf + sw128_chunk(r0 + u * kStep, l % 8));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 x = __bfloat1622float2(h[i]);
-          // fp16 holds the scaled channels down to 2^-24 and what the first part leaves
-          const __half2 y = __floats2half2_rn(x.x * f, x.y * f);
-          const uint32_t a8 = f16_to_e4m3(y);
-          const uint32_t b8 = f16_to_e4m3(__hsub2(y, e4m3_to_f16(a8)));
-          hi[i / 2] = i % 2 ? hi[i / 2] | a8 << 16 : a8;
-          lo[i / 2] = i % 2 ? lo[i / 2] | b8 << 16 : b8;
+        for (int u = 0; u < kBatch; ++u) {
+          const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&raw[u]);
+          top[u] = __hmax2(__hmax2(__habs2(h[0]), __habs2(h[1])), __hmax2(__habs2(h[2]), __habs2(h[3])));
         }
-        const uint32_t to = tile + sw128_chunk(r, l / 2) + l % 2 * 8;
-        st_shared_v2(to, hi[0], hi[1]);
-        if constexpr (D == 128) st_shared_v2(to + Ly::kTile16 / 2, lo[0], lo[1]);
-        else st_shared_v2(tile + sw128_chunk(r, 4 + l / 2) + l % 2 * 8, lo[0], lo[1]);
-        if (l == 0) ctl.q_scale[nq & 1][s * kRows + r] = ldexpf(1.f, E - 7);
+#pragma unroll
+        for (int o = kLanesQ / 2; o > 0; o >>= 1)
+#pragma unroll
+          for (int u = 0; u < kBatch; ++u)
+            top[u] = __hmax2(top[u], __shfl_xor_sync(0xffffffffu, top[u], o));
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const int r = r0 + u * kStep;
+          const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&raw[u]);
+          const float amax = fmaxf(__low2float(top[u]), __high2float(top[u]));
+          // amax in [2^E, 2^(E+1)) goes to [2^7, 2^8).  (Below 2^-119 to less: 2^(7 - E)
+          // has to be a float.)  e4m3 has no infinities: a row with one becomes NaN, as
+          // its scores would.
+          const int E = amax > 0.f ? max((int)(__float_as_uint(amax) >> 23) - 127, -119) : 7;
+          float f = __uint_as_float((uint32_t)(127 + 7 - E) << 23);
+          if (!(amax < INFINITY)) f = NAN;
+          if (a.neg_q) f = -f;
+          uint32_t hi[2], lo[2];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 x = __bfloat1622float2(h[i]);
+            // fp16 holds the scaled channels down to 2^-24 and what the first part leaves
+            const __half2 y = __floats2half2_rn(x.x * f, x.y * f);
+            const uint32_t a8 = f16_to_e4m3(y);
+            const uint32_t b8 = f16_to_e4m3(__hsub2(y, e4m3_to_f16(a8)));
+            hi[i / 2] = i % 2 ? hi[i / 2] | a8 << 16 : a8;
+            lo[i / 2] = i % 2 ? lo[i / 2] | b8 << 16 : b8;
+          }
+          for (int to = r; to < kRows && r < kRows / reps; to += kRows / reps) {
+            st_shared_v2(tile + sw128_chunk(to, l / 2) + l % 2 * 8, hi[0], hi[1]);
+            if constexpr (D == 128)
+              st_shared_v2(tile + Ly::kTile16 / 2 + sw128_chunk(to, l / 2) + l % 2 * 8, lo[0], lo[1]);
+            else st_shared_v2(tile + sw128_chunk(to, 4 + l / 2) + l % 2 * 8, lo[0], lo[1]);
+            if (l == 0) ctl.q_scale[nq & 1][s * kRows + to] = ldexpf(1.f, E - 7);
+          }
+        }
       }
     }
     fence_async_smem();
@@ -846,21 +881,30 @@ __device__ bool convert_role(uint32_t sbase, CtlQ8 &ctl, const AttnArgs &a) {
       const uint32_t at = e + entry_v(i, n), st = at % Ly::kStages, to = (v0 + i) % Ly::kWide;
       if (!warp_wait(&ctl.kv_full[st], (at / Ly::kStages) & 1)) return false;
       if (v0 + i >= Ly::kWide && !warp_wait(&ctl.v_empty[to], ((v0 + i) / Ly::kWide - 1) & 1)) return false;
+      const uint32_t src = sbase + Ly::kStage + st * Ly::kTile + v_src;
+      const uint32_t dst = sbase + Ly::kV16 + to * Ly::kTile16 + v_dst;
       // Slots behind the request's last key may hold anything: their weights are zero,
       // and so must their values be.
-      const int left = w.o.kv - (w.o.tile0 + i) * kKeys;
-      const uint32_t src = sbase + Ly::kStage + st * Ly::kTile + lane * 16;
-      const int c = lane % kLanesV;  // 16 channels: chunks 2c and 2c + 1
-      const uint32_t dst = sbase + Ly::kV16 + to * Ly::kTile16 + (c / 4) * kHalf;
+      const int left = w.o.kv - (w.o.tile0 + i) * kKeys - v_row;
+      constexpr int kBatch = 4;
 #pragma unroll
-      for (int r0 = 0; r0 < kKeys / kConvertWarps; r0 += kRowsV) {
-        const int first = warp * (kKeys / kConvertWarps) + r0, r = first + lane / kLanesV;
-        uint4 raw = ld_shared_v4(src + first * D);
-        if (r >= left) raw = make_uint4(0, 0, 0, 0);
-        uint32_t h[8];
-        e4m3_to_f16(raw, h);
-        st_shared_v4(dst + sw128_chunk(r, c % 4 * 2), h[0], h[1], h[2], h[3]);
-        st_shared_v4(dst + sw128_chunk(r, c % 4 * 2 + 1), h[4], h[5], h[6], h[7]);
+      for (int r = 0; r < kKeys / kConvertWarps; r += kBatch * kRowsV) {
+        uint4 raw[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) raw[u] = ld_shared_v4(src + (r + u * kRowsV) * D);
+        if (left < kKeys / kConvertWarps)
+#pragma unroll
+          for (int u = 0; u < kBatch; ++u)
+            if (r + u * kRowsV >= left) raw[u] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          uint32_t h[8];
+          e4m3_to_f16(raw[u], h);
+          // (the rows of every other turn have the other value of bit 2)
+          const uint32_t at = (dst ^ (kRowsV % 8 && u % 2 ? 64u : 0u)) + (r + u * kRowsV) * 128;
+          st_shared_v4(at, h[0], h[1], h[2], h[3]);
+          st_shared_v4(at ^ 16u, h[4], h[5], h[6], h[7]);
+        }
       }
       fence_async_smem();
       warp_arrive(&ctl.v_full[to]);
@@ -1022,18 +1066,149 @@ __device__ void join_pieces(const PagedAttnPlan &p, const PagedPiece &o, int r0,
   else join_rows<D, 2, 8>(p, o, r0, r1, warp, n_warps, r1 - r0 <= n_warps);
 }
 
-template <int D, bool LONG, bool Q8>
+// Q8: a thread's row.
+struct RowState {
+  float c;       // exponents per score: |scale| log2(e) and the scale of the row's query
+  float ref, l;  // reference and sum
+  bool live, first;  // first: its first tile
+};
+// Weights of a row's first maximum (2^kHead) and of a tile's sum at most, so that fp16
+// weights neither overflow nor lose much.
+constexpr float kHead = 6.f, kMostSum = 32768.f;
+
+// Q8: weights of a tile's columns [32 NQ part, 32 NQ (part + 1)), zeros in the others.  As
+// for the 16-bit cache (see softmax_role), but the exponents take the scales of the
+// columns' blocks, the reference is that of the weights with the values' scales, and the
+// row's sum takes them without.  own(): waits until P and O are this tile's; read():
+// the scores have been read.
+template <int D, int NQ, typename Own, typename Read>
+__device__ __forceinline__ bool tile_q8(uint32_t ts, uint32_t tp, uint32_t to,
+                                        const float (&sc)[3][kTileBlocks], int part, int left,
+                                        RowState &st, Own own, Read read) {
+  const int q0 = part * NQ;
+  uint32_t x[NQ][32];
+#pragma unroll
+  for (int q = 0; q < NQ; ++q) tmem_ld32_async(ts + (q0 + q) * 32, x[q]);
+  struct Two {  // of two blocks: c times the keys' scale, log2 of the values'
+    float k[2], v[2];
+  };
+  auto scales_of = [&](int q) {
+    const float2 ks = *reinterpret_cast<const float2 *>(&sc[0][2 * (q0 + q)]);
+    const float2 vs = *reinterpret_cast<const float2 *>(&sc[1][2 * (q0 + q)]);
+    return Two{{st.c * ks.x, st.c * ks.y}, {vs.x, vs.y}};
+  };
+  Two now = scales_of(0);
+  tmem_wait_ld();
+#pragma unroll
+  for (int q = 0; q < NQ; ++q) reg_fence(x[q]);
+  read();
+  if (__any_sync(0xffffffffu, st.live && left < kKeys)) {
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      const int n = min(32, max(0, left - (q0 + q) * 32));
+      const uint32_t bits = n == 32 ? 0xffffffffu : (1u << n) - 1u;
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (!(bits >> i & 1u)) x[q][i] = 0xff800000u;  // -inf
+    }
+  }
+  float sum = 0.f, l = 0.f;
+  for (bool again = st.first;; again = true) {
+    if (again) {
+      float all = -INFINITY;
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        const Two two = scales_of(q);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float top = fmaxf(__uint_as_float(x[q][16 * h]), __uint_as_float(x[q][16 * h + 1]));
+#pragma unroll
+          for (int i = 2; i < 16; i += 2)
+            top = max3(top, __uint_as_float(x[q][16 * h + i]), __uint_as_float(x[q][16 * h + i + 1]));
+          all = fmaxf(all, fmaf(top, two.k[h], two.v[h]));
+        }
+      }
+      const float tm = all - kHead;
+      if (st.first) {
+        if (st.live) st.ref = tm > -INFINITY ? tm : -FLT_MAX;
+      } else {
+        const bool move = st.live && !(sum <= kMostSum) && tm > st.ref;
+        const float keep = move ? ex2_approx(st.ref - tm) : 1.f;
+        if (move) st.ref = tm;
+        st.l *= keep;
+        if (!own()) return false;
+        tmem_wait_st();
+        tc_fence_after();
+#pragma unroll
+        for (int q = 0; q < D / 16; ++q) {
+          uint32_t o[16];
+          tmem_ld16_async(to + q * 16, o);
+          tmem_wait_ld();
+          reg_fence16(o);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
+          tmem_st16(to + q * 16, o);
+        }
+      }
+    }
+    sum = l = 0.f;
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      // (asked for ahead: the last chunk's are for a second pass)
+      const Two next = scales_of((q + 1) % NQ);
+      const float2 inv = *reinterpret_cast<const float2 *>(&sc[2][2 * (q0 + q)]);
+      uint32_t pk[16];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float by = now.v[h] - st.ref;
+        const uint64_t k2 = pair(now.k[h], now.k[h]), by2 = pair(by, by);
+        uint64_t s2[2] = {0ull, 0ull};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float a, b;
+          unpair(fma2(pair(__uint_as_float(x[q][16 * h + 2 * i]),
+                           __uint_as_float(x[q][16 * h + 2 * i + 1])), k2, by2), a, b);
+          a = ex2_approx(a);
+          b = ex2_approx(b);
+          s2[i & 1] = i < 2 ? pair(a, b) : add2(s2[i & 1], pair(a, b));
+          pk[8 * h + i] = pack_f16x2(a, b);
+        }
+        float a, b;
+        unpair(add2(s2[0], s2[1]), a, b);
+        sum += a + b;
+        l = fmaf(a + b, h ? inv.y : inv.x, l);
+      }
+      now = next;
+      if (q == 0) {
+        if (!own()) return false;
+        if constexpr (NQ < 4) {
+          const uint32_t none[16] = {};
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (u / NQ != part) tmem_st16(tp + u * 16, none);
+        }
+      }
+      tmem_st16(tp + (q0 + q) * 16, pk);
+    }
+    if (again || !__any_sync(0xffffffffu, st.live && !(sum <= kMostSum))) break;
+  }
+  st.l += l;
+  return true;
+}
+
+template <int D, bool LONG, bool Q8, bool FEW>
 __device__ bool softmax_role(CtlOf<Q8> &ctl, const AttnArgs &a, uint32_t tmem, int s) {
   const PagedAttnPlan &p = a.p;
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
-  const int r = warp * 32 + lane;          // this thread's row of the tile
-  const int t = r / p.G, g = r - t * p.G;  // its token and head
+  const int r = warp * 32 + lane;    // this thread's row of the tile
+  int t = r / p.G, g = r - t * p.G;  // its token and head
+  // FEW, a tile of rows with 64 or 32 of them at most (decode): the rows are there two or
+  // four times, a copy for every 64 or 32 of the keys' columns, so that all warps work on
+  // the tile's weights; the copies are joined at the end.
+  [[maybe_unused]] int reps = 1, part = 0;
   const int tpt = a.tpt;
   const uint32_t lanes = (uint32_t)(warp * 32) << 16;
   using Ly = Layout<D, Q8>;
-  // Weights of a row's first maximum (2^kHead) and of a tile's sum at most, so that
-  // fp16 weights neither overflow nor lose much.
-  constexpr float kHead = Q8 ? 6.f : 0.f, kMostSum = Q8 ? 32768.f : 65536.f;
   const uint32_t ts = tmem + lanes + s * 128, to = tmem + lanes + Ly::kO + s * D;
   const uint32_t tp = tmem + lanes + Ly::kP + s * Ly::kStepP;
   float c = a.c;
@@ -1046,6 +1221,12 @@ __device__ bool softmax_role(CtlOf<Q8> &ctl, const AttnArgs &a, uint32_t tmem, i
     if (!wp) return false;
     const Work &w = *wp;
     if (w.o.n == 0) return true;
+    if constexpr (FEW) {
+      reps = copies<FEW>(w, p.G);
+      part = warp * reps / 4;
+      const int row = r & (kRows / reps - 1);
+      t = row / p.G, g = row - t * p.G;
+    }
     const int row_tok = w.split ? t : s * tpt + t;  // token of this row within the item
     const bool live = t < tpt && row_tok < w.o.n;
     const int cnt = s ? w.cnt1 : w.cnt0;
@@ -1057,6 +1238,38 @@ __device__ bool softmax_role(CtlOf<Q8> &ctl, const AttnArgs &a, uint32_t tmem, i
     for (int j = 0; j < cnt; ++j) {
       if (!warp_wait(&ctl.s_full[s], n_s & 1)) return false;
       ++n_s;
+      if constexpr (Q8) {
+        if (warp_live) {
+          tc_fence_after();
+          const int tile = w.o.tile0 + (w.split ? 2 * j + s : j);
+          if (j == 0)  // (not below 2^-99: times a scale it is never 0, see tile_q8)
+            c = fmaxf(a.c * ctl.q_scale[n_item & 1][(w.split ? 0 : s * kRows) + r], 0x1p-99f);
+          const auto &sc = ctl.scales[(tiles + tile - w.o.tile0) % kScaleSlots];
+          const int left = seen - tile * kKeys;
+          const bool mine = !Ly::kApart || n_s == 1;  // (as below)
+          auto own = [&] { return mine || warp_wait(&ctl.p_empty[s], n_s & 1); };
+          auto read = [&] {
+            if constexpr (Ly::kApart) {
+              tc_fence_before();
+              warp_arrive(&ctl.s_empty[s]);
+            }
+          };
+          RowState st = {c, ref, l, live, j == 0};
+          bool done;
+          if (FEW && reps == 4) done = tile_q8<D, 1>(ts, tp, to, sc, part, left, st, own, read);
+          else if (FEW && reps == 2) done = tile_q8<D, 2>(ts, tp, to, sc, part, left, st, own, read);
+          else done = tile_q8<D, 4>(ts, tp, to, sc, 0, left, st, own, read);
+          if (!done) return false;
+          ref = st.ref, l = st.l;
+          tmem_wait_st();
+          tc_fence_before();
+        } else if constexpr (Ly::kApart) {
+          warp_arrive(&ctl.s_empty[s]);
+          if (n_s > 1 && !warp_wait(&ctl.p_empty[s], n_s & 1)) return false;
+        }
+        warp_arrive(&ctl.p_full[s]);
+        continue;
+      }
       if (warp_live) {
         tc_fence_after();
         const int tile = w.o.tile0 + (w.split ? 2 * j + s : j);
@@ -1064,24 +1277,6 @@ __device__ bool softmax_role(CtlOf<Q8> &ctl, const AttnArgs &a, uint32_t tmem, i
         uint32_t x[4][32];
 #pragma unroll
         for (int q = 0; q < 4; ++q) tmem_ld32_async(ts + q * 32, x[q]);
-        // Q8: the scales of blocks 2q and 2q + 1: of the keys, with the row's, and the rest
-        [[maybe_unused]] const float(*sc)[kTileBlocks] = nullptr;
-        if constexpr (Q8) {
-          // (not below 2^-99: times a scale it is never 0, so that a masked score stays -inf
-          // in powers of two)
-          if (j == 0) c = fmaxf(a.c * ctl.q_scale[n_item & 1][(w.split ? 0 : s * kRows) + r], 0x1p-99f);
-          sc = ctl.scales[(tiles + tile - w.o.tile0) % kScaleSlots];
-        }
-        struct Two {
-          float k[2], v[2];
-        };
-        auto scales_of = [&](int q) {
-          const float2 k = *reinterpret_cast<const float2 *>(&sc[0][2 * q]);
-          const float2 v = *reinterpret_cast<const float2 *>(&sc[1][2 * q]);
-          return Two{{c * k.x, c * k.y}, {v.x, v.y}};
-        };
-        [[maybe_unused]] Two now;
-        if constexpr (Q8) now = scales_of(0);
         tmem_wait_ld();
 #pragma unroll
         for (int q = 0; q < 4; ++q) reg_fence(x[q]);
@@ -1113,40 +1308,23 @@ __device__ bool softmax_role(CtlOf<Q8> &ctl, const AttnArgs &a, uint32_t tmem, i
         // (Each row for itself: what a row comes to does not depend on the rows
         // that share its warp.)
         float sum_j = 0.f;
-        [[maybe_unused]] float l_j = 0.f;  // Q8: the sum of the weights over their values' scales
         for (bool again = j == 0;; again = true) {
           if (again) {
             float top[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              if constexpr (Q8) {
-                float half[2];
-                const Two two = scales_of(q);
+              top[q] = fmaxf(__uint_as_float(x[q][0]), __uint_as_float(x[q][1]));
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  half[h] = fmaxf(__uint_as_float(x[q][16 * h]), __uint_as_float(x[q][16 * h + 1]));
-#pragma unroll
-                  for (int i = 2; i < 16; i += 2)
-                    half[h] = max3(half[h], __uint_as_float(x[q][16 * h + i]),
-                                   __uint_as_float(x[q][16 * h + i + 1]));
-                  half[h] = fmaf(half[h], two.k[h], two.v[h]);
-                }
-                top[q] = fmaxf(half[0], half[1]);
-              } else {
-                top[q] = fmaxf(__uint_as_float(x[q][0]), __uint_as_float(x[q][1]));
-#pragma unroll
-                for (int i = 2; i < 32; i += 2)
-                  top[q] = max3(top[q], __uint_as_float(x[q][i]), __uint_as_float(x[q][i + 1]));
-              }
+              for (int i = 2; i < 32; i += 2)
+                top[q] = max3(top[q], __uint_as_float(x[q][i]), __uint_as_float(x[q][i + 1]));
             }
-            const float all = fmaxf(max3(top[0], top[1], top[2]), top[3]);
-            const float tm = Q8 ? all - kHead : all * c;
+            const float tm = fmaxf(max3(top[0], top[1], top[2]), top[3]) * c;
             if (j == 0) {
               // (a row whose scores are all -inf so far takes the next tile's maximum,
               // whatever that is: its weights then sum to more than 2^16)
               if (live) ref = tm > -INFINITY ? tm : -FLT_MAX;
             } else {
-              const bool move = live && !(sum_j <= kMostSum) && tm > ref;
+              const bool move = live && !(sum_j <= 65536.f) && tm > ref;
               const float keep = move ? ex2_approx(ref - tm) : 1.f;
               if (move) ref = tm;
               l *= keep;
@@ -1167,56 +1345,30 @@ __device__ bool softmax_role(CtlOf<Q8> &ctl, const AttnArgs &a, uint32_t tmem, i
               }
             }
           }
-          [[maybe_unused]] uint64_t c2 = pair(c, c), ref2 = pair(-ref, -ref);
+          const uint64_t c2 = pair(c, c), ref2 = pair(-ref, -ref);
           uint64_t sum[2] = {0ull, 0ull};
-          if constexpr (Q8) sum_j = l_j = 0.f;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             uint32_t pk[16];
-            [[maybe_unused]] Two next = now;
-            [[maybe_unused]] float2 inv;
-            if constexpr (Q8) {
-              next = scales_of((q + 1) & 3);  // (q = 3: for the pass after this one)
-              inv = *reinterpret_cast<const float2 *>(&sc[2][2 * q]);
-            }
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               float u, v;
-              if constexpr (Q8) {
-                if (i % 8 == 0) {  // a block
-                  const float by = now.v[i / 8] - ref;
-                  c2 = pair(now.k[i / 8], now.k[i / 8]), ref2 = pair(by, by);
-                  sum[0] = 0ull;
-                }
-              }
               unpair(fma2(pair(__uint_as_float(x[q][2 * i]), __uint_as_float(x[q][2 * i + 1])), c2,
                           ref2), u, v);
               u = ex2_approx(u);
               v = ex2_approx(v);
-              uint64_t &to = sum[Q8 ? 0 : i & 1];
-              to = add2(to, pair(u, v));
-              pk[i] = Q8 ? pack_f16x2(u, v) : pack_bf16x2(u, v);
-              if constexpr (Q8) {
-                if (i % 8 == 7) {
-                  float su, sv;
-                  unpair(sum[0], su, sv);
-                  sum_j += su + sv;
-                  l_j = fmaf(su + sv, i < 8 ? inv.x : inv.y, l_j);
-                }
-              }
+              sum[i & 1] = add2(sum[i & 1], pair(u, v));
+              pk[i] = pack_bf16x2(u, v);
             }
-            if constexpr (Q8) now = next;
             if (q == 0 && !own()) return false;
             tmem_st16(tp + q * 16, pk);
           }
-          if constexpr (!Q8) {
-            float su, sv;
-            unpair(add2(sum[0], sum[1]), su, sv);
-            sum_j = su + sv;
-          }
-          if (again || !__any_sync(0xffffffffu, live && !(sum_j <= kMostSum))) break;
+          float su, sv;
+          unpair(add2(sum[0], sum[1]), su, sv);
+          sum_j = su + sv;
+          if (again || !__any_sync(0xffffffffu, live && !(sum_j <= 65536.f))) break;
         }
-        l += Q8 ? l_j : sum_j;
+        l += sum_j;
         tmem_wait_st();
         tc_fence_before();
       } else if constexpr (Ly::kApart) {
@@ -1259,6 +1411,25 @@ __device__ bool softmax_role(CtlOf<Q8> &ctl, const AttnArgs &a, uint32_t tmem, i
       l0 = w0 * l + w1 * l1;
     }
     tc_fence_after();
+    if constexpr (FEW) {
+      if (reps > 1) {  // the copies of a row: their common reference and sum
+        ctl.copy_ml[r][0] = mm;
+        ctl.copy_ml[r][1] = l0;
+        named_bar_sync(1 + s, 128);
+        if (ctl.gave_up[s]) return false;
+        float top = -INFINITY, sum = 0.f;
+        for (int x = r & (kRows / reps - 1); x < kRows; x += kRows / reps)
+          top = fmaxf(top, ctl.copy_ml[x][0]);
+        const float zero = top == -INFINITY ? 0.f : top;
+        for (int x = r & (kRows / reps - 1); x < kRows; x += kRows / reps) {
+          const float m = ctl.copy_ml[x][0], lx = ctl.copy_ml[x][1];
+          sum += lx == 0.f ? 0.f : exp2f(m - zero) * lx;
+        }
+        const float mine = l0 == 0.f ? 0.f : exp2f(mm - zero);
+        w0 *= mine, w1 *= mine;
+        mm = top, l0 = sum;
+      }
+    }
     const bool parts = w.o.n_pieces > 0 || (LONG && (w.runs & 2));  // a partial result
     const int item_row = row_tok * p.G + g;
     int64_t part_at =
@@ -1287,7 +1458,7 @@ __device__ bool softmax_role(CtlOf<Q8> &ctl, const AttnArgs &a, uint32_t tmem, i
       int64_t to_row[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        to_row[k] = __shfl_sync(0xffffffffu, live ? mine : (int64_t)-1, (lane & ~3) + k);
+        to_row[k] = __shfl_sync(0xffffffffu, live && part == 0 ? mine : (int64_t)-1, (lane & ~3) + k);
 #pragma unroll 1
       for (int q = 0; q < D / 32; ++q) {
         float y[32];
@@ -1310,7 +1481,7 @@ __device__ bool softmax_role(CtlOf<Q8> &ctl, const AttnArgs &a, uint32_t tmem, i
           for (int i = 0; i < 32; ++i) y[i] = fmaf(__uint_as_float(o[i]), f1, y[i]);
         }
         if constexpr (LONG) {
-          if (w2 != 0.f) {
+          if (w2 != 0.f && part == 0) {
             const float *src = p.part + part_at * D + q * 32;
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
@@ -1322,6 +1493,21 @@ __device__ bool softmax_role(CtlOf<Q8> &ctl, const AttnArgs &a, uint32_t tmem, i
             }
           }
           __syncwarp();  // other lanes write this row's new sums
+        }
+        if constexpr (FEW) {
+          if (reps > 1) {  // the first copy takes the others' sums
+            float *buf = &ctl.copies[0][0][lane];
+            if (q > 0) named_bar_sync(1 + s, 128);  // (the chunk before has been taken)
+            if (part > 0) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) buf[((warp - 4 / reps) * 32 + i) * 32] = y[i];
+            }
+            named_bar_sync(1 + s, 128);
+            if (part > 0) continue;
+            for (int x = warp; x < 4 - 4 / reps; x += 4 / reps)
+#pragma unroll
+              for (int i = 0; i < 32; ++i) y[i] += buf[(x * 32 + i) * 32];
+          }
         }
         uint32_t v[16];
         if (parts && few) {  // (transposing takes longer than a few rows' stores)
@@ -1361,7 +1547,7 @@ __device__ bool softmax_role(CtlOf<Q8> &ctl, const AttnArgs &a, uint32_t tmem, i
     if (join) warp_arrive(&ctl.o_empty[1]);
 
     if (parts) {
-      if (live) {
+      if (live && part == 0) {
         p.part_ml[part_at * 2] = mm;
         p.part_ml[part_at * 2 + 1] = l0;
       }
@@ -1383,7 +1569,7 @@ __device__ bool softmax_role(CtlOf<Q8> &ctl, const AttnArgs &a, uint32_t tmem, i
 }
 
 // ------------------------------------------------------------------ kernel
-template <int D, bool LONG, bool Q8>
+template <int D, bool LONG, bool Q8, bool FEW>
 __global__ void __launch_bounds__(kThreads<Q8>, 1)
 attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
             const __grid_constant__ CUtensorMap tv, const AttnArgs a) {
@@ -1446,7 +1632,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
   } else if (warp < kSoftmaxWarps) {
     if constexpr (Q8) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-    ok = softmax_role<D, LONG, Q8>(ctl, a, tmem, warp >> 2);
+    ok = softmax_role<D, LONG, Q8, FEW>(ctl, a, tmem, warp >> 2);
     if (!ok) {
       // The barriers of a stream's warps have no time limit: one that gave up a wait
       // is counted in at the next one, the first of a cut piece, where the others
@@ -1465,7 +1651,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
     } else if (warp == kLoadWarp) {
       ok = load_role<D, Q8>(sbase, ctl, a, &tq, &tk, &tv);
     } else if (Q8 && warp >= kConvertWarp) {
-      if constexpr (Q8) ok = convert_role<D>(sbase, ctl, a);
+      if constexpr (Q8) ok = convert_role<D, FEW>(sbase, ctl, a);
     } else if (tid == kSchedWarp * 32) {
       ok = sched_role<LONG>(ctl, a, sched);
     }
@@ -1515,10 +1701,10 @@ bool make_map(CUtensorMap *map, const void *base, uint64_t d, uint64_t heads, ui
                   box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int D, bool LONG, bool Q8>
+template <int D, bool LONG, bool Q8, bool FEW>
 cudaError_t launch_d(const PagedAttnPlan &p) {
   static_assert(smem_bytes<D, Q8>() <= 232448, "shared memory of one CTA");
-  const void *f = reinterpret_cast<const void *>(attn_kernel<D, LONG, Q8>);
+  const void *f = reinterpret_cast<const void *>(attn_kernel<D, LONG, Q8, FEW>);
   const cudaError_t e = set_smem_limit_once(f, smem_bytes<D, Q8>());
   if (e != cudaSuccess) return e;
   CUtensorMap tq, tk, tv;
@@ -1539,19 +1725,19 @@ cudaError_t launch_d(const PagedAttnPlan &p) {
   a.c = fmaxf(fabsf(p.scale) * 1.4426950408889634f, FLT_TRUE_MIN);
   a.neg_q = p.scale < 0.f;
   a.tpt = kRows / p.G;
-  attn_kernel<D, LONG, Q8>
+  attn_kernel<D, LONG, Q8, FEW>
       <<<kPagedMaxCtas, kThreads<Q8>, smem_bytes<D, Q8>(), p.stream>>>(tq, tk, tv, a);
   return cudaGetLastError();
 }
 
-template <bool Q8>
+template <bool Q8, bool FEW>
 cudaError_t launch(const PagedAttnPlan &p) {
   // Only a table of more pages can name a piece of more than one run.  (One token over
   // 777 keys: 12.2 us, with a wide table 12.6; over 30000: 24.8 and 26.0; the cases of a
   // millisecond: the same.)
   const bool wide = (int64_t)p.max_pages * p.page_size > (int64_t)kLongRun * kKeys;
-  if (p.d == 128) return wide ? launch_d<128, true, Q8>(p) : launch_d<128, false, Q8>(p);
-  return wide ? launch_d<64, true, Q8>(p) : launch_d<64, false, Q8>(p);
+  if (p.d == 128) return wide ? launch_d<128, true, Q8, FEW>(p) : launch_d<128, false, Q8, FEW>(p);
+  return wide ? launch_d<64, true, Q8, FEW>(p) : launch_d<64, false, Q8, FEW>(p);
 }
 
 }  // namespace

@@ -47,10 +47,11 @@ __device__ __forceinline__ uint32_t f16_to_e4m3(__half2 x) {
 __device__ __forceinline__ void e4m3_to_f16(const uint4 &w, uint32_t (&x)[8]) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const __half2 h = e4m3_to_f16(u[i >> 1] >> (16 * (i & 1)));
-    x[i] = *reinterpret_cast<const uint32_t *>(&h);
-  }
+  for (int i = 0; i < 4; ++i)
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(x[2 * i]), "=r"(x[2 * i + 1])
+        : "r"(u[i]));
 }
 // Four values, rounded to nearest; beyond 448 they become 448.
 __device__ __forceinline__ uint32_t f32_to_e4m3(float a, float b, float c, float d) {
