@@ -144,6 +144,7 @@ cudaError_t launch_paged_append_q8(const AppendPlan &p);
 cudaError_t launch_paged_attn_q8_f32(const PagedAttnPlan &p);
 cudaError_t launch_paged_attn_q8_wide(const PagedAttnPlan &p);
 cudaError_t launch_paged_attn_q8_few(const PagedAttnPlan &p);
+cudaError_t launch_paged_attn_q8_decode(const PagedAttnPlan &p);
 cudaError_t launch_logprobs(const LogprobsPlan &p);
 
 // launches of the last successful call on this host thread (kda_api.cu)
