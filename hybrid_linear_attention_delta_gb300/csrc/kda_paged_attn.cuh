@@ -80,10 +80,10 @@ constexpr int kLongRun = 1024;
 constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kLoadWarp = 10, kSchedWarp = 11, kConvertWarp = 12;
 constexpr int kStreamWarps = kSoftmaxWarps / 2, kConvertWarps = 4;
 // readers of a published piece: the softmax, the MMA, the load and the converting warps
-template <bool Q8> constexpr int kPieceReaders = kSoftmaxWarps + 3 + (Q8 ? kConvertWarps : 0);
-// Q8: tiles whose scales are kept.  (The loading warp is at most 11 tiles ahead of a
-// softmax: a stage of values is free once it is converted, its fp16 tile once its
-// product has ended.)
+template <bool Q8> constexpr int kPieceReaders = kSoftmaxWarps + 3 + (Q8 ? 1 + kConvertWarps : 0);
+// Q8: tiles whose scales are kept.  (The loading warp is at most 6 tiles ahead of a
+// softmax: a stage of keys is free once the scores have been made, these once the
+// softmax has read the ones before.)
 constexpr int kScaleSlots = 16, kTileBlocks = kKeys / kScaleTokens;
 
 // Bytes of one half (64 channels) of a 128-row tile.
@@ -95,6 +95,8 @@ struct Layout {
   static constexpr uint32_t kTile16 = kHalves * kHalf;       // a tile of 16-bit elements
   static constexpr uint32_t kTile = Q8 ? kTile16 / 2 : kTile16;  // K or V tile of the cache
   static constexpr int kStages = D == 128 ? 5 : 8;
+  // Q8: the first stages are a ring of keys, the others of values
+  static constexpr int kStagesK = D == 128 ? 3 : 4, kStagesV = kStages - kStagesK;
   static constexpr int kWide = !Q8 ? 0 : D == 128 ? 2 : 4;   // fp16 tiles of values
   static constexpr uint32_t kQ = 0;  // two tiles
   static constexpr uint32_t kStage = 2 * kTile16;
@@ -230,12 +232,16 @@ struct PieceReader {
 };
 
 // ------------------------------------------------------------------ pieces
+// One thread's: cuts the work and publishes its pieces.
 template <bool LONG>
-__device__ bool sched_role(Ctl &ctl, const AttnArgs &a, PagedSched<kKeys> &sched) {
-  const int tpt = a.tpt;
+struct Publisher {
+  uint32_t n = 0;       // pieces published
   int at = 0, end = 0;  // LONG: the piece's next tile, and its end
   PagedPiece o;
-  for (uint32_t n = 0;; ++n) {
+  bool more = true;     // (the last one published says that there are no more)
+
+  __device__ bool publish(Ctl &ctl, const AttnArgs &a, PagedSched<kKeys> &sched) {
+    const int tpt = a.tpt;
     const uint32_t slot = n % kPieces;
     Work w;
     if constexpr (LONG) {
@@ -265,8 +271,17 @@ __device__ bool sched_role(Ctl &ctl, const AttnArgs &a, PagedSched<kKeys> &sched
       return false;
     ctl.work[slot] = w;
     mbar_arrive(smem_u32(&ctl.piece_full[slot]));
-    if (w.o.n == 0) return true;
+    ++n;
+    more = w.o.n != 0;
+    return true;
   }
+};
+template <bool LONG>
+__device__ bool sched_role(Ctl &ctl, const AttnArgs &a, PagedSched<kKeys> &sched) {
+  Publisher<LONG> out;
+  while (out.more)
+    if (!out.publish(ctl, a, sched)) return false;
+  return true;
 }
 
 // Ring entries of a piece of n key tiles, in the order they are needed: K_0,
@@ -275,25 +290,22 @@ __device__ __forceinline__ int entry_k(int i) { return i == 0 ? 0 : 2 * i - 1; }
 __device__ __forceinline__ int entry_v(int i, int n) { return i < n - 1 ? 2 * i + 2 : 2 * n - 1; }
 
 // ------------------------------------------------------------------ loads
-template <int D, bool Q8>
-__device__ bool load_role(uint32_t sbase, CtlOf<Q8> &ctl, const AttnArgs &a, const CUtensorMap *tq,
+template <int D>
+__device__ bool load_role(uint32_t sbase, Ctl &ctl, const AttnArgs &a, const CUtensorMap *tq,
                           const CUtensorMap *tk, const CUtensorMap *tv) {
-  using Ly = Layout<D, Q8>;
-  constexpr int kBoxes = Q8 ? 1 : Ly::kHalves;      // of a page
-  constexpr uint32_t kRowBytes = Q8 ? D : 128;      // a row of a box
+  using Ly = Layout<D, false>;
   const PagedAttnPlan &p = a.p;
   const int lane = threadIdx.x & 31;
   const int rs = min(p.page_shift, 7), rows = 1 << rs;  // key rows of a box
   const int tpt = a.tpt;
   const uint32_t q_bytes = (uint32_t)(tpt * p.G * 128 * Ly::kHalves);
-  // lane l fetches half l % kBoxes of page l / kBoxes of a tile
-  const int half = lane % kBoxes, box = lane / kBoxes;
-  const uint32_t lane_dst = sbase + Ly::kStage + half * kHalf + box * rows * kRowBytes;
+  // lane l fetches half l % kHalves of page l / kHalves of a tile
+  const int half = lane % Ly::kHalves, box = lane / Ly::kHalves;
+  const uint32_t lane_dst = sbase + Ly::kStage + half * kHalf + box * rows * 128;
   const uint32_t full0 = smem_u32(&ctl.kv_full[0]);
   PieceReader pieces;
   uint32_t e = 0, nq = 0;  // ring entries and Q tiles requested so far
   uint32_t st = 0, flip = 1;  // the next entry's stage, and the parity that frees it
-  uint32_t tiles = 0;         // key tiles requested so far
   bool ok = true;
   for (;; pieces.release(ctl)) {
     const Work *wp = pieces.next(ctl);
@@ -312,11 +324,11 @@ __device__ bool load_role(uint32_t sbase, CtlOf<Q8> &ctl, const AttnArgs &a, con
     int here = pages_at(base), ahead = pages_at(base + 32);
     if (nq > 0 && !(ok = warp_wait(&ctl.q_empty, (nq - 1) & 1))) break;
     if (lane == 0) {
-      const uint32_t bar = smem_u32(Q8 ? &ctl.q_raw : &ctl.q_full);
+      const uint32_t bar = smem_u32(&ctl.q_full);
       mbar_expect_tx(bar, w.split ? q_bytes : 2 * q_bytes);
       for (int s = 0; s < (w.split ? 1 : 2); ++s)
         for (int h = 0; h < Ly::kHalves; ++h)
-          tma_load_3d(sbase + Ly::kQ + s * Ly::kTile16 + h * kHalf, tq, h * 64, w.o.head * p.G,
+          tma_load_3d(sbase + Ly::kQ + s * Ly::kTile + h * kHalf, tq, h * 64, w.o.head * p.G,
                       w.o.tok0 + s * tpt, bar);
     }
     ++nq;
@@ -330,7 +342,6 @@ __device__ bool load_role(uint32_t sbase, CtlOf<Q8> &ctl, const AttnArgs &a, con
     // Where this lane's box of the next tile lies: head y, slot z.
     struct At {
       int y, z, nb;
-      float scale;  // Q8: lanes 0-7: of the keys of block l, 8-15: of the values
     };
     auto place = [&](bool is_last) {
       At t;
@@ -349,69 +360,175 @@ __device__ bool load_role(uint32_t sbase, CtlOf<Q8> &ctl, const AttnArgs &a, con
         t.y = heads;
         t.z = 0;
       }
-      if constexpr (Q8) {
-        // (asked for a tile ahead of their use; 1 where nothing is read)
-        const int b = lane & (kTileBlocks - 1);
-        const int at = __shfl_sync(0xffffffffu, here, (first - base + (b >> (rs - 4))) & 31);
-        t.scale = 1.f;
-        if (lane < 2 * kTileBlocks && key + b * kScaleTokens < w.o.kv && (uint32_t)at < (uint32_t)p.n_pages) {
-          const int off = (key & (p.page_size - 1)) + ((b * kScaleTokens) & (rows - 1));
-          const int64_t block = ((int64_t)at << (p.page_shift - 4)) + off / kScaleTokens;
-          t.scale = __ldg((lane < kTileBlocks ? p.k_scales : p.v_scales) + block * heads + head);
-        }
-      }
       key += kKeys;
       return t;
     };
     // A tile of keys or values into the next stage, a box a lane.
-    auto fetch = [&](const CUtensorMap *map, const At &t, bool keys) {
+    auto fetch = [&](const CUtensorMap *map, const At &t) {
       const uint32_t bar = full0 + st * 8, dst = lane_dst + st * Ly::kTile;
       if (e >= Ly::kStages && !warp_wait(&ctl.kv_empty[st], flip)) return false;
-      if constexpr (Q8) {
+      if (lane == 0) mbar_expect_tx(bar, (uint32_t)(t.nb << rs) * (128 * Ly::kHalves));
+      __syncwarp();
+      if (box < t.nb) tma_load_3d(dst, map, half * 64, t.y, t.z, bar);
+      ++e;
+      if (++st == Ly::kStages) st = 0, flip ^= 1;
+      return true;
+    };
+    At now = place(n == 1);
+    if (!(ok = fetch(tk, now))) break;
+    for (int i = 1; i < n && ok; ++i) {
+      const At next = place(i == n - 1);
+      ok = fetch(tk, next) && fetch(tv, now);
+      now = next;
+    }
+    if (!(ok = ok && fetch(tv, now))) break;
+  }
+  if (!ok) {  // copies in flight land before the CTA leaves
+    for (uint32_t i = e > Ly::kStages ? e - Ly::kStages : 0; i < e; ++i)
+      warp_wait(&ctl.kv_full[i % Ly::kStages], (i / Ly::kStages) & 1);
+    if (nq > 0) warp_wait(&ctl.q_full, (nq - 1) & 1);
+  }
+  return ok;
+}
+
+// Q8: two warps load, one the keys, with their scales and the queries, one (VALUES) the
+// values; it also cuts the work.  (One warp for both takes 1500 cycles for a tile of four
+// pages; 64 x 8 tokens verified in 311 us.)
+template <int D, bool LONG, bool VALUES>
+__device__ bool load_role_q8(uint32_t sbase, CtlQ8 &ctl, const AttnArgs &a, const CUtensorMap *tq,
+                             const CUtensorMap *map, PagedSched<kKeys> &sched) {
+  using Ly = Layout<D, true>;
+  const PagedAttnPlan &p = a.p;
+  const int lane = threadIdx.x & 31;
+  const int rs = min(p.page_shift, 7), rows = 1 << rs;  // key rows of a box
+  const int tpt = a.tpt;
+  const uint32_t q_bytes = (uint32_t)(tpt * p.G * 128 * (D / 64));
+  // lane l fetches page l of a tile
+  const uint32_t lane_dst = sbase + Ly::kStage + lane * rows * D;
+  const uint32_t full0 = smem_u32(&ctl.kv_full[0]);
+  Publisher<LONG> out;
+  auto publish = [&] {
+    bool ok = true;
+    if (lane == 0 && out.more) ok = out.publish(ctl, a, sched);
+    return __all_sync(0xffffffffu, ok) != 0;
+  };
+  PieceReader pieces;
+  constexpr uint32_t kRing = VALUES ? Ly::kStagesV : Ly::kStagesK, kFirst = VALUES ? Ly::kStagesK : 0;
+  uint32_t t0 = 0, nq = 0;  // key tiles and items of the pieces before
+  uint32_t asked = 0;       // tiles asked for
+  // two pieces ahead of their use
+  bool ok = !VALUES || (publish() && publish());
+  for (; ok; pieces.release(ctl)) {
+    const Work *wp = pieces.next(ctl);
+    if (!(ok = wp != nullptr) || wp->o.n == 0) break;
+    const Work &w = *wp;
+    const int n = w.o.tile1 - w.o.tile0;
+    if (n > 0) {
+      // The request's row of the block table, 32 pages at a time (as for the 16-bit cache)
+      const int32_t *row = p.table + (int64_t)w.o.req * p.max_pages;
+      const int held = (w.o.kv + p.page_size - 1) >> p.page_shift;
+      auto pages_at = [&](int first) { return first + lane < held ? row[first + lane] : 0; };
+      int key = w.o.tile0 * kKeys;  // the next tile's first key
+      int base = key >> p.page_shift;
+      int here = pages_at(base), ahead = pages_at(base + 32);
+      if constexpr (!VALUES) {
+        if (nq > 0 && !(ok = warp_wait(&ctl.q_empty, (nq - 1) & 1))) break;
+        if (lane == 0) {
+          const uint32_t bar = smem_u32(&ctl.q_raw);
+          mbar_expect_tx(bar, w.split ? q_bytes : 2 * q_bytes);
+          for (int s = 0; s < (w.split ? 1 : 2); ++s)
+            for (int h = 0; h < D / 64; ++h)
+              tma_load_3d(sbase + Ly::kQ + s * Ly::kTile16 + h * kHalf, tq, h * 64, w.o.head * p.G,
+                          w.o.tok0 + s * tpt, bar);
+        }
+        ++nq;
+      }
+      // boxes of the piece's last tile: pages that hold a key of the request
+      const int last = (min(kKeys, w.o.kv - (w.o.tile1 - 1) * kKeys) + rows - 1) >> rs;
+      const int heads = p.Hkv, head = w.o.head;
+      // Where this lane's box of the next tile lies: head y, slot z.
+      struct At {
+        int y, z, nb;
+        float scale;  // lanes 0-7: of the keys of block l, 8-15: of the values
+      };
+      auto place = [&](bool is_last) {
+        At t;
+        t.nb = is_last ? last : kKeys >> rs;
+        const int first = key >> p.page_shift;
+        if (first >= base + 32) {
+          base += 32;
+          here = ahead;
+          ahead = pages_at(base + 32);
+        }
+        const int page = __shfl_sync(0xffffffffu, here, (first - base + (rs < 7 ? lane : 0)) & 31);
+        t.y = head;
+        t.z = (page << p.page_shift) + (key & (p.page_size - 1));
+        if (lane < t.nb && (uint32_t)page >= (uint32_t)p.n_pages) {
+          raise_error(p.err, ERR_BAD_PAGE);  // reads as zeros: a head behind the last one
+          t.y = heads;
+          t.z = 0;
+        }
+        t.scale = 1.f;
+        if constexpr (!VALUES) {  // (1 where nothing is read)
+          const int b = lane & (kTileBlocks - 1);
+          const int at = __shfl_sync(0xffffffffu, here, (first - base + (b >> (rs - 4))) & 31);
+          if (lane < 2 * kTileBlocks && key + b * kScaleTokens < w.o.kv &&
+              (uint32_t)at < (uint32_t)p.n_pages) {
+            const int off = (key & (p.page_size - 1)) + ((b * kScaleTokens) & (rows - 1));
+            const int64_t block = ((int64_t)at << (p.page_shift - 4)) + off / kScaleTokens;
+            t.scale = __ldg((lane < kTileBlocks ? p.k_scales : p.v_scales) + block * heads + head);
+          }
+        }
+        key += kKeys;
+        return t;
+      };
+      // Tile i into its stage, a box a lane.
+      auto fetch = [&](int i, const At &t) {
+        const uint32_t round = (t0 + i) / kRing, st = kFirst + (t0 + i) % kRing;
+        const uint32_t bar = full0 + st * 8;
+        if (round > 0 && !warp_wait(&ctl.kv_empty[st], (round - 1) & 1)) return false;
         // (the barrier's phase ends with the arrival, whatever has landed before it)
-        if (box < t.nb) tma_load_3d(dst, map, 0, t.y, t.z, bar);
-        if (keys) {
-          float(*to)[kTileBlocks] = ctl.scales[tiles++ % kScaleSlots];
+        if (lane < t.nb) tma_load_3d(lane_dst + st * Ly::kTile, map, 0, t.y, t.z, bar);
+        if constexpr (!VALUES) {
+          float(*to)[kTileBlocks] = ctl.scales[(t0 + i) % kScaleSlots];
           const uint32_t good = __ballot_sync(0xffffffffu, good_scale(t.scale));
           const bool both = good >> (lane & 7) & good >> ((lane & 7) + 8) & 1;
           if (!both && lane < kTileBlocks) raise_error(p.err, ERR_BAD_SCALE);
           if (lane < kTileBlocks) {
             to[0][lane] = both ? t.scale : 1.f;
           } else if (lane < 2 * kTileBlocks) {
-            to[1][lane - kTileBlocks] = both ? log2f(t.scale) : -INFINITY;
-            to[2][lane - kTileBlocks] = both ? 1.f / t.scale : 0.f;
+            to[1][lane - kTileBlocks] = both ? __log2f(t.scale) : -INFINITY;
+            to[2][lane - kTileBlocks] = both ? __fdividef(1.f, t.scale) : 0.f;
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_expect_tx(bar, (uint32_t)(t.nb << rs) * kRowBytes);
+        if (lane == 0) mbar_expect_tx(bar, (uint32_t)(t.nb << rs) * D);
+        ++asked;
+        return true;
+      };
+      // keys: placed two tiles ahead, for the scales' way from memory
+      if constexpr (VALUES) {
+        for (int i = 0; i < n && ok; ++i) ok = fetch(i, place(i == n - 1));
       } else {
-        if (lane == 0) mbar_expect_tx(bar, (uint32_t)(t.nb << rs) * (128 * Ly::kHalves));
-        __syncwarp();
-        if (box < t.nb) tma_load_3d(dst, map, half * 64, t.y, t.z, bar);
+        At now = place(n == 1), next = now;
+        if (n > 1) next = place(n == 2);
+        for (int i = 0; i < n && ok; ++i) {
+          At after = next;
+          if (i + 2 < n) after = place(i + 3 == n);
+          ok = fetch(i, now);
+          now = next;
+          next = after;
+        }
       }
-      ++e;
-      if (++st == Ly::kStages) st = 0, flip ^= 1;
-      return true;
-    };
-    // (Q8: placed a tile earlier, for the scales' way from memory)
-    constexpr int kEarly = Q8 ? 2 : 1;
-    At now = place(n == 1), next = now;
-    if (Q8 && n > 1) next = place(n == 2);
-    if (!(ok = fetch(tk, now, true))) break;
-    for (int i = 1; i < n && ok; ++i) {
-      At after = next;
-      if (i + kEarly <= n) after = place(i + kEarly == n);
-      if (!Q8) next = after;
-      ok = fetch(tk, next, true) && fetch(tv, now, false);
-      now = next;
-      if (Q8) next = after;
+      if (!ok) break;
+      t0 += n;
     }
-    if (!(ok = ok && fetch(tv, now, false))) break;
+    if (VALUES && !(ok = publish())) break;
   }
   if (!ok) {  // copies in flight land before the CTA leaves
-    for (uint32_t i = e > Ly::kStages ? e - Ly::kStages : 0; i < e; ++i)
-      warp_wait(&ctl.kv_full[i % Ly::kStages], (i / Ly::kStages) & 1);
-    if (nq > 0) warp_wait(Q8 ? &ctl.q_raw : &ctl.q_full, (nq - 1) & 1);
+    for (uint32_t t = asked > kRing ? asked - kRing : 0; t < asked; ++t)
+      warp_wait(&ctl.kv_full[kFirst + t % kRing], (t / kRing) & 1);
+    if (!VALUES && nq > 0) warp_wait(&ctl.q_raw, (nq - 1) & 1);
   }
   return ok;
 }
@@ -627,9 +744,8 @@ __device__ bool mma_role(uint32_t sbase, Ctl &ctl, const AttnArgs &a, uint32_t t
   return ok;
 }
 
-// Q8: the products of stream s.  Keys come from the ring, values from the fp16 tiles; both
-// streams wait for every tile of either and hand it back (a stage of keys takes four
-// arrivals, two of each stream).
+// Q8: the products of stream s.  Keys come from their ring, values from the fp16 tiles; both
+// streams wait for every tile of either and hand it back.
 template <int D>
 __device__ bool mma_role_q8(uint32_t sbase, CtlQ8 &ctl, uint32_t tmem, int s) {
   using Ly = Layout<D, true>;
@@ -640,7 +756,7 @@ __device__ bool mma_role_q8(uint32_t sbase, CtlQ8 &ctl, uint32_t tmem, int s) {
   const uint32_t ds = uniform(tmem + s * 128), d_o = uniform(tmem + Ly::kO + s * D);
   const uint32_t dp = uniform(tmem + Ly::kP + s * Ly::kStepP);
   PieceReader pieces;
-  uint32_t e = 0, v0 = 0, nq = 0;      // ring entries, fp16 tiles and items of the pieces before
+  uint32_t t0 = 0, nq = 0;             // key tiles and items of the pieces before
   uint32_t n_s = 0, n_p = 0, n_o = 0;  // scores, weights and outputs of the stream so far
   uint32_t n_go = 0;                   // rounds so far
   bool ok = true, any = false;
@@ -649,27 +765,25 @@ __device__ bool mma_role_q8(uint32_t sbase, CtlQ8 &ctl, uint32_t tmem, int s) {
   uint64_t q = 0;
 
   auto key_landed = [&](int i) {
-    const uint32_t at = e + entry_k(i);
-    return warp_wait(&ctl.kv_full[at % Ly::kStages], (at / Ly::kStages) & 1);
+    const uint32_t t = t0 + i;
+    return warp_wait(&ctl.kv_full[t % Ly::kStagesK], (t / Ly::kStagesK) & 1);
   };
   auto pass_keys = [&](int upto) {  // tiles that only the other stream uses
     for (; xk < upto; ++xk) {
       if (!key_landed(xk)) return false;
-      __syncwarp();
-      if ((threadIdx.x & 31) == 0)
-        mbar_arrive_n(smem_u32(&ctl.kv_empty[(e + entry_k(xk)) % Ly::kStages]), 2);
+      warp_arrive(&ctl.kv_empty[(t0 + xk) % Ly::kStagesK]);
     }
     return true;
   };
   auto take_keys = [&](int i) { return pass_keys(i) && key_landed(xk++); };
   auto values_made = [&](int i) {
-    const uint32_t at = v0 + i;
-    return warp_wait(&ctl.v_full[at % Ly::kWide], (at / Ly::kWide) & 1);
+    const uint32_t t = t0 + i;
+    return warp_wait(&ctl.v_full[t % Ly::kWide], (t / Ly::kWide) & 1);
   };
   auto pass_values = [&](int upto) {
     for (; xv < upto; ++xv) {
       if (!values_made(xv)) return false;
-      warp_arrive(&ctl.v_empty[(v0 + xv) % Ly::kWide]);
+      warp_arrive(&ctl.v_empty[(t0 + xv) % Ly::kWide]);
     }
     return true;
   };
@@ -699,7 +813,6 @@ __device__ bool mma_role_q8(uint32_t sbase, CtlQ8 &ctl, uint32_t tmem, int s) {
         }
         mma_commit(smem_u32(&ctl.s_full[s]));
         mma_commit(smem_u32(&ctl.kv_empty[sk]));
-        mbar_arrive(smem_u32(&ctl.kv_empty[sk]));
         if (last) mma_commit(smem_u32(&ctl.q_empty));
       }
     }
@@ -724,7 +837,7 @@ __device__ bool mma_role_q8(uint32_t sbase, CtlQ8 &ctl, uint32_t tmem, int s) {
   // i < 0: scores only, i_next < 0: no more scores.
   auto turn = [&](int i, int j, int i_next) {
     const uint32_t more = uniform(j > 0);
-    const uint32_t sv = (v0 + max(i, 0)) % Ly::kWide, sk = (e + entry_k(max(i_next, 0))) % Ly::kStages;
+    const uint32_t sv = (t0 + max(i, 0)) % Ly::kWide, sk = (t0 + max(i_next, 0)) % Ly::kStagesK;
     if (i_next >= 0) {
       if (!take_keys(i_next)) return false;
       if constexpr (Ly::kApart) {
@@ -771,7 +884,7 @@ __device__ bool mma_role_q8(uint32_t sbase, CtlQ8 &ctl, uint32_t tmem, int s) {
       if (ok) end_round();
     }
     if (!(ok = ok && pass_keys(n) && pass_values(n))) break;
-    e += 2 * n, v0 += n;
+    t0 += n;
     xk = xv = 0;
   }
   if (!ok && any) {  // products in flight end before tensor memory is freed
@@ -807,7 +920,7 @@ __device__ bool convert_role(uint32_t sbase, CtlQ8 &ctl, const AttnArgs &a) {
   const uint32_t v_src = v_row * D + c * 16;
   const uint32_t v_dst = c / 4 * kHalf + sw128_chunk(v_row, c % 4 * 2);
   PieceReader pieces;
-  uint32_t e = 0, v0 = 0, nq = 0;
+  uint32_t t0 = 0, nq = 0;  // key tiles and items of the pieces before
   for (;; pieces.release(ctl)) {
     const Work *wp = pieces.next(ctl);
     if (!wp) return false;
@@ -878,9 +991,9 @@ __device__ bool convert_role(uint32_t sbase, CtlQ8 &ctl, const AttnArgs &a) {
     warp_arrive(&ctl.q_full);
     ++nq;
     for (int i = 0; i < n; ++i) {
-      const uint32_t at = e + entry_v(i, n), st = at % Ly::kStages, to = (v0 + i) % Ly::kWide;
-      if (!warp_wait(&ctl.kv_full[st], (at / Ly::kStages) & 1)) return false;
-      if (v0 + i >= Ly::kWide && !warp_wait(&ctl.v_empty[to], ((v0 + i) / Ly::kWide - 1) & 1)) return false;
+      const uint32_t t = t0 + i, st = Ly::kStagesK + t % Ly::kStagesV, to = t % Ly::kWide;
+      if (!warp_wait(&ctl.kv_full[st], (t / Ly::kStagesV) & 1)) return false;
+      if (t >= Ly::kWide && !warp_wait(&ctl.v_empty[to], (t / Ly::kWide - 1) & 1)) return false;
       const uint32_t src = sbase + Ly::kStage + st * Ly::kTile + v_src;
       const uint32_t dst = sbase + Ly::kV16 + to * Ly::kTile16 + v_dst;
       // Slots behind the request's last key may hold anything: their weights are zero,
@@ -910,7 +1023,7 @@ __device__ bool convert_role(uint32_t sbase, CtlQ8 &ctl, const AttnArgs &a) {
       warp_arrive(&ctl.v_full[to]);
       warp_arrive(&ctl.kv_empty[st]);
     }
-    e += 2 * n, v0 += n;
+    t0 += n;
   }
 }
 
@@ -1585,7 +1698,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
   if (tid == kSchedWarp * 32) {  // (the first warp has requests to look at)
     for (int i = 0; i < Ly::kStages; ++i) {
       mbar_init(smem_u32(&ctl.kv_full[i]), 1);
-      mbar_init(smem_u32(&ctl.kv_empty[i]), Q8 ? 4 : 2);
+      mbar_init(smem_u32(&ctl.kv_empty[i]), Q8 && i >= Ly::kStagesK ? kConvertWarps : 2);
     }
     for (int i = 0; i < Ly::kWide; ++i) {
       mbar_init(smem_u32(&ctl.v_full[i]), kConvertWarps);
@@ -1626,11 +1739,11 @@ attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
 
   // a softmax thread holds a row of 128 scores: registers go from the last
   // warpgroup to the other two (168 a thread at the launch, 2 * 216 + 72 = 3 * 168; Q8:
-  // 128, 2 * 192 + 72 + 56 = 4 * 128)
+  // 128, 2 * 200 + 2 * 56 = 4 * 128)
   bool ok = true;
   if (!work) {  // bad cu_seqlens
   } else if (warp < kSoftmaxWarps) {
-    if constexpr (Q8) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    if constexpr (Q8) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     ok = softmax_role<D, LONG, Q8, FEW>(ctl, a, tmem, warp >> 2);
     if (!ok) {
@@ -1643,15 +1756,18 @@ attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
       named_bar_arrive(1 + (warp >> 2), 128);
     }
   } else {
-    if (Q8 && warp >= kConvertWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if constexpr (Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp < kLoadWarp) {
       if constexpr (Q8) ok = mma_role_q8<D>(sbase, ctl, tmem, warp - kMmaWarp);
       else ok = mma_role<D>(sbase, ctl, a, tmem, warp - kMmaWarp);
     } else if (warp == kLoadWarp) {
-      ok = load_role<D, Q8>(sbase, ctl, a, &tq, &tk, &tv);
+      if constexpr (Q8) ok = load_role_q8<D, LONG, false>(sbase, ctl, a, &tq, &tk, sched);
+      else ok = load_role<D>(sbase, ctl, a, &tq, &tk, &tv);
     } else if (Q8 && warp >= kConvertWarp) {
       if constexpr (Q8) ok = convert_role<D, FEW>(sbase, ctl, a);
+    } else if (Q8) {
+      if constexpr (Q8) ok = load_role_q8<D, LONG, true>(sbase, ctl, a, &tq, &tv, sched);
     } else if (tid == kSchedWarp * 32) {
       ok = sched_role<LONG>(ctl, a, sched);
     }
