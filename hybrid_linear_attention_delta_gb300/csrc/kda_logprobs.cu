@@ -31,11 +31,14 @@ using sm100::ex2_approx;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kCtas = 4;       // of an SM
 constexpr int kMaxCluster = 8;
 constexpr int kMaxTop = 64;
 constexpr int kU = 4;          // vectors of a thread in flight
 constexpr int kSegs = 16;      // segments of a thread at most
 constexpr int kCand = 1024;    // candidates kept
+constexpr int kHits = 512;     // segments they are in
+static_assert(kHits >= kMaxTop, "more segments than places");
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Sums below a reference: l = sum 2^(c x - ref), w = sum 2^(c x - ref) (c x - ref);
@@ -92,6 +95,79 @@ __device__ __forceinline__ float below(float t) {
 
 template <typename T> constexpr int kVec = 16 / (int)sizeof(T);
 
+// What is done to logits as they lie, two 16-bit ones at a time.
+template <typename T>
+struct Raw;
+template <>
+struct Raw<float> {
+  using V = float;  // a threshold
+  static constexpr uint32_t kNone = 0xff800000u;  // -inf
+  static __device__ V threshold(float x, bool at_it) { return at_it ? below(x) : x; }
+  static __device__ float top(const uint4 (&w)[kU]) {
+    float t = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+      t = max_nan(t, max_nan(max_nan(__uint_as_float(w[u].x), __uint_as_float(w[u].y)),
+                             max_nan(__uint_as_float(w[u].z), __uint_as_float(w[u].w))));
+    return t;
+  }
+  // the values, not below -1e30 (0 times -inf is no 0)
+  static __device__ void values(const uint4 &w, float (&x)[4]) {
+    x[0] = fmaxf(__uint_as_float(w.x), -1e30f), x[1] = fmaxf(__uint_as_float(w.y), -1e30f);
+    x[2] = fmaxf(__uint_as_float(w.z), -1e30f), x[3] = fmaxf(__uint_as_float(w.w), -1e30f);
+  }
+  // how many pass v (a NaN is passed by all)
+  template <int U>
+  static __device__ int passing(const uint4 *w, V v) {
+    int n = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      n += !(__uint_as_float(w[u].x) <= v) + !(__uint_as_float(w[u].y) <= v) +
+           !(__uint_as_float(w[u].z) <= v) + !(__uint_as_float(w[u].w) <= v);
+    return n;
+  }
+};
+template <>
+struct Raw<__nv_bfloat16> {
+  using V = __nv_bfloat162;
+  static constexpr uint32_t kNone = 0xff80ff80u;
+  static __device__ __nv_bfloat162 two(uint32_t w) { return *reinterpret_cast<__nv_bfloat162 *>(&w); }
+  static __device__ V threshold(float x, bool at_it) {
+    if (at_it) {  // the next lower value of the type
+      if (x == -INFINITY) x = NAN;
+      else if (x == 0.f) x = __uint_as_float(0x80010000u);
+      else x = __uint_as_float(__float_as_uint(x) + (x > 0.f ? -0x10000 : 0x10000));
+    }
+    return __bfloat162bfloat162(__float2bfloat16(x));
+  }
+  static __device__ float top(const uint4 (&w)[kU]) {
+    __nv_bfloat162 t = two(w[0].x);
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+      t = __hmax2_nan(t, __hmax2_nan(__hmax2_nan(two(w[u].x), two(w[u].y)),
+                                     __hmax2_nan(two(w[u].z), two(w[u].w))));
+    return max_nan(__low2float(t), __high2float(t));
+  }
+  static __device__ void values(const uint4 &w, float (&x)[8]) {
+    const __nv_bfloat162 least = __float2bfloat162_rn(-1e30f);
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __bfloat1622float2(__hmax2(two(u[i]), least));
+      x[2 * i] = f.x, x[2 * i + 1] = f.y;
+    }
+  }
+  template <int U>
+  static __device__ int passing(const uint4 *w, V v) {
+    __nv_bfloat162 n = __float2bfloat162_rn(0.f);  // (whole numbers up to 256 are exact)
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      n = __hadd2(n, __hadd2(__hadd2(__hgtu2(two(w[u].x), v), __hgtu2(two(w[u].y), v)),
+                             __hadd2(__hgtu2(two(w[u].z), v), __hgtu2(two(w[u].w), v))));
+    return (int)(__low2float(n) + __high2float(n));
+  }
+};
+
 struct Shared {
   float seg[kSegs][kThreads];
   uint64_t cand[kCand];
@@ -99,12 +175,14 @@ struct Shared {
   Stats stats[kMaxCluster];
   Stats warp[kWarps];
   Stats all;
-  int32_t n_cand;
+  uint32_t key[kThreads], bound;  // the threads' maxima; what K of them reach
+  uint32_t hits[kHits];          // segments that reach it: which << 16 | thread
+  int32_t n_cand, n_hits;
 };
 
 // span: steps of the loop (kU vectors a thread) that make a segment.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(LogprobsPlan p, int span) {
+__global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(LogprobsPlan p, int span) {
   __shared__ Shared sm;
   constexpr int N = kVec<T>;
   cg::cluster_group cluster = cg::this_cluster();
@@ -136,63 +214,59 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(LogprobsPlan p, i
 
   Stats s = {-INFINITY, 0.f, 0.f, 0.f, 0};
   auto add = [&](float x) {  // one element
-    const float d = fmaxf(fmaf(x, c, -s.ref), -1000.f), e = ex2_approx(d);
+    const float d = fmaf(fmaxf(x, -1e30f), c, -s.ref), e = ex2_approx(d);
     s.l += e;
     s.w = fmaf(e, d, s.w);
   };
   float seg_max = -INFINITY;
   int step = 0;
-  for (int base = v0 + tid; base - tid < v1; base += kU * kThreads, ++step) {
-    uint4 raw[kU];
+  using R = Raw<T>;
+  const typename R::V pass = R::threshold(xt, false), pass_before = R::threshold(xt, true);
+  // A step's vectors first + u kThreads + tid; whole: all of them are there.
+  auto load = [&](uint4 (&r)[kU], int first, bool whole) {
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const int v = base + u * kThreads;
-      constexpr uint32_t none = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;  // -inf
-      raw[u] = v < v1 ? __ldg(vecs + v) : make_uint4(none, none, none, none);
+      const int v = first + u * kThreads + tid;
+      r[u] = whole || v < v1 ? __ldcs(vecs + v) : make_uint4(R::kNone, R::kNone, R::kNone, R::kNone);
     }
-    float x[kU][N];
-    float top = -INFINITY;
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const T *t = reinterpret_cast<const T *>(&raw[u]);
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        x[u][i] = to_f32<T>(t[i]);
-        top = max_nan(top, x[u][i]);
-      }
-    }
+  };
+  constexpr int kStepVecs = kU * kThreads;
+  auto work = [&](const uint4 (&raw)[kU], int first) {
+    const float top = R::top(raw);
     seg_max = max_nan(seg_max, top);
     if (!(top <= s.m)) raise_ref(s, top, c);
-    const uint64_t c2 = pair(c, c), ref2 = pair(-s.ref, -s.ref);
-    uint64_t l2 = pair(0.f, 0.f), w2 = pair(0.f, 0.f);
+    // (one at a time: two per instruction want their operands side by side, and the moves
+    // that see to it cost more than they save)
+    float l[2] = {0.f, 0.f}, w[2] = {0.f, 0.f};
 #pragma unroll
-    for (int u = 0; u < kU; ++u)
+    for (int u = 0; u < kU; ++u) {
+      float x[N];
+      R::values(raw[u], x);
 #pragma unroll
-      for (int i = 0; i < N; i += 2) {
-        float a, b;
-        unpair(fma2(pair(x[u][i], x[u][i + 1]), c2, ref2), a, b);
-        a = fmaxf(a, -1000.f), b = fmaxf(b, -1000.f);  // (0 times -inf is no 0)
-        const uint64_t e2 = pair(ex2_approx(a), ex2_approx(b));
-        l2 = add2(l2, e2);
-        w2 = fma2(e2, pair(a, b), w2);
+      for (int i = 0; i < N; ++i) {
+        const float d = fmaf(x[i], c, -s.ref), e = ex2_approx(d);
+        l[i & 1] += e;
+        w[i & 1] = fmaf(e, d, w[i & 1]);
       }
-    float a, b;
-    unpair(l2, a, b);
-    s.l += a + b;
-    unpair(w2, a, b);
-    s.w += a + b;
+    }
+    s.l += l[0] + l[1];
+    s.w += w[0] + w[1];
     if (!(top <= xt_before)) {
+      // (the whole CTA's step before the token, or behind it, nearly always)
+      const int e0 = head + first * N, e1 = e0 + kStepVecs * N;
+      if (e1 <= token && first + kStepVecs <= v1) {
+        s.before += R::template passing<kU>(raw, pass_before);
+      } else if (e0 > token && first + kStepVecs <= v1) {
+        s.before += R::template passing<kU>(raw, pass);
+      } else {
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int e0 = head + (base + u * kThreads) * N;
-        if (base + u * kThreads >= v1) continue;
-        if (e0 <= token && token < e0 + N) {
+        for (int u = 0; u < kU; ++u) {
+          const int v = first + u * kThreads + tid, i0 = head + v * N;
+          if (v >= v1) continue;
+          const T *t = reinterpret_cast<const T *>(&raw[u]);
 #pragma unroll
-          for (int i = 0; i < N; ++i) s.before += !(x[u][i] <= (e0 + i < token ? xt_before : xt));
-        } else {
-          const float thr = e0 < token ? xt_before : xt;
-#pragma unroll
-          for (int i = 0; i < N; ++i) s.before += !(x[u][i] <= thr);
+          for (int i = 0; i < N; ++i)
+            s.before += !(to_f32<T>(t[i]) <= (i0 + i < token ? xt_before : xt));
         }
       }
     }
@@ -200,6 +274,21 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(LogprobsPlan p, i
       sm.seg[step / span][tid] = seg_max;
       seg_max = -INFINITY;
     }
+    ++step;
+  };
+  // the next step's loads in flight while one is worked on, in turn into two sets
+  uint4 even[kU], odd[kU];
+  int at = v0;
+  load(even, at, at + kStepVecs <= v1);
+#pragma unroll 1
+  for (; at < v1; at += 2 * kStepVecs) {
+    if (at + 2 * kStepVecs <= v1) load(odd, at + kStepVecs, true);
+    else load(odd, at + kStepVecs, false);
+    work(even, at);
+    if (at + kStepVecs >= v1) break;
+    if (at + 3 * kStepVecs <= v1) load(even, at + 2 * kStepVecs, true);
+    else load(even, at + 2 * kStepVecs, false);
+    work(odd, at + kStepVecs);
   }
   if (step % span) sm.seg[step / span][tid] = seg_max;
   const int n_segs = (step + span - 1) / span;
@@ -212,37 +301,52 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(LogprobsPlan p, i
   }
   const float mine = s.m;  // this thread's largest logit
 
-  // ---- the row's sums
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    Stats b;
-    b.m = __shfl_xor_sync(0xffffffffu, s.m, o);
-    b.ref = __shfl_xor_sync(0xffffffffu, s.ref, o);
-    b.l = __shfl_xor_sync(0xffffffffu, s.l, o);
-    b.w = __shfl_xor_sync(0xffffffffu, s.w, o);
-    b.before = __shfl_xor_sync(0xffffffffu, s.before, o);
-    merge(s, b);
-  }
+  // ---- the row's sums, and the K-th largest of the threads' maxima
+  auto merge_lanes = [&](int lanes) {
+    for (int o = lanes / 2; o > 0; o >>= 1) {
+      Stats b;
+      b.m = __shfl_xor_sync(0xffffffffu, s.m, o);
+      b.ref = __shfl_xor_sync(0xffffffffu, s.ref, o);
+      b.l = __shfl_xor_sync(0xffffffffu, s.l, o);
+      b.w = __shfl_xor_sync(0xffffffffu, s.w, o);
+      b.before = __shfl_xor_sync(0xffffffffu, s.before, o);
+      merge(s, b);
+    }
+  };
+  merge_lanes(32);
   if (lane == 0) sm.warp[tid >> 5] = s;
-  if (tid == 0) sm.n_cand = 0;
-  __syncthreads();
-  if (tid == 0) {
-    s = sm.warp[0];
-    for (int w = 1; w < kWarps; ++w) merge(s, sm.warp[w]);
-    if (n_ranks == 1) sm.all = s;
-  }
+  sm.key[tid] = ordered(mine);
+  if (tid == 0) sm.n_cand = sm.n_hits = 0;
   if (n_ranks > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   Shared *first = n_ranks > 1 ? cluster.map_shared_rank(&sm, 0) : &sm;
+  __syncthreads();
+  const int K = p.n_top;
+  if (tid >= 32 && tid < 64) {
+    s = sm.warp[lane % kWarps];
+    merge_lanes(kWarps);
+    if (lane == 0) {
+      if (n_ranks > 1) first->stats[rank] = s; else sm.all = s;
+    }
+  } else if (tid < 32 && K > 0) {
+    // bit by bit, in one warp: the others' scheduler slots go to other rows
+    uint32_t key[kThreads / 32], bound = 0;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) key[i] = sm.key[i * 32 + lane];
+    // (a 16-bit logit is in the upper half of its key)
+    for (uint32_t bit = 0x80000000u; bit >= (sizeof(T) == 2 ? 0x10000u : 1u); bit >>= 1) {
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < kThreads / 32; ++i) n += key[i] >= (bound | bit);
+      if (__reduce_add_sync(0xffffffffu, n) >= K) bound |= bit;
+    }
+    if (lane == 0) sm.bound = max(bound, 0x007fffffu);  // (-inf's: below it are NaNs)
+  }
+  __syncthreads();
 
   // ---- this CTA's most likely tokens
-  const int K = p.n_top;
   int n_list = 0;
   if (K > 0) {
-    // the K-th largest of the threads' maxima, bit by bit
-    const uint32_t key = ordered(mine);
-    uint32_t bound = 0;
-    for (uint32_t bit = 0x80000000u; bit; bit >>= 1)
-      if (__syncthreads_count(key >= (bound | bit)) >= K) bound |= bit;
+    const uint32_t bound = sm.bound;
     // all that reach it: f(value, index) for every logit >= low
     auto each = [&](float low, auto f) {
       for (int g = 0; g < n_segs; ++g) {
@@ -263,16 +367,49 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(LogprobsPlan p, i
       }
       if (edge >= 0 && edge_x >= low && edge_x > -INFINITY) f(edge_x, (uint32_t)edge);
     };
-    each(value_of(bound), [&](float y, uint32_t i) {
+    auto keep = [&](float y, uint32_t i) {
       const int at = atomicAdd(&sm.n_cand, 1);
       if (at < kCand) sm.cand[at] = key_of(y, i);
-    });
+    };
+    // The segments that reach it are listed, then shared out a vector a thread: read where
+    // they were found, they are a chain of loads in one lane of a warp or another (1200
+    // rows of 128001 logits with 20 places: 98 us).
+    const float low = value_of(bound);
+    for (int g = 0; g < n_segs; ++g) {
+      const float top = sm.seg[g][tid];
+      const bool hit = top >= low && top > -INFINITY;
+      const uint32_t hits = __ballot_sync(0xffffffffu, hit);
+      if (hits == 0) continue;
+      int at = 0;
+      if (lane == 0) at = atomicAdd(&sm.n_hits, __popc(hits));
+      at = __shfl_sync(0xffffffffu, at, 0) + __popc(hits & ((1u << lane) - 1u));
+      if (hit && at < kHits) sm.hits[at] = g << 16 | tid;
+    }
     __syncthreads();
-    int n_cand = sm.n_cand;
+    const int n_hits = sm.n_hits, per = span * kU;
+    if (n_hits <= kHits) {
+      for (int x = tid; x < n_hits * per; x += kThreads) {
+        const uint32_t h = sm.hits[x / per];
+        const int q = (int)(h >> 16) * span * kU + x % per;  // (of the thread's vectors)
+        const int v = v0 + (int)(h & 0xffffu) + q * kThreads;
+        if (v >= v1) continue;
+        const uint4 raw = __ldg(vecs + v);
+        const T *t = reinterpret_cast<const T *>(&raw);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const float y = to_f32<T>(t[i]);
+          if (y >= low && y > -INFINITY) keep(y, (uint32_t)(head + v * N + i));
+        }
+      }
+      if (edge >= 0 && edge_x >= low && edge_x > -INFINITY) keep(edge_x, (uint32_t)edge);
+    }
+    __syncthreads();
+    int n_cand = n_hits <= kHits ? sm.n_cand : kCand + 1;
     if (n_cand > kCand) {
-      // Bisection: at least kCand + 1 keys reach lo, fewer than K reach hi.
+      // Bisection: K keys and more reach lo (every segment listed has one), fewer reach hi.
+      // Keys are unique, so that it ends after 64 halvings.
       uint64_t lo = (uint64_t)bound << 32, hi = ~0ull;
-      for (;;) {
+      for (int halvings = 0; halvings <= 64; ++halvings) {
         const uint64_t mid = lo + (hi - lo) / 2;
         __syncthreads();
         if (tid == 0) sm.n_cand = 0;
@@ -290,6 +427,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(LogprobsPlan p, i
         else if (n_cand < K) hi = mid;
         else break;
       }
+      n_cand = min(n_cand, kCand);
     }
     // in order: the place of a candidate is the number of those before it
     n_list = min(K, n_cand);
@@ -302,13 +440,12 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(LogprobsPlan p, i
     for (int i = n_list + tid; i < K; i += kThreads) first->list[rank][i] = 0;
   }
   if (n_ranks > 1) {
-    if (tid == 0) first->stats[rank] = s;
     cluster.sync();
     if (rank > 0) return;
-    if (tid == 0) {
-      s = sm.stats[0];
-      for (int r = 1; r < n_ranks; ++r) merge(s, sm.stats[r]);
-      sm.all = s;
+    if (tid < 32) {
+      s = sm.stats[lane % n_ranks];
+      merge_lanes(n_ranks);
+      if (lane == 0) sm.all = s;
     }
   }
   __syncthreads();
@@ -367,7 +504,7 @@ cudaError_t launch_t(const LogprobsPlan &p) {
   const int n_vec = p.V / kVec<T>;
   // CTAs of a row: more while all of them run at once and each has a step of the loop
   int ranks = 1;
-  while (ranks < kMaxCluster && (int64_t)p.N * ranks * 2 <= 2 * kPagedMaxCtas &&
+  while (ranks < kMaxCluster && (int64_t)p.N * ranks * 2 <= kCtas * kPagedMaxCtas &&
          n_vec >= ranks * 2 * kThreads)
     ranks *= 2;
   const int steps = ((n_vec + ranks - 1) / ranks + kU * kThreads - 1) / (kU * kThreads);
