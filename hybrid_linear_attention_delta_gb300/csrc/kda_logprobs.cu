@@ -29,9 +29,9 @@ namespace {
 
 using sm100::ex2_approx;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kCtas = 4;       // of an SM
+constexpr int kCtas = 8;       // of an SM
 constexpr int kMaxCluster = 8;
 constexpr int kMaxTop = 64;
 constexpr int kU = 4;          // vectors of a thread in flight
@@ -153,8 +153,9 @@ struct Raw<__nv_bfloat16> {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 f = __bfloat1622float2(__hmax2(two(u[i]), least));
-      x[2 * i] = f.x, x[2 * i + 1] = f.y;
+      const __nv_bfloat162 h = __hmax2(two(u[i]), least);
+      const uint32_t b = *reinterpret_cast<const uint32_t *>(&h);
+      x[2 * i] = __uint_as_float(b << 16), x[2 * i + 1] = __uint_as_float(b & 0xffff0000u);
     }
   }
   template <int U>
@@ -244,9 +245,12 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(LogprobsPlan 
       R::values(raw[u], x);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const float d = fmaf(x[i], c, -s.ref), e = ex2_approx(d);
-        l[i & 1] += e;
-        w[i & 1] = fmaf(e, d, w[i & 1]);
+        if (i & 1) continue;
+        const uint64_t d2 = fma2(pair(x[i], x[i + 1]), pair(c, c), pair(-s.ref, -s.ref));
+        float d0, d1; unpair(d2, d0, d1);
+        const uint64_t e2 = pair(ex2_approx(d0), ex2_approx(d1));
+        unpair(add2(pair(l[0], l[1]), e2), l[0], l[1]);
+        unpair(fma2(e2, d2, pair(w[0], w[1])), w[0], w[1]);
       }
     }
     s.l += l[0] + l[1];

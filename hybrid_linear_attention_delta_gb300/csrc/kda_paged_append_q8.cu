@@ -35,7 +35,7 @@ template <typename T, bool HALVES>
 __device__ __forceinline__ Place place(int l, int rot) {
   constexpr int N = kVec<T>, M = N / 2;
   Place c;
-  c.turned = l * N < rot;  // (rot is a multiple of 16: whole lanes)
+  c.turned = l * N < rot;  // (rot is a multiple of 16: whole lanes; without a table it is 0)
   c.a = HALVES && c.turned ? l * M : l * N;
   c.b = HALVES && c.turned ? rot / 2 + l * M : l * N + M;
   return c;
@@ -61,15 +61,63 @@ __device__ __forceinline__ uint4 load_row(const T *head, const Place &c) {
 
 template <typename T>
 __device__ __forceinline__ void unpack(const uint4 &w, float (&x)[kVec<T>]) {
-  const T *t = reinterpret_cast<const T *>(&w);
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-  for (int i = 0; i < kVec<T>; ++i) x[i] = to_f32<T>(t[i]);
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 2) {
+      x[2 * i] = __uint_as_float(u[i] << 16), x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    } else {
+      x[i] = __uint_as_float(u[i]);
+    }
+  }
+}
+// The largest magnitude of a lane's channels as they lie.
+template <typename T>
+__device__ __forceinline__ float largest(const uint4 &w) {
+  if constexpr (sizeof(T) == 2) {
+    const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&w);
+    const __nv_bfloat162 m = __hmax2(__hmax2(__habs2(h[0]), __habs2(h[1])), __hmax2(__habs2(h[2]), __habs2(h[3])));
+    return fmaxf(__low2float(m), __high2float(m));
+  } else {
+    return fmaxf(fmaxf(fabsf(__uint_as_float(w.x)), fabsf(__uint_as_float(w.y))),
+                 fmaxf(fabsf(__uint_as_float(w.z)), fabsf(__uint_as_float(w.w))));
+  }
+}
+
+// A lane's channels of a norm's weight, and its cosines and sines of a position.
+template <typename T>
+struct Lane {
+  float w[kVec<T>], cos[kVec<T> / 2], sin[kVec<T> / 2];
+};
+template <int N>
+__device__ __forceinline__ void load_floats(const float *p, float *x) {
+  if constexpr (N == 4) {
+    const float4 f = __ldg(reinterpret_cast<const float4 *>(p));
+    x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
+  } else {
+    const float2 f = __ldg(reinterpret_cast<const float2 *>(p));
+    x[0] = f.x, x[1] = f.y;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void load_norm(Lane<T> &v, const float *norm, const Place &c) {
+  constexpr int M = kVec<T> / 2;
+  if (!norm) return;
+  load_floats<M>(norm + c.a, v.w);
+  load_floats<M>(norm + c.b, v.w + M);
+}
+template <typename T>
+__device__ __forceinline__ void load_rope(Lane<T> &v, const float *row, const Place &c, int l, int rot) {
+  constexpr int M = kVec<T> / 2;
+  if (!c.turned) return;
+  load_floats<M>(row + l * M, v.cos);
+  load_floats<M>(row + rot / 2 + l * M, v.sin);
 }
 
 // RMSNorm and rotation of a lane's channels.  All lanes of a head call this.
 template <typename T, int D, bool HALVES>
-__device__ __forceinline__ void turn(float (&x)[kVec<T>], const Place &c, const float *norm,
-                                     float eps, const float *rope_row, int l, int rot) {
+__device__ __forceinline__ void turn(float (&x)[kVec<T>], const Place &c, const Lane<T> &v, bool norm,
+                                     float eps) {
   constexpr int N = kVec<T>, M = N / 2, LPH = D / N;
   if (norm) {
     float ss = 0.f;
@@ -77,19 +125,19 @@ __device__ __forceinline__ void turn(float (&x)[kVec<T>], const Place &c, const 
     for (int i = 0; i < N; ++i) ss = fmaf(x[i], x[i], ss);
 #pragma unroll
     for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float r = rsqrtf(ss * (1.f / D) + eps);
+    // (rounded to nearest: with rsqrtf, off by up to two steps, twice as many values land
+    // on another e4m3 value than the exact ones do)
+    const float r = __frsqrt_rn(ss * (1.f / D) + eps);
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = x[i] * r * __ldg(norm + (i < M ? c.a + i : c.b + i - M));
+    for (int i = 0; i < N; ++i) x[i] = x[i] * r * v.w[i];
   }
-  if (c.turned && rope_row) {
-    const float *cs = rope_row + l * M;
+  if (c.turned) {
 #pragma unroll
     for (int i = 0; i < M; ++i) {
-      const float co = __ldg(cs + i), si = __ldg(cs + rot / 2 + i);
       float &a = x[HALVES ? i : 2 * i], &b = x[HALVES ? i + M : 2 * i + 1];
       const float a0 = a, b0 = b;
-      a = a0 * co - b0 * si;
-      b = a0 * si + b0 * co;
+      a = a0 * v.cos[i] - b0 * v.sin[i];
+      b = a0 * v.sin[i] + b0 * v.cos[i];
     }
   }
 }
@@ -137,14 +185,16 @@ __device__ __forceinline__ void store_e4m3(uint8_t *head, const Place &c, const 
   }
 }
 
-// rows: rows of a CTA (at most kMaxRows); grid y shares out their units.
-template <typename T, int D, bool HALVES>
-__global__ void __launch_bounds__(kThreads) append_kernel(AppendPlan p, int rows) {
+// rows: rows of a CTA (at most kMaxRows); grid y shares out their units.  ROWS: a unit of
+// queries is a whole row.
+template <typename T, int D, bool HALVES, bool ROWS>
+__global__ void __launch_bounds__(kThreads, ROWS ? 3 : 2) append_kernel(AppendPlan p, int rows) {
   constexpr int N = kVec<T>;
   constexpr int LPH = D / N;     // lanes of a head
   constexpr int HPP = 32 / LPH;  // rows (or heads) of a pass
   constexpr int P = kScaleTokens / HPP;  // passes of a run
   constexpr int kNear = kScaleTokens - 1;
+  constexpr int kBatch = 4;  // passes (32 lanes' worth) of q heads at a time
   // slot (-1: none) and position of this CTA's rows, the 15 before and the 15 behind
   __shared__ int32_t s_slot[64], s_pos[64];
   __shared__ int32_t s_start[kMaxRows], s_live[kMaxRows];  // first rows of runs, rows with a slot
@@ -191,7 +241,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendPlan p, int rows
   const Place c = place<T, HALVES>(l, p.rot);
   const int64_t row = (int64_t)(p.Hq + 2 * p.Hkv) * D;
   const T *qkv = static_cast<const T *>(p.qkv) + t0 * row;
-  const int n_kv = s_n[0] * 2 * p.Hkv, nq = (p.Hq + HPP - 1) / HPP;
+  const int n_kv = s_n[0] * 2 * p.Hkv, nq = ROWS ? 1 : (p.Hq + kBatch * HPP - 1) / (kBatch * HPP);
   const int units = n_kv + s_n[1] * nq;
   for (int u = blockIdx.y * kWarps + warp; u < units; u += gridDim.y * kWarps) {
     if (u < n_kv) {  // a run's keys or values of one head
@@ -220,19 +270,31 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendPlan p, int rows
           old = kMinScale;
         }
       }
-      float y[P][N];
+      Lane<T> of;
+      if (!is_v) load_norm(of, p.k_norm, c);
+      // Made twice, for the largest of them and to be stored: kept as fp32 in between they
+      // take 64 registers, and a third of the warps.
+      auto made = [&](int x, float (&y)[N]) {
+        unpack<T>(raw[x], y);
+        if (!is_v) {
+          // (a row that is not of the run is zeros, turned by any position)
+          const int r = run >> (x * HPP + sub) & 1 ? x * HPP + sub : __ffs(run) - 1;
+          load_rope(of, p.rope + (int64_t)s_pos[i + r] * p.rot, c, l, p.rot);
+          turn<T, D, HALVES>(y, c, of, p.k_norm, p.eps);
+        }
+      };
       float amax = 0.f;
 #pragma unroll
       for (int x = 0; x < P; ++x) {
-        unpack<T>(raw[x], y[x]);
         if (!(run >> (x * HPP) & ((1u << HPP) - 1u))) continue;
-        if (!is_v) {
-          const float *rope =
-              p.rot > 0 && run >> (x * HPP + sub) & 1 ? p.rope + (int64_t)s_pos[i + x * HPP + sub] * p.rot : nullptr;
-          turn<T, D, HALVES>(y[x], c, p.k_norm, p.eps, rope, l, p.rot);
+        if (is_v) {
+          amax = fmaxf(amax, largest<T>(raw[x]));
+          continue;
         }
+        float y[N];
+        made(x, y);
 #pragma unroll
-        for (int j = 0; j < N; ++j) amax = fmaxf(amax, fabsf(y[x][j]));
+        for (int j = 0; j < N; ++j) amax = fmaxf(amax, fabsf(y[j]));
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
@@ -252,19 +314,48 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendPlan p, int rows
       if (lane == 0 && (off == 0 || s != held)) *scale = s;
 #pragma unroll
       for (int x = 0; x < P; ++x) {
+        if (!(run >> (x * HPP) & ((1u << HPP) - 1u))) continue;
         const int r = x * HPP + sub;
+        float y[N];
+        made(x, y);
         if (run >> r & 1)
-          store_e4m3<T, HALVES>(dst + s_slot[i + r] % kScaleTokens * step, c, y[x], inv);
+          store_e4m3<T, HALVES>(dst + s_slot[i + r] % kScaleTokens * step, c, y, inv);
       }
-    } else {  // HPP q heads of a row
-      const int v = u - n_kv, i = s_live[v / nq], h = v % nq * HPP + sub;
-      const T *src = qkv + i * row + (int64_t)h * D;
-      float y[N];
-      unpack<T>(h < p.Hq ? load_row<T, HALVES>(src, c) : make_uint4(0, 0, 0, 0), y);
-      const float *rope = p.rot > 0 ? p.rope + (int64_t)s_pos[i] * p.rot : nullptr;
-      turn<T, D, HALVES>(y, c, p.q_norm, p.eps, rope, l, p.rot);
-      if (h < p.Hq)
-        store_q<T, HALVES>(static_cast<T *>(p.q) + ((t0 + i) * p.Hq + h) * D, c, y);
+    } else {
+      // A row's q heads, kBatch passes at a time; all of them (ROWS), the next passes' loads
+      // in flight, or one batch.
+      const int v = u - n_kv, i = s_live[v / nq];
+      const int h_begin = ROWS ? sub : v % nq * kBatch * HPP + sub;
+      const int h_end = ROWS ? p.Hq : min(p.Hq, h_begin - sub + kBatch * HPP);
+      const T *src = qkv + i * row;
+      uint4 raw[kBatch], next[kBatch];
+      auto load = [&](uint4 (&r)[kBatch], int h0) {
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) {
+          const int h = h0 + x * HPP;
+          r[x] = h < h_end ? load_row<T, HALVES>(src + (int64_t)h * D, c) : make_uint4(0, 0, 0, 0);
+        }
+      };
+      load(raw, h_begin);
+      Lane<T> of;
+      load_norm(of, p.q_norm, c);
+      load_rope(of, p.rope + (int64_t)s_pos[i] * p.rot, c, l, p.rot);
+      T *dst = static_cast<T *>(p.q) + (t0 + i) * p.Hq * D;
+      for (int h0 = h_begin; h0 - sub < h_end; h0 += kBatch * HPP) {
+        if (ROWS) load(next, h0 + kBatch * HPP);
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) {
+          const int h = h0 + x * HPP;
+          if (h - sub >= h_end) break;
+          float y[N];
+          unpack<T>(raw[x], y);
+          turn<T, D, HALVES>(y, c, of, p.q_norm, p.eps);
+          if (h < h_end) store_q<T, HALVES>(dst + (int64_t)h * D, c, y);
+        }
+        if (ROWS)
+#pragma unroll
+          for (int x = 0; x < kBatch; ++x) raw[x] = next[x];
+      }
     }
   }
 }
@@ -275,7 +366,8 @@ cudaError_t launch_h(const AppendPlan &p) {
   while (rows > 1 && (int64_t)p.T < (int64_t)rows * 2 * kPagedMaxCtas) rows /= 2;
   const unsigned grid = (unsigned)((p.T + rows - 1) / rows);
   const unsigned share = grid < 4 * kPagedMaxCtas ? 4 : 1;
-  append_kernel<T, D, HALVES><<<dim3(grid, share), kThreads, 0, p.stream>>>(p, rows);
+  if (rows == kMaxRows) append_kernel<T, D, HALVES, true><<<dim3(grid, share), kThreads, 0, p.stream>>>(p, rows);
+  else append_kernel<T, D, HALVES, false><<<dim3(grid, share), kThreads, 0, p.stream>>>(p, rows);
   return cudaGetLastError();
 }
 template <typename T, int D>
