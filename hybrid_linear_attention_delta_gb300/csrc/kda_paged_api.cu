@@ -189,8 +189,8 @@ kda_status attn(const void *q, const void *k_pages, const void *v_pages, const f
   // 78, 96; 200 tokens over 500 keys, 128 channels, 63, 85, 107, 137; 100 over 8000 90, 91,
   // 118, 97; 8 requests of up to 301 120, 120, 120, 142; 8 x 1000 tokens the same.)
   const bool wide = (int64_t)a->T_total * G >= 128ll * a->B, bf16 = a->dtype == KDA_BF16;
-  p.min_stretch = bf16 && wide ? 896 : 384;
-  p.item_cost = !bf16 ? 128 : wide ? 320 : 256;
+  p.min_stretch = decode ? 256 : bf16 && wide ? 896 : 384;
+  p.item_cost = decode ? 512 : !bf16 ? 128 : wide ? 320 : 256;
   p.stream = static_cast<cudaStream_t>(a->stream);
   return launch(a->stream, a->ev_begin, a->ev_end, [&] {
     if (q8)

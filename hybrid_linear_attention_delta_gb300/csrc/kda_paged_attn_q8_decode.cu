@@ -42,7 +42,7 @@ constexpr int kLongRun = 8192;
 
 template <int D>
 struct Smem {
-  static constexpr int kStages = D == 128 ? 6 : 10;
+  static constexpr int kStages = D == 128 ? 5 : 8;
   static constexpr int kBytes = kStep * D;  // of the keys, or the values, of a step
   union {
     uint8_t ring[kWarps][kStages][2][kBytes];
@@ -50,7 +50,7 @@ struct Smem {
   };
   float sum[kRows][D];         // runs before this one
   float ml[kWarps + 1][kRows][2];
-  PagedPiece piece;
+  PagedPiece piece[2];
   int64_t scratch[kThreads / 16 + 4];
   int last;
 };
@@ -120,12 +120,21 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(PagedAttnPlan p, floa
   if (!sched.template init<kThreads>(p, kRows / p.G, sm.scratch)) return;
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(&sm.ring[warp][0][0][0]);
   const int64_t row_bytes = (int64_t)p.Hkv * D;
+  // a lane's part of a step's copies: chunk lane % kChunks of every (32 / kChunks)-th row
+  constexpr int kCopies = kStep * kChunks / 32;
+  const int64_t lane_at = lane / kChunks * row_bytes + lane % kChunks * 16;
+  const int64_t copy_step = 32 / kChunks * row_bytes;
+  uint32_t key_to[kCopies], value_to[kCopies];
+#pragma unroll
+  for (int x = 0; x < kCopies; ++x) {
+    const int k = (x * 32 + lane) / kChunks, c = lane % kChunks;
+    key_to[x] = key_at<D>(k, c), value_to[x] = value_at<D>(k, c);
+  }
 
-  for (;;) {
+  if (tid == 0) sm.piece[0] = sched.next(p);
+  for (int n_pieces = 0;; ++n_pieces) {
     __syncthreads();
-    if (tid == 0) sm.piece = sched.next(p);
-    __syncthreads();
-    const PagedPiece o = sm.piece;
+    const PagedPiece o = sm.piece[n_pieces & 1];
     if (o.n == 0) break;
     const int rows = o.n * p.G;
 
@@ -171,17 +180,24 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(PagedAttnPlan p, floa
     // A step into its stage: 16 rows of keys and of values.
     const uint8_t *kp = static_cast<const uint8_t *>(p.k) + o.head * D;
     const uint8_t *vp = static_cast<const uint8_t *>(p.v) + o.head * D;
-    auto copy = [&](int i, int page) {
+    auto copy = [&](int i, int page, int stage) {
       const int key = (first + kWarps * i) * kStep;
       const int64_t slot = ((int64_t)max(page, 0) << p.page_shift) + (key & (p.page_size - 1));
-      const uint32_t to = ring + (uint32_t)(i % kStages) * (2 * S::kBytes);
+      const uint32_t to = ring + (uint32_t)stage * (2 * S::kBytes);
+      const int64_t at = slot * row_bytes + lane_at;
+      if (page >= 0 && key + kStep <= o.kv) {
 #pragma unroll
-      for (int x = 0; x < kStep * kChunks / 32; ++x) {
-        const int id = x * 32 + lane, k = id / kChunks, c = id % kChunks;
-        const int64_t at = (slot + k) * row_bytes + c * 16;
-        const bool real = page >= 0 && key + k < o.kv;
-        copy16(to + key_at<D>(k, c), real ? kp + at : kp, real);
-        copy16(to + S::kBytes + value_at<D>(k, c), real ? vp + at : vp, real);
+        for (int x = 0; x < kCopies; ++x) {
+          copy16(to + key_to[x], kp + at + x * copy_step, true);
+          copy16(to + S::kBytes + value_to[x], vp + at + x * copy_step, true);
+        }
+      } else {  // rows behind the last key, and of a page that is none, are zeros
+#pragma unroll
+        for (int x = 0; x < kCopies; ++x) {
+          const bool real = page >= 0 && key + (x * 32 + lane) / kChunks < o.kv;
+          copy16(to + key_to[x], real ? kp + at + x * copy_step : kp, real);
+          copy16(to + S::kBytes + value_to[x], real ? vp + at + x * copy_step : vp, real);
+        }
       }
     };
 
@@ -208,9 +224,11 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(PagedAttnPlan p, floa
 #pragma unroll
       for (int i = 0; i < kStages - 1; ++i) {
         const int page = __shfl_sync(0xffffffffu, info.page, i);
-        if (i < n_steps) copy(i, page);
+        if (i < n_steps) copy(i, page, i);
         copies_commit();
       }
+      // (cutting the next piece takes a microsecond: while these are on their way)
+      if (tid == 0) sm.piece[(n_pieces + 1) & 1] = sched.next(p);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         __nv_bfloat162 top = __float2bfloat162_rn(0.f);
@@ -254,6 +272,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(PagedAttnPlan p, floa
 #pragma unroll
       for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
 
+      int stage = 0;  // of step i
 #pragma unroll 1
       for (int i = run0; i < run1; ++i) {
         if ((i & 31) == 0 && i > 0) {  // the next run of 32 steps
@@ -266,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(PagedAttnPlan p, floa
           const int at = i + kStages - 1;
           const int page = __shfl_sync(0xffffffffu, (at ^ i) & ~31 ? ahead : info.page, at & 31);
           __syncwarp();
-          if (at < n_steps) copy(at, page);
+          if (at < n_steps) copy(at, page, stage == 0 ? kStages - 1 : stage - 1);
           copies_commit();
         }
         const float ks = __shfl_sync(0xffffffffu, info.k, i & 31);
@@ -274,7 +293,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(PagedAttnPlan p, floa
         const float iv = __shfl_sync(0xffffffffu, info.inv_v, i & 31);
         copies_wait<kStages - 1>();
         __syncwarp();
-        const uint8_t *kt = sm.ring[warp][i % kStages][0], *vt = sm.ring[warp][i % kStages][1];
+        const uint8_t *kt = sm.ring[warp][stage][0], *vt = sm.ring[warp][stage][1];
+        if (++stage == kStages) stage = 0;
 
         // scores of keys 0-7 and 8-15
         float s[2][4] = {};
@@ -429,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(PagedAttnPlan p, floa
         for (int i = run1; i < run1 + kStages - 1; ++i) {
           // (run1 is a multiple of 32: these steps are in the run behind the loop's)
           const int page = __shfl_sync(0xffffffffu, ahead, i & 31);
-          if (run1 == run0 + kLongRun && i < n_steps) copy(i, page);
+          if (run1 == run0 + kLongRun && i < n_steps) copy(i, page, i - run1);
           copies_commit();
         }
         continue;
