@@ -175,7 +175,9 @@ kda_status attn(const void *q, const void *k_pages, const void *v_pages, const f
   p.part = reinterpret_cast<float *>(ws + lay.part_off);
   p.part_ml = reinterpret_cast<float *>(ws + lay.ml_off);
   // (16 rows a request on average: the kernel of small register products)
-  const bool decode = q8 && a->dtype == KDA_BF16 && G <= 16 && (int64_t)a->T_total * G <= 16ll * a->B;
+  const bool few = q8 && a->dtype == KDA_BF16 && G <= 16 && (int64_t)a->T_total * G <= 16ll * a->B;
+  const bool decode = few || (q8 && a->dtype == KDA_BF16 && a->d == 64 && G <= 32 &&
+                              (int64_t)a->T_total * G <= 32ll * a->B);
   p.part_rows = kda::paged_part_rows(a->T_total, G, decode ? (int32_t)KDA_F32 : a->dtype);
   // What an item's start and end cost, and the shortest stretch worth a join, in
   // keys.  In bf16 both are longer where requests bring a tile of rows and more.  (bf16,
@@ -195,9 +197,8 @@ kda_status attn(const void *q, const void *k_pages, const void *v_pages, const f
   return launch(a->stream, a->ev_begin, a->ev_end, [&] {
     if (q8)
       return !bf16    ? kda::launch_paged_attn_q8_f32(p)
-             : decode ? kda::launch_paged_attn_q8_decode(p)
-             : wide   ? kda::launch_paged_attn_q8_wide(p)
-                      : kda::launch_paged_attn_q8_few(p);
+             : decode ? kda::launch_paged_attn_q8_decode(p, few ? 16 : 32)
+                      : kda::launch_paged_attn_q8_bf16(p);
     return bf16 ? kda::launch_paged_attn_bf16(p) : kda::launch_paged_attn_f32(p);
   });
 }

@@ -3,6 +3,6 @@
 
 namespace kda {
 
-cudaError_t launch_paged_attn_bf16(const PagedAttnPlan &p) { return launch<false, false>(p); }
+cudaError_t launch_paged_attn_bf16(const PagedAttnPlan &p) { return launch<false>(p); }
 
 }  // namespace kda

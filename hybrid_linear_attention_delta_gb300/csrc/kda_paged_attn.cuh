@@ -142,8 +142,6 @@ struct CtlQ8 : Ctl {
   // a tile's: the keys', and log2 and inverse of the values' (-inf and 0: block left out)
   alignas(16) float scales[kScaleSlots][3][kTileBlocks];
   float q_scale[2][2 * kRows];               // of the rows of an item and the next
-  float copy_ml[kRows][2];                   // references and sums of the copies of rows
-  float copies[3][32][32];                   // 32 channels of the copies but the first
 };
 template <bool Q8> using CtlOf = std::conditional_t<Q8, CtlQ8, Ctl>;
 
@@ -895,16 +893,9 @@ __device__ bool mma_role_q8(uint32_t sbase, CtlQ8 &ctl, uint32_t tmem, int s) {
   return ok;
 }
 
-// FEW: how often the rows of an item are in its tile (see softmax_role).
-template <bool FEW>
-__device__ __forceinline__ int copies(const Work &w, int G) {
-  const int rows = w.o.n * G;
-  return !FEW || !w.split || rows > kRows / 2 ? 1 : rows > kRows / 4 ? 2 : 4;
-}
-
 // ------------------------------------------------------------------ conversions
 // Q8: the queries of an item into two e4m3 parts, the values of a tile into fp16.
-template <int D, bool FEW>
+template <int D>
 __device__ bool convert_role(uint32_t sbase, CtlQ8 &ctl, const AttnArgs &a) {
   using Ly = Layout<D, true>;
   const PagedAttnPlan &p = a.p;
@@ -930,7 +921,6 @@ __device__ bool convert_role(uint32_t sbase, CtlQ8 &ctl, const AttnArgs &a) {
     if (n == 0) continue;
     // Queries: the lanes that hold a row read all of it, then write its parts over it.
     if (!warp_wait(&ctl.q_raw, nq & 1)) return false;
-    const int reps = copies<FEW>(w, p.G);
     for (int s = 0; s < (w.split ? 1 : 2); ++s) {
       const int rows = min(a.tpt, w.o.n - s * a.tpt) * p.G;
       const int l = lane % kLanesQ, sub = lane / kLanesQ;  // channels 8 l ...
@@ -977,13 +967,11 @@ __device__ bool convert_role(uint32_t sbase, CtlQ8 &ctl, const AttnArgs &a) {
             hi[i / 2] = i % 2 ? hi[i / 2] | a8 << 16 : a8;
             lo[i / 2] = i % 2 ? lo[i / 2] | b8 << 16 : b8;
           }
-          for (int to = r; to < kRows && r < kRows / reps; to += kRows / reps) {
-            st_shared_v2(tile + sw128_chunk(to, l / 2) + l % 2 * 8, hi[0], hi[1]);
-            if constexpr (D == 128)
-              st_shared_v2(tile + Ly::kTile16 / 2 + sw128_chunk(to, l / 2) + l % 2 * 8, lo[0], lo[1]);
-            else st_shared_v2(tile + sw128_chunk(to, 4 + l / 2) + l % 2 * 8, lo[0], lo[1]);
-            if (l == 0) ctl.q_scale[nq & 1][s * kRows + to] = ldexpf(1.f, E - 7);
-          }
+          const uint32_t to = tile + sw128_chunk(r, l / 2) + l % 2 * 8;
+          st_shared_v2(to, hi[0], hi[1]);
+          if constexpr (D == 128) st_shared_v2(to + Ly::kTile16 / 2, lo[0], lo[1]);
+          else st_shared_v2(tile + sw128_chunk(r, 4 + l / 2) + l % 2 * 8, lo[0], lo[1]);
+          if (l == 0) ctl.q_scale[nq & 1][s * kRows + r] = ldexpf(1.f, E - 7);
         }
       }
     }
@@ -1189,25 +1177,24 @@ struct RowState {
 // weights neither overflow nor lose much.
 constexpr float kHead = 6.f, kMostSum = 32768.f;
 
-// Q8: weights of a tile's columns [32 NQ part, 32 NQ (part + 1)), zeros in the others.  As
-// for the 16-bit cache (see softmax_role), but the exponents take the scales of the
-// columns' blocks, the reference is that of the weights with the values' scales, and the
-// row's sum takes them without.  own(): waits until P and O are this tile's; read():
-// the scores have been read.
-template <int D, int NQ, typename Own, typename Read>
+// Q8: a tile's weights.  As for the 16-bit cache (see softmax_role), but the exponents take
+// the scales of the columns' blocks, the reference is that of the weights with the
+// values' scales, and the row's sum takes them without.  left: keys of the tile that the
+// row sees; own(): waits until P and O are this tile's; read(): the scores have been read.
+template <int D, typename Own, typename Read>
 __device__ __forceinline__ bool tile_q8(uint32_t ts, uint32_t tp, uint32_t to,
-                                        const float (&sc)[3][kTileBlocks], int part, int left,
-                                        RowState &st, Own own, Read read) {
-  const int q0 = part * NQ;
+                                        const float (&sc)[3][kTileBlocks], int left, RowState &st,
+                                        Own own, Read read) {
+  constexpr int NQ = 4;  // 32 columns at a time
   uint32_t x[NQ][32];
 #pragma unroll
-  for (int q = 0; q < NQ; ++q) tmem_ld32_async(ts + (q0 + q) * 32, x[q]);
+  for (int q = 0; q < NQ; ++q) tmem_ld32_async(ts + q * 32, x[q]);
   struct Two {  // of two blocks: c times the keys' scale, log2 of the values'
     float k[2], v[2];
   };
   auto scales_of = [&](int q) {
-    const float2 ks = *reinterpret_cast<const float2 *>(&sc[0][2 * (q0 + q)]);
-    const float2 vs = *reinterpret_cast<const float2 *>(&sc[1][2 * (q0 + q)]);
+    const float2 ks = *reinterpret_cast<const float2 *>(&sc[0][2 * q]);
+    const float2 vs = *reinterpret_cast<const float2 *>(&sc[1][2 * q]);
     return Two{{st.c * ks.x, st.c * ks.y}, {vs.x, vs.y}};
   };
   Two now = scales_of(0);
@@ -1218,7 +1205,7 @@ __device__ __forceinline__ bool tile_q8(uint32_t ts, uint32_t tp, uint32_t to,
   if (__any_sync(0xffffffffu, st.live && left < kKeys)) {
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
-      const int n = min(32, max(0, left - (q0 + q) * 32));
+      const int n = min(32, max(0, left - q * 32));
       const uint32_t bits = n == 32 ? 0xffffffffu : (1u << n) - 1u;
 #pragma unroll
       for (int i = 0; i < 32; ++i)
@@ -1269,7 +1256,7 @@ __device__ __forceinline__ bool tile_q8(uint32_t ts, uint32_t tp, uint32_t to,
     for (int q = 0; q < NQ; ++q) {
       // (asked for ahead: the last chunk's are for a second pass)
       const Two next = scales_of((q + 1) % NQ);
-      const float2 inv = *reinterpret_cast<const float2 *>(&sc[2][2 * (q0 + q)]);
+      const float2 inv = *reinterpret_cast<const float2 *>(&sc[2][2 * q]);
       uint32_t pk[16];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -1292,16 +1279,8 @@ __device__ __forceinline__ bool tile_q8(uint32_t ts, uint32_t tp, uint32_t to,
         l = fmaf(a + b, h ? inv.y : inv.x, l);
       }
       now = next;
-      if (q == 0) {
-        if (!own()) return false;
-        if constexpr (NQ < 4) {
-          const uint32_t none[16] = {};
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            if (u / NQ != part) tmem_st16(tp + u * 16, none);
-        }
-      }
-      tmem_st16(tp + (q0 + q) * 16, pk);
+      if (q == 0 && !own()) return false;
+      tmem_st16(tp + q * 16, pk);
     }
     if (again || !__any_sync(0xffffffffu, st.live && !(sum <= kMostSum))) break;
   }
@@ -1309,16 +1288,12 @@ __device__ __forceinline__ bool tile_q8(uint32_t ts, uint32_t tp, uint32_t to,
   return true;
 }
 
-template <int D, bool LONG, bool Q8, bool FEW>
+template <int D, bool LONG, bool Q8>
 __device__ bool softmax_role(CtlOf<Q8> &ctl, const AttnArgs &a, uint32_t tmem, int s) {
   const PagedAttnPlan &p = a.p;
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
-  const int r = warp * 32 + lane;    // this thread's row of the tile
-  int t = r / p.G, g = r - t * p.G;  // its token and head
-  // FEW, a tile of rows with 64 or 32 of them at most (decode): the rows are there two or
-  // four times, a copy for every 64 or 32 of the keys' columns, so that all warps work on
-  // the tile's weights; the copies are joined at the end.
-  [[maybe_unused]] int reps = 1, part = 0;
+  const int r = warp * 32 + lane;          // this thread's row of the tile
+  const int t = r / p.G, g = r - t * p.G;  // its token and head
   const int tpt = a.tpt;
   const uint32_t lanes = (uint32_t)(warp * 32) << 16;
   using Ly = Layout<D, Q8>;
@@ -1334,12 +1309,6 @@ __device__ bool softmax_role(CtlOf<Q8> &ctl, const AttnArgs &a, uint32_t tmem, i
     if (!wp) return false;
     const Work &w = *wp;
     if (w.o.n == 0) return true;
-    if constexpr (FEW) {
-      reps = copies<FEW>(w, p.G);
-      part = warp * reps / 4;
-      const int row = r & (kRows / reps - 1);
-      t = row / p.G, g = row - t * p.G;
-    }
     const int row_tok = w.split ? t : s * tpt + t;  // token of this row within the item
     const bool live = t < tpt && row_tok < w.o.n;
     const int cnt = s ? w.cnt1 : w.cnt0;
@@ -1368,11 +1337,7 @@ __device__ bool softmax_role(CtlOf<Q8> &ctl, const AttnArgs &a, uint32_t tmem, i
             }
           };
           RowState st = {c, ref, l, live, j == 0};
-          bool done;
-          if (FEW && reps == 4) done = tile_q8<D, 1>(ts, tp, to, sc, part, left, st, own, read);
-          else if (FEW && reps == 2) done = tile_q8<D, 2>(ts, tp, to, sc, part, left, st, own, read);
-          else done = tile_q8<D, 4>(ts, tp, to, sc, 0, left, st, own, read);
-          if (!done) return false;
+          if (!tile_q8<D>(ts, tp, to, sc, left, st, own, read)) return false;
           ref = st.ref, l = st.l;
           tmem_wait_st();
           tc_fence_before();
@@ -1524,25 +1489,6 @@ __device__ bool softmax_role(CtlOf<Q8> &ctl, const AttnArgs &a, uint32_t tmem, i
       l0 = w0 * l + w1 * l1;
     }
     tc_fence_after();
-    if constexpr (FEW) {
-      if (reps > 1) {  // the copies of a row: their common reference and sum
-        ctl.copy_ml[r][0] = mm;
-        ctl.copy_ml[r][1] = l0;
-        named_bar_sync(1 + s, 128);
-        if (ctl.gave_up[s]) return false;
-        float top = -INFINITY, sum = 0.f;
-        for (int x = r & (kRows / reps - 1); x < kRows; x += kRows / reps)
-          top = fmaxf(top, ctl.copy_ml[x][0]);
-        const float zero = top == -INFINITY ? 0.f : top;
-        for (int x = r & (kRows / reps - 1); x < kRows; x += kRows / reps) {
-          const float m = ctl.copy_ml[x][0], lx = ctl.copy_ml[x][1];
-          sum += lx == 0.f ? 0.f : exp2f(m - zero) * lx;
-        }
-        const float mine = l0 == 0.f ? 0.f : exp2f(mm - zero);
-        w0 *= mine, w1 *= mine;
-        mm = top, l0 = sum;
-      }
-    }
     const bool parts = w.o.n_pieces > 0 || (LONG && (w.runs & 2));  // a partial result
     const int item_row = row_tok * p.G + g;
     int64_t part_at =
@@ -1571,7 +1517,7 @@ __device__ bool softmax_role(CtlOf<Q8> &ctl, const AttnArgs &a, uint32_t tmem, i
       int64_t to_row[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        to_row[k] = __shfl_sync(0xffffffffu, live && part == 0 ? mine : (int64_t)-1, (lane & ~3) + k);
+        to_row[k] = __shfl_sync(0xffffffffu, live ? mine : (int64_t)-1, (lane & ~3) + k);
 #pragma unroll 1
       for (int q = 0; q < D / 32; ++q) {
         float y[32];
@@ -1594,7 +1540,7 @@ __device__ bool softmax_role(CtlOf<Q8> &ctl, const AttnArgs &a, uint32_t tmem, i
           for (int i = 0; i < 32; ++i) y[i] = fmaf(__uint_as_float(o[i]), f1, y[i]);
         }
         if constexpr (LONG) {
-          if (w2 != 0.f && part == 0) {
+          if (w2 != 0.f) {
             const float *src = p.part + part_at * D + q * 32;
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
@@ -1606,21 +1552,6 @@ __device__ bool softmax_role(CtlOf<Q8> &ctl, const AttnArgs &a, uint32_t tmem, i
             }
           }
           __syncwarp();  // other lanes write this row's new sums
-        }
-        if constexpr (FEW) {
-          if (reps > 1) {  // the first copy takes the others' sums
-            float *buf = &ctl.copies[0][0][lane];
-            if (q > 0) named_bar_sync(1 + s, 128);  // (the chunk before has been taken)
-            if (part > 0) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) buf[((warp - 4 / reps) * 32 + i) * 32] = y[i];
-            }
-            named_bar_sync(1 + s, 128);
-            if (part > 0) continue;
-            for (int x = warp; x < 4 - 4 / reps; x += 4 / reps)
-#pragma unroll
-              for (int i = 0; i < 32; ++i) y[i] += buf[(x * 32 + i) * 32];
-          }
         }
         uint32_t v[16];
         if (parts && few) {  // (transposing takes longer than a few rows' stores)
@@ -1660,7 +1591,7 @@ __device__ bool softmax_role(CtlOf<Q8> &ctl, const AttnArgs &a, uint32_t tmem, i
     if (join) warp_arrive(&ctl.o_empty[1]);
 
     if (parts) {
-      if (live && part == 0) {
+      if (live) {
         p.part_ml[part_at * 2] = mm;
         p.part_ml[part_at * 2 + 1] = l0;
       }
@@ -1682,7 +1613,7 @@ __device__ bool softmax_role(CtlOf<Q8> &ctl, const AttnArgs &a, uint32_t tmem, i
 }
 
 // ------------------------------------------------------------------ kernel
-template <int D, bool LONG, bool Q8, bool FEW>
+template <int D, bool LONG, bool Q8>
 __global__ void __launch_bounds__(kThreads<Q8>, 1)
 attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
             const __grid_constant__ CUtensorMap tv, const AttnArgs a) {
@@ -1745,7 +1676,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
   } else if (warp < kSoftmaxWarps) {
     if constexpr (Q8) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-    ok = softmax_role<D, LONG, Q8, FEW>(ctl, a, tmem, warp >> 2);
+    ok = softmax_role<D, LONG, Q8>(ctl, a, tmem, warp >> 2);
     if (!ok) {
       // The barriers of a stream's warps have no time limit: one that gave up a wait
       // is counted in at the next one, the first of a cut piece, where the others
@@ -1765,7 +1696,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
       if constexpr (Q8) ok = load_role_q8<D, LONG, false>(sbase, ctl, a, &tq, &tk, sched);
       else ok = load_role<D>(sbase, ctl, a, &tq, &tk, &tv);
     } else if (Q8 && warp >= kConvertWarp) {
-      if constexpr (Q8) ok = convert_role<D, FEW>(sbase, ctl, a);
+      if constexpr (Q8) ok = convert_role<D>(sbase, ctl, a);
     } else if (Q8) {
       if constexpr (Q8) ok = load_role_q8<D, LONG, true>(sbase, ctl, a, &tq, &tv, sched);
     } else if (tid == kSchedWarp * 32) {
@@ -1817,10 +1748,10 @@ bool make_map(CUtensorMap *map, const void *base, uint64_t d, uint64_t heads, ui
                   box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int D, bool LONG, bool Q8, bool FEW>
+template <int D, bool LONG, bool Q8>
 cudaError_t launch_d(const PagedAttnPlan &p) {
   static_assert(smem_bytes<D, Q8>() <= 232448, "shared memory of one CTA");
-  const void *f = reinterpret_cast<const void *>(attn_kernel<D, LONG, Q8, FEW>);
+  const void *f = reinterpret_cast<const void *>(attn_kernel<D, LONG, Q8>);
   const cudaError_t e = set_smem_limit_once(f, smem_bytes<D, Q8>());
   if (e != cudaSuccess) return e;
   CUtensorMap tq, tk, tv;
@@ -1841,19 +1772,19 @@ cudaError_t launch_d(const PagedAttnPlan &p) {
   a.c = fmaxf(fabsf(p.scale) * 1.4426950408889634f, FLT_TRUE_MIN);
   a.neg_q = p.scale < 0.f;
   a.tpt = kRows / p.G;
-  attn_kernel<D, LONG, Q8, FEW>
+  attn_kernel<D, LONG, Q8>
       <<<kPagedMaxCtas, kThreads<Q8>, smem_bytes<D, Q8>(), p.stream>>>(tq, tk, tv, a);
   return cudaGetLastError();
 }
 
-template <bool Q8, bool FEW>
+template <bool Q8>
 cudaError_t launch(const PagedAttnPlan &p) {
   // Only a table of more pages can name a piece of more than one run.  (One token over
   // 777 keys: 12.2 us, with a wide table 12.6; over 30000: 24.8 and 26.0; the cases of a
   // millisecond: the same.)
   const bool wide = (int64_t)p.max_pages * p.page_size > (int64_t)kLongRun * kKeys;
-  if (p.d == 128) return wide ? launch_d<128, true, Q8, FEW>(p) : launch_d<128, false, Q8, FEW>(p);
-  return wide ? launch_d<64, true, Q8, FEW>(p) : launch_d<64, false, Q8, FEW>(p);
+  if (p.d == 128) return wide ? launch_d<128, true, Q8>(p) : launch_d<128, false, Q8>(p);
+  return wide ? launch_d<64, true, Q8>(p) : launch_d<64, false, Q8>(p);
 }
 
 }  // namespace

@@ -64,21 +64,12 @@ __device__ __forceinline__ int64_t row_offset(const PagedAttnPlan &p, const Page
 }
 
 __device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
-  const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(p);
-  const float2 a = __bfloat1622float2(h[0]), b = __bfloat1622float2(h[1]);
-  return make_float4(a.x, a.y, b.x, b.y);
-}
-__device__ __forceinline__ void store4(__nv_bfloat16 *p, float a, float b, float c, float d) {
-  reinterpret_cast<__nv_bfloat162 *>(p)[0] = __floats2bfloat162_rn(a, b);
-  reinterpret_cast<__nv_bfloat162 *>(p)[1] = __floats2bfloat162_rn(c, d);
-}
 __device__ __forceinline__ void store4(float *p, float a, float b, float c, float d) {
   *reinterpret_cast<float4 *>(p) = make_float4(a, b, c, d);
 }
 
 // A piece, RA rows a thread (rows ty + TY i of the item, i < RA).
-template <typename T, int D, int R, int TY, int RA, bool Q8>
+template <int D, int R, int TY, int RA, bool Q8>
 __device__ __forceinline__ void run_piece(const PagedAttnPlan &p, Smem<D, R, TY, Q8> &sm,
                                           const PagedPiece &o, float c) {
   using S = Smem<D, R, TY, Q8>;
@@ -86,7 +77,7 @@ __device__ __forceinline__ void run_piece(const PagedAttnPlan &p, Smem<D, R, TY,
   constexpr int NC = D / 16;  // output channels of a thread, in groups of four
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
   const int rows = o.n * p.G;
-  const T *q = static_cast<const T *>(p.q);
+  const float *q = static_cast<const float *>(p.q);
   for (int i = tid; i < kRows * (D / 4); i += kThreads) {
     const int r = i / (D / 4), e = (i % (D / 4)) * 4;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -324,7 +315,7 @@ __device__ __forceinline__ void run_piece(const PagedAttnPlan &p, Smem<D, R, TY,
     const int r = ty + TY * i;
     if (r >= rows) continue;
     const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];  // a row without keys: zeros
-    T *out = static_cast<T *>(p.out) + row_offset(p, o, r);
+    float *out = static_cast<float *>(p.out) + row_offset(p, o, r);
 #pragma unroll
     for (int j = 0; j < NC; j += 4)
       store4(out + j * 16 + tx * 4, acc[i][j] * inv, acc[i][j + 1] * inv, acc[i][j + 2] * inv,
@@ -332,7 +323,7 @@ __device__ __forceinline__ void run_piece(const PagedAttnPlan &p, Smem<D, R, TY,
   }
 }
 
-template <typename T, int D, int R, int TY, bool Q8>
+template <int D, int R, int TY, bool Q8>
 __global__ void __launch_bounds__(TY * 16, D == 64 ? 2 : 1) attn_kernel(PagedAttnPlan p) {
   extern __shared__ __align__(16) unsigned char raw[];
   using S = Smem<D, R, TY, Q8>;
@@ -351,32 +342,32 @@ __global__ void __launch_bounds__(TY * 16, D == 64 ? 2 : 1) attn_kernel(PagedAtt
     if (o.n == 0) break;
     // an item of a few rows leaves the others out (8 decodes, 8 / 2 heads of 64
     // channels: 47 -> 33 us)
-    if (o.n * p.G <= TY) run_piece<T, D, R, TY, 1, Q8>(p, sm, o, c);
-    else run_piece<T, D, R, TY, R, Q8>(p, sm, o, c);
+    if (o.n * p.G <= TY) run_piece<D, R, TY, 1, Q8>(p, sm, o, c);
+    else run_piece<D, R, TY, R, Q8>(p, sm, o, c);
   }
 }
 
-template <typename T, int D, int R, int TY, bool Q8>
+template <int D, int R, int TY, bool Q8>
 cudaError_t launch_r(const PagedAttnPlan &p) {
   using S = Smem<D, R, TY, Q8>;
-  const void *f = reinterpret_cast<const void *>(attn_kernel<T, D, R, TY, Q8>);
+  const void *f = reinterpret_cast<const void *>(attn_kernel<D, R, TY, Q8>);
   const cudaError_t e = set_smem_limit_once(f, sizeof(S));
   if (e != cudaSuccess) return e;
   static_assert(S::kRows <= kPagedF32Rows, "rows of a partial result");
   static_assert(sizeof(S) <= (D == 64 ? 113 : 227) * 1024, "shared memory");
   // two CTAs fit an SM with 64 channels, one with 128
   constexpr int kCtas = D == 64 ? kPagedF32Ctas : kPagedMaxCtas;
-  attn_kernel<T, D, R, TY, Q8><<<kCtas, S::kThreads, sizeof(S), p.stream>>>(p);
+  attn_kernel<D, R, TY, Q8><<<kCtas, S::kThreads, sizeof(S), p.stream>>>(p);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_paged_attn_f32(const PagedAttnPlan &p) {
-  return p.d == 128 ? launch_r<float, 128, 4, 16, false>(p) : launch_r<float, 64, 8, 8, false>(p);
+  return p.d == 128 ? launch_r<128, 4, 16, false>(p) : launch_r<64, 8, 8, false>(p);
 }
 cudaError_t launch_paged_attn_q8_f32(const PagedAttnPlan &p) {
-  return p.d == 128 ? launch_r<float, 128, 4, 16, true>(p) : launch_r<float, 64, 8, 8, true>(p);
+  return p.d == 128 ? launch_r<128, 4, 16, true>(p) : launch_r<64, 8, 8, true>(p);
 }
 
 }  // namespace kda
