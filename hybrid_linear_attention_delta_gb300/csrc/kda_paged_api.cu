@@ -174,7 +174,11 @@ kda_status attn(const void *q, const void *k_pages, const void *v_pages, const f
   p.arrivals = reinterpret_cast<uint32_t *>(ws + lay.arrivals_off);
   p.part = reinterpret_cast<float *>(ws + lay.part_off);
   p.part_ml = reinterpret_cast<float *>(ws + lay.ml_off);
-  // (16 rows a request on average: the kernel of small register products)
+  // The 8-bit cache, bf16: requests with few rows on average take the kernel of small
+  // register products, in items of 16 rows or, with 64 channels, 32.  (64 requests over 1000
+  // to 9000 keys, 32 / 8 heads, against the tensor-core kernel: 4 to 16 rows 110 to 113 and
+  // 170 us with 64 channels, 133 to 137 and 201 to 206 us with 128; 20 to 32 rows 153 and
+  // 172 us, 226 and 210 us.)
   const bool few = q8 && a->dtype == KDA_BF16 && G <= 16 && (int64_t)a->T_total * G <= 16ll * a->B;
   const bool decode = few || (q8 && a->dtype == KDA_BF16 && a->d == 64 && G <= 32 &&
                               (int64_t)a->T_total * G <= 32ll * a->B);
@@ -189,10 +193,14 @@ kda_status attn(const void *q, const void *k_pages, const void *v_pages, const f
   // cost 32, 64, 128, 256: 8 requests of up to 301 tokens 148, 134, 129, 140 us; shortest
   // stretch 384, 512, 768, 1024: a prompt of 1000 tokens, 8/2 heads of 64 channels, 66, 71,
   // 78, 96; 200 tokens over 500 keys, 128 channels, 63, 85, 107, 137; 100 over 8000 90, 91,
-  // 118, 97; 8 requests of up to 301 120, 120, 120, 142; 8 x 1000 tokens the same.)
+  // 118, 97; 8 requests of up to 301 120, 120, 120, 142; 8 x 1000 tokens the same.  8-bit
+  // cache, item cost 320, 576, 768, 1024: a prompt of 1000 tokens 46, 43, 41.5, 42 us, mixed
+  // batch of 24 1094, 1038, 1052, 1061, with 128 channels 1981, 1790, 1808, 1813; small
+  // products, 64, 128, 256, 512: 256 decodes 453, 448, 434, 421 us, 64 x 4 tokens of 4 heads
+  // a group 153, 146, 135, 117.)
   const bool wide = (int64_t)a->T_total * G >= 128ll * a->B, bf16 = a->dtype == KDA_BF16;
   p.min_stretch = decode ? 256 : bf16 && wide ? 896 : 384;
-  p.item_cost = decode ? 512 : !bf16 ? 128 : wide ? 320 : 256;
+  p.item_cost = !bf16 ? 128 : decode ? 512 : q8 ? 768 : wide ? 320 : 256;
   p.stream = static_cast<cudaStream_t>(a->stream);
   return launch(a->stream, a->ev_begin, a->ev_end, [&] {
     if (q8)
