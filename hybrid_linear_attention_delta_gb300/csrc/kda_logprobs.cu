@@ -5,7 +5,8 @@
 //
 // One pass over the logits.  A thread keeps the maximum of what it has seen, the sum
 // of powers of two below it and that sum weighted with the exponents (from which the
-// entropy follows), and counts the logits that stand before the given token's.
+// entropy follows), and counts the logits that stand before the given token's.  (Threads
+// whose logits are far from 0 take a second one.)
 //
 // The most likely tokens come out of the same pass: a thread also keeps the maximum of
 // every segment of its logits (a few vectors).  The K-th largest of the threads'
@@ -15,7 +16,14 @@
 // logits) narrow the bound by bisection over (value, index), which are unique.
 //
 // A row is worked on by a cluster of one to eight CTAs, whose parts meet in the shared
-// memory of the first.
+// memory of the first; more while all of them run at once.  CTAs are small, 128 threads
+// and eight of an SM, so that one row's end, of few threads and many waits, lies under
+// others' loads (512 threads: 127 us for the largest case below).
+//
+// HBM bounds large calls, latency small ones: 2047 rows of 128001 bf16 logits 112 us (4.7
+// TB/s; the rest is what the second wave of rows leaves idle and its ends), 256 of 131072
+// fp32 34.8 us (3.9 TB/s: 20 us of loads, then the end of all rows at once), 4 rows of
+// 50257 10 us.
 #include <cfloat>
 #include <cooperative_groups.h>
 
@@ -42,7 +50,9 @@ static_assert(kHits >= kMaxTop, "more segments than places");
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Sums below a reference: l = sum 2^(c x - ref), w = sum 2^(c x - ref) (c x - ref);
-// ref: c times the largest logit, rounded (any reference does).
+// ref: c times the largest logit m, rounded (any reference does).  Where that is far
+// from 0, or overflows, what rounding leaves of c m - ref is no small number any more:
+// there the reference is c m itself, and exponents are c (x - m).
 struct Stats {
   float m, ref, l, w;
   int32_t before;
@@ -52,21 +62,30 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
+__device__ __forceinline__ bool far(float ref) { return !(fabsf(ref) < 0x1p26f); }
+// 2^kFar is 0, and stays finite in a product with a sum.
+constexpr float kFar = -0x1p20f;
+// How far a's reference lies below that of (m, ref).
+__device__ __forceinline__ float gap(const Stats &a, float m, float ref, float c) {
+  const float d = far(a.ref) ? (far(ref) ? (a.m - m) * c : fmaf(a.m, c, -ref))
+                             : (far(ref) ? fmaf(-m, c, a.ref) : a.ref - ref);
+  return fmaxf(d, kFar);  // (also where nothing is summed yet)
+}
 __device__ __forceinline__ void raise_ref(Stats &s, float top, float c) {
   const float m = max_nan(s.m, top), ref = m * c;  // (a NaN stays)
-  // (nothing summed yet: there is no reference)
-  const float shift = s.m == -INFINITY ? 0.f : s.ref - ref;
-  const float f = s.m == -INFINITY ? 0.f : ex2_approx(shift);
-  s.w = f * fmaf(shift, s.l, s.w);
-  s.l *= f;
+  const float shift = s.ref - ref, f = ex2_approx(shift);
+  // (else nothing of the sums is left, whatever a reference far from 0 made of them)
+  const bool keep = shift > -1000.f;
+  s.w = keep ? f * fmaf(shift, s.l, s.w) : 0.f;
+  s.l = keep ? f * s.l : 0.f;
   s.m = m;
   s.ref = ref;
 }
-__device__ __forceinline__ void merge(Stats &a, const Stats &b) {
+__device__ __forceinline__ void merge(Stats &a, const Stats &b, float c) {
   const float m = max_nan(a.m, b.m);
   const float ref = m == a.m ? a.ref : b.ref;
-  const float da = a.l == 0.f ? 0.f : a.ref - ref, db = b.l == 0.f ? 0.f : b.ref - ref;
-  const float fa = a.l == 0.f ? 0.f : ex2_approx(da), fb = b.l == 0.f ? 0.f : ex2_approx(db);
+  const float da = gap(a, m, ref, c), db = gap(b, m, ref, c);
+  const float fa = ex2_approx(da), fb = ex2_approx(db);
   a.w = fa * fmaf(da, a.l, a.w) + fb * fmaf(db, b.l, b.w);
   a.l = fa * a.l + fb * b.l;
   a.m = m;
@@ -111,10 +130,10 @@ struct Raw<float> {
                              max_nan(__uint_as_float(w[u].z), __uint_as_float(w[u].w))));
     return t;
   }
-  // the values, not below -1e30 (0 times -inf is no 0)
-  static __device__ void values(const uint4 &w, float (&x)[4]) {
-    x[0] = fmaxf(__uint_as_float(w.x), -1e30f), x[1] = fmaxf(__uint_as_float(w.y), -1e30f);
-    x[2] = fmaxf(__uint_as_float(w.z), -1e30f), x[3] = fmaxf(__uint_as_float(w.w), -1e30f);
+  // the values, not below the least (0 times -inf is no 0)
+  static __device__ void values(const uint4 &w, V least, float (&x)[4]) {
+    x[0] = fmaxf(__uint_as_float(w.x), least), x[1] = fmaxf(__uint_as_float(w.y), least);
+    x[2] = fmaxf(__uint_as_float(w.z), least), x[3] = fmaxf(__uint_as_float(w.w), least);
   }
   // how many pass v (a NaN is passed by all)
   template <int U>
@@ -148,8 +167,7 @@ struct Raw<__nv_bfloat16> {
                                      __hmax2_nan(two(w[u].z), two(w[u].w))));
     return max_nan(__low2float(t), __high2float(t));
   }
-  static __device__ void values(const uint4 &w, float (&x)[8]) {
-    const __nv_bfloat162 least = __float2bfloat162_rn(-1e30f);
+  static __device__ void values(const uint4 &w, V least, float (&x)[8]) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -192,6 +210,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(LogprobsPlan 
   const int64_t n = blockIdx.x / n_ranks;
   const T *row = static_cast<const T *>(p.logits) + n * p.stride;
   const float c = p.scale * kLog2e;
+  // For references near 0: logits count no further down, so that no product overflows (a
+  // bf16 value).
+  const float least = __uint_as_float(__float_as_uint(fmaxf(-0x1p126f / c, -FLT_MAX)) & 0xffff0000u);
 
   // Vectors of the row that lie in it whole: elements [head, head + n_vec N); before and
   // behind them there are fewer than N.  This CTA takes vectors [v0, v1).
@@ -213,9 +234,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(LogprobsPlan 
   const float xt = asked ? to_f32<T>(row[token]) : INFINITY;
   const float xt_before = asked ? below(xt) : INFINITY;  // for logits of lower index
 
-  Stats s = {-INFINITY, 0.f, 0.f, 0.f, 0};
+  Stats s = {-INFINITY, -INFINITY, 0.f, 0.f, 0};
   auto add = [&](float x) {  // one element
-    const float d = fmaf(fmaxf(x, -1e30f), c, -s.ref), e = ex2_approx(d);
+    const float d = fmaxf(far(s.ref) ? (x - s.m) * c : fmaf(x, c, -s.ref), kFar), e = ex2_approx(d);
     s.l += e;
     s.w = fmaf(e, d, s.w);
   };
@@ -223,6 +244,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(LogprobsPlan 
   int step = 0;
   using R = Raw<T>;
   const typename R::V pass = R::threshold(xt, false), pass_before = R::threshold(xt, true);
+  const typename R::V floor = R::threshold(least, false);
   // A step's vectors first + u kThreads + tid; whole: all of them are there.
   auto load = [&](uint4 (&r)[kU], int first, bool whole) {
 #pragma unroll
@@ -236,16 +258,13 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(LogprobsPlan 
     const float top = R::top(raw);
     seg_max = max_nan(seg_max, top);
     if (!(top <= s.m)) raise_ref(s, top, c);
-    // (one at a time: two per instruction want their operands side by side, and the moves
-    // that see to it cost more than they save)
     float l[2] = {0.f, 0.f}, w[2] = {0.f, 0.f};
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       float x[N];
-      R::values(raw[u], x);
+      R::values(raw[u], floor, x);
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        if (i & 1) continue;
+      for (int i = 0; i < N; i += 2) {
         const uint64_t d2 = fma2(pair(x[i], x[i + 1]), pair(c, c), pair(-s.ref, -s.ref));
         float d0, d1; unpair(d2, d0, d1);
         const uint64_t e2 = pair(ex2_approx(d0), ex2_approx(d1));
@@ -300,10 +319,24 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(LogprobsPlan 
   if (edge >= 0) {
     edge_x = to_f32<T>(row[edge]);
     if (!(edge_x <= s.m)) raise_ref(s, edge_x, c);
-    add(edge_x);
+    if (!far(s.ref)) add(edge_x);
     s.before += !(edge_x <= (edge < token ? xt_before : xt));
   }
+
   const float mine = s.m;  // this thread's largest logit
+  if (far(s.ref)) {
+    // nothing, masks of large numbers only, or logits far from 0: once more, from the end
+    s.l = s.w = 0.f;
+    if (s.m > -INFINITY) {
+#pragma unroll 1
+      for (int v = v0 + tid; v < v1; v += kThreads) {
+        const uint4 raw = __ldg(vecs + v);
+#pragma unroll
+        for (int i = 0; i < N; ++i) add(to_f32<T>(reinterpret_cast<const T *>(&raw)[i]));
+      }
+      if (edge >= 0) add(edge_x);
+    }
+  }
 
   // ---- the row's sums, and the K-th largest of the threads' maxima
   auto merge_lanes = [&](int lanes) {
@@ -314,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(LogprobsPlan 
       b.l = __shfl_xor_sync(0xffffffffu, s.l, o);
       b.w = __shfl_xor_sync(0xffffffffu, s.w, o);
       b.before = __shfl_xor_sync(0xffffffffu, s.before, o);
-      merge(s, b);
+      merge(s, b, c);
     }
   };
   merge_lanes(32);
@@ -454,10 +487,13 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(LogprobsPlan 
   }
   __syncthreads();
   s = sm.all;
-  const bool empty = s.m == -INFINITY, bad = !(fabsf(s.ref) < INFINITY) || !(s.m < INFINITY);
+  const bool empty = s.m == -INFINITY, bad = !(s.m < INFINITY);
   const float log_l = log2f(s.l);
   auto lp = [&](float x) {
-    return bad ? NAN : empty ? -INFINITY : (fmaf(x, c, -s.ref) - log_l) * kLn2;
+    if (bad || empty) return bad ? NAN : -INFINITY;
+    if (far(s.ref)) return fminf((x - s.m) * p.scale - log_l * kLn2, 0.f);
+    // (below the least: so far down that nothing else counts)
+    return x < least ? x * p.scale : fminf((fmaf(x, c, -s.ref) - log_l) * kLn2, 0.f);
   };
   if (tid == 0) {
     if (bad) raise_error(p.err, ERR_BAD_LOGIT);

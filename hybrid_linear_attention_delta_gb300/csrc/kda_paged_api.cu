@@ -128,7 +128,6 @@ kda_status append(const void *qkv, const int32_t *positions, const int32_t *slot
   });
 }
 
-
 // kda_paged_attn, and kda_paged_attn_q8 with scales.
 kda_status attn(const void *q, const void *k_pages, const void *v_pages, const float *k_scales,
                 const float *v_scales, bool q8, const int32_t *block_table,
@@ -326,7 +325,7 @@ kda_status kda_token_logprobs(const void *logits, const int32_t *tokens, float *
   kda::set_last_launches(0);
   if (!a || (a->dtype != KDA_F32 && a->dtype != KDA_BF16)) return KDA_ERR_INVALID_ARG;
   if (a->N < 0 || a->V <= 0 || a->n_top < 0 || a->stride < a->V) return KDA_ERR_INVALID_ARG;
-  if (!(a->scale > 0.f) || !std::isfinite(a->scale * 1.4426950408889634f)) return KDA_ERR_INVALID_ARG;
+  if (!(a->scale >= 0x1p-64f) || !(a->scale <= 0x1p64f)) return KDA_ERR_INVALID_ARG;
   if (a->V > (1 << 24) || a->N > (1 << 20) || a->n_top > 64) return KDA_ERR_UNSUPPORTED;
   const kda_status st = check_workspace(a->workspace, a->workspace_bytes, 256);
   if (st != KDA_OK) return st;

@@ -296,9 +296,9 @@ kda_status kda_paged_attn_q8(const void *q, const void *k_pages, const void *v_p
  * top_logprobs [N][n_top] fp32   their lp (-inf for -1)
  *
  * Sums are fp32 in a fixed order.  A row without a finite logit (bit 4096): logprobs
- * -inf, entropy 0, top_ids -1.  A row with a NaN or +inf, or whose largest scaled logit
- * overflows (bit 16384): logprobs, entropy and top_logprobs NaN, ranks and top_ids -1.  A
- * token beyond V (bit 2048) counts as negative.
+ * -inf, entropy 0, top_ids -1.  A row with a NaN or +inf (bit 16384): logprobs, entropy and
+ * top_logprobs NaN, ranks and top_ids -1.  A token beyond V (bit 2048) counts as negative.
+ * Finite logits are taken as they are, to the types' lowest and largest values.
  */
 typedef struct {
   int32_t N;          /* rows, up to 2^20 */
@@ -306,7 +306,7 @@ typedef struct {
   int32_t n_top;      /* 0 .. 64 */
   int32_t dtype;      /* kda_dtype of the logits */
   int64_t stride;     /* elements between rows, >= V */
-  float scale;        /* > 0: one over the temperature; finite, as scale * log2(e) is too */
+  float scale;        /* one over the temperature, 2^-64 .. 2^64 */
   int32_t reserved;   /* 0 */
   void *stream;       /* cudaStream_t */
   void *workspace;    /* >= 256 bytes, zero-filled once (the error word) */

@@ -38,9 +38,9 @@ def _call(logits, tokens, K, scale=1.0, ws=None, stream=None, want=("lp", "ent",
 
 
 def _tolerance(V, d_max):
-    """Absolute error of a log probability in 32-bit sums.  A thread adds at most c
-    terms one after another (V / 256 of them, in runs of 16, and 20 joins): c half steps
-    of the sum.  A term 2^d is off by 2^-22 and by the rounding of its exponent, |d| U
+    """Absolute error of a log probability in 32-bit sums.  A thread adds up to V / 128
+    terms in runs of 16, to a sum that is half of the last one on average; with the runs'
+    own additions and the joins that is c half steps of the sum.  A term 2^d is off by 2^-22 and by the rounding of its exponent, |d| U
     ln 2; weighted with the term itself that is at most 0.6 U.  Then the logit's own
     distance to the largest is rounded a few times."""
     c = V / 256 / 16 + 40
@@ -196,6 +196,77 @@ def test_masked_tokens(kind, V, left):
     x[hide.cuda()] = -math.inf
     gone = int(hide[2].nonzero()[5])
     _check(x, torch.tensor([int(keep[0, 0]), int(keep[1, -1]), gone, -1], dtype=torch.int32), 20)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [5, 1003, 50257])
+@pytest.mark.parametrize("at", [-3e38, -1e30, -1e9, -9e5, 9e5, 1e9, 1e30, 3e38])
+def test_logits_far_from_zero(kind, V, at):
+    """Rows around a number of any size: the distribution is that of the differences, which
+    are a few steps of the type there, at a scale that brings them to a few units."""
+    g = torch.Generator().manual_seed(V)
+    near = torch.tensor(at).to(DT[kind]).float()
+    eps = 2.0 ** (torch.frexp(near).exponent.item() - (8 if kind == "bf16" else 24))
+    x = (near.double() + eps * torch.randint(-9, 9, (3, V), generator=g)).to(DT[kind])
+    t = _tokens(3, V, 3)
+    scale = max(2.0 ** -64, 1 / eps)
+    top = x.double().max(-1, keepdim=True).values
+    ref = _reference(x.double() - top, t, 4, scale)
+    r, ws = _call(x.cuda(), t.cuda(), 4, scale)
+    assert kda.kda_device_status(ws) == (kda.KDA_OK, 0)
+    tol = _tolerance(V, 20 + float((top - x.double().min()).max()) * scale)
+    assert r["ids"].tolist() == ref["ids"] and r["rank"].tolist() == ref["rank"]
+    for name, want in (("lp", ref["lp"]), ("ent", ref["ent"]), ("top", ref["top"])):
+        want = torch.tensor(want, dtype=torch.float64)
+        off = tol * (1 + (want.abs() if name == "ent" else 0))
+        assert ((r[name].double().cpu() - want).abs() <= off).all(), name
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("low,scale", [(None, 2.0 ** -60), (None, 0.3), (None, 1.0), (None, 1e5),
+                                       (-1e30, 1.0), (-1e9, 0.7), (-1e5, 10.0)])
+@pytest.mark.parametrize("N,V,left", [(4, 6, 2), (4, 1000, 3), (2, 131072, 40), (400, 9001, 2000)])
+def test_masks_of_low_values(kind, low, scale, N, V, left):
+    """The type's lowest value, or another far below the others, in place of some -inf:
+    what is left has the same distribution, the masked tokens come behind it; alone they are
+    equal ones, also beside -inf."""
+    x = _logits(N, V, kind, 11)
+    x = (x.float() * min(1.0, 1 / scale)).to(DT[kind]) if scale > 1 else x
+    low = float(torch.tensor(low).to(DT[kind])) if low else torch.finfo(DT[kind]).min
+    g = torch.Generator().manual_seed(left)
+    hide = torch.rand((N, V), generator=g) < 1 - left / V
+    hide[:, V // 3] = False
+    some = torch.tensor([low, -math.inf], dtype=DT[kind])[torch.randint(0, 2, (N, V), generator=g)]
+    t = torch.full((N,), V // 3, dtype=torch.int32)
+    t[1] = int(hide[1].nonzero()[0])
+    hard = x.masked_fill(hide.cuda(), -math.inf)
+    soft = torch.where(hide.cuda(), some.cuda(), x)
+    ref = _reference(hard, t, 5, scale)
+    r, ws = _call(soft, t.cuda(), 5, scale)
+    assert kda.kda_device_status(ws) == (kda.KDA_OK, 0)
+    seen = hard.float()[~hide.cuda()]
+    # 2^-60: the lowest value is still 2^68 below the others when scaled
+    tol = _tolerance(V, float(seen.max() - seen.min()) * scale + 20)
+    rows = torch.arange(N) != 1
+    assert ((r["lp"].cpu().double() - torch.tensor(ref["lp"]))[rows].abs() <= tol).all()
+    # (a sum and two products of 32 bits)
+    masked = float(soft[1, int(t[1])]) * scale - float(torch.logsumexp(hard[1].double() * scale, 0))
+    assert r["lp"][1].item() == pytest.approx(masked, rel=1e-6) or masked < -3.4e38 and (
+        r["lp"][1].item() == -math.inf)
+    ent = torch.tensor(ref["ent"])
+    assert ((r["ent"].cpu().double() - ent).abs() <= tol * (1 + ent.abs())).all()
+    order = torch.sort(soft.double().cpu(), descending=True, stable=True)
+    ids = torch.where(order.values > -math.inf, order.indices, -1)[:, :5]
+    assert r["ids"].cpu().tolist() == ids.tolist()
+    assert r["rank"][0] == ref["rank"][0]
+    # nothing but masks: the lowest values share the row
+    some[:, 0] = low
+    r, ws = _call(some.cuda(), t.cuda(), 5, scale)
+    assert kda.kda_device_status(ws) == (kda.KDA_OK, 0)
+    n = (some > -math.inf).sum(-1).double()
+    tol = _tolerance(V, 20)
+    assert ((r["ent"].cpu().double() - n.log()).abs() <= tol * (1 + n.log())).all()
+    assert ((r["top"][:, 0].cpu().double() + n.log()).abs() <= tol).all()
 
 
 @pytest.mark.parametrize("kind", ["bf16", "f32"])

@@ -124,6 +124,7 @@ def _logprobs(lib, ptrs=None, **kw):
     (dict(N=-1), BAD), (dict(V=0), BAD), (dict(n_top=-1), BAD), (dict(dtype=2), BAD),
     (dict(stride=127), BAD), (dict(scale=0.0), BAD), (dict(scale=-1.0), BAD),
     (dict(scale=float("nan")), BAD), (dict(scale=float("inf")), BAD), (dict(scale=3e38), BAD),
+    (dict(scale=2.0 ** 65), BAD), (dict(scale=2.0 ** -65), BAD),
     (dict(V=(1 << 24) + 1, stride=1 << 25), UNSUP), (dict(N=(1 << 20) + 1), UNSUP),
     (dict(n_top=65), UNSUP), (dict(stride=1 << 50), UNSUP), (dict(workspace=None), BAD),
     (dict(workspace_bytes=255), BAD)])
