@@ -14,6 +14,11 @@
 // warp holds a run's rows of one head in registers (up to 16 rows, 8 channels of
 // 16-bit inputs a lane), so that every element is read once and written once.  A CTA
 // owns the runs whose first row is among its rows, and the q heads of its rows.
+//
+// HBM bounds it as far as bytes go: 32767 tokens of 32 / 8 heads of 128 channels, bf16, 181
+// us, 4.1 TB/s (the floor is 110 us).  The rest is instructions (a key is made twice, a q
+// head has a reduction and a rotation) and latency: a warp's loads are one run or four
+// passes of q heads, with the next four on their way.  64 tokens: 3.8 us, the launch.
 #include "kda_paged_e4m3.cuh"
 
 namespace kda {
@@ -125,8 +130,9 @@ __device__ __forceinline__ void turn(float (&x)[kVec<T>], const Place &c, const 
     for (int i = 0; i < N; ++i) ss = fmaf(x[i], x[i], ss);
 #pragma unroll
     for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    // (rounded to nearest: with rsqrtf, off by up to two steps, twice as many values land
-    // on another e4m3 value than the exact ones do)
+    // (rounded to nearest: with rsqrtf, off by up to two steps, more values that lie between
+    // two e4m3 values go the other way; 2.7e-5 against 1.4e-5 relative difference from the
+    // exact ones' cache)
     const float r = __frsqrt_rn(ss * (1.f / D) + eps);
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = x[i] * r * v.w[i];

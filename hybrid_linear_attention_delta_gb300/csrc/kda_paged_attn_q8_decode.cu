@@ -3,8 +3,9 @@
 //
 //     out = sum_j softmax_j(scale q . (ks k8)_j) (vs v8)_j
 //
-// A decode reads every key once for up to 16 rows (tokens times heads of the group), so
-// HBM bounds it, and what matters is that loads never stop.  tcgen05 products of 128
+// A decode reads every key once for up to 16 rows (tokens times heads of the group; 32 with
+// 64 channels, a warp for each half), so HBM bounds it, and what matters is that loads never
+// stop.  tcgen05 products of 128
 // rows, with their tensor memory, barriers and warps of several roles, take 2800 cycles
 // for 128 keys there, twice what the loads do.  Here every warp works alone, on 16 keys at
 // a time, which are one block of the scales: it copies them into a ring of its own, several
@@ -19,6 +20,12 @@
 //     fp16 exactly down to 2^-25 of their largest channel.
 //   * Weights and references as in kda_paged_attn.cuh: P = 2^(c ks S + log2 vs - m) in
 //     fp16, the reference m moves when a weight passes 2^15.
+//
+// Measured: 256 requests over 511 to 8191 keys, 32 / 8 heads of 128 channels, 0.408 ms, 5.9
+// TB/s (87% of a copy; the tensor-core kernel 0.80 ms); 64 channels 0.36 ms, where a row of
+// a key is 64 bytes and the memory moves 128, the next head's too, twice the bytes for the
+// two CTAs that come by at different times.  One token over 777 keys: latency, 11 us in a
+// graph.
 #include <cfloat>
 
 #include "kda_paged_e4m3.cuh"

@@ -269,7 +269,10 @@ kda_status kda_paged_append_q8(const void *qkv, const int32_t *positions, const 
  * k_scales, v_scales [n_pages][page_size / 16][Hkv] fp32; read for blocks that hold a
  *                    key of the request
  * Workspace: as for kda_paged_attn.  A block whose scale of keys or of values is outside
- * its bounds (bit 8192) is left out of the requests that hold it.
+ * its bounds (bit 8192) is left out of the requests that hold it; its bytes must still be
+ * finite.  In bf16 a row's largest channel keeps all its bits from 2^-119 up, and keys count
+ * down to 2^-30 of a row's largest product of weight and scale of the values.  scale * q . k
+ * must be finite with the keys' scales.
  */
 kda_status kda_paged_attn_q8(const void *q, const void *k_pages, const void *v_pages,
                              const float *k_scales, const float *v_scales,
