@@ -246,7 +246,8 @@ struct Publisher {
   PagedPiece o;
   bool more = true;     // (the last one published says that there are no more)
 
-  __device__ bool publish(Ctl &ctl, const AttnArgs &a, PagedSched<kKeys> &sched) {
+  template <class Sched>
+  __device__ bool publish(Ctl &ctl, const AttnArgs &a, Sched &sched) {
     const int tpt = a.tpt;
     const uint32_t slot = n % kPieces;
     Work w;
@@ -402,7 +403,7 @@ __device__ bool load_role(uint32_t sbase, Ctl &ctl, const AttnArgs &a, const CUt
 // pages: 64 x 8 tokens verified in 311 us, with two warps in 293.)
 template <int D, bool LONG, bool VALUES>
 __device__ bool load_role_q8(uint32_t sbase, CtlQ8 &ctl, const AttnArgs &a, const CUtensorMap *tq,
-                             const CUtensorMap *map, PagedSched<kKeys> &sched) {
+                             const CUtensorMap *map, PagedSched<kKeys, true> &sched) {
   using Ly = Layout<D, true>;
   const PagedAttnPlan &p = a.p;
   const int lane = threadIdx.x & 31;
@@ -1671,7 +1672,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
   }
   if (warp == kMmaWarp) tmem_alloc(smem_u32(&ctl.tmem), 512);
   tc_fence_before();
-  PagedSched<kKeys> sched;  // (its barriers are the set-up's too)
+  PagedSched<kKeys, Q8> sched;  // (its barriers are the set-up's too)
   const bool work = sched.template init<kThreads<Q8>>(a.p, 2 * a.tpt, ctl.scratch);
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&ctl.tmem);
@@ -1703,10 +1704,9 @@ attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
     } else if (warp == kLoadWarp) {
       if constexpr (Q8) ok = load_role_q8<D, LONG, false>(sbase, ctl, a, &tq, &tk, sched);
       else ok = load_role<D>(sbase, ctl, a, &tq, &tk, &tv);
-    } else if (Q8 && warp >= kConvertWarp) {
-      if constexpr (Q8) ok = convert_role<D>(sbase, ctl, a);
-    } else if (Q8) {
-      if constexpr (Q8) ok = load_role_q8<D, LONG, true>(sbase, ctl, a, &tq, &tv, sched);
+    } else if constexpr (Q8) {
+      if (warp >= kConvertWarp) ok = convert_role<D>(sbase, ctl, a);
+      else ok = load_role_q8<D, LONG, true>(sbase, ctl, a, &tq, &tv, sched);
     } else if (tid == kSchedWarp * 32) {
       ok = sched_role<LONG>(ctl, a, sched);
     }

@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(PagedAttnPlan p, floa
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, q = lane & 3;
   const int row0 = warp % GROUPS * kRows;  // this warp's rows
-  PagedSched<kTile> sched;
+  PagedSched<kTile, true> sched;
   if (!sched.template init<kThreads>(p, GROUPS * kRows / p.G, sm.scratch)) return;
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(&sm.ring[warp][0][0][0]);
   const int64_t row_bytes = (int64_t)p.Hkv * D;

@@ -74,14 +74,15 @@ __device__ __forceinline__ int64_t paged_div(int64_t a, int64_t b) {
   return ((a | b) >> 31) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
-// TILE: keys of a tile; tokens: query tokens of an item at most.
-template <int TILE>
+// TILE: keys of a tile; tokens: query tokens of an item at most.  BY_HEAD: the line goes
+// over the heads first and the requests within, not the other way round.
+template <int TILE, bool BY_HEAD = false>
 struct PagedSched {
   int32_t tokens, item_cost;
   bool apart;              // every item starts a stretch
   int64_t pos, end, base;  // place on the line, end of the stretch, start of request b
   int64_t per_cta;
-  int32_t b;
+  int32_t b, head;         // head: BY_HEAD, the one that pos is in
   PagedReq r;
 
   // What an item of the request and one head takes of the line.
@@ -95,6 +96,8 @@ struct PagedSched {
   __device__ bool init(const PagedAttnPlan &p, int tokens_per_item, int64_t *scratch) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int W = THREADS / 32;
+    // the line's parts that a request has side by side, and how often all come
+    const int heads = BY_HEAD ? 1 : p.Hkv, times = BY_HEAD ? p.Hkv : 1;
     tokens = tokens_per_item;
     item_cost = p.item_cost;
     const int run = (p.B + THREADS - 1) / THREADS;
@@ -115,9 +118,9 @@ struct PagedSched {
       if (blockIdx.x == 0 && (kvl < 0 || (int64_t)kvl > (int64_t)p.max_pages * p.page_size))
         raise_error(p.err, ERR_BAD_LEN);
       const int64_t c = paged_head_cost(q, tokens, p.causal, item_cost);
-      mine += c * p.Hkv;
+      mine += c * heads;
       mine_s += q.n > tokens ? 1ll << 32  // several items: not apart
-                             : paged_div(c - less + per_cta - 1, per_cta) * p.Hkv;
+                             : paged_div(c - less + per_cta - 1, per_cta) * heads;
     }
     bad |= cu0 != 0 || cuB > p.T;
     int64_t inc = mine, inc_s = mine_s;
@@ -143,22 +146,26 @@ struct PagedSched {
         total += scratch[w], total_s += scratch[W + w];
       }
     }
-    apart = total_s <= gridDim.x;
+    apart = total_s * times <= gridDim.x;
     if (apart) {
       item_cost -= less;
       before = before_s * per_cta, mine = mine_s * per_cta, total = total_s * per_cta;
     } else {
       per_cta = max(max(per_cta, (int64_t)2 * TILE + item_cost),
-                    paged_div(total + gridDim.x - 1, gridDim.x));
+                    paged_div(total * times + gridDim.x - 1, gridDim.x));
     }
     pos = blockIdx.x * per_cta;
-    end = min(total, pos + per_cta);
+    end = min(total * times, pos + per_cta);
+    if constexpr (BY_HEAD) {
+      head = pos < end ? (int32_t)paged_div(pos, total) : 0;
+      before += head * total;
+    }
     if (pos < end && before <= pos && pos < before + mine) {  // this thread's requests hold it
       int64_t at = before;
       int i = b0;
       for (; i + 1 < b1; ++i) {  // (the last one is at hand)
         const PagedReq x = paged_request(p, i, tokens);
-        const int64_t c = stride(paged_head_cost(x, tokens, p.causal, item_cost)) * p.Hkv;
+        const int64_t c = stride(paged_head_cost(x, tokens, p.causal, item_cost)) * heads;
         if (pos < at + c) {
           q = x;
           break;
@@ -195,17 +202,21 @@ struct PagedSched {
     o.n = 0;
     while (pos < end) {
       const int64_t head_cost = stride(paged_head_cost(r, tokens, p.causal, item_cost));
-      if (pos >= base + head_cost * p.Hkv) {  // on to the next request with work
-        base += head_cost * p.Hkv;
+      const int64_t all_cost = BY_HEAD ? head_cost : head_cost * p.Hkv;
+      if (pos >= base + all_cost) {  // on to the next request with work
+        base += all_cost;
         if (++b >= p.B) {
-          pos = end;
-          break;
+          if (!BY_HEAD || ++head >= p.Hkv) {
+            pos = end;
+            break;
+          }
+          b = 0;
         }
         r = paged_request(p, b, tokens);
         continue;
       }
-      const int head = (int)paged_div(pos - base, head_cost);
-      const int64_t head_base = base + head * head_cost;
+      const int at_head = BY_HEAD ? 0 : (int)paged_div(pos - base, head_cost);
+      const int64_t head_base = base + at_head * head_cost;
       int lo = 0, hi = r.runs - 1;  // largest run that starts at or before pos
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -216,7 +227,7 @@ struct PagedSched {
       const int64_t stop = min(end, start + cost);
       o.n = min(tokens, r.n - lo * tokens);
       o.tok0 = r.tok0 + lo * tokens;
-      o.head = head;
+      o.head = BY_HEAD ? head : at_head;
       o.req = b;
       o.kv = r.kv;
       o.seen0 = p.causal ? r.kv - r.n + lo * tokens + 1 : r.kv;
