@@ -143,8 +143,7 @@ cudaError_t launch_verify(const VerifyPlan &p);
 cudaError_t launch_paged_append_q8(const AppendPlan &p);
 cudaError_t launch_paged_attn_q8_f32(const PagedAttnPlan &p);
 cudaError_t launch_paged_attn_q8_bf16(const PagedAttnPlan &p);
-// items of up to 16 or 32 rows
-cudaError_t launch_paged_attn_q8_decode(const PagedAttnPlan &p, int rows);
+cudaError_t launch_paged_attn_q8_decode(const PagedAttnPlan &p);  // items of up to 16 rows
 cudaError_t launch_logprobs(const LogprobsPlan &p);
 
 // launches of the last successful call on this host thread (kda_api.cu)

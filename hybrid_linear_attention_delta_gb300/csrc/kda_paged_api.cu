@@ -174,13 +174,11 @@ kda_status attn(const void *q, const void *k_pages, const void *v_pages, const f
   p.part = reinterpret_cast<float *>(ws + lay.part_off);
   p.part_ml = reinterpret_cast<float *>(ws + lay.ml_off);
   // The 8-bit cache, bf16: requests with few rows on average take the kernel of small
-  // register products, in items of 16 rows or, with 64 channels, 32.  (64 requests over 1000
-  // to 9000 keys, 32 / 8 heads, against the tensor-core kernel: 4 to 16 rows 110 to 113 and
-  // 170 us with 64 channels, 133 to 137 and 201 to 206 us with 128; 20 to 32 rows 153 and
-  // 172 us, 226 and 210 us.)
-  const bool few = q8 && a->dtype == KDA_BF16 && G <= 16 && (int64_t)a->T_total * G <= 16ll * a->B;
-  const bool decode = few || (q8 && a->dtype == KDA_BF16 && a->d == 64 && G <= 32 &&
-                              (int64_t)a->T_total * G <= 32ll * a->B);
+  // register products, in items of 16 rows.  (64 requests over 1000 to 9000 keys, 32 / 8
+  // heads, against the tensor-core kernel: 4 to 16 rows 85 to 86 and 141 to 144 us with 64
+  // channels, 125 to 128 and 194 to 199 us with 128; items of 32 rows, 20 to 32 of them, 149 to
+  // 151 and 145 us, 224 and 199 us.)
+  const bool decode = q8 && a->dtype == KDA_BF16 && G <= 16 && (int64_t)a->T_total * G <= 16ll * a->B;
   p.part_rows = kda::paged_part_rows(a->T_total, G, decode ? (int32_t)KDA_F32 : a->dtype);
   // What an item's start and end cost, and the shortest stretch worth a join, in
   // keys.  In bf16 both are longer where requests bring a tile of rows and more.  (bf16,
@@ -194,9 +192,10 @@ kda_status attn(const void *q, const void *k_pages, const void *v_pages, const f
   // 78, 96; 200 tokens over 500 keys, 128 channels, 63, 85, 107, 137; 100 over 8000 90, 91,
   // 118, 97; 8 requests of up to 301 120, 120, 120, 142; 8 x 1000 tokens the same.  8-bit
   // cache, item cost 320, 576, 768, 1024: a prompt of 1000 tokens 46, 43, 41.5, 42 us, mixed
-  // batch of 24 1094, 1038, 1052, 1061, with 128 channels 1981, 1790, 1808, 1813; small
-  // products, 64, 128, 256, 512: 256 decodes 453, 448, 434, 421 us, 64 x 4 tokens of 4 heads
-  // a group 153, 146, 135, 117.)
+  // batch of 24 1094, 1038, 1052, 1061, with 128 channels 1981, 1790, 1808, 1813, 64 x 8
+  // tokens, 448, 576, 768, 1024, 262, 261, 258, 258; small products, 64, 128, 256, 512: 256
+  // decodes 453, 448, 434, 421 us, 64 x 4 tokens of 4 heads a group 153, 146, 135, 117, and cut
+  // head by head, 256, 512, 768, 1024, 395, 395, 398, 401 and 109, 106, 107, 111.)
   const bool wide = (int64_t)a->T_total * G >= 128ll * a->B, bf16 = a->dtype == KDA_BF16;
   p.min_stretch = decode ? 256 : bf16 && wide ? 896 : 384;
   p.item_cost = !bf16 ? 128 : decode ? 512 : q8 ? 768 : wide ? 320 : 256;
@@ -204,7 +203,7 @@ kda_status attn(const void *q, const void *k_pages, const void *v_pages, const f
   return launch(a->stream, a->ev_begin, a->ev_end, [&] {
     if (q8)
       return !bf16    ? kda::launch_paged_attn_q8_f32(p)
-             : decode ? kda::launch_paged_attn_q8_decode(p, few ? 16 : 32)
+             : decode ? kda::launch_paged_attn_q8_decode(p)
                       : kda::launch_paged_attn_q8_bf16(p);
     return bf16 ? kda::launch_paged_attn_bf16(p) : kda::launch_paged_attn_f32(p);
   });

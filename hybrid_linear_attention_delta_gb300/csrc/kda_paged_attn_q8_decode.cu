@@ -3,9 +3,8 @@
 //
 //     out = sum_j softmax_j(scale q . (ks k8)_j) (vs v8)_j
 //
-// A decode reads every key once for up to 16 rows (tokens times heads of the group; 32 with
-// 64 channels, a warp for each half), so HBM bounds it, and what matters is that loads never
-// stop.  tcgen05 products of 128
+// A decode reads every key once for up to 16 rows (tokens times heads of the group), so
+// HBM bounds it, and what matters is that loads never stop.  tcgen05 products of 128
 // rows, with their tensor memory, barriers and warps of several roles, take 2800 cycles
 // for 128 keys there, twice what the loads do.  Here every warp works alone, on 16 keys at
 // a time, which are one block of the scales: it copies them into a ring of its own, several
@@ -21,11 +20,12 @@
 //   * Weights and references as in kda_paged_attn.cuh: P = 2^(c ks S + log2 vs - m) in
 //     fp16, the reference m moves when a weight passes 2^15.
 //
-// Measured: 256 requests over 511 to 8191 keys, 32 / 8 heads of 128 channels, 0.408 ms, 5.9
-// TB/s (87% of a copy; the tensor-core kernel 0.80 ms); 64 channels 0.36 ms, where a row of
-// a key is 64 bytes and the memory moves 128, the next head's too, twice the bytes for the
-// two CTAs that come by at different times.  One token over 777 keys: latency, 11 us in a
-// graph.
+// Measured: 256 requests over 511 to 8191 keys, 32 / 8 heads of 128 channels, 0.394 ms, 6.2
+// TB/s (91% of a copy; the tensor-core kernel 0.80 ms), 64 channels 0.259 ms, 4.7 TB/s.  The
+// work is cut head by head (PagedSched), so that the CTAs of a request's heads read its
+// rows, which lie side by side, at the same time: request by request, 64 channels take 0.36
+// ms, as the memory moves two heads' 64 bytes for either.  One token over 777 keys: latency,
+// 11 us in a graph.
 #include <cfloat>
 
 #include "kda_paged_e4m3.cuh"
@@ -47,9 +47,7 @@ constexpr float kHead = 6.f, kMost = 32768.f;
 // bits below the sum; then the sums are put aside in fp32.
 constexpr int kLongRun = 8192;
 
-// GROUPS: groups of 16 rows, which an item has at most; a warp each works on the same
-// keys, so that kWarps / GROUPS of them share the item's steps.
-template <int D, int GROUPS>
+template <int D>
 struct Smem {
   // (2, 3, 4, 5 stages: 256 decodes over 511 to 8191 keys, 128 channels, 434, 408, 411,
   // 428 us; 64 channels, with 3, 4, 8: 360, 361, 385)
@@ -59,7 +57,7 @@ struct Smem {
     uint8_t ring[kWarps][kStages][2][kBytes];
     float o[kWarps][kRows][D + 4];
   };
-  float sum[GROUPS * kRows][D];  // runs before this one
+  float sum[kRows][D];  // runs before this one
   float ml[kWarps][kRows][2];
   PagedPiece piece[2];
   int64_t scratch[kThreads / 16 + 4];
@@ -116,11 +114,10 @@ struct StepInfo {
   float k, v, inv_v;  // of the keys; log2 and inverse of the values' (-inf and 0: left out)
 };
 
-template <int D, int GROUPS>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 2) attn_kernel(PagedAttnPlan p, float scale) {
-  using S = Smem<D, GROUPS>;
+  using S = Smem<D>;
   constexpr int kStages = S::kStages;
-  constexpr int kShare = kWarps / GROUPS;  // warps that share the steps
   constexpr int KS = D / 16;         // products of the channels of a score
   constexpr int NT = D / 8;          // products of the channels of the outputs
   constexpr int kChunks = D / 16;    // 16-byte chunks of a row
@@ -128,9 +125,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(PagedAttnPlan p, floa
   S &sm = *reinterpret_cast<S *>(raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, q = lane & 3;
-  const int row0 = warp % GROUPS * kRows;  // this warp's rows
   PagedSched<kTile, true> sched;
-  if (!sched.template init<kThreads>(p, GROUPS * kRows / p.G, sm.scratch)) return;
+  if (!sched.template init<kThreads>(p, kRows / p.G, sm.scratch)) return;
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(&sm.ring[warp][0][0][0]);
   const int64_t row_bytes = (int64_t)p.Hkv * D;
   // a lane's part of a step's copies: chunk lane % kChunks of every (32 / kChunks)-th row
@@ -151,16 +147,16 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(PagedAttnPlan p, floa
     if (o.n == 0) break;
     const int rows = o.n * p.G;
 
-    // ---- the steps of this warp: first + kShare i, i < n_steps
+    // ---- the steps of this warp: first + kWarps i, i < n_steps
     const int seen_all = min(o.kv, p.causal ? o.seen0 + o.n - 1 : o.kv);  // keys of the last row
-    const int first = o.tile0 * kWarps + warp / GROUPS;
+    const int first = o.tile0 * kWarps + warp;
     const int end = min(o.tile1 * kWarps, (max(0, seen_all) + kStep - 1) / kStep);
-    const int n_steps = max(0, (end - first + kShare - 1) / kShare);
+    const int n_steps = max(0, (end - first + kWarps - 1) / kWarps);
     const int32_t *table = p.table + (int64_t)o.req * p.max_pages;
     auto page_of = [&](int i) {
       int page = -1;
       if (i < n_steps) {
-        page = __ldg(table + ((int64_t)(first + kShare * i) * kStep >> p.page_shift));
+        page = __ldg(table + ((int64_t)(first + kWarps * i) * kStep >> p.page_shift));
         if ((uint32_t)page >= (uint32_t)p.n_pages) {
           raise_error(p.err, ERR_BAD_PAGE);
           page = -1;
@@ -169,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(PagedAttnPlan p, floa
       return page;
     };
     auto block_of = [&](int i, int page) {
-      const int key = (first + kShare * i) * kStep;
+      const int key = (first + kWarps * i) * kStep;
       return (((int64_t)page << p.page_shift) + (key & (p.page_size - 1))) / kScaleTokens * p.Hkv + o.head;
     };
     // Lane l keeps what belongs to step 32 run + l, and the pages of the run behind it.
@@ -194,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(PagedAttnPlan p, floa
     const uint8_t *kp = static_cast<const uint8_t *>(p.k) + o.head * D;
     const uint8_t *vp = static_cast<const uint8_t *>(p.v) + o.head * D;
     auto copy = [&](int i, int page, int stage) {
-      const int key = (first + kShare * i) * kStep;
+      const int key = (first + kWarps * i) * kStep;
       const int64_t slot = ((int64_t)max(page, 0) << p.page_shift) + (key & (p.page_size - 1));
       const uint32_t to = ring + (uint32_t)stage * (2 * S::kBytes);
       const int64_t at = slot * row_bytes + lane_at;
@@ -222,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(PagedAttnPlan p, floa
       uint2 in[2][KS];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int r = row0 + g + 8 * h;
+        const int r = g + 8 * h;
         const bool live = r < rows;  // (the others are zeros, and go nowhere)
         lim[h] = live && p.causal ? min(o.kv, o.seen0 + r / p.G) : o.kv;
         const __nv_bfloat16 *row = static_cast<const __nv_bfloat16 *>(p.q) + (live ? row_offset(p, o, r) : 0);
@@ -325,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(PagedAttnPlan p, floa
             }
           }
         }
-        const int key0 = (first + kShare * i) * kStep;
+        const int key0 = (first + kWarps * i) * kStep;
         if (key0 + kStep > min(lim[0], lim[1])) {
 #pragma unroll
           for (int t = 0; t < 2; ++t)
@@ -418,19 +414,17 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(PagedAttnPlan p, floa
           sm.o[warp][g + 8 * h][NT * (2 * q + 1) + j] = acc[j][2 * h + 1];
         }
       __syncthreads();
-      constexpr int kLanes = kThreads / (GROUPS * kRows), kCh = D / kLanes;  // threads of a row; channels of one
+      constexpr int kLanes = kThreads / kRows, kCh = D / kLanes;  // threads of a row; channels of one
       const int r = tid / kLanes, ch0 = tid % kLanes * 4;        // channels ch0 + 4 kLanes x ..
       float top = earlier ? result_m : -INFINITY;
-      const int rw = r % kRows;  // in warps r / kRows + GROUPS w
-      auto of = [&](int w) { return r / kRows + GROUPS * w; };
 #pragma unroll
-      for (int w = 0; w < kShare; ++w) top = fmaxf(top, sm.ml[of(w)][rw][0]);
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm.ml[w][r][0]);
       const float zero = top == -INFINITY ? 0.f : top;
-      float wt[kShare], sum_l = 0.f;
+      float wt[kWarps], sum_l = 0.f;
 #pragma unroll
-      for (int w = 0; w < kShare; ++w) {
-        const float lw = sm.ml[of(w)][rw][1];
-        wt[w] = lw == 0.f ? 0.f : exp2f(sm.ml[of(w)][rw][0] - zero);
+      for (int w = 0; w < kWarps; ++w) {
+        const float lw = sm.ml[w][r][1];
+        wt[w] = lw == 0.f ? 0.f : exp2f(sm.ml[w][r][0] - zero);
         sum_l += wt[w] * lw;
       }
       const float w_before = earlier && result_l != 0.f ? exp2f(result_m - zero) : 0.f;
@@ -445,8 +439,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(PagedAttnPlan p, floa
           y = make_float4(w_before * z.x, w_before * z.y, w_before * z.z, w_before * z.w);
         }
 #pragma unroll
-        for (int w = 0; w < kShare; ++w) {
-          const float4 z = *reinterpret_cast<const float4 *>(&sm.o[of(w)][rw][ch]);
+        for (int w = 0; w < kWarps; ++w) {
+          const float4 z = *reinterpret_cast<const float4 *>(&sm.o[w][r][ch]);
           // (a warp in which the row saw no key: whatever its products left)
           if (wt[w] != 0.f) {
             y.x = fmaf(wt[w], z.x, y.x), y.y = fmaf(wt[w], z.y, y.y);
@@ -531,27 +525,22 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(PagedAttnPlan p, floa
   }
 }
 
-template <int D, int GROUPS>
+template <int D>
 cudaError_t launch_d(const PagedAttnPlan &p) {
-  using S = Smem<D, GROUPS>;
-  const void *f = reinterpret_cast<const void *>(attn_kernel<D, GROUPS>);
+  using S = Smem<D>;
+  const void *f = reinterpret_cast<const void *>(attn_kernel<D>);
   const cudaError_t e = set_smem_limit_once(f, sizeof(S));
   if (e != cudaSuccess) return e;
   static_assert(sizeof(S) <= 113 * 1024, "two CTAs of an SM");
-  static_assert(GROUPS * kRows <= kPagedF32Rows, "rows of a partial result");
-  attn_kernel<D, GROUPS><<<kPagedF32Ctas, kThreads, sizeof(S), p.stream>>>(
-      p, p.scale * 1.4426950408889634f);
+  static_assert(kRows <= kPagedF32Rows, "rows of a partial result");
+  attn_kernel<D><<<kPagedF32Ctas, kThreads, sizeof(S), p.stream>>>(p, p.scale * 1.4426950408889634f);
   return cudaGetLastError();
-}
-template <int GROUPS>
-cudaError_t launch(const PagedAttnPlan &p) {
-  return p.d == 128 ? launch_d<128, GROUPS>(p) : launch_d<64, GROUPS>(p);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_attn_q8_decode(const PagedAttnPlan &p, int rows) {
-  return rows <= kRows ? launch<1>(p) : launch<2>(p);
+cudaError_t launch_paged_attn_q8_decode(const PagedAttnPlan &p) {
+  return p.d == 128 ? launch_d<128>(p) : launch_d<64>(p);
 }
 
 }  // namespace kda
