@@ -235,6 +235,39 @@ def test_mixed_batch_of_many_requests():
 
 
 @pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G", [1, 3, 4, 16])
+@pytest.mark.parametrize("causal", [True, False])
+def test_a_chunk_in_a_padded_batch(d, G, causal):
+    """Few rows a request on average, nearly all of them one request's: many items of it."""
+    new = [0, 0, 150, 0, 1] + [0] * (12 * G + 100) + [1, 2, 0]
+    total = [9, 0, 700, 0, 3000] + [0] * (12 * G + 100) + [40, 2, 7]
+    _check(Q8AttnCase(new, total, Hq=3 * G, Hkv=3, d=d, page=32, dtype="bf16", seed=G, pad=9),
+           causal)
+
+
+@pytest.mark.parametrize("d,G", [(64, 1), (128, 2), (64, 16), (128, 24)])
+@pytest.mark.parametrize("Hkv", [2, 5, 8])
+def test_stretches_that_cross_heads(d, G, Hkv):
+    """More items than CTAs, of a request or of many: a CTA goes from the last request of
+    one head to the first of the next, past empty ones at either end."""
+    g = torch.Generator().manual_seed(Hkv + d)
+    new = [0, 0] + torch.randint(0, 4, (90,), generator=g).tolist() + [0, 0, 0]
+    total = [n + c for n, c in zip(new, torch.randint(0, 300, (95,), generator=g).tolist())]
+    _check(Q8AttnCase(new, total, Hq=G * Hkv, Hkv=Hkv, d=d, page=16, dtype="bf16", seed=Hkv))
+    _check(Q8AttnCase([3], [9], Hq=G * Hkv, Hkv=Hkv, d=d, page=16, dtype="bf16", seed=Hkv))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_few_rows_that_see_nothing(d):
+    """As test_rows_that_see_nothing, with no more rows than the small products take."""
+    case = Q8AttnCase([4, 2, 1, 6], [0, 1, 50, 3], Hq=2, Hkv=2, d=d, page=16, dtype="bf16", seed=4)
+    out = _check(case)
+    assert (out[:5] == 0).all() and (out[7:10] == 0).all()
+    assert (out[5:7] != 0).any() and (out[10:13] != 0).any()
+    assert (_check(case, causal=False)[4:] != 0).any()
+
+
+@pytest.mark.parametrize("d", [64, 128])
 def test_chunk_against_a_long_prefix(d):
     _check(Q8AttnCase([519], [4100], Hq=8, Hkv=2, d=d, page=128, dtype="bf16", seed=21))
 
