@@ -191,14 +191,14 @@ kda_status attn(const void *q, const void *k_pages, const void *v_pages, const f
   // stretch 384, 512, 768, 1024: a prompt of 1000 tokens, 8/2 heads of 64 channels, 66, 71,
   // 78, 96; 200 tokens over 500 keys, 128 channels, 63, 85, 107, 137; 100 over 8000 90, 91,
   // 118, 97; 8 requests of up to 301 120, 120, 120, 142; 8 x 1000 tokens the same.  8-bit
-  // cache, item cost 320, 576, 768, 1024: a prompt of 1000 tokens 46, 43, 41.5, 42 us, mixed
-  // batch of 24 1094, 1038, 1052, 1061, with 128 channels 1981, 1790, 1808, 1813, 64 x 8
-  // tokens, 448, 576, 768, 1024, 262, 261, 258, 258; small products, 64, 128, 256, 512: 256
-  // decodes 453, 448, 434, 421 us, 64 x 4 tokens of 4 heads a group 153, 146, 135, 117, and cut
-  // head by head, 256, 512, 768, 1024, 395, 395, 398, 401 and 109, 106, 107, 111.)
+  // cache, keys of items with two tiles of rows counted twice, item cost 768, 1024, 1536 with
+  // such requests: mixed batch of 24 1054, 1052, 1038, a prompt of 1000 tokens 49, 47, 45;
+  // shortest stretch 896, 1280, 1792 the same; 448, 576, 768, 1024 without: 64 x 8 tokens 262,
+  // 261, 258, 258; small products, cut head by head, 256, 512, 768, 1024: 256 decodes 395, 395,
+  // 398, 401, 64 x 4 tokens of 4 heads a group 109, 106, 107, 111.)
   const bool wide = (int64_t)a->T_total * G >= 128ll * a->B, bf16 = a->dtype == KDA_BF16;
-  p.min_stretch = decode ? 256 : bf16 && wide ? 896 : 384;
-  p.item_cost = !bf16 ? 128 : decode ? 512 : q8 ? 768 : wide ? 320 : 256;
+  p.min_stretch = decode ? 256 : !bf16 || !wide ? 384 : 896;
+  p.item_cost = !bf16 ? 128 : decode ? 512 : q8 ? (wide ? 1536 : 768) : wide ? 320 : 256;
   p.stream = static_cast<cudaStream_t>(a->stream);
   return launch(a->stream, a->ev_begin, a->ev_end, [&] {
     if (q8)

@@ -403,7 +403,7 @@ __device__ bool load_role(uint32_t sbase, Ctl &ctl, const AttnArgs &a, const CUt
 // pages: 64 x 8 tokens verified in 311 us, with two warps in 293.)
 template <int D, bool LONG, bool VALUES>
 __device__ bool load_role_q8(uint32_t sbase, CtlQ8 &ctl, const AttnArgs &a, const CUtensorMap *tq,
-                             const CUtensorMap *map, PagedSched<kKeys, true> &sched) {
+                             const CUtensorMap *map, PagedSched<kKeys, true, true> &sched) {
   using Ly = Layout<D, true>;
   const PagedAttnPlan &p = a.p;
   const int lane = threadIdx.x & 31;
@@ -1672,7 +1672,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
   }
   if (warp == kMmaWarp) tmem_alloc(smem_u32(&ctl.tmem), 512);
   tc_fence_before();
-  PagedSched<kKeys, Q8> sched;  // (its barriers are the set-up's too)
+  PagedSched<kKeys, Q8, Q8> sched;  // (its barriers are the set-up's too)
   const bool work = sched.template init<kThreads<Q8>>(a.p, 2 * a.tpt, ctl.scratch);
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&ctl.tmem);

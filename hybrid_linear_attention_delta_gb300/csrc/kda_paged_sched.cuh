@@ -15,6 +15,12 @@
 // lie side by side.  (8-bit cache: 64 x 8 tokens over 1000 to 32760 keys, 4 heads, 273 and 258
 // us, 256 decodes with 64 channels 360 and 259 us, with 128 the same.)
 //
+// A tile of keys takes about as long with one tile of rows as with two would take a stream of
+// its own, so where a kernel works on two streams, an item with two costs twice as much a key
+// (PAIRS).  (8-bit cache: 256 decodes over 4000 keys and 512 tokens over 8000, in the kernel of
+// tiles, 998 and 608 us; 64 requests of 1 to 40 tokens 590 and 541, a chunk of 8192 2704 and
+// 2680, the mixed batch of 24 the same.)
+//
 // A batch of few short items (decodes) leaves most of the grid idle at the
 // shortest stretch.  Then every item starts a stretch of its own, so that no
 // CTA works on the end of one item and the start of another; the fixed cost
@@ -51,17 +57,13 @@ struct PagedPiece {
                        // 2 * (first_cta + k)
 };
 
-// Cost of the request's first i runs of one head.
+// Cost of the request's first i runs of one head.  weight: of a key.
 __device__ __forceinline__ int64_t paged_prefix(const PagedReq &r, int64_t i, int tokens,
-                                                bool causal, int item_cost) {
-  if (!causal || r.kv < r.n) return i * (r.kv + item_cost);
-  int64_t c = i * (r.kv - r.n + item_cost) + (int64_t)tokens * (i * (i + 1) / 2);
+                                                bool causal, int item_cost, int weight) {
+  if (!causal || r.kv < r.n) return i * ((int64_t)r.kv * weight + item_cost);
+  int64_t c = i * (r.kv - r.n) + (int64_t)tokens * (i * (i + 1) / 2);
   if (i == r.runs) c += r.n - (int64_t)r.runs * tokens;  // the last run is shorter
-  return c;
-}
-__device__ __forceinline__ int64_t paged_head_cost(const PagedReq &r, int tokens, bool causal,
-                                                   int item_cost) {
-  return paged_prefix(r, r.runs, tokens, causal, item_cost);
+  return c * weight + i * item_cost;
 }
 
 __device__ __forceinline__ PagedReq paged_request(const PagedAttnPlan &p, int b, int tokens) {
@@ -80,8 +82,9 @@ __device__ __forceinline__ int64_t paged_div(int64_t a, int64_t b) {
 }
 
 // TILE: keys of a tile; tokens: query tokens of an item at most.  BY_HEAD: the line goes
-// over the heads first and the requests within, not the other way round.
-template <int TILE, bool BY_HEAD = false>
+// over the heads first and the requests within, not the other way round.  PAIRS: a key costs
+// twice as much where a request brings more than half an item's tokens (two tiles of rows).
+template <int TILE, bool BY_HEAD = false, bool PAIRS = false>
 struct PagedSched {
   int32_t tokens, item_cost;
   bool apart;              // every item starts a stretch
@@ -93,6 +96,16 @@ struct PagedSched {
   // What an item of the request and one head takes of the line.
   __device__ __forceinline__ int64_t stride(int64_t cost) const {
     return apart ? paged_div(cost + per_cta - 1, per_cta) * per_cta : cost;
+  }
+
+  __device__ __forceinline__ int weight(const PagedReq &q) const {
+    return PAIRS && 2 * (int64_t)q.n > tokens ? 2 : 1;
+  }
+  __device__ __forceinline__ int64_t prefix(const PagedReq &q, int64_t i, bool causal) const {
+    return paged_prefix(q, i, tokens, causal, item_cost, weight(q));
+  }
+  __device__ __forceinline__ int64_t head_cost(const PagedReq &q, bool causal) const {
+    return prefix(q, q.runs, causal);
   }
 
   // All threads of the CTA; scratch: THREADS / 16 + 4 words of 64 bits.  False:
@@ -110,7 +123,8 @@ struct PagedSched {
     // a cut costs a round trip of partials (see min_stretch); two tiles and an
     // item's fixed cost at least, so that a stretch inside an item has a tile
     const int less = max(0, item_cost - kApartCost);
-    per_cta = max(p.min_stretch, 2 * TILE + item_cost - less);
+    const int two = PAIRS && 2 * (int64_t)p.T > tokens ? 4 * TILE : 2 * TILE;
+    per_cta = max(p.min_stretch, two + item_cost - less);
     int64_t mine = 0, mine_s = 0;  // this thread's requests: cost, and stretches of per_cta
     // (both asked for at once)
     const int cu0 = tid == 0 ? p.cu[0] : 0, cuB = tid == 0 ? p.cu[p.B] : 0;
@@ -122,7 +136,7 @@ struct PagedSched {
       const int kvl = p.kv_lens[i];
       if (blockIdx.x == 0 && (kvl < 0 || (int64_t)kvl > (int64_t)p.max_pages * p.page_size))
         raise_error(p.err, ERR_BAD_LEN);
-      const int64_t c = paged_head_cost(q, tokens, p.causal, item_cost);
+      const int64_t c = head_cost(q, p.causal);
       mine += c * heads;
       mine_s += q.n > tokens ? 1ll << 32  // several items: not apart
                              : paged_div(c - less + per_cta - 1, per_cta) * heads;
@@ -156,7 +170,7 @@ struct PagedSched {
       item_cost -= less;
       before = before_s * per_cta, mine = mine_s * per_cta, total = total_s * per_cta;
     } else {
-      per_cta = max(max(per_cta, (int64_t)2 * TILE + item_cost),
+      per_cta = max(max(per_cta, (int64_t)two + item_cost),
                     paged_div(total * times + gridDim.x - 1, gridDim.x));
     }
     pos = blockIdx.x * per_cta;
@@ -170,7 +184,7 @@ struct PagedSched {
       int i = b0;
       for (; i + 1 < b1; ++i) {  // (the last one is at hand)
         const PagedReq x = paged_request(p, i, tokens);
-        const int64_t c = stride(paged_head_cost(x, tokens, p.causal, item_cost)) * heads;
+        const int64_t c = stride(head_cost(x, p.causal)) * heads;
         if (pos < at + c) {
           q = x;
           break;
@@ -193,12 +207,12 @@ struct PagedSched {
   // that brings more tokens than it has keys (their cost does not follow the
   // keys they see) are left whole.
   static __device__ __forceinline__ int cut(int64_t x, int64_t cost, int tiles, bool whole,
-                                            int item_cost) {
+                                            int item_cost, int weight) {
     if (x <= 0) return 0;
     if (x >= cost) return tiles;
     if (whole) return 0;
-    const int64_t k = x - item_cost + TILE / 2;
-    return k <= 0 ? 0 : (int)min((int64_t)tiles, k / TILE);
+    const int64_t k = x - item_cost + weight * (TILE / 2);
+    return k <= 0 ? 0 : (int)min((int64_t)tiles, (weight == 2 ? k >> 1 : k) / TILE);
   }
 
   // The next piece of the stretch (n = 0 when there is none).
@@ -206,8 +220,9 @@ struct PagedSched {
     PagedPiece o;
     o.n = 0;
     while (pos < end) {
-      const int64_t head_cost = stride(paged_head_cost(r, tokens, p.causal, item_cost));
-      const int64_t all_cost = BY_HEAD ? head_cost : head_cost * p.Hkv;
+      const int64_t one_head = stride(head_cost(r, p.causal));
+      const int64_t all_cost = BY_HEAD ? one_head : one_head * p.Hkv;
+      const int of = weight(r);
       if (pos >= base + all_cost) {  // on to the next request with work
         base += all_cost;
         if (++b >= p.B) {
@@ -220,15 +235,15 @@ struct PagedSched {
         r = paged_request(p, b, tokens);
         continue;
       }
-      const int at_head = BY_HEAD ? 0 : (int)paged_div(pos - base, head_cost);
-      const int64_t head_base = base + at_head * head_cost;
+      const int at_head = BY_HEAD ? 0 : (int)paged_div(pos - base, one_head);
+      const int64_t head_base = base + at_head * one_head;
       int lo = 0, hi = r.runs - 1;  // largest run that starts at or before pos
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (head_base + paged_prefix(r, mid, tokens, p.causal, item_cost) <= pos) lo = mid; else hi = mid - 1;
+        if (head_base + prefix(r, mid, p.causal) <= pos) lo = mid; else hi = mid - 1;
       }
-      const int64_t start = head_base + paged_prefix(r, lo, tokens, p.causal, item_cost);
-      const int64_t cost = head_base + paged_prefix(r, lo + 1, tokens, p.causal, item_cost) - start;
+      const int64_t start = head_base + prefix(r, lo, p.causal);
+      const int64_t cost = head_base + prefix(r, lo + 1, p.causal) - start;
       const int64_t stop = min(end, start + cost);
       o.n = min(tokens, r.n - lo * tokens);
       o.tok0 = r.tok0 + lo * tokens;
@@ -240,8 +255,8 @@ struct PagedSched {
       const int tiles = (keys + TILE - 1) / TILE;
       const bool whole = p.causal && r.kv < r.n;
       const bool starts = pos == start;
-      o.tile0 = cut(pos - start, cost, tiles, whole, item_cost);
-      o.tile1 = cut(stop - start, cost, tiles, whole, item_cost);
+      o.tile0 = cut(pos - start, cost, tiles, whole, item_cost, of);
+      o.tile1 = cut(stop - start, cost, tiles, whole, item_cost, of);
       o.n_pieces = o.index = o.first_cta = o.first_slot = 0;
       pos = apart ? end : stop;
       const int64_t cta = blockIdx.x;
@@ -251,8 +266,8 @@ struct PagedSched {
         // an item without keys belongs to the CTA it starts in
         if (tiles == 0 ? !starts : o.tile0 == o.tile1) continue;
         // only the first and the last stretch can be left without a tile
-        const bool skip0 = cut((c0 + 1) * per_cta - start, cost, tiles, whole, item_cost) == 0;
-        const bool skip1 = cut(c1 * per_cta - start, cost, tiles, whole, item_cost) == tiles;
+        const bool skip0 = cut((c0 + 1) * per_cta - start, cost, tiles, whole, item_cost, of) == 0;
+        const bool skip1 = cut(c1 * per_cta - start, cost, tiles, whole, item_cost, of) == tiles;
         const int n = (int)(c1 - c0) + 1 - skip0 - skip1;
         if (tiles > 0 && !whole && n > 1) {
           o.n_pieces = n;
