@@ -177,7 +177,10 @@ kda_status attn(const void *q, const void *k_pages, const void *v_pages, const f
   // register products, in items of 16 rows.  (64 requests over 1000 to 9000 keys, 32 / 8
   // heads, against the tensor-core kernel: 4 to 16 rows 85 to 86 and 141 to 144 us with 64
   // channels, 125 to 128 and 194 to 199 us with 128; items of 32 rows, 20 to 32 of them, 149 to
-  // 151 and 145 us, 224 and 199 us.)
+  // 151 and 145 us, 224 and 199 us.  256 decodes over 4000 keys beside a chunk of 512 tokens
+  // over 8000 or 32000: 660 and 611, 1560 and 725 us.  Both kernels one behind the other, with
+  // the requests shared out between them: 466 and 605 us, but 6 to 12 us for the empty one where
+  // all requests are alike, and 5% of the tiles' speed for the scheduler that passes over them.)
   const bool decode = q8 && a->dtype == KDA_BF16 && G <= 16 && (int64_t)a->T_total * G <= 16ll * a->B;
   p.part_rows = kda::paged_part_rows(a->T_total, G, decode ? (int32_t)KDA_F32 : a->dtype);
   // What an item's start and end cost, and the shortest stretch worth a join, in

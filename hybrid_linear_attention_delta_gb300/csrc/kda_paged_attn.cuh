@@ -54,8 +54,8 @@
 //     the scaled weights, so O / sum holds whatever the scales.
 //   * Two warps load, one the keys and one the values; the registers go to the softmax
 //     (200 a thread, 56 for the others).
-// The chunk of above takes 2.70 ms, 1.42 PFLOP/s, 64 x 8 tokens 0.258 ms, 4.3 TB/s, the
-// mixed batch of 24 1.02 ms.  The products take as long as the 16-bit cache's; a softmax
+// The chunk of above takes 2.67 ms, 1.44 PFLOP/s, 64 x 8 tokens 0.254 ms, 4.4 TB/s, the
+// mixed batch of 24 1.03 ms.  The products take as long as the 16-bit cache's; a softmax
 // has the scales' exponents and sums besides, and a tile of values is read, written and read
 // again in shared memory on its way.  What bounds it is the chain of a tile, no pipe (chunk:
 // tensor 59% busy, issue 39%; mixed batch 31% and 46%; 64 x 8 tokens 39% and 25%).
@@ -139,7 +139,7 @@ struct Ctl {
   uint64_t q_raw;                  // Q8: the queries before they are converted
   Work work[kPieces];
   float ml[kRows][2];    // stream 1's references and sums when the streams are joined
-  int64_t scratch[kThreads<true> / 16 + 4];
+  int64_t scratch[kThreads<true> / 16 + 5];
   uint32_t tmem;
   int32_t last[2];
   int32_t gave_up[2];  // a warp of the stream gave up a wait

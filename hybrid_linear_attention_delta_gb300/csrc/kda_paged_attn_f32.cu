@@ -40,7 +40,7 @@ struct Smem {
   float p[kRows * kLdP];
   float c[kKeys / kScaleTokens];  // Q8: 0, or -inf for blocks that are left out
   PagedPiece piece;
-  int64_t scratch[kThreads / 16 + 4];
+  int64_t scratch[kThreads / 16 + 5];
   int last;
 };
 

@@ -60,7 +60,7 @@ struct Smem {
   float sum[kRows][D];  // runs before this one
   float ml[kWarps][kRows][2];
   PagedPiece piece[2];
-  int64_t scratch[kThreads / 16 + 4];
+  int64_t scratch[kThreads / 16 + 5];
   int last;
 };
 

@@ -90,7 +90,7 @@ struct PagedSched {
   bool apart;              // every item starts a stretch
   int64_t pos, end, base;  // place on the line, end of the stretch, start of request b
   int64_t per_cta;
-  int32_t b, head;         // head: BY_HEAD, the one that pos is in
+  int32_t b, head, n_req;  // BY_HEAD: the head that pos is in, requests up to the last with work
   PagedReq r;
 
   // What an item of the request and one head takes of the line.
@@ -108,7 +108,7 @@ struct PagedSched {
     return prefix(q, q.runs, causal);
   }
 
-  // All threads of the CTA; scratch: THREADS / 16 + 4 words of 64 bits.  False:
+  // All threads of the CTA; scratch: THREADS / 16 + 5 words of 64 bits.  False:
   // bad cu_seqlens (nothing is to be done).
   template <int THREADS>
   __device__ bool init(const PagedAttnPlan &p, int tokens_per_item, int64_t *scratch) {
@@ -129,6 +129,7 @@ struct PagedSched {
     // (both asked for at once)
     const int cu0 = tid == 0 ? p.cu[0] : 0, cuB = tid == 0 ? p.cu[p.B] : 0;
     bool bad = false;
+    int last = 0;
     PagedReq q = {0, 0, 0, 0};
     for (int i = b0; i < b1; ++i) {
       bad |= p.cu[i + 1] < p.cu[i];
@@ -137,6 +138,7 @@ struct PagedSched {
       if (blockIdx.x == 0 && (kvl < 0 || (int64_t)kvl > (int64_t)p.max_pages * p.page_size))
         raise_error(p.err, ERR_BAD_LEN);
       const int64_t c = head_cost(q, p.causal);
+      if (q.runs > 0) last = i + 1;
       mine += c * heads;
       mine_s += q.n > tokens ? 1ll << 32  // several items: not apart
                              : paged_div(c - less + per_cta - 1, per_cta) * heads;
@@ -176,6 +178,8 @@ struct PagedSched {
     pos = blockIdx.x * per_cta;
     end = min(total * times, pos + per_cta);
     if constexpr (BY_HEAD) {
+      // (a padded batch's empty requests are passed over at once, not head by head)
+      if (mine > 0 && before + mine == total) scratch[2 * W + 4] = last;
       head = pos < end ? (int32_t)paged_div(pos, total) : 0;
       before += head * total;
     }
@@ -198,6 +202,7 @@ struct PagedSched {
     __syncthreads();
     b = (int32_t)scratch[2 * W];
     base = scratch[2 * W + 1];
+    if constexpr (BY_HEAD) n_req = (int32_t)scratch[2 * W + 4];
     if (b < 0) pos = end = 0;
     else r = reinterpret_cast<PagedReq *>(scratch)[W + 1];
     return true;
@@ -225,12 +230,25 @@ struct PagedSched {
       const int of = weight(r);
       if (pos >= base + all_cost) {  // on to the next request with work
         base += all_cost;
-        if (++b >= p.B) {
+        if (++b >= (BY_HEAD ? n_req : p.B)) {
           if (!BY_HEAD || ++head >= p.Hkv) {
             pos = end;
             break;
           }
           b = 0;
+        }
+        // Past requests without tokens; the last has some.  (10 decodes, 500 requests without
+        // and 40 tokens: 57 us, one by one 184.  The kernel of tiles, whose loading warp has no
+        // registers for it, goes one by one: 64 x 8 tokens 254 us, with this 268.)
+        if constexpr (BY_HEAD && !PAIRS) {
+          const int32_t at = p.cu[b];
+          if (p.cu[b + 1] == at) {
+            int32_t hi = n_req - 1;
+            while (b < hi) {
+              const int32_t mid = (b + hi) >> 1;
+              if (p.cu[mid + 1] == at) b = mid + 1; else hi = mid;
+            }
+          }
         }
         r = paged_request(p, b, tokens);
         continue;

@@ -273,6 +273,9 @@ kda_status kda_paged_append_q8(const void *qkv, const int32_t *positions, const 
  * finite.  In bf16 a row's largest channel keeps all its bits from 2^-119 up, and keys count
  * down to 2^-30 of a row's largest product of weight and scale of the values.  scale * q . k
  * must be finite with the keys' scales.
+ * Which kernel runs is decided by the mean number of new tokens: a chunk of a prompt
+ * among hundreds of decodes, with less than 16 rows (tokens times Hq / Hkv) a request
+ * on average, is better a call of its own.
  */
 kda_status kda_paged_attn_q8(const void *q, const void *k_pages, const void *v_pages,
                              const float *k_scales, const float *v_scales,
