@@ -52,10 +52,9 @@
 //   * Scales: the keys' multiply the scores, the values' the weights, as exponents:
 //     P = 2^(c ks S + log2 vs - m); the row's sum takes P / vs.  The reference m is that of
 //     the scaled weights, so O / sum holds whatever the scales.
-//   * Two warps load, one the keys and one the values; the registers go to the softmax
-//     (200 a thread, 56 for the others).
+//   * Two warps load, one the keys and one the values; the registers go to the softmax.
 // The chunk of above takes 2.67 ms, 1.44 PFLOP/s, 64 x 8 tokens 0.254 ms, 4.4 TB/s, the
-// mixed batch of 24 1.03 ms.  The products take as long as the 16-bit cache's; a softmax
+// mixed batch of 24 1.00 ms.  The products take as long as the 16-bit cache's; a softmax
 // has the scales' exponents and sums besides, and a tile of values is read, written and read
 // again in shared memory on its way.  What bounds it is the chain of a tile, no pipe (chunk:
 // tensor 59% busy, issue 39%; mixed batch 31% and 46%; 64 x 8 tokens 39% and 25%).
@@ -1679,11 +1678,14 @@ attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
 
   // a softmax thread holds a row of 128 scores: registers go from the last
   // warpgroup to the other two (168 a thread at the launch, 2 * 216 + 72 = 3 * 168; Q8:
-  // 128, 2 * 200 + 2 * 56 = 4 * 128)
+  // 128, 2 * 200 + 2 * 56 or 2 * 208 + 2 * 48 = 4 * 128.  192 and 64, 200 and 56, 208 and 48, 216
+  // and 40: mixed batch of 24, 64 channels, 1037, 1033, 995, 1124 us; with 128 1460, 1369, 1389,
+  // 1622, 64 x 8 tokens 265, 256, 268, 335, a chunk 2.83, 2.68, 2.65, 3.25 ms.)
   bool ok = true;
   if (!work) {  // bad cu_seqlens
   } else if (warp < kSoftmaxWarps) {
-    if constexpr (Q8) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    if constexpr (Q8 && D == 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    else if constexpr (Q8) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     ok = softmax_role<D, LONG, Q8>(ctl, a, tmem, warp >> 2);
     if (!ok) {
@@ -1696,7 +1698,8 @@ attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
       named_bar_arrive(1 + (warp >> 2), 128);
     }
   } else {
-    if constexpr (Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if constexpr (Q8 && D == 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    else if constexpr (Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp < kLoadWarp) {
       if constexpr (Q8) ok = mma_role_q8<D>(sbase, ctl, tmem, warp - kMmaWarp);
