@@ -57,7 +57,7 @@
 // mixed batch of 24 1.00 ms.  The products take as long as the 16-bit cache's; a softmax
 // has the scales' exponents and sums besides, and a tile of values is read, written and read
 // again in shared memory on its way.  What bounds it is the chain of a tile, no pipe (chunk:
-// tensor 59% busy, issue 39%; mixed batch 31% and 46%; 64 x 8 tokens 39% and 25%).
+// tensor 59% busy, issue 40%; mixed batch 33% and 49%; 64 x 8 tokens 46% and 28%).
 #pragma once
 
 #include <cuda.h>
