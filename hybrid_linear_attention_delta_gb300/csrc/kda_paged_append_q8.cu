@@ -191,10 +191,57 @@ __device__ __forceinline__ void store_e4m3(uint8_t *head, const Place &c, const 
   }
 }
 
+// A warp's runs (units u, u + step, ... below n_kv) once more, those into blocks whose old
+// scale is no power of two.  The append makes none, and stores products with the inverse,
+// which may lie on the other side of a border between two e4m3 values than x / s; here the
+// rows are read and stored again as quotients.  A function of its own, called at the end, so
+// that it holds no registers above (within the loop over the units: 16000 tokens 124 -> 130 us).
+template <typename T, int D, bool HALVES>
+__device__ __noinline__ void store_quotients(const AppendPlan &p, const int32_t *s_start,
+                                             const int32_t *s_slot, const int32_t *s_pos, int n_kv,
+                                             int64_t t0) {
+  constexpr int N = kVec<T>, LPH = D / N, HPP = 32 / LPH;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPH, sub = lane / LPH;
+  const Place c = place<T, HALVES>(l, p.rot);
+  const int64_t row = (int64_t)(p.Hq + 2 * p.Hkv) * D, step = (int64_t)p.Hkv * D;
+  const T *qkv = static_cast<const T *>(p.qkv) + t0 * row;
+#pragma unroll 1
+  for (int u = blockIdx.y * kWarps + warp; u < n_kv; u += gridDim.y * kWarps) {
+    const int i = s_start[u / (2 * p.Hkv)], h = u % (2 * p.Hkv);
+    const bool is_v = h >= p.Hkv;
+    const int head = is_v ? h - p.Hkv : h;
+    const int block = s_slot[i] / kScaleTokens;
+    const float *scale = (is_v ? p.v_scales : p.k_scales) + (int64_t)block * p.Hkv + head;
+    const float s = __shfl_sync(0xffffffffu, lane == 0 ? *scale : 0.f, 0);  // (which wrote it)
+    if ((__float_as_uint(s) & 0x7fffffu) == 0) continue;
+    const int near = lane < kScaleTokens ? s_slot[i + lane] : -1;
+    const uint32_t run = __ballot_sync(0xffffffffu, near >= 0 && near / kScaleTokens == block);
+    const T *src = qkv + i * row + (int64_t)(p.Hq + h) * D;
+    uint8_t *dst = static_cast<uint8_t *>(is_v ? p.v_pages : p.k_pages) +
+                   ((int64_t)block * kScaleTokens * p.Hkv + head) * D;
+    Lane<T> of;
+    if (!is_v) load_norm(of, p.k_norm, c);
+#pragma unroll 1
+    for (int r = sub; r - sub < kScaleTokens; r += HPP) {
+      const bool real = run >> r & 1;
+      float y[N];
+      unpack<T>(real ? load_row<T, HALVES>(src + r * row, c) : make_uint4(0, 0, 0, 0), y);
+      if (!is_v) {
+        load_rope(of, p.rope + (int64_t)s_pos[real ? i + r : i] * p.rot, c, l, p.rot);
+        turn<T, D, HALVES>(y, c, of, p.k_norm, p.eps);
+      }
+#pragma unroll
+      for (int j = 0; j < N; ++j) y[j] = quotient_for_e4m3(y[j], s);
+      if (real) store_e4m3<T, HALVES>(dst + s_slot[i + r] % kScaleTokens * step, c, y, 1.f);
+    }
+  }
+}
+
 // rows: rows of a CTA (at most kMaxRows); grid y shares out their units.  ROWS: a unit of
 // queries is a whole row.
 template <typename T, int D, bool HALVES, bool ROWS>
-__global__ void __launch_bounds__(kThreads, ROWS ? 3 : 2) append_kernel(AppendPlan p, int rows) {
+__global__ void __launch_bounds__(kThreads, ROWS ? 3 : 2)
+append_kernel(const __grid_constant__ AppendPlan p, int rows) {
   constexpr int N = kVec<T>;
   constexpr int LPH = D / N;     // lanes of a head
   constexpr int HPP = 32 / LPH;  // rows (or heads) of a pass
@@ -249,6 +296,7 @@ __global__ void __launch_bounds__(kThreads, ROWS ? 3 : 2) append_kernel(AppendPl
   const T *qkv = static_cast<const T *>(p.qkv) + t0 * row;
   const int n_kv = s_n[0] * 2 * p.Hkv, nq = ROWS ? 1 : (p.Hq + kBatch * HPP - 1) / (kBatch * HPP);
   const int units = n_kv + s_n[1] * nq;
+  bool fractions = false;  // an old scale of this warp's runs is no power of two
   for (int u = blockIdx.y * kWarps + warp; u < units; u += gridDim.y * kWarps) {
     if (u < n_kv) {  // a run's keys or values of one head
       const int i = s_start[u / (2 * p.Hkv)], h = u % (2 * p.Hkv);
@@ -271,6 +319,7 @@ __global__ void __launch_bounds__(kThreads, ROWS ? 3 : 2) append_kernel(AppendPl
       float held = 0.f, old = 0.f;
       if (off > 0) {
         old = held = *scale;
+        fractions |= (__float_as_uint(old) & 0x7fffffu) != 0;
         if (!good_scale(old)) {
           if (lane == 0) raise_error(p.err, ERR_BAD_SCALE);
           old = kMinScale;
@@ -309,12 +358,14 @@ __global__ void __launch_bounds__(kThreads, ROWS ? 3 : 2) append_kernel(AppendPl
                      ((int64_t)block * kScaleTokens * p.Hkv + head) * D;
       const int64_t step = (int64_t)p.Hkv * D;
       if (off > 0 && s > old) {  // what the block holds, rounded again: 4 bytes a lane
-        const float ratio = old / s;
+        const float ratio = old / s;  // (s is a power of two here)
         for (int e = lane; e < off * (D / 4); e += 32) {
           uint32_t *w = reinterpret_cast<uint32_t *>(dst + e / (D / 4) * step + e % (D / 4) * 4);
           float z[4];
           e4m3_to_f32(*w, z);
-          *w = f32_to_e4m3(z[0] * ratio, z[1] * ratio, z[2] * ratio, z[3] * ratio);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) z[j] = product_for_e4m3(z[j], ratio);
+          *w = f32_to_e4m3(z[0], z[1], z[2], z[3]);
         }
       }
       if (lane == 0 && (off == 0 || s != held)) *scale = s;
@@ -364,6 +415,7 @@ __global__ void __launch_bounds__(kThreads, ROWS ? 3 : 2) append_kernel(AppendPl
       }
     }
   }
+  if (fractions) store_quotients<T, D, HALVES>(p, s_start, s_slot, s_pos, n_kv, t0);
 }
 
 template <typename T, int D, bool HALVES>

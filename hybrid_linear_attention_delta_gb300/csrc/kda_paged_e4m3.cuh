@@ -60,6 +60,25 @@ __device__ __forceinline__ uint32_t f32_to_e4m3(float a, float b, float c, float
   return lo | hi << 16;
 }
 
+// A value that is rounded to 8 bits as the exact result is: x is it rounded to fp32, rest
+// has the sign of what is missing (0: nothing).  Of the two fp32 neighbours of an inexact
+// result this is the one whose last bit is 1, which is neither an e4m3 value nor half way
+// between two; rounded to nearest, results beside a half would become it.  (Values outside
+// these bounds become 0 or 448 either way.)
+__device__ __forceinline__ float odd_neighbour(float x, float rest) {
+  const uint32_t b = __float_as_uint(x);
+  const bool inexact = rest != 0.f && fabsf(x) > 0x1p-12f && fabsf(x) < 1024.f;
+  return !inexact || (b & 1u) ? x : __uint_as_float((rest > 0.f) == (x > 0.f) ? b + 1u : b - 1u);
+}
+__device__ __forceinline__ float product_for_e4m3(float a, float b) {
+  const float x = a * b;
+  return odd_neighbour(x, fmaf(a, b, -x));
+}
+__device__ __forceinline__ float quotient_for_e4m3(float a, float b) {  // b > 0
+  const float x = a / b;
+  return odd_neighbour(x, fmaf(-x, b, a));
+}
+
 // The smallest power of two p with amax <= 448 p (448 = 1.75 * 2^8), within the
 // scales' bounds.
 __device__ __forceinline__ float scale_for(float amax) {

@@ -705,6 +705,60 @@ def test_append_old_scales_outside_their_range(bad):
         assert float(scales[i][2, 0, 0]) == float(scale_for(x[2].abs().max()))
 
 
+def _borders(d, ties):
+    """d numbers between two neighbouring e4m3 values each (ties), from 2^-10 to 2^7."""
+    at = torch.arange(d)
+    e = (at // 8 % 16 - 8).double()
+    x = (8 + at % 8 + (0.5 if ties else 0.0)) / 8 * torch.exp2(e)
+    low = (at % 8 + 8 * (e + 8) + 0.5) * 2.0 ** -9      # below 2^-6 the grid is even
+    return torch.where(e < -6, low, x)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_append_into_scales_that_are_no_powers_of_two(kind, d):
+    """A continued block may have any scale: new values that lie on a border between two
+    e4m3 values when divided by it, or (fp32) next to one, are stored as the exact
+    quotient's rounding."""
+    g = torch.Generator().manual_seed(d)
+    Hkv, page, n = 2, 16, 128                  # a block each
+    cache = Cache(n, page, Hkv, d, g)
+    m = torch.arange(128, 256).double() / 128 if kind == "bf16" else 1 + torch.rand(128, generator=g).double()
+    tokens = 3
+    slots = (torch.arange(n)[:, None] * page + torch.tensor([3, 4, 5])).flatten()
+    qkv = torch.zeros((n * tokens, 3 * Hkv, d), dtype=DT[kind])
+    for i in range(2):
+        scale = torch.stack([m[torch.randperm(128, generator=g)] * 2.0 ** (3 * h - 4 + i) for h in range(Hkv)], 1)
+        cache.scales[i][:, 0] = scale.float()
+        x = (cache.scales[i][:, 0].double()[..., None] * _borders(d, True)).to(DT[kind])
+        off = x, torch.nextafter(x.float(), torch.tensor(1e9)), torch.nextafter(x.float(), torch.tensor(0.0))
+        for k in range(tokens):
+            qkv[k::tokens, (1 + i) * Hkv:(2 + i) * Hkv] = off[k].to(DT[kind])
+    _check_append(cache, qkv, slots, Hkv, Hkv, kind)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_append_grows_scales_that_are_no_powers_of_two(kind):
+    """Old scales whose products with an e4m3 value lie next to a border between two
+    others, nearer than an fp32 product tells: rounded again as the exact product."""
+    g = torch.Generator().manual_seed(8)
+    Hkv, d, page = 2, 64, 16
+    odd = torch.arange(17, 32, 2).double()
+    scales = torch.cat([torch.round(odd * 2.0 ** 23 / y) + o for y in (9.0, 11.0, 13.0, 15.0) for o in (-1, 0, 1)])
+    scales = scales[(scales >= 2.0 ** 23) & (scales < 2.0 ** 24)] * 2.0 ** -23
+    n = len(scales)
+    cache = Cache(n, page, Hkv, d, g)
+    for i in range(2):
+        byte = torch.randint(0, 127, (n, page, Hkv, d), generator=g) + 128 * torch.randint(0, 2, (n, page, Hkv, d), generator=g)
+        cache.pages[i] = byte.to(torch.uint8).view(E4M3)
+        for h in range(Hkv):
+            cache.scales[i][:, 0, h] = scales[torch.randperm(n, generator=g)].float()
+    slots = torch.arange(n) * page + 15
+    qkv = torch.randn((n, 3 * Hkv, d), generator=g)
+    qkv[..., 7] = (448 * torch.exp2(1 + torch.arange(n) % 3))[:, None]     # grows to 2, 4 or 8
+    _check_append(cache, qkv.to(DT[kind]), slots, Hkv, Hkv, kind)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
 def test_append_beyond_32_bit_offsets(kind):
     """A pool and a batch of more than 2^31 elements."""
