@@ -578,6 +578,20 @@ def test_append_shapes(kind, lengths, Hq, Hkv, d, page):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [4863, 4865, 9727, 9729, 65700])
+def test_append_long_prompts(kind, T):
+    """Lengths on either side of those where rows and units of a CTA change."""
+    g = torch.Generator().manual_seed(T)
+    lengths = [T // 3, 1, 17, T - T // 3 - 18]
+    n_pages = sum(-(-n // 128) + 1 for n in lengths)
+    slots = _runs(lengths, 128, g, n_pages)
+    qkv = torch.randn((T, 4, 64), generator=g).to(DT[kind])
+    _check_append(Cache(n_pages, 128, 1, 64, g), qkv, slots, 2, 1, kind, q_norm=torch.ones(64),
+                  rope=kda.rope_table(64, 32, device="cpu"),
+                  positions=torch.randint(0, 64, (T,), generator=g).int())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
 def test_append_magnitudes(kind):
     """Blocks that outgrow their scale by anything, blocks far below it, zeros, values
     at the borders of a scale, values beyond the largest and below the smallest scale."""
