@@ -238,8 +238,9 @@ kda_status kda_verify_drafts(const void *target_probs, const void *draft_probs,
  * kda_paged_plan serves it as it is.  Scales are in [2^-50, 2^50]; where a call
  * needs one that is not, bit 8192 is raised.
  *
- * kda_paged_append with an 8-bit cache.  Norm, rotation and q_out are those of
- * kda_paged_append.  A block's scale is
+ * kda_paged_append with an 8-bit cache.  Norm, rotation and q_out have the formulas of
+ * kda_paged_append; computed in another order, q_out agrees with that call's to fp32's
+ * rounding, not to the bit.  A block's scale is
  *
  *     s = max(old, p),  p the smallest power of two in [2^-50, 2^50] with max|x| <= 448 p
  *

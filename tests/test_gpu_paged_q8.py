@@ -802,6 +802,32 @@ def test_append_beyond_32_bit_offsets(kind):
         assert not pages[i][:-1].view(torch.uint8).any()
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("mode", ["half", "interleaved"])
+def test_queries_of_both_appends(kind, d, mode):
+    """q_out of the 8-bit append and of the other: the same formula, each with fp32's
+    errors (as in _check_append) and one rounding."""
+    g = torch.Generator().manual_seed(d)
+    Hq, Hkv, T, rot = 6, 2, 90, 48
+    qkv = torch.randn((T, Hq + 2 * Hkv, d), generator=g).to(DT[kind])
+    slots, pos = torch.arange(16, 16 + T), torch.randint(0, 500, (T,), generator=g).int()
+    norms = [1 + 0.1 * torch.randn(d, generator=g) for _ in range(2)]
+    rope = kda.rope_table(500, rot, device="cpu")
+    q, *_ = _append(Cache(8, 16, Hkv, d, g), qkv, slots, Hq, Hkv, q_norm=norms[0], k_norm=norms[1],
+                    rope=rope, positions=pos, mode=mode)
+    pages = [torch.zeros((8, 16, Hkv, d), dtype=DT[kind], device="cuda") for _ in range(2)]
+    other = torch.empty((T, Hq, d), dtype=DT[kind], device="cuda")
+    ws = kda.paged_workspace_for()
+    kda.kda_paged_append(qkv.cuda(), norms[0].cuda(), norms[1].cuda(), rope.cuda(), pos.cuda(),
+                         slots.int().cuda(), other, *pages, rope_mode=mode, workspace=ws)
+    assert kda.kda_device_status(ws) == (kda.KDA_OK, 0)
+    (ref, size), _, _ = append_reference(qkv, *norms, rope, pos, Hq, Hkv, mode, 1e-6)
+    u, half = half_step(F32), half_step(DT[kind])
+    off = 2 * (half * ref.abs() * 1.01 + (d + 16) * u * size * 2) + 1e-30
+    assert ((q.double() - other.double().cpu()).abs() <= off).all()
+
+
 def test_append_zero_tokens():
     g = torch.Generator().manual_seed(5)
     cache = Cache(2, 16, 1, 64, g)
