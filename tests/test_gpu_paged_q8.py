@@ -333,6 +333,45 @@ def test_sums_over_millions_of_keys(d, Hkv, G, B, T, lg):
     assert float(err.norm() / ref.norm()) <= TOL["bf16"]
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_sums_of_few_rows_over_millions_of_keys(d):
+    """A token a request over some 2^23 keys, the same sixteen pages again and again: pieces
+    of more than 2^19 keys, whose sums are put aside on the way, and lengths that end each of
+    a CTA's warps at another step."""
+    g = torch.Generator(device="cuda").manual_seed(d)
+    page, n_pages, Hkv, G, B = 256, 16, 2, 4, 20
+    period = page * n_pages
+    kv = [(1 << 23) + 16 * 5 * b + b % 7 for b in range(B)]
+    k8 = (64 * torch.randn((n_pages, page, Hkv, d), generator=g, device="cuda")).clamp(-448, 448).to(E4M3)
+    v8 = (32 * torch.rand((n_pages, page, Hkv, d), generator=g, device="cuda") + 16).to(E4M3)
+    scales = torch.full((n_pages, page // BLOCK, Hkv), 2.0 ** -6, device="cuda")
+    q = torch.randn((B, Hkv * G, d), generator=g, device="cuda").bfloat16()
+    table = (torch.arange(-(-max(kv) // page), device="cuda") % n_pages).int().repeat(B, 1)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    t = dict(q=q, k8=k8, v8=v8, k_scales=scales, v_scales=scales, table=table,
+             cu=i32(list(range(B + 1))), kv=i32(kv))
+    ws = kda.paged_workspace_for(B, Hkv * G, Hkv, d)
+    outs = [torch.zeros_like(q) for _ in range(2)]
+    for out in outs:
+        _call(t, out, ws)
+        assert kda.kda_device_status(ws) == (kda.KDA_OK, 0)
+    assert torch.equal(*outs)
+    # how often a request sees each of the keys
+    at = torch.arange(period, device="cuda")
+    often = torch.stack([(n // period + (at < n % period)).double() for n in kv])
+    ref = torch.empty(q.shape, dtype=torch.float64, device="cuda")
+    for h in range(Hkv * G):
+        K, W = (x[:, :, h // G].flatten(0, 1).double() * 2.0 ** -6 for x in (k8, v8))
+        s = q[:, h].double() @ K.T * d ** -0.5
+        w = often * torch.exp(s - s.amax(-1, keepdim=True))
+        ref[:, h] = w @ W / w.sum(-1, keepdim=True)
+    # Weights (2^-11) and outputs (2^-8) are rounded once; a run of 8192 additions, each off
+    # by at most 2^-23 (products) or 2^-24 (weights) of its sum.
+    err = (outs[0].double() - ref).abs()
+    assert (err <= ref.abs() * (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -10 + 2.0 ** -11) * 1.01).all()
+    assert float(err.norm() / ref.norm()) <= TOL["bf16"]
+
+
 def test_captured_graphs_share_a_workspace_and_follow_the_lengths():
     cases = [Q8AttnCase([1, 1], [900, 300], Hq=8, Hkv=2, d=128, page=16, dtype="bf16", seed=1),
              Q8AttnCase([40, 9], [140, 2000], Hq=8, Hkv=2, d=128, page=32, dtype="bf16", seed=2)]
