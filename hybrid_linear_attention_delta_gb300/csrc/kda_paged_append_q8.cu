@@ -223,6 +223,7 @@ __device__ __noinline__ void store_quotients(const AppendPlan &p, const int32_t 
     if (!is_v) load_norm(of, p.k_norm, c);
 #pragma unroll 1
     for (int r = sub; r - sub < kScaleTokens; r += HPP) {
+      if (!(run >> (r - sub) & ((1u << HPP) - 1u))) continue;
       const bool real = run >> r & 1;
       float y[N];
       unpack<T>(real ? load_row<T, HALVES>(src + r * row, c) : make_uint4(0, 0, 0, 0), y);
