@@ -20,6 +20,7 @@ enum PagedErrBits : uint32_t {
 };
 
 constexpr int kMaxRequests = 8192;
+constexpr int kScaleTokens = 16;  // tokens of a scale of the 8-bit cache
 
 struct PagedPlanArgs {
   const int32_t *cu, *cached, *held, *ring;

@@ -12,8 +12,6 @@ bool aligned(const void *p, uintptr_t n) { return p && (reinterpret_cast<uintptr
 
 int64_t elem_bytes(int32_t dtype) { return dtype == KDA_F32 ? 4 : 2; }
 
-constexpr int kScaleTokens = 16;  // tokens of a scale of the 8-bit cache
-
 kda_status check_workspace(const void *ws, size_t bytes, size_t need) {
   return aligned(ws, 256) && bytes >= need ? KDA_OK : KDA_ERR_INVALID_ARG;
 }
@@ -105,7 +103,7 @@ kda_status append(const void *qkv, const int32_t *positions, const int32_t *slot
   const int64_t row = (int64_t)a->d * elem_bytes(a->dtype), T = a->T_total;
   const int64_t slots = (int64_t)a->n_pages * a->page_size;
   const int64_t pool = slots * a->Hkv * (q8 ? a->d : row);
-  const int64_t scales = q8 ? slots / kScaleTokens * a->Hkv * 4 : 0;
+  const int64_t scales = q8 ? slots / kda::kScaleTokens * a->Hkv * 4 : 0;
   if (overlap({{q_out, T * a->Hq * row}, {k_pages, pool}, {v_pages, pool}, {a->workspace, 256},
                {k_scales, scales}, {v_scales, scales},
                {qkv, T * (a->Hq + 2 * a->Hkv) * row}, {slot_map, T * 4},
@@ -154,7 +152,7 @@ kda_status attn(const void *q, const void *k_pages, const void *v_pages, const f
   const int64_t row = (int64_t)a->d * elem_bytes(a->dtype), rows = row * a->T_total * a->Hq;
   const int64_t slots = (int64_t)a->n_pages * a->page_size;
   const int64_t pool = slots * a->Hkv * (q8 ? a->d : row);
-  const int64_t scales = q8 ? slots / kScaleTokens * a->Hkv * 4 : 0;
+  const int64_t scales = q8 ? slots / kda::kScaleTokens * a->Hkv * 4 : 0;
   if (overlap({{out, rows}, {a->workspace, (int64_t)lay.total}, {q, q == out ? 0 : rows},
                {k_pages, pool}, {v_pages, pool}, {block_table, 4ll * a->B * a->max_pages},
                {cu_seqlens, 4ll * a->B + 4}, {kv_lens, 4ll * a->B}, {k_scales, scales},

@@ -49,16 +49,9 @@ __device__ __forceinline__ Place place(int l, int rot) {
 template <typename T, bool HALVES>
 __device__ __forceinline__ uint4 load_row(const T *head, const Place &c) {
   if constexpr (HALVES) {
-    const T *a = head + c.a, *b = head + c.b;
-    if constexpr (sizeof(T) == 2) {
-      const uint2 u = __ldcs(reinterpret_cast<const uint2 *>(a));
-      const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(b));
-      return make_uint4(u.x, u.y, v.x, v.y);
-    } else {
-      const uint2 u = __ldcs(reinterpret_cast<const uint2 *>(a));
-      const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(b));
-      return make_uint4(u.x, u.y, v.x, v.y);
-    }
+    const uint2 u = __ldcs(reinterpret_cast<const uint2 *>(head + c.a));
+    const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(head + c.b));
+    return make_uint4(u.x, u.y, v.x, v.y);
   } else {
     return __ldcs(reinterpret_cast<const uint4 *>(head + c.a));
   }

@@ -82,13 +82,6 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// the two fp16 pairs of four e4m3 bytes
-__device__ __forceinline__ void widen(uint32_t w, uint32_t &lo, uint32_t &hi) {
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(w));
-}
 
 // Where 16 bytes of a step lie: chunk c of key k.  Swizzled so that the reads below, of
 // two keys' and of four even or odd values' chunks, fall into all banks.
@@ -316,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(PagedAttnPlan p, floa
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               uint32_t b0, b1;
-              widen(u[j], b0, b1);
+              e4m3_to_f16(u[j], b0, b1);
               mma(s[t], qf[4 * x + j], b0, b1);
             }
           }
@@ -383,8 +376,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(PagedAttnPlan p, floa
           for (int half = 0; half < 2; ++half) {
             const uint32_t sel = half ? 0x7362 : 0x5140;
             uint32_t b[2][2];
-            widen(__byte_perm(v[0][x], v[1][x], sel), b[0][0], b[1][0]);
-            widen(__byte_perm(v[2][x], v[3][x], sel), b[0][1], b[1][1]);
+            e4m3_to_f16(__byte_perm(v[0][x], v[1][x], sel), b[0][0], b[1][0]);
+            e4m3_to_f16(__byte_perm(v[2][x], v[3][x], sel), b[0][1], b[1][1]);
             mma(acc[4 * x + 2 * half], pf, b[0][0], b[0][1]);
             mma(acc[4 * x + 2 * half + 1], pf, b[1][0], b[1][1]);
           }

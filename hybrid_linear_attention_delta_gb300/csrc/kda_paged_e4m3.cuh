@@ -8,7 +8,6 @@
 
 namespace kda {
 
-constexpr int kScaleTokens = 16;  // tokens of a scale
 // Scales.  Within these bounds the largest ratio of two, 2^100, times any weight that
 // counts (2^-24 of the row's largest) is a normal float.
 constexpr float kMinScale = 0x1p-50f, kMaxScale = 0x1p50f;
@@ -44,14 +43,17 @@ __device__ __forceinline__ __half2 e4m3_to_f16(uint32_t w) {
 __device__ __forceinline__ uint32_t f16_to_e4m3(__half2 x) {
   return __nv_cvt_halfraw2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
 }
+// The two fp16 pairs of four values, and those of 16.
+__device__ __forceinline__ void e4m3_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
 __device__ __forceinline__ void e4m3_to_f16(const uint4 &w, uint32_t (&x)[8]) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-        : "=r"(x[2 * i]), "=r"(x[2 * i + 1])
-        : "r"(u[i]));
+  for (int i = 0; i < 4; ++i) e4m3_to_f16(u[i], x[2 * i], x[2 * i + 1]);
 }
 // Four values, rounded to nearest; beyond 448 they become 448.
 __device__ __forceinline__ uint32_t f32_to_e4m3(float a, float b, float c, float d) {
