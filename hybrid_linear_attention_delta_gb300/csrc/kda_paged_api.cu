@@ -176,7 +176,10 @@ kda_status attn(const void *q, const void *k_pages, const void *v_pages, const f
   // heads, against the tensor-core kernel: 4 to 16 rows 85 to 86 and 141 to 144 us with 64
   // channels, 125 to 128 and 194 to 199 us with 128; items of 32 rows, 20 to 32 of them, 149 to
   // 151 and 145 us, 224 and 199 us.  256 decodes over 4000 keys beside a chunk of 512 tokens
-  // over 8000 or 32000: 660 and 611, 1560 and 725 us.  Both kernels one behind the other, with
+  // over 8000 or 32000: 660 and 611, 1560 and 725 us.  The mean counts empty requests, which
+  // the host cannot tell from others: 4096 tokens over 4096, 8192 or 32768 keys 179, 360 and
+  // 1447 us as one request, 774, 1990 and 9340 padded to 1024; 10 decodes over 4000 keys and
+  // 2048 tokens over 8192 251 and 1178.  Both kernels one behind the other, with
   // the requests shared out between them: 466 and 605 us, but 6 to 12 us for the empty one where
   // all requests are alike, and 5% of the tiles' speed for the scheduler that passes over them.)
   const bool decode = q8 && a->dtype == KDA_BF16 && G <= 16 && (int64_t)a->T_total * G <= 16ll * a->B;

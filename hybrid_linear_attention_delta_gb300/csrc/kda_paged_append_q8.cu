@@ -15,10 +15,11 @@
 // 16-bit inputs a lane), so that every element is read once and written once.  A CTA
 // owns the runs whose first row is among its rows, and the q heads of its rows.
 //
-// HBM bounds it as far as bytes go: 32767 tokens of 32 / 8 heads of 128 channels, bf16, 181
-// us, 4.1 TB/s (the floor is 110 us).  The rest is instructions (a key is made twice, a q
-// head has a reduction and a rotation) and latency: a warp's loads are one run or four
-// passes of q heads, with the next four on their way.  64 tokens: 3.8 us, the launch.
+// HBM bounds it as far as bytes go: 32767 tokens of 32 / 8 heads of 128 channels, bf16, 188
+// us, 4.0 TB/s (the floor is 110 us), fp32 296 us, 4.8 TB/s.  The rest is instructions (a key
+// is made twice, norm and all, a q head has a reduction and a rotation) and latency: a warp's
+// loads are one run or four passes of q heads, with the next four on their way.  64 tokens:
+// 4 us, the launch; 8.5 where every block outgrows its scale.
 #include "kda_paged_e4m3.cuh"
 
 namespace kda {
@@ -232,7 +233,9 @@ __device__ __noinline__ void store_quotients(const AppendPlan &p, const int32_t 
 }
 
 // rows: rows of a CTA (at most kMaxRows); grid y shares out their units.  ROWS: a unit of
-// queries is a whole row.
+// queries is a whole row.  (Three CTAs an SM then: 80 registers, with 128 channels 108 to 168
+// bytes of spills, as queries and keys share them; two without spills: 32767 tokens 188 and
+// 199 us, 64 channels 103 and 116, fp32 295 and 311, 16000 tokens 104 and 102.)
 template <typename T, int D, bool HALVES, bool ROWS>
 __global__ void __launch_bounds__(kThreads, ROWS ? 3 : 2)
 append_kernel(const __grid_constant__ AppendPlan p, int rows) {

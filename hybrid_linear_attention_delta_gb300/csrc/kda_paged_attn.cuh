@@ -1680,7 +1680,9 @@ attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
   // warpgroup to the other two (168 a thread at the launch, 2 * 216 + 72 = 3 * 168; Q8:
   // 128, 2 * 200 + 2 * 56 or 2 * 208 + 2 * 48 = 4 * 128.  192 and 64, 200 and 56, 208 and 48, 216
   // and 40: mixed batch of 24, 64 channels, 1037, 1033, 995, 1124 us; with 128 1460, 1369, 1389,
-  // 1622, 64 x 8 tokens 265, 256, 268, 335, a chunk 2.83, 2.68, 2.65, 3.25 ms.)
+  // 1622, 64 x 8 tokens 265, 256, 268, 335, a chunk 2.83, 2.68, 2.65, 3.25 ms.  Q8 spills 228
+  // to 288 bytes a thread with 128 channels and 410 to 450 with 64; without the warp that
+  // loads the values and cuts the work it would be 64 to 88, so they are a piece's, not a tile's.)
   bool ok = true;
   if (!work) {  // bad cu_seqlens
   } else if (warp < kSoftmaxWarps) {

@@ -49,8 +49,8 @@ constexpr int kLongRun = 8192;
 
 template <int D>
 struct Smem {
-  // (2, 3, 4, 5 stages: 256 decodes over 511 to 8191 keys, 128 channels, 434, 408, 411,
-  // 428 us; 64 channels, with 3, 4, 8: 360, 361, 385)
+  // (2, 3, 4, 5, 6 stages: 256 decodes over 511 to 8191 keys, 128 channels, 421, 390, 391,
+  // 390, 396 us, 64 channels 303, 257, 255, 255, 255; 64 x 4 tokens 122, 111, 111, 111, 112)
   static constexpr int kStages = 3;
   static constexpr int kBytes = kStep * D;  // of the keys, or the values, of a step
   union {

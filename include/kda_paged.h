@@ -273,10 +273,14 @@ kda_status kda_paged_append_q8(const void *qkv, const int32_t *positions, const 
  * its bounds (bit 8192) is left out of the requests that hold it; its bytes must still be
  * finite.  In bf16 a row's largest channel keeps all its bits from 2^-119 up, and keys count
  * down to 2^-30 of a row's largest product of weight and scale of the values.  scale * q . k
- * must be finite with the keys' scales.
- * Which kernel runs is decided by the mean number of new tokens: a chunk of a prompt
- * among hundreds of decodes, with less than 16 rows (tokens times Hq / Hkv) a request
- * on average, is better a call of its own.
+ * must be finite with the keys' scales, as must scale times a query's largest channel times
+ * a key's scale be.
+ * In bf16 the mean number of rows (new tokens times Hq / Hkv) of all B requests, those
+ * without new tokens included, decides which kernel runs: up to 16 the one for few rows,
+ * which reads a request's keys again for every 16 of its rows.  A chunk of a prompt is slow
+ * there, among hundreds of decodes as in a batch padded to many requests (4096 tokens, 32 / 8
+ * heads of 128 channels, over 4096 keys: 179 us alone, 774 padded to 1024 requests; over
+ * 32768 keys 1.45 and 9.3 ms).  It is better a call of its own, with a B of its own.
  */
 kda_status kda_paged_attn_q8(const void *q, const void *k_pages, const void *v_pages,
                              const float *k_scales, const float *v_scales,
@@ -305,7 +309,9 @@ kda_status kda_paged_attn_q8(const void *q, const void *k_pages, const void *v_p
  * Sums are fp32 in a fixed order.  A row without a finite logit (bit 4096): logprobs
  * -inf, entropy 0, top_ids -1.  A row with a NaN or +inf (bit 16384): logprobs, entropy and
  * top_logprobs NaN, ranks and top_ids -1.  A token beyond V (bit 2048) counts as negative.
- * Finite logits are taken as they are, to the types' lowest and largest values.
+ * Finite logits are taken as they are, to the types' lowest and largest values.  (A mask is
+ * best -inf: rows in which finite masks leave fewer tokens than n_top fill their places with
+ * masked ones by their index, at ten to twenty times the time.)
  */
 typedef struct {
   int32_t N;          /* rows, up to 2^20 */
