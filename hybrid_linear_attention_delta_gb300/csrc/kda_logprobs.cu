@@ -498,7 +498,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(LogprobsPlan 
   const float log_l = log2f(s.l);
   auto lp = [&](float x) {
     if (bad || empty) return bad ? NAN : -INFINITY;
-    if (far(s.ref)) return fminf((x - s.m) * p.scale - log_l * kLn2, 0.f);
+    // (of halves: a difference of two floats may be none)
+    if (far(s.ref))
+      return fminf((0.5f * x - 0.5f * s.m) * (2.f * p.scale) - log_l * kLn2, 0.f);
     // (below the least: so far down that nothing else counts)
     return x < least ? x * p.scale : fminf((fmaf(x, c, -s.ref) - log_l) * kLn2, 0.f);
   };

@@ -135,6 +135,31 @@ def test_most_likely_tokens_as_given_tokens(kind):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [2.0 ** -64, 1e-12, 0.25, 0.9, 1.0])
+@pytest.mark.parametrize("V", [5, 3001])
+def test_logits_further_apart_than_the_largest_float(kind, scale, V):
+    """The largest logit and a token at the type's lowest value, whose difference is no
+    float while its product with the scale may be one."""
+    low, high = torch.finfo(DT[kind]).min, torch.finfo(DT[kind]).max
+    x = _logits(4, V, kind, 6)
+    x[:, 1] = low
+    x[:, 3] = torch.tensor([high, high / 2, high / 64, 3e38], device="cuda").to(DT[kind])
+    x[2, 4] = x[2, 3]
+    K = 5
+    r, ws = _call(x, torch.full((4,), 1, dtype=torch.int32, device="cuda"), K, scale)
+    assert kda.kda_device_status(ws) == (kda.KDA_OK, 0)
+    d = (x.double() - x.double().amax(1, keepdim=True)) * scale
+    lp = (d - torch.logsumexp(d, 1, keepdim=True)).cpu()
+    order = torch.sort(x.double(), descending=True, stable=True).indices[:, :K].cpu()
+    assert torch.equal(r["ids"].cpu().long(), order)
+    # (the scale, a difference, its product with it and the sum's logarithm are rounded once each)
+    for got, want in ((r["lp"].cpu(), lp[:, 1]), (r["top"].cpu(), lp.gather(1, order))):
+        inf = want < -torch.finfo(F32).max
+        assert (got[inf] == -math.inf).all()
+        assert ((got.double() - want).abs() <= 4 * U * want.abs() + 4 * U)[~inf].all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
 @pytest.mark.parametrize("N", [1, 3, 300])
 def test_rows_of_any_stride_and_alignment(kind, N):
     """Rows that start on any element, with NaNs between them."""
